@@ -273,7 +273,7 @@ def _round8(x, rnd, mant, emin):
     drop = 23 - mant
     mag = x.abs()
     up = ((mag.view(torch.int32) + (rnd << (drop - 16))) >> drop) << drop
-    sub = torch.floor(mag * 2.0 ** (mant - emin) + rnd.float() * 2.0 ** -16) * 2.0 ** (emin - mant)
+    sub = (((mag.clamp(max=2.0 ** emin) * 2.0 ** (mant - emin + 16)).to(torch.int32) + rnd) >> 16).float() * 2.0 ** (emin - mant)
     return torch.copysign(torch.where(mag < 2.0 ** emin, sub, up.view(torch.float32)), x)
 
 
