@@ -13,11 +13,10 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
-#include <cstring>
 #include <initializer_list>
 #include <mutex>
 
-#include "../../include/wqmlp.h"
+#include "abi_common.h"
 #include "launch.h"
 
 // Static scratch of mlp_fp8w_run_noalloc: one array per device, part of the library's code object; the
@@ -29,84 +28,7 @@ static __device__ __align__(256) uint8_t scratch[WQ_STATIC_SCRATCH_BYTES];
 
 namespace {
 
-thread_local int g_last_hip = 0;
-
-struct Rng {
-  const void* p;
-  size_t n;
-};
-
-bool overlaps(Rng a, Rng b) {
-  if (a.n == 0 || b.n == 0) return false;
-  const uintptr_t a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
-  return a0 < b0 + b.n && b0 < a0 + a.n;
-}
-
-bool any_overlap(std::initializer_list<Rng> outs, std::initializer_list<Rng> ins) {
-  for (const Rng& o : outs)
-    for (const Rng& i : ins)
-      if (overlaps(o, i)) return true;
-  // outputs must not overlap each other either
-  for (auto a = outs.begin(); a != outs.end(); ++a)
-    for (auto b = a + 1; b != outs.end(); ++b)
-      if (overlaps(*a, *b)) return true;
-  return false;
-}
-
-bool all_aligned(std::initializer_list<const void*> ps) {
-  for (const void* p : ps)
-    if (((uintptr_t)p & 15u) != 0) return false;
-  return true;
-}
-
-bool any_null(std::initializer_list<const void*> ps) {
-  for (const void* p : ps)
-    if (p == nullptr) return true;
-  return false;
-}
-
-size_t align256(size_t v) { return (v + 255) / 256 * 256; }
-
-// ---- device checks (phase 2) ---------------------------------------------------------------------
-constexpr int kMaxDev = 64;
-std::once_flag g_arch_once[kMaxDev];
-int g_arch_ok[kMaxDev];
-
-int check_device(std::initializer_list<const void*> ptrs) {
-  int dev = -1;
-  hipError_t e = hipGetDevice(&dev);
-  if (e != hipSuccess || dev < 0 || dev >= kMaxDev) {
-    g_last_hip = (int)e;
-    return WQ_EDEVICE;
-  }
-  std::call_once(g_arch_once[dev], [dev] {
-    hipDeviceProp_t p;
-    g_arch_ok[dev] = hipGetDeviceProperties(&p, dev) == hipSuccess && std::strncmp(p.gcnArchName, "gfx950", 6) == 0;
-  });
-  if (!g_arch_ok[dev]) return WQ_EARCH;
-  for (const void* p : ptrs) {
-    if (p == nullptr) continue;
-    hipPointerAttribute_t a;
-    e = hipPointerGetAttributes(&a, p);
-    if (e != hipSuccess) {
-      (void)hipGetLastError();  // clear the sticky error left by an unknown pointer
-      g_last_hip = (int)e;
-      return WQ_EDEVICE;
-    }
-    if (a.type != hipMemoryTypeDevice || a.device != dev) return WQ_EDEVICE;
-  }
-  return WQ_OK;
-}
-
-int launched(hipError_t e) {
-  if (e != hipSuccess) {
-    g_last_hip = (int)e;
-    return WQ_ELAUNCH;
-  }
-  return WQ_OK;
-}
-
-size_t xsize(int dt) { return dt == WQ_F32 ? 4 : 2; }
+using namespace wq::abi;
 
 // GEMV activation staging must fit one workgroup's LDS (160 KiB on gfx950).
 bool gemv_fits(int fmt, int64_t K, int dt) {
@@ -115,14 +37,7 @@ bool gemv_fits(int fmt, int64_t K, int dt) {
   return per_row <= 160 * 1024;
 }
 
-constexpr int64_t kMaxDim = WQ_MAX_DIM;
-// rows x columns of any activation or output matrix (keeps tile and grid counts in int)
-constexpr int64_t kMaxElems = WQ_MAX_ELEMS;
 bool elems_ok(int64_t M, int64_t a, int64_t b) { return M * std::max(a, b) <= kMaxElems; }
-
-size_t wbytes(int fmt, int64_t N, int64_t K) {
-  return fmt == WQ_FMT_FP8W ? (size_t)N * (size_t)K : (size_t)N * (size_t)(K / 64) * 36;
-}
 
 // AUTO: the MFMA GEMM for M >= WQ_MFMA_MIN_ROWS, and for shorter batches of at least the format's
 // WQ_NARROW_MIN_ROWS_* rows when the call's weights hold at least WQ_NARROW_MIN_WEIGHT_BYTES and both
