@@ -35,5 +35,7 @@ from .mlp import silu, swiglu_mlp, mlp_fp8w_ref, mlp_nvfp4_ref, mlp_nvfp4_w4a8_r
 from .actquant import token_exponent, e4m3_encode_rne, quant_e4m3_per_token
 from .moe import moe_awq_m1_ref, moe_w13_stage_ref, moe_w2_stage_ref, moe_bruteforce
 from .metric import normwise_rel_err
+from .adapters import (lora_ref, lora_backward_ref, adamw_ref, adamw8_states, adamw_random_bits, stochastic_code,
+                       E4M3_GRID, E5M2_GRID)
 
 __all__ = [n for n in dir() if not n.startswith("_")]

@@ -1,4 +1,4 @@
-"""Python binding of libwqmlp (the C ABI declared in include/wqmlp.h).
+"""Python binding of libwqmlp (the C ABI declared in include/wqmlp.h and include/wqmlp_adapters.h).
 
 Argument marshalling only: torch tensors provide device memory and the
 current HIP stream; every step of the computation runs in the library's
@@ -20,6 +20,8 @@ __all__ = [
     "WQ_STATIC_SCRATCH_BYTES", "mlp_workspace_bytes", "mlp_fp8w_run", "mlp_fp8w_run_noalloc", "mlp_nvfp4_run", "awq_bank_bytes", "moe_awq_m1_run",
     "nvfp4_pack_block64", "awq_pack_bank", "fp8w_dequant_f32", "nvfp4_dequant_f32", "awq_dequant_f16",
     "qlinear_workspace_bytes", "qlinear_run", "wq_read_probe",
+    "WQ_LORA_MAX_RANK", "WQ_ADAMW_BLOCK", "lora_workspace_bytes", "lora_run", "lora_backward",
+    "qlinear_backward_workspace_bytes", "qlinear_backward", "adamw_table_bytes", "AdamWTable", "adamw_table", "adamw_run",
 ]
 
 WQ_F32, WQ_BF16, WQ_F16 = 0, 1, 2
@@ -28,6 +30,8 @@ WQ_PATH_AUTO, WQ_PATH_GEMV, WQ_PATH_MFMA = 0, 1, 2
 WQ_STAGE_GATEUP_ONLY, WQ_STAGE_DOWN_ONLY = 4, 8
 WQ_ACT_E4M3 = 16
 WQ_STATIC_SCRATCH_BYTES = 32 << 20
+WQ_LORA_MAX_RANK = 256
+WQ_ADAMW_BLOCK = 256
 _PATHS = {"auto": WQ_PATH_AUTO, "gemv": WQ_PATH_GEMV, "mfma": WQ_PATH_MFMA}
 _STAGES = {None: 0, "gateup": WQ_STAGE_GATEUP_ONLY, "down": WQ_STAGE_DOWN_ONLY}
 _ACTS = {None: 0, "e4m3": WQ_ACT_E4M3}
@@ -41,6 +45,7 @@ _I64 = ctypes.c_int64
 _INT = ctypes.c_int
 _F = ctypes.c_float
 _SZ = ctypes.c_size_t
+_D = ctypes.c_double
 _SIGS = {
     "wq_abi_version": (_INT, []),
     "wq_strerror": (ctypes.c_char_p, [_INT]),
@@ -59,7 +64,21 @@ _SIGS = {
     "qlinear_workspace_bytes": (_SZ, [_INT, _I64, _I64, _I64, _INT]),
     "qlinear_run": (_INT, [_INT, _I64, _I64, _I64, _P, _INT, _P, _P, _F, _P, _SZ, _P, _INT, _P]),
     "wq_read_probe": (_INT, [_P, _SZ, _P, _INT, _P]),
+    "lora_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I64, _INT]),
+    "lora_run": (_INT, [_I64, _I64, _I64, _I64, _I64, _P, _INT, _P, _P, _INT, _P, _P, _P, _P, _SZ, _P, _P]),
+    "lora_backward": (_INT, [_I64, _I64, _I64, _I64, _I64, _P, _INT, _P, _INT, _P, _P, _INT, _P, _P, _P, _INT, _P, _SZ,
+                             _P, _P, _P, _P]),
+    "qlinear_backward_workspace_bytes": (_SZ, [_INT, _I64, _I64, _I64, _INT]),
+    "qlinear_backward": (_INT, [_INT, _I64, _I64, _I64, _P, _INT, _P, _P, _F, _P, _SZ, _P, _INT, _P]),
+    "adamw_table_bytes": (_SZ, [_I64]),
+    "adamw_table_build": (_INT, [_I64, _P, _INT, _P, _SZ, _P]),
+    "adamw_run": (_INT, [_I64, _I64, _INT, _P, _P, _P, _D, _D, _D, _D, _F, ctypes.c_uint32, _P]),
 }
+
+
+class _AdamWTensor(ctypes.Structure):   # wq_adamw_tensor
+    _fields_ = [("n", _I64), ("p", _P), ("g", _P), ("m", _P), ("v", _P), ("m_scale", _P), ("v_scale", _P), ("copy", _P),
+                ("g_dtype", ctypes.c_int32), ("copy_dtype", ctypes.c_int32)]
 
 
 class WQError(RuntimeError):
@@ -342,3 +361,180 @@ def wq_read_probe(src, sink, nbytes=None, grid=None):
     if grid > sink.numel() or nbytes > src.numel() * src.element_size():
         raise ValueError("grid exceeds sink or nbytes exceeds src")
     _check("wq_read_probe", lib().wq_read_probe(_ptr(src), nbytes, _ptr(sink), grid, _stream(dev)))
+
+
+_FLOATS = {torch.float32: WQ_F32, torch.bfloat16: WQ_BF16, torch.float16: WQ_F16}
+
+
+def _float_code(dtype, name, allowed=(torch.float32, torch.bfloat16, torch.float16)):
+    if dtype not in allowed:
+        raise TypeError(f"{name} must be one of {[str(d) for d in allowed]}, got {dtype}")
+    return _FLOATS[dtype]
+
+
+def lora_workspace_bytes(M, K, N, E, R, backward=False):
+    return lib().lora_workspace_bytes(M, K, N, E, R, int(backward))
+
+
+def _lora_args(x, a, b, scale, ids):
+    """Checks shared by the forward and the backward call; (M, K, N, E, R, x code, weight code)."""
+    if x.dim() != 2 or a.dim() != 3 or b.dim() != 3:
+        raise ValueError("x must be [M, K], a [E, R, K] and b [E, N, R]")
+    dev = x.device
+    M, K = x.shape
+    E, R, _ = a.shape
+    N = b.shape[1]
+    if tuple(a.shape) != (E, R, K) or tuple(b.shape) != (E, N, R):
+        raise ValueError(f"a must be [E, R, {K}] and b [E, N, R], got {tuple(a.shape)} and {tuple(b.shape)}")
+    xt, wt = _float_code(x.dtype, "x"), _float_code(a.dtype, "a")
+    _need(x, "x", x.dtype, dev)
+    _need(a, "a", a.dtype, dev)
+    _need(b, "b", a.dtype, dev)
+    _need(scale, "scale", torch.float32, dev, E)
+    _need(ids, "ids", torch.int32, dev, M)
+    return M, K, N, E, R, xt, wt
+
+
+def lora_run(x, a, b, scale, ids, y, out=None, workspace=None):
+    """out[m] = y[m] + scale[e] * (x[m] a[e]^T) b[e]^T with e = ids[m]; out[m] = y[m] where ids[m] is outside [0, E).
+
+    x [M,K] f32/bf16/f16; a [E,R,K] and b [E,N,R] f32/bf16/f16; scale [E] f32; ids [M] int32; y [M,N] f32 (a
+    projection's result) or None for zeros.  out [M,N] f32 (may be y: in place)."""
+    M, K, N, E, R, xt, wt = _lora_args(x, a, b, scale, ids)
+    dev = x.device
+    if y is not None:
+        _need(y, "y", torch.float32, dev, M * N)
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.float32, device=dev)
+    _need(out, "out", torch.float32, dev, M * N)
+    ws = _workspace(lora_workspace_bytes(M, K, N, E, R), dev, workspace)
+    rc = lib().lora_run(M, K, N, E, R, _ptr(x), xt, _ptr(a), _ptr(b), wt, _ptr(scale), _ptr(ids), _ptr(y), _ptr(ws),
+                        ws.numel(), _ptr(out), _stream(dev))
+    _check("lora_run", rc)
+    return out
+
+
+def lora_backward(dy, x, a, b, scale, ids, dx0=None, dx=None, da=None, db=None, workspace=None, dx_dtype=None,
+                  need=(True, True, True)):
+    """Gradients of lora_run: (dx, da, db).  dx = dx0 (None: zeros) + the adapters' part, of dx0's type (or dx_dtype,
+    default x's); da, db float32, summed over each adapter's rows.  need: which of (dx, da, db) to compute (others
+    None).  dx may be dx0 (in place)."""
+    M, K, N, E, R, xt, wt = _lora_args(x, a, b, scale, ids)
+    dev = x.device
+    dyt = _float_code(dy.dtype, "dy", (torch.float32, torch.bfloat16))
+    _need(dy, "dy", dy.dtype, dev, M * N)
+    want = dx.dtype if dx is not None else dx0.dtype if dx0 is not None else dx_dtype or x.dtype
+    dxt = _float_code(want, "dx")
+    if dx0 is not None:
+        _need(dx0, "dx0", want, dev, M * K)
+    outs = []
+    for t, name, shape, dtype, wanted in ((dx, "dx", (M, K), want, need[0]), (da, "da", (E, R, K), torch.float32, need[1]),
+                                          (db, "db", (E, N, R), torch.float32, need[2])):
+        if not wanted:
+            outs.append(None)
+            continue
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=dev)
+        outs.append(_need(t, name, dtype, dev, shape[0] * shape[1] * (shape[2] if len(shape) == 3 else 1)))
+    ws = _workspace(lora_workspace_bytes(M, K, N, E, R, True), dev, workspace)
+    rc = lib().lora_backward(M, K, N, E, R, _ptr(dy), dyt, _ptr(x), xt, _ptr(a), _ptr(b), wt, _ptr(scale), _ptr(ids),
+                             _ptr(dx0), dxt, _ptr(ws), ws.numel(), _ptr(outs[0]), _ptr(outs[1]), _ptr(outs[2]), _stream(dev))
+    _check("lora_backward", rc)
+    return tuple(outs)
+
+
+def qlinear_backward_workspace_bytes(fmt, M, N, K, dx_dtype=torch.float32):
+    return lib().qlinear_backward_workspace_bytes(fmt, M, N, K, _FLOATS[dx_dtype])
+
+
+def qlinear_backward(fmt, dy, w, scale=None, global_scale=1.0, dtype=None, out=None, workspace=None):
+    """dx = dy dq(W): the gradient of qlinear_run with respect to its input.  dy [M,N] f32/bf16; w, scale and
+    global_scale as for qlinear_run; dx [M,K] f32/bf16 (out's type, or dtype, default dy's)."""
+    dev = dy.device
+    M, N = dy.shape
+    dyt = _float_code(dy.dtype, "dy", (torch.float32, torch.bfloat16))
+    _need(dy, "dy", dy.dtype, dev)
+    _need(w, "w", torch.uint8, dev)
+    if w.shape[0] != N:
+        raise ValueError(f"w must have {N} rows, has {w.shape[0]}")
+    K = w.numel() // 36 * 64 // N if fmt == WQ_FMT_NVFP4 else w.numel() // N
+    _need(w, "w", torch.uint8, dev, N * (K // 64) * 36 if fmt == WQ_FMT_NVFP4 else N * K)
+    if scale is not None:
+        _need(scale, "scale", torch.float32, dev, N)
+    want = out.dtype if out is not None else dtype or dy.dtype
+    dxt = _float_code(want, "dx", (torch.float32, torch.bfloat16))
+    if out is None:
+        out = torch.empty((M, K), dtype=want, device=dev)
+    _need(out, "out", want, dev, M * K)
+    ws = _workspace(qlinear_backward_workspace_bytes(fmt, M, N, K, want), dev, workspace)
+    rc = lib().qlinear_backward(fmt, M, N, K, _ptr(dy), dyt, _ptr(w), _ptr(scale), float(global_scale), _ptr(ws), ws.numel(),
+                                _ptr(out), dxt, _stream(dev))
+    _check("qlinear_backward", rc)
+    return out
+
+
+def adamw_table_bytes(count):
+    return lib().adamw_table_bytes(count)
+
+
+class AdamWTable:
+    """A built AdamW table: the device buffer and references to the tensors whose addresses it holds."""
+
+    def __init__(self, table, count, elems, bits, tensors):
+        self.table, self.count, self.elems, self.bits, self.tensors = table, count, elems, bits, tensors
+
+
+def adamw_table(params, grads, m, v, copies=None, m_scales=None, v_scales=None):
+    """Table of the tensors adamw_run steps over (lists of equal length): params f32, grads f32/bf16, states m and v
+    f32, or, with m_scales and v_scales (f32, one per WQ_ADAMW_BLOCK elements), 8-bit codes (float8_e4m3fn and
+    float8_e5m2, or their uint8 views); copies: bf16/f16 tensors that receive the rounded parameters (entries may be
+    None).  The table holds addresses: rebuild it when a tensor is replaced.  Waits for the current stream."""
+    count = len(params)
+    bits = 8 if m_scales is not None else 32
+    if (m_scales is None) != (v_scales is None):
+        raise ValueError("m_scales and v_scales come together")
+    lists = {"grads": grads, "m": m, "v": v, "copies": copies, "m_scales": m_scales, "v_scales": v_scales}
+    for name, ts in lists.items():
+        if ts is not None and len(ts) != count:
+            raise ValueError(f"{name} must have {count} entries, has {len(ts)}")
+    if count == 0:
+        raise ValueError("no tensors")
+    dev = params[0].device
+    kinds = {"m": (torch.float8_e4m3fn, torch.uint8), "v": (torch.float8_e5m2, torch.uint8)}
+    arr = (_AdamWTensor * count)()
+    for i, p in enumerate(params):
+        n = p.numel()
+        _need(p, f"params[{i}]", torch.float32, dev)
+        t = arr[i]
+        t.n, t.p = n, _ptr(p)
+        t.g_dtype = _float_code(grads[i].dtype, f"grads[{i}]", (torch.float32, torch.bfloat16))
+        t.g = _ptr(_need(grads[i], f"grads[{i}]", grads[i].dtype, dev, n))
+        for name, s in (("m", m[i]), ("v", v[i])):
+            if bits == 8 and s.dtype not in kinds[name]:
+                raise TypeError(f"{name}[{i}] must be {kinds[name][0]} or torch.uint8, got {s.dtype}")
+            setattr(t, name, _ptr(_need(s, f"{name}[{i}]", s.dtype if bits == 8 else torch.float32, dev, n)))
+        if bits == 8:
+            blocks = (n + WQ_ADAMW_BLOCK - 1) // WQ_ADAMW_BLOCK
+            t.m_scale = _ptr(_need(m_scales[i], f"m_scales[{i}]", torch.float32, dev, blocks))
+            t.v_scale = _ptr(_need(v_scales[i], f"v_scales[{i}]", torch.float32, dev, blocks))
+        c = copies[i] if copies is not None else None
+        if c is not None:
+            t.copy_dtype = _float_code(c.dtype, f"copies[{i}]", (torch.bfloat16, torch.float16))
+            t.copy = _ptr(_need(c, f"copies[{i}]", c.dtype, dev, n))
+    table = torch.empty(max(adamw_table_bytes(count), 1), dtype=torch.uint8, device=dev)
+    _check("adamw_table_build", lib().adamw_table_build(count, arr, bits, _ptr(table), table.numel(), _stream(dev)))
+    torch.cuda.current_stream(dev).synchronize()      # built once: steps on any stream may follow
+    keep = (list(params), list(grads), list(m), list(v), copies and list(copies), m_scales and list(m_scales),
+            v_scales and list(v_scales))
+    return AdamWTable(table, count, sum(p.numel() for p in params), bits, keep)
+
+
+def adamw_run(table, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, grad_scale=1.0, seed=0):
+    """One AdamW step over the table's tensors, in place.  step: int64 device tensor holding t >= 1; lr: float32
+    device tensor (both read on the device when the step runs); seed: of the 8-bit states' stochastic rounding."""
+    dev = table.table.device
+    _need(step, "step", torch.int64, dev, 1)
+    _need(lr, "lr", torch.float32, dev, 1)
+    rc = lib().adamw_run(table.count, table.elems, table.bits, _ptr(table.table), _ptr(step), _ptr(lr), beta1, beta2, eps,
+                         weight_decay, grad_scale, seed & 0xFFFFFFFF, _stream(dev))
+    _check("adamw_run", rc)

@@ -97,6 +97,45 @@ hipError_t launch_moe_awq_m1(int E, int topk, int H, int I, const uint16_t* x, c
                              const float* router_w, const uint8_t* w13, const uint8_t* w2, int meta_layout,
                              uint16_t* act, uint16_t* out, hipStream_t st);
 
+// ---- low-rank adapters, input gradient, AdamW (include/wqmlp_adapters.h) ---------------------------
+// Scratch bytes are functions of the shape alone; ws may be null where they are 0.
+size_t lora_scratch_bytes(int M, int K, int N, int E, int R, bool backward);
+hipError_t launch_lora(int M, int K, int N, int E, int R, const void* x, XType xt, const void* a, const void* b, XType wt,
+                       const float* scale, const int32_t* ids, const float* y, void* ws, float* out, hipStream_t st);
+// dx, da, db may each be null (not computed); M may be 0 (da and db become zeros).
+hipError_t launch_lora_backward(int M, int K, int N, int E, int R, const void* dy, XType dyt, const void* x, XType xt,
+                                const void* a, const void* b, XType wt, const float* scale, const int32_t* ids,
+                                const void* dx0, XType dxt, void* ws, void* dx, float* da, float* db, hipStream_t st);
+size_t linear_grad_scratch_bytes(int fmt, int M, int N, int K, XType dxt);
+hipError_t launch_linear_grad(int fmt, int M, int N, int K, const void* dy, XType dyt, const uint8_t* w, const float* scale,
+                              float inv, void* ws, void* dx, XType dxt, hipStream_t st);
+
+// One tensor of an AdamW table; chunk0: number of chunks (adamw_chunks) of the tensors before it.
+struct AdamwEntry {
+  int64_t n, chunk0;
+  float* p;
+  const void* g;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  void* copy;
+  int32_t g_dtype, copy_dtype;
+};
+constexpr int kAdamwBatch = 32;   // entries one table launch writes (they travel as kernel arguments)
+// table: int64 {count, total chunks, state bits}, int64 chunk0[count + 1], entries
+constexpr int64_t kAdamwHead = 3;
+constexpr int64_t adamw_entries_offset(int64_t count) { return (kAdamwHead + count + 1) * 8; }
+constexpr int64_t adamw_layout_bytes(int64_t count) {
+  return adamw_entries_offset(count) + count * (int64_t)sizeof(AdamwEntry);
+}
+int64_t adamw_chunks(int64_t n);
+hipError_t launch_adamw_table(int64_t count, int64_t first, int n, int64_t total, int bits, const AdamwEntry* e,
+                              void* table, hipStream_t st);
+hipError_t launch_adamw(int64_t count, int64_t elems, int bits, const void* table, const int64_t* step, const float* lr,
+                        double beta1, double beta2, double eps, double weight_decay, float grad_scale, uint32_t seed,
+                        hipStream_t st);
+
 // ---- packers and debug decoders -------------------------------------------------------------
 hipError_t launch_nvfp4_pack(int64_t N, int64_t K, const uint8_t* wp, const uint8_t* ws, uint8_t* blk,
                              hipStream_t st);
