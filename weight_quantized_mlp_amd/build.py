@@ -13,6 +13,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 SOURCES = ["abi.cpp", "abi_adapters.cpp", "adamw.hip", "gemv.hip", "gemv_fast.hip", "linear_grad.hip", "lora.hip",
+           "lora_expand.hip", "lora_outer.hip", "lora_shrink.hip",
            "mfma.hip", "moe.hip", "pack.hip", "probe.hip"]
 LIB = os.path.join(HERE, "libwqmlp.so")
 ARCH = "gfx950"

@@ -1,0 +1,232 @@
+// Low-rank adapters, the weight gradients (gfx950): g[e][r,d] = scale[e] sum over the rows m of adapter e of
+// t[m,r] v[m,d]  (db from t = x a^T and v = dy, da from t = dy b and v = x).
+//
+// v is the bytes, read once per adapter that a block of rows names.  A workgroup owns one adapter, 64 columns d and
+// up to 64 ranks; its 4 waves take blocks of 32 rows in turn, each with its own accumulators, so no barrier stands
+// between blocks, and add them through LDS at the end.  Which blocks hold rows of the adapter is found first, from
+// the ids, as one 32-bit mask per block; other blocks are never loaded, and rows of other adapters enter as zeros
+// (in v as well, so that nothing a foreign row holds can reach the sum).  Both operands have the contraction (rows)
+// as their slow index, so both go through the wave's transposing LDS tiles; the next block's loads are issued before
+// this block's MFMAs.  Long batches with few adapters split the rows over up to 8 workgroups, joined in order by a
+// second kernel.
+#include <algorithm>
+
+#include "lora_common.h"
+
+namespace wq {
+
+namespace {
+
+using namespace lora;
+
+constexpr int kD = 64;               // columns of a workgroup
+constexpr int kScan = 4096;          // rows whose masks are held at once
+
+template <int VT, int NR> constexpr int outer_wave_lds() { return terms<VT>() * tr_plane<kD>() + 3 * tr_plane<16 * NR>(); }
+template <int VT, int NR> constexpr int outer_lds() {
+  const int stage = 4 * outer_wave_lds<VT, NR>(), red = 4 * 16 * NR * kD * 4;
+  return stage > red ? stage : red;
+}
+
+// Rows of one workgroup's part: a multiple of kRows.
+inline int outer_part_rows(int M, int parts) { return ((M + parts - 1) / parts + kRows - 1) / kRows * kRows; }
+
+template <int VT, int NR, bool RCONTIG>
+__global__ void __launch_bounds__(256) lora_outer_kernel(int M, int D, int E, int R, int S, int parts, int part_rows,
+                                                         int64_t total, const float* __restrict__ t,
+                                                         const uint8_t* __restrict__ v, const float* __restrict__ scale,
+                                                         const int32_t* __restrict__ ids, float* __restrict__ g) {
+  constexpr int C = 16 * NR, NV = terms<VT>();
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  __shared__ uint32_t masks[kScan / kRows];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int l16 = lane & 15, gr = lane >> 4;
+  const int nd = (D + kD - 1) / kD, RC = (R + C - 1) / C;
+  uint8_t* vt = lds + wave * outer_wave_lds<VT, NR>();
+  uint8_t* ut = vt + NV * tr_plane<kD>();
+  for (int64_t wg = blockIdx.x; wg < total; wg += gridDim.x) {
+    // columns fastest, then rank chunks, parts and adapters
+    const int d0 = (int)(wg % nd) * kD;
+    const int64_t w1 = wg / nd, w2 = w1 / RC;
+    const int r0 = (int)(w1 % RC) * C, part = (int)(w2 % parts), e = (int)(w2 / parts);
+    const int mb = part * part_rows, me = min(mb + part_rows, M);
+    f32x4 acc[NR][4];
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    float f = 0.f;
+
+    for (int s0 = mb; s0 < me; s0 += kScan) {
+      __syncthreads();                                  // the masks' and the tiles' last readers
+#pragma unroll 4
+      for (int i = wave; i < kScan / 64; i += 4) {
+        const int m = s0 + 64 * i + lane;
+        const uint64_t b = __ballot(m < me && ids[min(m, me - 1)] == e);
+        if (lane < 2) masks[2 * i + lane] = (uint32_t)(b >> (32 * lane));
+      }
+      __syncthreads();
+      const int blocks = (min(kScan, me - s0) + kRows - 1) / kRows;
+      auto next = [&](int b) {
+        while (b < blocks && masks[b] == 0) b += 4;
+        return b;
+      };
+      // one block's loads: v as 4 chunks of 8 columns per lane, t as NR groups of... 32 x C float32, 4 at a time
+      Raw<VT> raw[4];
+      f32x4 u[2 * NR];
+      uint32_t mask = 0;
+      auto load = [&](int b) {
+        mask = masks[b];
+        const int m0 = s0 + kRows * b;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int c = lane + 64 * q, row = c >> 3, d = d0 + 8 * (c & 7);
+          const bool on = (mask >> row & 1) != 0;
+          const uint8_t* p = v + ((size_t)(m0 + row) * D + d) * esize<VT>();
+          if (on && d + 8 <= D) raw_load<VT, false>(p, raw[q]);
+          else raw_load_part<VT>(p, on ? D - d : 0, raw[q]);
+        }
+#pragma unroll
+        for (int q = 0; q < 2 * NR; ++q) {
+          const int c = lane + 64 * q, row = c / (C / 4), r = r0 + 4 * (c % (C / 4));
+          u[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+          if ((mask >> row & 1) && r < R) {
+            const float* p = t + (size_t)(m0 + row) * R + r;
+            for (int s = 0; s < S; ++s, p += (size_t)M * R) u[q] += *reinterpret_cast<const f32x4*>(p);
+          }
+        }
+      };
+      int b = next(wave);
+      if (b < blocks) {
+        f = scale[e];
+        load(b);
+      }
+      while (b < blocks) {
+        wave_lds_fence();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tr_write<VT, kD>(vt, lane + 64 * q, raw[q]);
+#pragma unroll
+        for (int q = 0; q < 2 * NR; ++q) {
+          const int c = lane + 64 * q, row = c / (C / 4), col = 4 * (c % (C / 4));
+          const bool on = (mask >> row & 1) != 0;        // 0 * scale could be NaN
+          float x[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) x[j] = on ? u[q][j] * f : 0.f;
+          bf16x4 th[3];
+          split3<4>(x, th);
+#pragma unroll
+          for (int i = 0; i < 3; ++i)
+            *reinterpret_cast<bf16x4*>(ut + i * tr_plane<C>() + row * tr_stride<C>() + 2 * col) = th[i];
+        }
+        wave_lds_fence();
+        b = next(b + 4);
+        if (b < blocks) load(b);
+        bf16x8 uf[NR][3];
+#pragma unroll
+        for (int i = 0; i < NR; ++i) tr_read<C, 3>(ut, i, uf[i]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          bf16x8 vf[NV];
+          tr_read<kD, NV>(vt, j, vf);
+#pragma unroll
+          for (int i = 0; i < NR; ++i)
+            acc[i][j] = RCONTIG ? mfma_terms<3, NV>(uf[i], vf, acc[i][j]) : mfma_terms<NV, 3>(vf, uf[i], acc[i][j]);
+        }
+      }
+    }
+
+    // the waves' sums in wave order; fragment (i, j), lane: RCONTIG ranks 16 i + 4 gr .. + 3 of column 16 j + l16,
+    // else columns 16 j + 4 gr .. + 3 of rank 16 i + l16
+    __syncthreads();
+    f32x4* red = reinterpret_cast<f32x4*>(lds);
+#pragma unroll
+    for (int i = 0; i < NR; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) red[(wave * 4 * NR + 4 * i + j) * 64 + lane] = acc[i][j];
+    __syncthreads();
+    float* ge = g + ((size_t)part * E + e) * (size_t)R * D;
+#pragma unroll
+    for (int fr = 0; fr < NR; ++fr) {
+      const int k = 4 * fr + wave, i = k >> 2, j = k & 3;
+      f32x4 s = red[k * 64 + lane];
+#pragma unroll
+      for (int q = 1; q < 4; ++q) s += red[(q * 4 * NR + k) * 64 + lane];
+      if constexpr (RCONTIG) {
+        const int d = d0 + 16 * j + l16, r = r0 + 16 * i + 4 * gr;
+        if (d < D && r < R) *reinterpret_cast<f32x4*>(ge + (size_t)d * R + r) = s;
+      } else {
+        const int d = d0 + 16 * j + 4 * gr, r = r0 + 16 * i + l16;
+        if (d < D && r < R) *reinterpret_cast<f32x4*>(ge + (size_t)r * D + d) = s;
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// out[i] = the sum of `parts` arrays of n float32 (a multiple of 4), in order.
+__global__ void __launch_bounds__(256) lora_join_kernel(int64_t n4, int parts, const f32x4* __restrict__ p,
+                                                        f32x4* __restrict__ out) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
+    f32x4 s = p[i];
+    for (int q = 1; q < parts; ++q) s += p[(int64_t)q * n4 + i];
+    out[i] = s;
+  }
+}
+
+inline int64_t outer_tiles(int D, int E, int R) {
+  const int C = R <= 16 ? 16 : (R <= 32 ? 32 : 64);
+  return (int64_t)E * ((D + kD - 1) / kD) * ((R + C - 1) / C);
+}
+// Parts of the rows: workgroups for four per CU, each part at least 256 rows, at most 8.
+inline int outer_parts(int M, int D, int E, int R) {
+  const int64_t tiles = outer_tiles(D, E, R);
+  int p = (int)std::min<int64_t>(8, 1024 / std::max<int64_t>(1, tiles));
+  p = std::min(p, M / 256);
+  if (p <= 1) return 1;
+  const int rows = outer_part_rows(M, p);
+  return (M + rows - 1) / rows;
+}
+
+template <int VT, int NR, bool RCONTIG>
+hipError_t go(int M, int D, int E, int R, int S, const float* t, const void* v, const float* scale, const int32_t* ids,
+              float* g, float* ws, hipStream_t st) {
+  if (!raise_lds_limit<lora_outer_kernel<VT, NR, RCONTIG>>()) return hipErrorInvalidValue;
+  const int parts = outer_parts(M, D, E, R);
+  const int64_t total = outer_tiles(D, E, R) * parts;
+  float* dst = parts > 1 ? ws : g;
+  hipLaunchKernelGGL((lora_outer_kernel<VT, NR, RCONTIG>), dim3((unsigned)std::min<int64_t>(total, 1 << 20)), dim3(256),
+                     (outer_lds<VT, NR>()), st, M, D, E, R, S, parts, outer_part_rows(std::max(M, 1), parts), total, t,
+                     reinterpret_cast<const uint8_t*>(v), scale, ids, dst);
+  if (parts > 1) {
+    const int64_t n4 = (int64_t)E * R * D / 4;
+    hipLaunchKernelGGL(lora_join_kernel, dim3((unsigned)std::min<int64_t>((n4 + 255) / 256, 2048)), dim3(256), 0, st, n4,
+                       parts, reinterpret_cast<const f32x4*>(ws), reinterpret_cast<f32x4*>(g));
+  }
+  return hipGetLastError();
+}
+template <int VT, bool RCONTIG, typename... A>
+hipError_t by_rank(int M, int D, int E, int R, A... a) {
+  if (R <= 16) return go<VT, 1, RCONTIG>(M, D, E, R, a...);
+  if (R <= 32) return go<VT, 2, RCONTIG>(M, D, E, R, a...);
+  return go<VT, 4, RCONTIG>(M, D, E, R, a...);
+}
+template <int VT, typename... A>
+hipError_t by_layout(bool rcontig, A... a) {
+  return rcontig ? by_rank<VT, true>(a...) : by_rank<VT, false>(a...);
+}
+
+}  // namespace
+
+size_t lora_outer_bytes(int M, int D, int E, int R) {
+  const int parts = outer_parts(M, D, E, R);
+  return parts > 1 ? (size_t)parts * E * R * D * 4 : 0;
+}
+
+hipError_t lora_outer(int M, int D, int E, int R, int S, const float* t, const void* v, XType vt, bool rcontig,
+                      const float* scale, const int32_t* ids, float* g, float* parts, hipStream_t st) {
+  if (vt == X_F32) return by_layout<X_F32>(rcontig, M, D, E, R, S, t, v, scale, ids, g, parts, st);
+  if (vt == X_BF16) return by_layout<X_BF16>(rcontig, M, D, E, R, S, t, v, scale, ids, g, parts, st);
+  return by_layout<X_F16>(rcontig, M, D, E, R, S, t, v, scale, ids, g, parts, st);
+}
+
+}  // namespace wq
