@@ -119,11 +119,13 @@ __device__ __forceinline__ void wave_lds_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// Columns 16 c .. 16 c + 15 as an operand: lane holds column lane % 16, rows 8 (lane / 16) .. + 7.
-template <int C, int NT>
+// Columns 16 c .. 16 c + 15 as an operand: lane holds column lane % 16, rows 8 (lane / 16) .. + 7.  IL: the 16 columns
+// are those of 32 (c / 2) .. + 31 whose 4's bit is c % 2 (fours taken alternately by the operands c and c + 1).
+template <int C, int NT, bool IL = false>
 __device__ __forceinline__ void tr_read(const uint8_t* tile, int c, bf16x8* t) {
   const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
-  const uint8_t* p = tile + (8 * g + (l >> 2)) * tr_stride<C>() + 32 * c + 8 * (l & 3);
+  const int col = IL ? 64 * (c >> 1) + 16 * (l & 3) + 8 * (c & 1) : 32 * c + 8 * (l & 3);   // bytes
+  const uint8_t* p = tile + (8 * g + (l >> 2)) * tr_stride<C>() + col;
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
     typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
@@ -164,18 +166,19 @@ __device__ __forceinline__ uint32_t tile_mask(int id, int e) { return (uint32_t)
 
 }  // namespace lora
 
-// Launchers of the three products (internal to the lora files).
-// t [S][M][R] float32: the S parts of sum_d x[m,d] w[e][r,d] (trans: w[e][d,r]), e = ids[m]; rows without an adapter
-// are not written.
-hipError_t lora_shrink(int M, int D, int E, int R, int S, const void* x, XType xt, const void* w, XType wt, bool trans,
-                       const int32_t* ids, float* t, hipStream_t st);
-int lora_shrink_parts(int M, int D, int R);
-// out[m,n] = base[m,n] + sum_r scale[e] t[m,r] w[e][n,r] (trans: w[e][r,n]); base may be null or out.
-hipError_t lora_expand(int M, int D, int E, int R, int S, const float* t, const void* w, XType wt, bool trans,
-                       const float* scale, const int32_t* ids, const void* base, void* out, XType ot, hipStream_t st);
-// g[e][r,d] (swap: g[e][d,r]) = sum_{m: ids[m] = e} scale[e] t[m,r] v[m,d]; parts: scratch of lora_outer_bytes.
-hipError_t lora_outer(int M, int D, int E, int R, int S, const float* t, const void* v, XType vt, bool rcontig,
-                      const float* scale, const int32_t* ids, float* g, float* parts, hipStream_t st);
+// Launchers of the three products (internal to the lora files).  The rank-R intermediate is held as its operand
+// terms, t [3][M][R] bfloat16 of scale[e] * sum, so that the many workgroups that read it neither add nor split it;
+// rows without an adapter are not written.
+// t = scale[e] * sum_d x[m,d] w[e][r,d] (trans: w[e][d,r]), e = ids[m]; parts: scratch of lora_shrink_bytes.
+hipError_t lora_shrink(int M, int D, int E, int R, const void* x, XType xt, const void* w, XType wt, bool trans,
+                       const float* scale, const int32_t* ids, uint16_t* t, float* parts, hipStream_t st);
+size_t lora_shrink_bytes(int M, int D, int R, XType xt);
+// out[m,n] = base[m,n] + sum_r t[m,r] w[e][n,r] (trans: w[e][r,n]); base may be null or out.
+hipError_t lora_expand(int M, int D, int E, int R, const uint16_t* t, const void* w, XType wt, bool trans,
+                       const int32_t* ids, const void* base, void* out, XType ot, hipStream_t st);
+// g[e][r,d] (rcontig: g[e][d,r]) = sum_{m: ids[m] = e} t[m,r] v[m,d]; parts: scratch of lora_outer_bytes.
+hipError_t lora_outer(int M, int D, int E, int R, const uint16_t* t, const void* v, XType vt, bool rcontig,
+                      const int32_t* ids, float* g, float* parts, hipStream_t st);
 size_t lora_outer_bytes(int M, int D, int E, int R);
 
 }  // namespace wq

@@ -1,5 +1,5 @@
-// Low-rank adapters, the weight gradients (gfx950): g[e][r,d] = scale[e] sum over the rows m of adapter e of
-// t[m,r] v[m,d]  (db from t = x a^T and v = dy, da from t = dy b and v = x).
+// Low-rank adapters, the weight gradients (gfx950): g[e][r,d] = sum over the rows m of adapter e of t[m,r] v[m,d]
+// (db from t = scale x a^T and v = dy, da from t = scale dy b and v = x).
 //
 // v is the bytes, read once per adapter that a block of rows names.  A workgroup owns one adapter, 64 columns d and
 // up to 64 ranks; its 4 waves take blocks of 32 rows in turn, each with its own accumulators, so no barrier stands
@@ -32,9 +32,8 @@ template <int VT, int NR> constexpr int outer_lds() {
 inline int outer_part_rows(int M, int parts) { return ((M + parts - 1) / parts + kRows - 1) / kRows * kRows; }
 
 template <int VT, int NR, bool RCONTIG>
-__global__ void __launch_bounds__(256) lora_outer_kernel(int M, int D, int E, int R, int S, int parts, int part_rows,
-                                                         int64_t total, const float* __restrict__ t,
-                                                         const uint8_t* __restrict__ v, const float* __restrict__ scale,
+__global__ void __launch_bounds__(256) lora_outer_kernel(int M, int D, int E, int R, int parts, int part_rows, int64_t total,
+                                                         const uint16_t* __restrict__ t, const uint8_t* __restrict__ v,
                                                          const int32_t* __restrict__ ids, float* __restrict__ g) {
   constexpr int C = 16 * NR, NV = terms<VT>();
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -55,8 +54,6 @@ __global__ void __launch_bounds__(256) lora_outer_kernel(int M, int D, int E, in
     for (int i = 0; i < NR; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    float f = 0.f;
-
     for (int s0 = mb; s0 < me; s0 += kScan) {
       __syncthreads();                                  // the masks' and the tiles' last readers
 #pragma unroll 4
@@ -71,12 +68,11 @@ __global__ void __launch_bounds__(256) lora_outer_kernel(int M, int D, int E, in
         while (b < blocks && masks[b] == 0) b += 4;
         return b;
       };
-      // one block's loads: v as 4 chunks of 8 columns per lane, t as NR groups of... 32 x C float32, 4 at a time
+      // one block's loads, in chunks of 8 columns: 4 of v and NR of each term of t per lane
       Raw<VT> raw[4];
-      f32x4 u[2 * NR];
-      uint32_t mask = 0;
+      u32x4 u[3][NR];
       auto load = [&](int b) {
-        mask = masks[b];
+        const uint32_t mask = masks[b];
         const int m0 = s0 + kRows * b;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -87,36 +83,27 @@ __global__ void __launch_bounds__(256) lora_outer_kernel(int M, int D, int E, in
           else raw_load_part<VT>(p, on ? D - d : 0, raw[q]);
         }
 #pragma unroll
-        for (int q = 0; q < 2 * NR; ++q) {
-          const int c = lane + 64 * q, row = c / (C / 4), r = r0 + 4 * (c % (C / 4));
-          u[q] = f32x4{0.f, 0.f, 0.f, 0.f};
-          if ((mask >> row & 1) && r < R) {
-            const float* p = t + (size_t)(m0 + row) * R + r;
-            for (int s = 0; s < S; ++s, p += (size_t)M * R) u[q] += *reinterpret_cast<const f32x4*>(p);
-          }
+        for (int q = 0; q < NR; ++q) {
+          const int c = lane + 64 * q, row = c / (C / 8), r = r0 + 8 * (c % (C / 8));
+          const bool on = (mask >> row & 1) != 0 && r < R;
+          const uint16_t* p = t + (size_t)(m0 + row) * R + r;
+#pragma unroll
+          for (int i = 0; i < 3; ++i)
+            u[i][q] = on ? *reinterpret_cast<const u32x4*>(p + i * (size_t)M * R) : u32x4{0u, 0u, 0u, 0u};
         }
       };
       int b = next(wave);
-      if (b < blocks) {
-        f = scale[e];
-        load(b);
-      }
+      if (b < blocks) load(b);
       while (b < blocks) {
         wave_lds_fence();
 #pragma unroll
         for (int q = 0; q < 4; ++q) tr_write<VT, kD>(vt, lane + 64 * q, raw[q]);
 #pragma unroll
-        for (int q = 0; q < 2 * NR; ++q) {
-          const int c = lane + 64 * q, row = c / (C / 4), col = 4 * (c % (C / 4));
-          const bool on = (mask >> row & 1) != 0;        // 0 * scale could be NaN
-          float x[4];
+        for (int q = 0; q < NR; ++q) {
+          const int c = lane + 64 * q;
+          uint8_t* p = ut + (c / (C / 8)) * tr_stride<C>() + (c % (C / 8)) * 16;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) x[j] = on ? u[q][j] * f : 0.f;
-          bf16x4 th[3];
-          split3<4>(x, th);
-#pragma unroll
-          for (int i = 0; i < 3; ++i)
-            *reinterpret_cast<bf16x4*>(ut + i * tr_plane<C>() + row * tr_stride<C>() + 2 * col) = th[i];
+          for (int i = 0; i < 3; ++i) *reinterpret_cast<u32x4*>(p + i * tr_plane<C>()) = u[i][q];
         }
         wave_lds_fence();
         b = next(b + 4);
@@ -188,15 +175,15 @@ inline int outer_parts(int M, int D, int E, int R) {
 }
 
 template <int VT, int NR, bool RCONTIG>
-hipError_t go(int M, int D, int E, int R, int S, const float* t, const void* v, const float* scale, const int32_t* ids,
-              float* g, float* ws, hipStream_t st) {
+hipError_t go(int M, int D, int E, int R, const uint16_t* t, const void* v, const int32_t* ids, float* g, float* ws,
+              hipStream_t st) {
   if (!raise_lds_limit<lora_outer_kernel<VT, NR, RCONTIG>>()) return hipErrorInvalidValue;
   const int parts = outer_parts(M, D, E, R);
   const int64_t total = outer_tiles(D, E, R) * parts;
   float* dst = parts > 1 ? ws : g;
   hipLaunchKernelGGL((lora_outer_kernel<VT, NR, RCONTIG>), dim3((unsigned)std::min<int64_t>(total, 1 << 20)), dim3(256),
-                     (outer_lds<VT, NR>()), st, M, D, E, R, S, parts, outer_part_rows(std::max(M, 1), parts), total, t,
-                     reinterpret_cast<const uint8_t*>(v), scale, ids, dst);
+                     (outer_lds<VT, NR>()), st, M, D, E, R, parts, outer_part_rows(std::max(M, 1), parts), total, t,
+                     reinterpret_cast<const uint8_t*>(v), ids, dst);
   if (parts > 1) {
     const int64_t n4 = (int64_t)E * R * D / 4;
     hipLaunchKernelGGL(lora_join_kernel, dim3((unsigned)std::min<int64_t>((n4 + 255) / 256, 2048)), dim3(256), 0, st, n4,
@@ -222,11 +209,11 @@ size_t lora_outer_bytes(int M, int D, int E, int R) {
   return parts > 1 ? (size_t)parts * E * R * D * 4 : 0;
 }
 
-hipError_t lora_outer(int M, int D, int E, int R, int S, const float* t, const void* v, XType vt, bool rcontig,
-                      const float* scale, const int32_t* ids, float* g, float* parts, hipStream_t st) {
-  if (vt == X_F32) return by_layout<X_F32>(rcontig, M, D, E, R, S, t, v, scale, ids, g, parts, st);
-  if (vt == X_BF16) return by_layout<X_BF16>(rcontig, M, D, E, R, S, t, v, scale, ids, g, parts, st);
-  return by_layout<X_F16>(rcontig, M, D, E, R, S, t, v, scale, ids, g, parts, st);
+hipError_t lora_outer(int M, int D, int E, int R, const uint16_t* t, const void* v, XType vt, bool rcontig,
+                      const int32_t* ids, float* g, float* parts, hipStream_t st) {
+  if (vt == X_F32) return by_layout<X_F32>(rcontig, M, D, E, R, t, v, ids, g, parts, st);
+  if (vt == X_BF16) return by_layout<X_BF16>(rcontig, M, D, E, R, t, v, ids, g, parts, st);
+  return by_layout<X_F16>(rcontig, M, D, E, R, t, v, ids, g, parts, st);
 }
 
 }  // namespace wq

@@ -2,12 +2,12 @@
 // forward (x, a) and, with w's rows along the contraction, of the backward pass (dy, b).
 //
 // x is read once and dominates the bytes for long batches; for a few tokens the used adapters do.  A workgroup takes
-// 32 rows and a part of the contraction; its 8 waves take blocks of 64 d in turn and add their 32 x R sums through
-// LDS at the end, so nothing is shared and no barrier stands in the loop; the loads of a wave's next block are in
-// flight during the MFMAs of this one.  A tile whose rows name several adapters is computed once per adapter, by
-// blockIdx.z-th workgroups of their own (a row's operands enter only its own row of the product, and only the
-// adapter's rows are loaded and written).  Short batches split the contraction over up to 8 workgroups, whose parts
-// the consumers of t add in order.
+// 32 rows; its waves take blocks of 64 d in turn and add their 32 x R sums through LDS at the end, so nothing is
+// shared and no barrier stands in the loop.  Operands of 16 bits leave room for 16 waves, which cover the latency by
+// their number; wider ones run 8 waves that load their next block during the MFMAs of this one.  A tile whose rows
+// name several adapters is computed once per adapter, by blockIdx.z-th workgroups of their own (a row's operands
+// enter only its own row of the product, and only the adapter's rows are loaded and written).  Where few tiles have a
+// long contraction, it is split over up to 8 workgroups and lora_terms_kernel adds their parts in order.
 #include <algorithm>
 
 #include "lora_common.h"
@@ -18,18 +18,32 @@ namespace {
 
 using namespace lora;
 
-constexpr int kWaves = 8;
+// Waves of a workgroup: 16 where a wave's registers (at most 128 then) hold a block and its sums.
+template <int XT, int WT, int NR> constexpr int shrink_waves() {
+  return (XT != X_F32 && WT != X_F32) || (XT == X_F32 && WT != X_F32 && NR <= 2) ? 16 : 8;
+}
+constexpr int kRed = 8;              // waves whose sums LDS holds at once
 
-template <int WT, bool TRANS, int NR> constexpr int shrink_lds() {
-  const int red = kWaves * kRows * 16 * NR * 4;
-  const int stage = TRANS ? kWaves * terms<WT>() * tr_plane<16 * NR>() : 0;
+template <int XT, int WT, bool TRANS, int NR> constexpr int shrink_lds() {
+  const int red = kRed * kRows * 16 * NR * 4;
+  const int stage = TRANS ? shrink_waves<XT, WT, NR>() * terms<WT>() * tr_plane<16 * NR>() : 0;
   return red > stage ? red : stage;
 }
 
+// The three bfloat16 terms of v, one per plane.
+__device__ __forceinline__ void put_terms(uint16_t* t, size_t plane, float v) {
+  __bf16 h[3][1];
+  split3<1>(&v, h);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) t[i * plane] = __builtin_bit_cast(uint16_t, h[i][0]);
+}
+
 template <int XT, int WT, bool TRANS, int NR>
-__global__ void __launch_bounds__(64 * kWaves) lora_shrink_kernel(int M, int D, int E, int R, int S, int RC,
-                                                                  const uint8_t* __restrict__ x, const uint8_t* __restrict__ w,
-                                                                  const int32_t* __restrict__ ids, float* __restrict__ t) {
+__global__ void __launch_bounds__((64 * shrink_waves<XT, WT, NR>()))
+    lora_shrink_kernel(int M, int D, int E, int R, int S, int RC, const uint8_t* __restrict__ x, const uint8_t* __restrict__ w,
+                       const float* __restrict__ scale, const int32_t* __restrict__ ids, uint16_t* __restrict__ t,
+                       float* __restrict__ parts) {
+  constexpr int kWaves = shrink_waves<XT, WT, NR>();
   constexpr int C = 16 * NR, NX = terms<XT>(), NW = terms<WT>();
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -116,51 +130,97 @@ __global__ void __launch_bounds__(64 * kWaves) lora_shrink_kernel(int M, int D, 
         }
       }
     };
-    Block k0, k1;
-    int b = b0 + wave;
-    if (b < b1) load(b, k0);
-    while (b < b1) {
-      const bool more = b + kWaves < b1;
-      if (more) load(b + kWaves, k1);
-      compute(k0);
-      if (!more) break;
-      b += kWaves;
-      if (b + kWaves < b1) load(b + kWaves, k0);
-      compute(k1);
-      b += kWaves;
+    if constexpr (kWaves == 16) {
+      Block k;
+      for (int b = b0 + wave; b < b1; b += kWaves) {
+        load(b, k);
+        compute(k);
+      }
+    } else {
+      Block k0, k1;
+      int b = b0 + wave;
+      if (b < b1) load(b, k0);
+      while (b < b1) {
+        const bool more = b + kWaves < b1;
+        if (more) load(b + kWaves, k1);
+        compute(k0);
+        if (!more) break;
+        b += kWaves;
+        if (b + kWaves < b1) load(b + kWaves, k0);
+        compute(k1);
+        b += kWaves;
+      }
     }
 
-    // sums of the 8 waves, in wave order; acc element q of lane: row 4 g + q of the block, column l16
-    __syncthreads();
+    // sums of the waves in a fixed order; acc element q of lane: row 4 g + q of the block, column l16
     float* red = reinterpret_cast<float*>(lds);
+    auto each = [&](auto f) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int j = 0; j < NR; ++j)
+        for (int j = 0; j < NR; ++j)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) red[(wave * kRows + 16 * i + 4 * g + q) * C + 16 * j + l16] = acc[i][j][q];
+          for (int q = 0; q < 4; ++q) f(i, j, q, ((wave % kRed) * kRows + 16 * i + 4 * g + q) * C + 16 * j + l16);
+    };
     __syncthreads();
+    if constexpr (kWaves == 16) {
+      if (wave >= kRed) each([&](int i, int j, int q, int at) { red[at] = acc[i][j][q]; });
+      __syncthreads();
+      if (wave < kRed) each([&](int i, int j, int q, int at) { red[at] = acc[i][j][q] + red[at]; });
+    } else {
+      each([&](int i, int j, int q, int at) { red[at] = acc[i][j][q]; });
+    }
+    __syncthreads();
+    const float f = scale[e];
     for (int o = threadIdx.x; o < kRows * C; o += 64 * kWaves) {
       const int row = o / C, r = r0 + o % C;
       if (!(mask >> row & 1) || r >= R) continue;
       float v = red[o];
 #pragma unroll
-      for (int q = 1; q < kWaves; ++q) v += red[q * kRows * C + o];
-      t[((size_t)s * M + m0 + row) * R + r] = v;
+      for (int q = 1; q < kRed; ++q) v += red[q * kRows * C + o];
+      const size_t at = (size_t)(m0 + row) * R + r, plane = (size_t)M * R;
+      if (S > 1) parts[s * plane + at] = v;
+      else put_terms(t + at, plane, v * f);
     }
     __syncthreads();
   }
 }
 
+// Terms of the sums of S parts, in order: one thread per element.
+__global__ void __launch_bounds__(256) lora_terms_kernel(int64_t plane, int E, int R, int S, const float* __restrict__ parts,
+                                                         const float* __restrict__ scale, const int32_t* __restrict__ ids,
+                                                         uint16_t* __restrict__ t) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < plane; i += (int64_t)gridDim.x * 256) {
+    const int e = ids[i / R];
+    if (e < 0 || e >= E) continue;
+    float v = parts[i];
+    for (int s = 1; s < S; ++s) v += parts[s * plane + i];
+    put_terms(t + i, plane, v * scale[e]);
+  }
+}
+
+// Parts of the contraction: where fewer than a workgroup per CU would read over 512 KB of x each, as many as bring that
+// to 256 KB, at most 8 and two workgroups per CU.
+int shrink_parts(int M, int D, int R, int es) {
+  const int tiles = ((M + kRows - 1) / kRows) * ((R + 63) / 64);
+  const int64_t bytes = (int64_t)kRows * D * es;
+  if (tiles >= 256 || bytes <= (512 << 10)) return 1;
+  const int s = (int)std::min<int64_t>(std::min(8, 512 / tiles), (bytes + (256 << 10) - 1) / (256 << 10));
+  if (s <= 1) return 1;
+  const int nb = (D + 63) / 64, per = (nb + s - 1) / s;
+  return (nb + per - 1) / per;             // no empty part
+}
+
 template <int XT, int WT, bool TRANS, int NR>
-hipError_t go(int M, int D, int E, int R, int S, const void* x, const void* w, const int32_t* ids, float* t, hipStream_t st) {
+hipError_t go(int M, int D, int E, int R, int S, const void* x, const void* w, const float* scale, const int32_t* ids,
+              uint16_t* t, float* parts, hipStream_t st) {
   if (!raise_lds_limit<lora_shrink_kernel<XT, WT, TRANS, NR>>()) return hipErrorInvalidValue;
   const int tiles = (M + kRows - 1) / kRows, RC = (R + 16 * NR - 1) / (16 * NR);
   // workgroups for further adapters of a tile: up to one per possible adapter while the launch stays small
   const int dz = std::max(1, std::min(std::min(E, kRows), 2048 / std::max(1, tiles * S * RC)));
-  hipLaunchKernelGGL((lora_shrink_kernel<XT, WT, TRANS, NR>), dim3(tiles, S * RC, dz), dim3(64 * kWaves),
-                     (shrink_lds<WT, TRANS, NR>()), st, M, D, E, R, S, RC, reinterpret_cast<const uint8_t*>(x),
-                     reinterpret_cast<const uint8_t*>(w), ids, t);
+  hipLaunchKernelGGL((lora_shrink_kernel<XT, WT, TRANS, NR>), dim3(tiles, S * RC, dz),
+                     dim3(64 * shrink_waves<XT, WT, NR>()), (shrink_lds<XT, WT, TRANS, NR>()), st, M, D, E, R, S, RC,
+                     reinterpret_cast<const uint8_t*>(x), reinterpret_cast<const uint8_t*>(w), scale, ids, t, parts);
   return hipGetLastError();
 }
 template <int XT, int WT, bool TRANS, typename... A>
@@ -178,24 +238,28 @@ hipError_t by_weight(XType wt, A... a) {
 
 }  // namespace
 
-// Parts of the contraction: enough workgroups for two per CU, each wave left at least one block of 64; at most 8.
-int lora_shrink_parts(int M, int D, int R) {
-  const int tiles = (M + kRows - 1) / kRows, RC = (R + 63) / 64;
-  const int s = std::min(std::min(8, 512 / std::max(1, tiles * RC)), (D + 64 * kWaves - 1) / (64 * kWaves));
-  if (s <= 1) return 1;
-  const int nb = (D + 63) / 64, per = (nb + s - 1) / s;
-  return (nb + per - 1) / per;             // no empty part
+size_t lora_shrink_bytes(int M, int D, int R, XType xt) {
+  const int s = shrink_parts(M, D, R, xt == X_F32 ? 4 : 2);
+  return s > 1 ? (size_t)s * M * R * 4 : 0;
 }
 
-hipError_t lora_shrink(int M, int D, int E, int R, int S, const void* x, XType xt, const void* w, XType wt, bool trans,
-                       const int32_t* ids, float* t, hipStream_t st) {
+hipError_t lora_shrink(int M, int D, int E, int R, const void* x, XType xt, const void* w, XType wt, bool trans,
+                       const float* scale, const int32_t* ids, uint16_t* t, float* parts, hipStream_t st) {
+  const int S = shrink_parts(M, D, R, xt == X_F32 ? 4 : 2);
+  hipError_t err;
   if (trans) {
-    if (xt == X_F32) return by_weight<X_F32, true>(wt, M, D, E, R, S, x, w, ids, t, st);
-    return by_weight<X_BF16, true>(wt, M, D, E, R, S, x, w, ids, t, st);
+    err = xt == X_F32 ? by_weight<X_F32, true>(wt, M, D, E, R, S, x, w, scale, ids, t, parts, st)
+                      : by_weight<X_BF16, true>(wt, M, D, E, R, S, x, w, scale, ids, t, parts, st);
+  } else {
+    err = xt == X_F32    ? by_weight<X_F32, false>(wt, M, D, E, R, S, x, w, scale, ids, t, parts, st)
+          : xt == X_BF16 ? by_weight<X_BF16, false>(wt, M, D, E, R, S, x, w, scale, ids, t, parts, st)
+                         : by_weight<X_F16, false>(wt, M, D, E, R, S, x, w, scale, ids, t, parts, st);
   }
-  if (xt == X_F32) return by_weight<X_F32, false>(wt, M, D, E, R, S, x, w, ids, t, st);
-  if (xt == X_BF16) return by_weight<X_BF16, false>(wt, M, D, E, R, S, x, w, ids, t, st);
-  return by_weight<X_F16, false>(wt, M, D, E, R, S, x, w, ids, t, st);
+  if (err != hipSuccess || S == 1) return err;
+  const int64_t plane = (int64_t)M * R;
+  hipLaunchKernelGGL(lora_terms_kernel, dim3((unsigned)std::min<int64_t>((plane + 255) / 256, 4096)), dim3(256), 0, st, plane, E,
+                     R, S, parts, scale, ids, t);
+  return hipGetLastError();
 }
 
 }  // namespace wq
