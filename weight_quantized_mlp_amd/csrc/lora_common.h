@@ -97,6 +97,25 @@ __device__ __forceinline__ void raw_terms(const Raw<T>& r, bf16x8* t) {
   }
 }
 
+template <int T>
+__device__ __forceinline__ void raw_f32(const Raw<T>& r, float* v) {
+  if constexpr (T == X_F32) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(r.v[j >> 2][j & 3]);
+  } else if constexpr (T == X_BF16) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t d = r.v[0][j];
+      v[2 * j] = __uint_as_float(d << 16);
+      v[2 * j + 1] = __uint_as_float(d & 0xFFFF0000u);
+    }
+  } else {
+    const f16x8 h = __builtin_bit_cast(f16x8, r.v[0]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = (float)h[j];
+  }
+}
+
 // acc += sum of the term products a[i] b[j], i + j <= 2.
 template <int NA, int NB>
 __device__ __forceinline__ f32x4 mfma_terms(const bf16x8* a, const bf16x8* b, f32x4 acc) {
@@ -119,13 +138,11 @@ __device__ __forceinline__ void wave_lds_fence() {
   __builtin_amdgcn_wave_barrier();
 }
 
-// Columns 16 c .. 16 c + 15 as an operand: lane holds column lane % 16, rows 8 (lane / 16) .. + 7.  IL: the 16 columns
-// are those of 32 (c / 2) .. + 31 whose 4's bit is c % 2 (fours taken alternately by the operands c and c + 1).
-template <int C, int NT, bool IL = false>
+// Columns 16 c .. 16 c + 15 as an operand: lane holds column lane % 16, rows 8 (lane / 16) .. + 7.
+template <int C, int NT>
 __device__ __forceinline__ void tr_read(const uint8_t* tile, int c, bf16x8* t) {
   const int lane = threadIdx.x & 63, l = lane & 15, g = lane >> 4;
-  const int col = IL ? 64 * (c >> 1) + 16 * (l & 3) + 8 * (c & 1) : 32 * c + 8 * (l & 3);   // bytes
-  const uint8_t* p = tile + (8 * g + (l >> 2)) * tr_stride<C>() + col;
+  const uint8_t* p = tile + (8 * g + (l >> 2)) * tr_stride<C>() + 32 * c + 8 * (l & 3);
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
     typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
@@ -165,6 +182,9 @@ __device__ __forceinline__ uint32_t tile_leaders(int id) {
 __device__ __forceinline__ uint32_t tile_mask(int id, int e) { return (uint32_t)__ballot(id == e); }
 
 }  // namespace lora
+
+// Whether a batch takes the row kernels (one row at a time, every row reading its adapter) instead of the tiles.
+inline bool lora_few_rows(int M, int R) { return (int64_t)M * R <= 2048; }
 
 // Launchers of the three products (internal to the lora files).  The rank-R intermediate is held as its operand
 // terms, t [3][M][R] bfloat16 of scale[e] * sum, so that the many workgroups that read it neither add nor split it;

@@ -3,11 +3,13 @@
 // (a, onto dx).
 //
 // base and out are the bytes: 8 per float32 element against 6 R flops (three terms of t).  A wave keeps the operand t
-// of its 32 rows in registers (all ranks, three bfloat16 terms) and walks over n in strips of 64, loading base and the
-// adapter's weights of the whole strip at once; there is no barrier and, forward, no LDS.  The output is computed
-// transposed (MFMA rows are n), so a lane holds 4 or 8 consecutive n of one row and moves base and out in 16-byte pieces.
-// A tile whose rows name several adapters is computed once per adapter, each storing its own rows; rows without an
-// adapter are copied by the first.
+// of its 32 rows in registers (all ranks, three bfloat16 terms) and walks over n in strips, the weights and base of the
+// next strip in flight during this strip's MFMAs; there is no barrier.  The sums leave the MFMAs a row per lane; adding
+// and storing them that way would touch a cache line per lane, so they pass through LDS of the wave's own and meet base
+// in whole lines (16 lanes on 256 consecutive bytes of a row).  A tile whose rows name several adapters is computed once
+// per adapter, each storing its own rows; rows without an adapter are copied by the first.
+//
+// Few rows (decode): see lora_expand_rows_kernel.
 #include <algorithm>
 
 #include "lora_common.h"
@@ -21,137 +23,121 @@ using namespace lora;
 // Columns a wave takes at a time, by rank steps: half as many where the operand t takes more registers.
 template <int NK> constexpr int kStrip = NK == 1 ? 64 : 32;
 
-// Output pieces.  float32: 4 consecutive elements from index n on (those at D and beyond read as 0 and are not written);
-// VEC: the 4 are aligned and inside.
-__device__ __forceinline__ f32x4 load_out4(const uint8_t* p, int n, int D, bool vec) {
-  if (vec) return *reinterpret_cast<const f32x4*>(p);
-  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+// 16 bytes of a row of the output: 4 float32 or 8 16-bit elements from n on; elements at D and beyond read as 0 and are not
+// written (16-bit rows end on a whole piece: D is a multiple of 16 there).
+template <bool W16>
+__device__ __forceinline__ u32x4 load_piece(const uint8_t* p, int n, int D, bool aligned) {
+  if (W16 || (aligned && n + 4 <= D)) return *reinterpret_cast<const u32x4*>(p);
+  u32x4 v = {0u, 0u, 0u, 0u};
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    if (n + j < D) v[j] = reinterpret_cast<const float*>(p)[j];
+    if (n + j < D) v[j] = reinterpret_cast<const uint32_t*>(p)[j];
   return v;
 }
-__device__ __forceinline__ void store_out4(uint8_t* p, int n, int D, bool vec, f32x4 v) {
-  if (vec) {
-    *reinterpret_cast<f32x4*>(p) = v;
+template <bool W16>
+__device__ __forceinline__ void store_piece(uint8_t* p, int n, int D, bool aligned, u32x4 v) {
+  if (W16 || (aligned && n + 4 <= D)) {
+    *reinterpret_cast<u32x4*>(p) = v;
     return;
   }
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    if (n + j < D) reinterpret_cast<float*>(p)[j] = v[j];
+    if (n + j < D) reinterpret_cast<uint32_t*>(p)[j] = v[j];
 }
-// 16-bit outputs: 8 consecutive elements, always aligned and inside (D is a multiple of 16 there).
-__device__ __forceinline__ void load_out8(const uint8_t* p, int ot, f32x4& a, f32x4& b) {
-  const u32x4 q = *reinterpret_cast<const u32x4*>(p);
-  float v[8];
+// piece + the sums at s (4 or 8 float32 in LDS), rounded to the output's type
+template <bool W16>
+__device__ __forceinline__ u32x4 add_piece(u32x4 v, const float* s, int ot) {
+  const f32x4 a = *reinterpret_cast<const f32x4*>(s);
+  if constexpr (!W16) {
+    u32x4 o;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t d = q[j];
-    v[2 * j] = ot == X_BF16 ? bf16_bits_to_f32(d & 0xFFFFu) : (float)f16_from_bits((uint16_t)d);
-    v[2 * j + 1] = ot == X_BF16 ? bf16_bits_to_f32(d >> 16) : (float)f16_from_bits((uint16_t)(d >> 16));
-  }
-  a = f32x4{v[0], v[1], v[2], v[3]};
-  b = f32x4{v[4], v[5], v[6], v[7]};
-}
-__device__ __forceinline__ void store_out8(uint8_t* p, int ot, f32x4 a, f32x4 b) {
-  uint32_t h[8];
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t d = v[j];
+      o[j] = __float_as_uint(__uint_as_float(d) + a[j]);
+    }
+    return o;
+  } else {
+    const f32x4 b = *reinterpret_cast<const f32x4*>(s + 4);
+    uint32_t h[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float f = j < 4 ? a[j & 3] : b[j & 3];
-    h[j] = ot == X_BF16 ? (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)f) : (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)f);
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t d = v[j >> 1], q = (j & 1) ? d >> 16 : d & 0xFFFFu;
+      const float f = (ot == X_BF16 ? bf16_bits_to_f32(q) : (float)f16_from_bits((uint16_t)q)) + (j < 4 ? a[j & 3] : b[j & 3]);
+      h[j] = ot == X_BF16 ? (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)f) : (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)f);
+    }
+    return u32x4{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
   }
-  *reinterpret_cast<u32x4*>(p) = u32x4{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
 }
 
-// NK: rank steps of 32.  W16: out has 16-bit elements, and a lane then holds 8 consecutive n (two MFMA row blocks
-// interleaved in fours), so that its piece of a row is 16 bytes there too.
+// A wave's LDS: the sums of a strip, 32 rows of float32 padded by 16 bytes, and for transposed weights their tile.
+template <int NK> constexpr int sum_row() { return kStrip<NK> + 4; }
+template <int WT, bool TRANS, int NK> constexpr int expand_wave_lds() {
+  return kRows * sum_row<NK>() * 4 + (TRANS ? terms<WT>() * tr_plane<kStrip<NK>>() : 0);
+}
+
+// NK: rank steps of 32.  W16: out has 16-bit elements.
 template <int WT, bool TRANS, int NK, bool W16>
 __global__ void __launch_bounds__(256) lora_expand_kernel(int M, int D, int E, int R, int strips, int nx,
                                                           const uint16_t* __restrict__ t, const uint8_t* __restrict__ w,
                                                           const int32_t* __restrict__ ids, const uint8_t* base, uint8_t* out,
                                                           int ot) {
   constexpr int NW = terms<WT>();
-  constexpr int ES = W16 ? 2 : 4;
-  constexpr int Q = kStrip<NK> / 16;           // MFMA row blocks of a strip
+  constexpr int ES = W16 ? 2 : 4, PE = 16 / ES;          // elements of a 16-byte piece
+  constexpr int SW = kStrip<NK>, Q = SW / 16;            // MFMA column blocks of a strip
+  constexpr int PL = SW / PE, PN = kRows * PL / 64;      // pieces of a row, pieces per lane
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   const int rt = (int)blockIdx.x / nx;
   const int m0 = rt * kRows;
-  const int n_begin = (((int)blockIdx.x - rt * nx) * 4 + wave) * kStrip<NK> * strips;
-  const int n_end = min(n_begin + kStrip<NK> * strips, D);
+  const int n_begin = (((int)blockIdx.x - rt * nx) * 4 + wave) * SW * strips, n_end = min(n_begin + SW * strips, D);
   const int id = tile_id(ids, m0, M, E);
   uint32_t lead = tile_leaders(id);
   const bool aligned = (D & 3) == 0;
-  // first n of the 4 that MFMA row block q leaves in this lane (accumulator rows 4 g .. + 3)
-  auto n_of = [&](int q) { return W16 ? 32 * (q >> 1) + 8 * g + 4 * (q & 1) : 16 * q + 4 * g; };
+  float* sums = reinterpret_cast<float*>(lds + wave * expand_wave_lds<WT, TRANS, NK>());
+  uint8_t* tile = reinterpret_cast<uint8_t*>(sums + kRows * sum_row<NK>());
 
-  // the strip's pieces of the rows whose bit in `rows` is set
-  auto load_rows = [&](uint32_t rows, int n0, f32x4 (&y)[Q][2]) {
+  // the strip's pieces of the rows whose bit in `rows` is set: piece q covers row c / PL, elements PE (c % PL) .., c = lane + 64 q
+  u32x4 y[PN];
+  auto load_rows = [&](uint32_t rows, int n0) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = 16 * i + l16;
-      const bool on = base != nullptr && (rows >> row & 1) != 0;
-      const uint8_t* p = base + (size_t)(m0 + row) * D * ES;
-#pragma unroll
-      for (int q = 0; q < Q; q += W16 ? 2 : 1) {
-        const int n = n0 + n_of(q);
-        y[q][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if constexpr (W16) {
-          y[q + 1][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-          if (on && n < n_end) load_out8(p + (size_t)n * ES, ot, y[q][i], y[q + 1][i]);
-        } else {
-          if (on && n < n_end) y[q][i] = load_out4(p + (size_t)n * ES, n, D, aligned && n + 4 <= D);
-        }
-      }
+    for (int q = 0; q < PN; ++q) {
+      const int c = lane + 64 * q, row = c / PL, n = n0 + PE * (c % PL);
+      y[q] = u32x4{0u, 0u, 0u, 0u};
+      if (base != nullptr && (rows >> row & 1) && n < n_end)
+        y[q] = load_piece<W16>(base + ((size_t)(m0 + row) * D + n) * ES, n, D, aligned);
     }
   };
-  auto store_rows = [&](uint32_t rows, int n0, const f32x4 (&y)[Q][2]) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = 16 * i + l16;
-      const bool on = (rows >> row & 1) != 0;
-      uint8_t* p = out + (size_t)(m0 + row) * D * ES;
-#pragma unroll
-      for (int q = 0; q < Q; q += W16 ? 2 : 1) {
-        const int n = n0 + n_of(q);
-        if (!on || n >= n_end) continue;
-        if constexpr (W16) store_out8(p + (size_t)n * ES, ot, y[q][i], y[q + 1][i]);
-        else store_out4(p + (size_t)n * ES, n, D, aligned && n + 4 <= D, y[q][i]);
-      }
-    }
-  };
-
   // rows without an adapter: out = base
   const uint32_t bare = (uint32_t)__ballot(id < 0 && m0 + (lane & 31) < M);
   if (blockIdx.z == 0 && bare != 0 && base != out) {
-    for (int n0 = n_begin; n0 < n_end; n0 += kStrip<NK>) {
-      f32x4 y[Q][2];
-      load_rows(bare, n0, y);
-      store_rows(bare, n0, y);
+    for (int n0 = n_begin; n0 < n_end; n0 += SW) {
+      load_rows(bare, n0);
+#pragma unroll
+      for (int q = 0; q < PN; ++q) {
+        const int c = lane + 64 * q, row = c / PL, n = n0 + PE * (c % PL);
+        if ((bare >> row & 1) && n < n_end) store_piece<W16>(out + ((size_t)(m0 + row) * D + n) * ES, n, D, aligned, y[q]);
+      }
     }
   }
 
-  uint8_t* tile = lds + wave * NW * tr_plane<kStrip<NK>>();
   for (int z = 0; lead != 0; ++z, lead &= lead - 1) {
     if (z % (int)gridDim.z != (int)blockIdx.z) continue;
     const int e = __builtin_amdgcn_readlane(id, __builtin_ctz(lead));
     const uint32_t mask = tile_mask(id, e);
     const uint8_t* we = w + (size_t)e * R * D * esize<WT>();
     const bool on[2] = {(mask >> l16 & 1) != 0, (mask >> (16 + l16) & 1) != 0};
-    f32x4 y[Q][2];
     Raw<WT> raw[Q];
     auto load_w = [&](int n0, int k) {
 #pragma unroll
       for (int q = 0; q < Q; ++q) {
         if constexpr (TRANS) {                         // rows r of D elements: chunk of the 32 x strip tile
-          constexpr int CW = kStrip<NK> / 8;
+          constexpr int CW = SW / 8;
           const int c = lane + 64 * q, r = 32 * k + c / CW, n = n0 + 8 * (c % CW);
           if (r < R && n < D) raw_load<WT, true>(we + ((size_t)r * D + n) * esize<WT>(), raw[q]);
           else raw_zero(raw[q]);
-        } else {                                       // operand row l16 of block q is n_of's n
-          const int r = 32 * k + 8 * g;
-          const int n = n0 + (W16 ? 32 * (q >> 1) + 8 * (l16 >> 2) + 4 * (q & 1) + (l16 & 3) : 16 * q + l16);
+        } else {
+          const int r = 32 * k + 8 * g, n = n0 + 16 * q + l16;
           if (r < R && n < D) raw_load<WT, true>(we + ((size_t)n * R + r) * esize<WT>(), raw[q]);
           else raw_zero(raw[q]);
         }
@@ -159,7 +145,7 @@ __global__ void __launch_bounds__(256) lora_expand_kernel(int M, int D, int E, i
     };
     if (n_begin < n_end) {
       load_w(n_begin, 0);
-      load_rows(mask, n_begin, y);
+      load_rows(mask, n_begin);
     }
     // t of the two 16-row blocks: lane holds row l16 of the block, ranks 32 k + 8 g .. + 7
     bf16x8 tf[2][NK][3];
@@ -175,7 +161,7 @@ __global__ void __launch_bounds__(256) lora_expand_kernel(int M, int D, int E, i
                                                                  : u32x4{0u, 0u, 0u, 0u});
       }
 
-    for (int n0 = n_begin; n0 < n_end; n0 += kStrip<NK>) {
+    for (int n0 = n_begin; n0 < n_end; n0 += SW) {
       f32x4 acc[Q][2];
 #pragma unroll
       for (int q = 0; q < Q; ++q)
@@ -187,7 +173,7 @@ __global__ void __launch_bounds__(256) lora_expand_kernel(int M, int D, int E, i
         if constexpr (TRANS) {
           wave_lds_fence();
 #pragma unroll
-          for (int q = 0; q < Q; ++q) tr_write<WT, kStrip<NK>>(tile, lane + 64 * q, raw[q]);
+          for (int q = 0; q < Q; ++q) tr_write<WT, SW>(tile, lane + 64 * q, raw[q]);
           wave_lds_fence();
         } else {
 #pragma unroll
@@ -195,20 +181,100 @@ __global__ void __launch_bounds__(256) lora_expand_kernel(int M, int D, int E, i
         }
         // the next weights (this strip's next rank step, or the next strip's first) fly during the MFMAs
         if (k + 1 < NK) load_w(n0, k + 1);
-        else if (n0 + kStrip<NK> < n_end) load_w(n0 + kStrip<NK>, 0);
+        else if (n0 + SW < n_end) load_w(n0 + SW, 0);
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
-          if constexpr (TRANS) tr_read<kStrip<NK>, NW, W16>(tile, q, wf[q]);
+          if constexpr (TRANS) tr_read<SW, NW>(tile, q, wf[q]);
 #pragma unroll
           for (int i = 0; i < 2; ++i) acc[q][i] = mfma_terms<NW, 3>(wf[q], tf[i][k], acc[q][i]);
         }
       }
+      // the sums, MFMA rows = n: lane holds columns 16 q + 4 g .. + 3 of row 16 i + l16
+      wave_lds_fence();
 #pragma unroll
       for (int q = 0; q < Q; ++q)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) acc[q][i] += y[q][i];
-      if (n0 + kStrip<NK> < n_end) load_rows(mask, n0 + kStrip<NK>, y);
-      store_rows(mask, n0, acc);
+        for (int i = 0; i < 2; ++i) *reinterpret_cast<f32x4*>(sums + (16 * i + l16) * sum_row<NK>() + 16 * q + 4 * g) = acc[q][i];
+      wave_lds_fence();
+      u32x4 o[PN];
+#pragma unroll
+      for (int q = 0; q < PN; ++q) {
+        const int c = lane + 64 * q;
+        o[q] = add_piece<W16>(y[q], sums + (c / PL) * sum_row<NK>() + PE * (c % PL), ot);
+      }
+      if (n0 + SW < n_end) load_rows(mask, n0 + SW);
+#pragma unroll
+      for (int q = 0; q < PN; ++q) {
+        const int c = lane + 64 * q, row = c / PL, n = n0 + PE * (c % PL);
+        if ((mask >> row & 1) && n < n_end) store_piece<W16>(out + ((size_t)(m0 + row) * D + n) * ES, n, D, aligned, o[q]);
+      }
+    }
+  }
+}
+
+// Few rows, forward: a workgroup takes one row and kRowCols columns.  The ranks of one n lie next to each other in b; G
+// lanes (a power of two covering R / 8) share an n, each holding its 8 ranks of t in registers, so a wave reads b in whole
+// lines; their float32 sums meet in log2 G exchanges.
+constexpr int kRowCols = 256;
+
+template <int WT, int G>
+__global__ void __launch_bounds__(256) lora_expand_rows_kernel(int M, int N, int E, int R, int nx, const uint16_t* __restrict__ t,
+                                                               const uint8_t* __restrict__ w, const int32_t* __restrict__ ids,
+                                                               const float* base, float* out) {
+  constexpr int NPW = 64 / G;                    // columns of a wave's step
+  constexpr int STEPS = kRowCols / (4 * NPW);    // steps of a wave
+  constexpr int U = STEPS < 8 ? STEPS : 8;       // of which are in flight
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int m = (int)blockIdx.x / nx, n0 = ((int)blockIdx.x - m * nx) * kRowCols + wave * (kRowCols / 4);
+  const int e = ids[m];
+  const float* yr = base ? base + (size_t)m * N : nullptr;
+  float* o = out + (size_t)m * N;
+  if (e < 0 || e >= E) {
+    if (base != out) {
+      const int n = n0 + lane;
+      if (n < N) o[n] = yr ? yr[n] : 0.f;
+    }
+    return;
+  }
+  const int c = lane % G, ln = lane / G;
+  const bool on = 8 * c < R;
+  float tr[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  const uint8_t* we = w + ((size_t)e * N * R + 8 * c) * esize<WT>();
+  const uint16_t* p = t + (size_t)m * R + 8 * c;
+  u32x4 th[3];
+#pragma unroll
+  for (int q = 0; q < 3; ++q) th[q] = on ? *reinterpret_cast<const u32x4*>(p + q * (size_t)M * R) : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int s = 0; s < STEPS; s += U) {
+    Raw<WT> raw[U];
+    float y[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int n = n0 + (s + u) * NPW + ln;
+      raw_zero(raw[u]);
+      if (on && n < N) raw_load<WT, true>(we + (size_t)n * R * esize<WT>(), raw[u]);
+      y[u] = yr && c == 0 && n < N ? yr[n] : 0.f;
+    }
+    if (s == 0) {
+#pragma unroll
+      for (int q = 2; q >= 0; --q) {             // the terms of t, smallest first: exact sums
+        float v[8];
+        Raw<X_BF16> r{{th[q]}};
+        raw_f32<X_BF16>(r, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) tr[j] += v[j];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int n = n0 + (s + u) * NPW + ln;
+      float v[8], a = 0.f;
+      raw_f32<WT>(raw[u], v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) a = fmaf(tr[j], v[j], a);
+#pragma unroll
+      for (int off = G / 2; off >= 1; off >>= 1) a += __shfl_xor(a, off, 64);
+      if (c == 0 && n < N) o[n] = y[u] + a;
     }
   }
 }
@@ -216,8 +282,8 @@ __global__ void __launch_bounds__(256) lora_expand_kernel(int M, int D, int E, i
 template <int WT, bool TRANS, int NK, bool W16>
 hipError_t go(int M, int D, int E, int R, const uint16_t* t, const void* w, const int32_t* ids, const void* base, void* out,
               int ot, hipStream_t st) {
-  constexpr int lds = TRANS ? 4 * terms<WT>() * tr_plane<kStrip<NK>>() : 0;
-  if (lds > 0 && !raise_lds_limit<lora_expand_kernel<WT, TRANS, NK, W16>>()) return hipErrorInvalidValue;
+  constexpr int lds = 4 * expand_wave_lds<WT, TRANS, NK>();
+  if (!raise_lds_limit<lora_expand_kernel<WT, TRANS, NK, W16>>()) return hipErrorInvalidValue;
   const int tiles = (M + kRows - 1) / kRows;
   // strips per wave: more while the launch keeps over 2048 workgroups (t is loaded once per wave)
   constexpr int kGroup = 4 * kStrip<NK>;
@@ -244,11 +310,34 @@ hipError_t by_weight(XType wt, A... a) {
   return by_rank<X_F16, TRANS, W16>(a...);
 }
 
+template <int WT, int G>
+hipError_t go_rows(int M, int N, int E, int R, const uint16_t* t, const void* w, const int32_t* ids, const void* base, void* out,
+                   hipStream_t st) {
+  const int nx = (N + kRowCols - 1) / kRowCols;
+  hipLaunchKernelGGL((lora_expand_rows_kernel<WT, G>), dim3((unsigned)(M * nx)), dim3(256), 0, st, M, N, E, R, nx, t,
+                     reinterpret_cast<const uint8_t*>(w), ids, reinterpret_cast<const float*>(base), reinterpret_cast<float*>(out));
+  return hipGetLastError();
+}
+template <int WT, typename... A>
+hipError_t rows_by_rank(int M, int N, int E, int R, A... a) {
+  if (R <= 8) return go_rows<WT, 1>(M, N, E, R, a...);
+  if (R <= 16) return go_rows<WT, 2>(M, N, E, R, a...);
+  if (R <= 32) return go_rows<WT, 4>(M, N, E, R, a...);
+  if (R <= 64) return go_rows<WT, 8>(M, N, E, R, a...);
+  if (R <= 128) return go_rows<WT, 16>(M, N, E, R, a...);
+  return go_rows<WT, 32>(M, N, E, R, a...);
+}
+
 }  // namespace
 
 // Forward (not trans) the output is float32, backward any type.
 hipError_t lora_expand(int M, int D, int E, int R, const uint16_t* t, const void* w, XType wt, bool trans,
                        const int32_t* ids, const void* base, void* out, XType ot, hipStream_t st) {
+  if (!trans && ot == X_F32 && lora_few_rows(M, R)) {
+    if (wt == X_F32) return rows_by_rank<X_F32>(M, D, E, R, t, w, ids, base, out, st);
+    if (wt == X_BF16) return rows_by_rank<X_BF16>(M, D, E, R, t, w, ids, base, out, st);
+    return rows_by_rank<X_F16>(M, D, E, R, t, w, ids, base, out, st);
+  }
   if (!trans) return ot == X_F32 ? by_weight<false, false>(wt, M, D, E, R, t, w, ids, base, out, (int)ot, st) : hipErrorInvalidValue;
   if (ot == X_F32) return by_weight<true, false>(wt, M, D, E, R, t, w, ids, base, out, (int)ot, st);
   return by_weight<true, true>(wt, M, D, E, R, t, w, ids, base, out, (int)ot, st);

@@ -1,13 +1,16 @@
 // Low-rank adapters, the contraction to the rank (gfx950): t[m,r] = sum_d x[m,d] w[e][r,d], e = ids[m], of the
 // forward (x, a) and, with w's rows along the contraction, of the backward pass (dy, b).
 //
-// x is read once and dominates the bytes for long batches; for a few tokens the used adapters do.  A workgroup takes
-// 32 rows; its waves take blocks of 64 d in turn and add their 32 x R sums through LDS at the end, so nothing is
-// shared and no barrier stands in the loop.  Operands of 16 bits leave room for 16 waves, which cover the latency by
-// their number; wider ones run 8 waves that load their next block during the MFMAs of this one.  A tile whose rows
-// name several adapters is computed once per adapter, by blockIdx.z-th workgroups of their own (a row's operands
-// enter only its own row of the product, and only the adapter's rows are loaded and written).  Where few tiles have a
-// long contraction, it is split over up to 8 workgroups and lora_terms_kernel adds their parts in order.
+// x is read once and dominates the bytes for long batches.  A workgroup takes 32 rows; its waves take blocks of 64 d in
+// turn and add their 32 x R sums through LDS at the end, so nothing is shared and no barrier stands in the loop.  An MFMA
+// operand wants a row per lane; loading it that way touches a cache line per lane (16 useful bytes each), which bounded
+// an earlier form at 2 TB/s, so a wave loads whole lines, writes them to LDS of its own and reads the operands there;
+// the next block's loads fly during this block's MFMAs.  A tile whose rows name several adapters is computed once per
+// adapter, by blockIdx.z-th workgroups of their own (a row's operands enter only its own row of the product, and only
+// the adapter's rows are loaded and written).  Where few tiles have a long contraction, it is split over up to 8
+// workgroups and lora_terms_kernel adds their parts in order.
+//
+// Few rows (decode): one wave per row and rank, plain float32 products; see lora_shrink_rows_kernel.
 #include <algorithm>
 
 #include "lora_common.h"
@@ -18,15 +21,19 @@ namespace {
 
 using namespace lora;
 
-// Waves of a workgroup: 16 where a wave's registers (at most 128 then) hold a block and its sums.
-template <int XT, int WT, int NR> constexpr int shrink_waves() {
-  return (XT != X_F32 && WT != X_F32) || (XT == X_F32 && WT != X_F32 && NR <= 2) ? 16 : 8;
+// A wave's LDS: 32 rows of x and, as rows (16 NR of them) or as a transposing tile, w; a row of 64 elements is padded by
+// 16 bytes, which spreads the operand reads of 16 rows over all banks.
+template <int T> constexpr int row_bytes() { return 64 * esize<T>() + 16; }
+template <int XT, int WT, bool TRANS, int NR> constexpr int shrink_wave_lds() {
+  return kRows * row_bytes<XT>() + (TRANS ? terms<WT>() * tr_plane<16 * NR>() : 16 * NR * row_bytes<WT>());
 }
-constexpr int kRed = 8;              // waves whose sums LDS holds at once
-
+// Waves of a workgroup: what fits a CU's LDS.
+template <int XT, int WT, bool TRANS, int NR> constexpr int shrink_waves() {
+  return 8 * shrink_wave_lds<XT, WT, TRANS, NR>() <= 160 * 1024 ? 8 : 4;
+}
 template <int XT, int WT, bool TRANS, int NR> constexpr int shrink_lds() {
-  const int red = kRed * kRows * 16 * NR * 4;
-  const int stage = TRANS ? shrink_waves<XT, WT, NR>() * terms<WT>() * tr_plane<16 * NR>() : 0;
+  constexpr int waves = shrink_waves<XT, WT, TRANS, NR>();
+  constexpr int red = waves * kRows * 16 * NR * 4, stage = waves * shrink_wave_lds<XT, WT, TRANS, NR>();
   return red > stage ? red : stage;
 }
 
@@ -39,12 +46,15 @@ __device__ __forceinline__ void put_terms(uint16_t* t, size_t plane, float v) {
 }
 
 template <int XT, int WT, bool TRANS, int NR>
-__global__ void __launch_bounds__((64 * shrink_waves<XT, WT, NR>()))
+__global__ void __launch_bounds__((64 * shrink_waves<XT, WT, TRANS, NR>()))
     lora_shrink_kernel(int M, int D, int E, int R, int S, int RC, const uint8_t* __restrict__ x, const uint8_t* __restrict__ w,
                        const float* __restrict__ scale, const int32_t* __restrict__ ids, uint16_t* __restrict__ t,
                        float* __restrict__ parts) {
-  constexpr int kWaves = shrink_waves<XT, WT, NR>();
+  constexpr int kWaves = shrink_waves<XT, WT, TRANS, NR>();
   constexpr int C = 16 * NR, NX = terms<XT>(), NW = terms<WT>();
+  constexpr int XP = 16 / esize<XT>(), WP = 16 / esize<WT>();       // elements of a 16-byte piece
+  constexpr int XL = 64 / XP, WL = 64 / WP;                          // pieces of a row of 64
+  constexpr int XN = kRows * XL / 64, WN = TRANS ? 1 : C * WL / 64;  // pieces per lane
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, g = lane >> 4;
@@ -54,16 +64,13 @@ __global__ void __launch_bounds__((64 * shrink_waves<XT, WT, NR>()))
   uint32_t lead = tile_leaders(id);
   const int nb = (D + 63) / 64, per = (nb + S - 1) / S;
   const int b0 = s * per, b1 = min(b0 + per, nb);
+  uint8_t* xt = lds + wave * shrink_wave_lds<XT, WT, TRANS, NR>();
+  uint8_t* wt = xt + kRows * row_bytes<XT>();
   for (int z = 0; lead != 0; ++z, lead &= lead - 1) {
     if (z % (int)gridDim.z != (int)blockIdx.z) continue;
     const int e = __builtin_amdgcn_readlane(id, __builtin_ctz(lead));
     const uint32_t mask = tile_mask(id, e);
     const uint8_t* we = w + (size_t)e * R * D * esize<WT>();
-    // rows of the two 16-row blocks that this lane loads
-    const bool on[2] = {(mask >> l16 & 1) != 0, (mask >> (16 + l16) & 1) != 0};
-    const uint8_t* xr[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) xr[i] = x + (size_t)(m0 + 16 * i + l16) * D * esize<XT>();
 
     f32x4 acc[2][NR];
 #pragma unroll
@@ -71,105 +78,118 @@ __global__ void __launch_bounds__((64 * shrink_waves<XT, WT, NR>()))
 #pragma unroll
       for (int j = 0; j < NR; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    // one block: 64 d as two MFMA steps of 32
-    struct Block {
-      Raw<XT> x[2][2];
-      Raw<WT> w[2][TRANS ? (C + 15) / 16 : NR];
-    };
-    auto load = [&](int b, Block& k) {
+    // a block as loaded: piece q of x covers row c / XL, elements XP (c % XL) .. of the block, c = lane + 64 q
+    u32x4 xr[XN], wr[WN];
+    Raw<WT> wtr[TRANS ? 2 : 1][NR];
+    auto load = [&](int b) {
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int d = 64 * b + 32 * q + 8 * g;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          if constexpr (TRANS) {                       // x = dy: D may be any number
-            if (on[i] && d + 8 <= D) raw_load<XT, false>(xr[i] + (size_t)d * esize<XT>(), k.x[q][i]);
-            else raw_load_part<XT>(xr[i] + (size_t)d * esize<XT>(), on[i] ? D - d : 0, k.x[q][i]);
-          } else {                                     // D is a multiple of 16
-            if (on[i] && d < D) raw_load<XT, true>(xr[i] + (size_t)d * esize<XT>(), k.x[q][i]);
-            else raw_zero(k.x[q][i]);
+      for (int q = 0; q < XN; ++q) {
+        const int c = lane + 64 * q, row = c / XL, d = 64 * b + XP * (c % XL);
+        const uint8_t* p = x + ((size_t)(m0 + row) * D + d) * esize<XT>();
+        const bool on = (mask >> row & 1) != 0;
+        xr[q] = u32x4{0u, 0u, 0u, 0u};
+        if constexpr (TRANS) {                         // x = dy: D may be any number
+          if (on && d + XP <= D) {
+            if constexpr (XT == X_F32) xr[q] = *reinterpret_cast<const u32x4_a4*>(p);
+            else xr[q] = *reinterpret_cast<const u32x4_a2*>(p);
+          } else if (on && d < D) {
+            Raw<XT> part;
+            raw_load_part<XT>(p, D - d, part);
+            xr[q] = part.v[0];
           }
+        } else {                                       // D is a multiple of 16
+          if (on && d < D) xr[q] = *reinterpret_cast<const u32x4*>(p);
         }
-        if constexpr (TRANS) {                         // rows d, R contiguous: chunk c of the 32 x C tile
+      }
+      if constexpr (TRANS) {                           // rows d, R contiguous: chunk c of the 32 x C tile of step k
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
           for (int j = 0; j < NR; ++j) {
-            const int c = lane + 64 * j, dr = 64 * b + 32 * q + c / (C / 8), r = r0 + 8 * (c % (C / 8));
-            if (dr < D && r < R) raw_load<WT, true>(we + ((size_t)dr * R + r) * esize<WT>(), k.w[q][j]);
-            else raw_zero(k.w[q][j]);
+            const int c = lane + 64 * j, dr = 64 * b + 32 * k + c / (C / 8), r = r0 + 8 * (c % (C / 8));
+            if (dr < D && r < R) raw_load<WT, true>(we + ((size_t)dr * R + r) * esize<WT>(), wtr[k][j]);
+            else raw_zero(wtr[k][j]);
           }
-        } else {
+      } else {
 #pragma unroll
-          for (int j = 0; j < NR; ++j) {
-            const int r = r0 + 16 * j + l16;
-            if (r < R && d < D) raw_load<WT, true>(we + ((size_t)r * D + d) * esize<WT>(), k.w[q][j]);
-            else raw_zero(k.w[q][j]);
-          }
+        for (int q = 0; q < WN; ++q) {
+          const int c = lane + 64 * q, r = r0 + c / WL, d = 64 * b + WP * (c % WL);
+          wr[q] = r < R && d < D ? *reinterpret_cast<const u32x4*>(we + ((size_t)r * D + d) * esize<WT>()) : u32x4{0u, 0u, 0u, 0u};
         }
       }
     };
-    uint8_t* tile = lds + wave * NW * tr_plane<C>();
-    auto compute = [&](const Block& k) {
+    auto lds_raw = [](const uint8_t* p, auto& r) {     // 8 elements of a row
+      r.v[0] = *reinterpret_cast<const u32x4*>(p);
+      if constexpr (sizeof(r) == 32) r.v[1] = *reinterpret_cast<const u32x4*>(p + 16);
+    };
+    int b = b0 + wave;
+    if (b < b1) load(b);
+    for (; b < b1; b += kWaves) {
+      wave_lds_fence();                                // the previous block's reads
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
+      for (int q = 0; q < XN; ++q) {
+        const int c = lane + 64 * q;
+        *reinterpret_cast<u32x4*>(xt + (c / XL) * row_bytes<XT>() + (c % XL) * 16) = xr[q];
+      }
+      if constexpr (!TRANS) {
+#pragma unroll
+        for (int q = 0; q < WN; ++q) {
+          const int c = lane + 64 * q;
+          *reinterpret_cast<u32x4*>(wt + (c / WL) * row_bytes<WT>() + (c % WL) * 16) = wr[q];
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < NR; ++j) tr_write<WT, C>(wt, lane + 64 * j, wtr[0][j]);
+      }
+      wave_lds_fence();
+      Raw<WT> second[NR];
+      if constexpr (TRANS) {
+#pragma unroll
+        for (int j = 0; j < NR; ++j) second[j] = wtr[1][j];
+      }
+      if (b + kWaves < b1) load(b + kWaves);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if constexpr (TRANS) {
+          if (k == 1) {                                // the tile holds one step of 32 d at a time
+            wave_lds_fence();
+#pragma unroll
+            for (int j = 0; j < NR; ++j) tr_write<WT, C>(wt, lane + 64 * j, second[j]);
+            wave_lds_fence();
+          }
+        }
         bf16x8 xf[2][NX];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) raw_terms<XT>(k.x[q][i], xf[i]);
-        if constexpr (TRANS) {
-          wave_lds_fence();                            // the previous step's reads
-#pragma unroll
-          for (int j = 0; j < NR; ++j) tr_write<WT, C>(tile, lane + 64 * j, k.w[q][j]);
-          wave_lds_fence();
+        for (int i = 0; i < 2; ++i) {
+          Raw<XT> r;
+          lds_raw(xt + (16 * i + l16) * row_bytes<XT>() + (32 * k + 8 * g) * esize<XT>(), r);
+          raw_terms<XT>(r, xf[i]);
         }
 #pragma unroll
         for (int j = 0; j < NR; ++j) {
           bf16x8 wf[NW];
-          if constexpr (TRANS) tr_read<C, NW>(tile, j, wf);
-          else raw_terms<WT>(k.w[q][j], wf);
+          if constexpr (TRANS) {
+            tr_read<C, NW>(wt, j, wf);
+          } else {
+            Raw<WT> r;
+            lds_raw(wt + (16 * j + l16) * row_bytes<WT>() + (32 * k + 8 * g) * esize<WT>(), r);
+            raw_terms<WT>(r, wf);
+          }
 #pragma unroll
           for (int i = 0; i < 2; ++i) acc[i][j] = mfma_terms<NX, NW>(xf[i], wf, acc[i][j]);
         }
       }
-    };
-    if constexpr (kWaves == 16) {
-      Block k;
-      for (int b = b0 + wave; b < b1; b += kWaves) {
-        load(b, k);
-        compute(k);
-      }
-    } else {
-      Block k0, k1;
-      int b = b0 + wave;
-      if (b < b1) load(b, k0);
-      while (b < b1) {
-        const bool more = b + kWaves < b1;
-        if (more) load(b + kWaves, k1);
-        compute(k0);
-        if (!more) break;
-        b += kWaves;
-        if (b + kWaves < b1) load(b + kWaves, k0);
-        compute(k1);
-        b += kWaves;
-      }
     }
 
-    // sums of the waves in a fixed order; acc element q of lane: row 4 g + q of the block, column l16
+    // sums of the waves in wave order; acc element q of lane: row 4 g + q of the block, column l16
     float* red = reinterpret_cast<float*>(lds);
-    auto each = [&](auto f) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < NR; ++j)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) f(i, j, q, ((wave % kRed) * kRows + 16 * i + 4 * g + q) * C + 16 * j + l16);
-    };
     __syncthreads();
-    if constexpr (kWaves == 16) {
-      if (wave >= kRed) each([&](int i, int j, int q, int at) { red[at] = acc[i][j][q]; });
-      __syncthreads();
-      if (wave < kRed) each([&](int i, int j, int q, int at) { red[at] = acc[i][j][q] + red[at]; });
-    } else {
-      each([&](int i, int j, int q, int at) { red[at] = acc[i][j][q]; });
-    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < NR; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) red[(wave * kRows + 16 * i + 4 * g + q) * C + 16 * j + l16] = acc[i][j][q];
     __syncthreads();
     const float f = scale[e];
     for (int o = threadIdx.x; o < kRows * C; o += 64 * kWaves) {
@@ -177,13 +197,52 @@ __global__ void __launch_bounds__((64 * shrink_waves<XT, WT, NR>()))
       if (!(mask >> row & 1) || r >= R) continue;
       float v = red[o];
 #pragma unroll
-      for (int q = 1; q < kRed; ++q) v += red[q * kRows * C + o];
+      for (int q = 1; q < kWaves; ++q) v += red[q * kRows * C + o];
       const size_t at = (size_t)(m0 + row) * R + r, plane = (size_t)M * R;
       if (S > 1) parts[s * plane + at] = v;
       else put_terms(t + at, plane, v * f);
     }
     __syncthreads();
   }
+}
+
+// Few rows: one wave per row and rank.  A lane takes 8 consecutive d of every 512, so a wave reads whole lines of x and of
+// the adapter's row, 4 steps in flight; the products are float32.
+template <int XT, int WT>
+__global__ void __launch_bounds__(256) lora_shrink_rows_kernel(int M, int D, int E, int R, const uint8_t* __restrict__ x,
+                                                               const uint8_t* __restrict__ w, const float* __restrict__ scale,
+                                                               const int32_t* __restrict__ ids, uint16_t* __restrict__ t) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int m = (int)blockIdx.x, r = (int)blockIdx.y * 4 + wave;     // R is a multiple of 8
+  const int e = ids[m];
+  if (e < 0 || e >= E) return;
+  const uint8_t* xr = x + (size_t)m * D * esize<XT>();
+  const uint8_t* wr = w + ((size_t)e * R + r) * D * esize<WT>();
+  float acc = 0.f;
+  for (int d0 = 8 * lane; d0 < D; d0 += 2048) {
+    Raw<XT> a[4];
+    Raw<WT> b[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int d = d0 + 512 * q;
+      raw_zero(a[q]);
+      raw_zero(b[q]);
+      if (d < D) {
+        raw_load<XT, true>(xr + (size_t)d * esize<XT>(), a[q]);
+        raw_load<WT, true>(wr + (size_t)d * esize<WT>(), b[q]);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float u[8], v[8];
+      raw_f32<XT>(a[q], u);
+      raw_f32<WT>(b[q], v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc = fmaf(u[j], v[j], acc);
+    }
+  }
+  acc = wave64_sum(acc);
+  if (lane == 0) put_terms(t + (size_t)m * R + r, (size_t)M * R, acc * scale[e]);
 }
 
 // Terms of the sums of S parts, in order: one thread per element.
@@ -219,7 +278,7 @@ hipError_t go(int M, int D, int E, int R, int S, const void* x, const void* w, c
   // workgroups for further adapters of a tile: up to one per possible adapter while the launch stays small
   const int dz = std::max(1, std::min(std::min(E, kRows), 2048 / std::max(1, tiles * S * RC)));
   hipLaunchKernelGGL((lora_shrink_kernel<XT, WT, TRANS, NR>), dim3(tiles, S * RC, dz),
-                     dim3(64 * shrink_waves<XT, WT, NR>()), (shrink_lds<XT, WT, TRANS, NR>()), st, M, D, E, R, S, RC,
+                     dim3(64 * shrink_waves<XT, WT, TRANS, NR>()), (shrink_lds<XT, WT, TRANS, NR>()), st, M, D, E, R, S, RC,
                      reinterpret_cast<const uint8_t*>(x), reinterpret_cast<const uint8_t*>(w), scale, ids, t, parts);
   return hipGetLastError();
 }
@@ -228,6 +287,19 @@ hipError_t by_rank(int M, int D, int E, int R, A... a) {
   if (R <= 16) return go<XT, WT, TRANS, 1>(M, D, E, R, a...);
   if (R <= 32) return go<XT, WT, TRANS, 2>(M, D, E, R, a...);
   return go<XT, WT, TRANS, 4>(M, D, E, R, a...);
+}
+template <int XT, int WT>
+hipError_t go_rows(int M, int D, int E, int R, const void* x, const void* w, const float* scale, const int32_t* ids, uint16_t* t,
+                   hipStream_t st) {
+  hipLaunchKernelGGL((lora_shrink_rows_kernel<XT, WT>), dim3(M, R / 4), dim3(256), 0, st, M, D, E, R,
+                     reinterpret_cast<const uint8_t*>(x), reinterpret_cast<const uint8_t*>(w), scale, ids, t);
+  return hipGetLastError();
+}
+template <int XT, typename... A>
+hipError_t rows_by_weight(XType wt, A... a) {
+  if (wt == X_F32) return go_rows<XT, X_F32>(a...);
+  if (wt == X_BF16) return go_rows<XT, X_BF16>(a...);
+  return go_rows<XT, X_F16>(a...);
 }
 template <int XT, bool TRANS, typename... A>
 hipError_t by_weight(XType wt, A... a) {
@@ -245,6 +317,11 @@ size_t lora_shrink_bytes(int M, int D, int R, XType xt) {
 
 hipError_t lora_shrink(int M, int D, int E, int R, const void* x, XType xt, const void* w, XType wt, bool trans,
                        const float* scale, const int32_t* ids, uint16_t* t, float* parts, hipStream_t st) {
+  if (!trans && lora_few_rows(M, R)) {
+    if (xt == X_F32) return rows_by_weight<X_F32>(wt, M, D, E, R, x, w, scale, ids, t, st);
+    if (xt == X_BF16) return rows_by_weight<X_BF16>(wt, M, D, E, R, x, w, scale, ids, t, st);
+    return rows_by_weight<X_F16>(wt, M, D, E, R, x, w, scale, ids, t, st);
+  }
   const int S = shrink_parts(M, D, R, xt == X_F32 ? 4 : 2);
   hipError_t err;
   if (trans) {
