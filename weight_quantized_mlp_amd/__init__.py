@@ -115,7 +115,13 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+# The current stream's handle; torch's own accessor of the raw handle spares 2 us of object making where it exists.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(dev):
+    if _raw_stream is not None and dev.index is not None:
+        return _raw_stream(dev.index)
     return torch.cuda.current_stream(dev).cuda_stream
 
 
@@ -376,22 +382,30 @@ def lora_workspace_bytes(M, K, N, E, R, backward=False):
     return lib().lora_workspace_bytes(M, K, N, E, R, int(backward))
 
 
+def _want(t, name, dtype, dev, numel):
+    """_need for the hot calls: one cheap test, and _need's own errors where it fails."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == dev.index and t.numel() == numel
+            and t.is_contiguous()):
+        _need(t, name, dtype, dev, numel)
+    return t
+
+
 def _lora_args(x, a, b, scale, ids):
     """Checks shared by the forward and the backward call; (M, K, N, E, R, x code, weight code)."""
-    if x.dim() != 2 or a.dim() != 3 or b.dim() != 3:
+    dev, xs, as_, bs = x.device, x.shape, a.shape, b.shape
+    if len(xs) != 2 or len(as_) != 3 or len(bs) != 3:
         raise ValueError("x must be [M, K], a [E, R, K] and b [E, N, R]")
-    dev = x.device
-    M, K = x.shape
-    E, R, _ = a.shape
-    N = b.shape[1]
-    if tuple(a.shape) != (E, R, K) or tuple(b.shape) != (E, N, R):
-        raise ValueError(f"a must be [E, R, {K}] and b [E, N, R], got {tuple(a.shape)} and {tuple(b.shape)}")
+    M, K = xs
+    E, R, Ka = as_
+    N = bs[1]
+    if Ka != K or bs[0] != E or bs[2] != R:
+        raise ValueError(f"a must be [E, R, {K}] and b [E, N, R], got {tuple(as_)} and {tuple(bs)}")
     xt, wt = _float_code(x.dtype, "x"), _float_code(a.dtype, "a")
-    _need(x, "x", x.dtype, dev)
-    _need(a, "a", a.dtype, dev)
-    _need(b, "b", a.dtype, dev)
-    _need(scale, "scale", torch.float32, dev, E)
-    _need(ids, "ids", torch.int32, dev, M)
+    _want(x, "x", x.dtype, dev, M * K)
+    _want(a, "a", a.dtype, dev, E * R * K)
+    _want(b, "b", a.dtype, dev, E * N * R)
+    _want(scale, "scale", torch.float32, dev, E)
+    _want(ids, "ids", torch.int32, dev, M)
     return M, K, N, E, R, xt, wt
 
 
@@ -403,10 +417,11 @@ def lora_run(x, a, b, scale, ids, y, out=None, workspace=None):
     M, K, N, E, R, xt, wt = _lora_args(x, a, b, scale, ids)
     dev = x.device
     if y is not None:
-        _need(y, "y", torch.float32, dev, M * N)
+        _want(y, "y", torch.float32, dev, M * N)
     if out is None:
         out = torch.empty((M, N), dtype=torch.float32, device=dev)
-    _need(out, "out", torch.float32, dev, M * N)
+    else:
+        _want(out, "out", torch.float32, dev, M * N)
     ws = _workspace(lora_workspace_bytes(M, K, N, E, R), dev, workspace)
     rc = lib().lora_run(M, K, N, E, R, _ptr(x), xt, _ptr(a), _ptr(b), wt, _ptr(scale), _ptr(ids), _ptr(y), _ptr(ws),
                         ws.numel(), _ptr(out), _stream(dev))
@@ -422,11 +437,11 @@ def lora_backward(dy, x, a, b, scale, ids, dx0=None, dx=None, da=None, db=None, 
     M, K, N, E, R, xt, wt = _lora_args(x, a, b, scale, ids)
     dev = x.device
     dyt = _float_code(dy.dtype, "dy", (torch.float32, torch.bfloat16))
-    _need(dy, "dy", dy.dtype, dev, M * N)
+    _want(dy, "dy", dy.dtype, dev, M * N)
     want = dx.dtype if dx is not None else dx0.dtype if dx0 is not None else dx_dtype or x.dtype
     dxt = _float_code(want, "dx")
     if dx0 is not None:
-        _need(dx0, "dx0", want, dev, M * K)
+        _want(dx0, "dx0", want, dev, M * K)
     outs = []
     for t, name, shape, dtype, wanted in ((dx, "dx", (M, K), want, need[0]), (da, "da", (E, R, K), torch.float32, need[1]),
                                           (db, "db", (E, N, R), torch.float32, need[2])):
@@ -435,7 +450,9 @@ def lora_backward(dy, x, a, b, scale, ids, dx0=None, dx=None, da=None, db=None, 
             continue
         if t is None:
             t = torch.empty(shape, dtype=dtype, device=dev)
-        outs.append(_need(t, name, dtype, dev, shape[0] * shape[1] * (shape[2] if len(shape) == 3 else 1)))
+        else:
+            _want(t, name, dtype, dev, shape[0] * shape[1] * (shape[2] if len(shape) == 3 else 1))
+        outs.append(t)
     ws = _workspace(lora_workspace_bytes(M, K, N, E, R, True), dev, workspace)
     rc = lib().lora_backward(M, K, N, E, R, _ptr(dy), dyt, _ptr(x), xt, _ptr(a), _ptr(b), wt, _ptr(scale), _ptr(ids),
                              _ptr(dx0), dxt, _ptr(ws), ws.numel(), _ptr(outs[0]), _ptr(outs[1]), _ptr(outs[2]), _stream(dev))
@@ -453,19 +470,19 @@ def qlinear_backward(fmt, dy, w, scale=None, global_scale=1.0, dtype=None, out=N
     dev = dy.device
     M, N = dy.shape
     dyt = _float_code(dy.dtype, "dy", (torch.float32, torch.bfloat16))
-    _need(dy, "dy", dy.dtype, dev)
-    _need(w, "w", torch.uint8, dev)
+    _want(dy, "dy", dy.dtype, dev, M * N)
     if w.shape[0] != N:
         raise ValueError(f"w must have {N} rows, has {w.shape[0]}")
     K = w.numel() // 36 * 64 // N if fmt == WQ_FMT_NVFP4 else w.numel() // N
-    _need(w, "w", torch.uint8, dev, N * (K // 64) * 36 if fmt == WQ_FMT_NVFP4 else N * K)
+    _want(w, "w", torch.uint8, dev, N * (K // 64) * 36 if fmt == WQ_FMT_NVFP4 else N * K)
     if scale is not None:
-        _need(scale, "scale", torch.float32, dev, N)
+        _want(scale, "scale", torch.float32, dev, N)
     want = out.dtype if out is not None else dtype or dy.dtype
     dxt = _float_code(want, "dx", (torch.float32, torch.bfloat16))
     if out is None:
         out = torch.empty((M, K), dtype=want, device=dev)
-    _need(out, "out", want, dev, M * K)
+    else:
+        _want(out, "out", want, dev, M * K)
     ws = _workspace(qlinear_backward_workspace_bytes(fmt, M, N, K, want), dev, workspace)
     rc = lib().qlinear_backward(fmt, M, N, K, _ptr(dy), dyt, _ptr(w), _ptr(scale), float(global_scale), _ptr(ws), ws.numel(),
                                 _ptr(out), dxt, _stream(dev))
@@ -533,8 +550,8 @@ def adamw_run(table, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.
     """One AdamW step over the table's tensors, in place.  step: int64 device tensor holding t >= 1; lr: float32
     device tensor (both read on the device when the step runs); seed: of the 8-bit states' stochastic rounding."""
     dev = table.table.device
-    _need(step, "step", torch.int64, dev, 1)
-    _need(lr, "lr", torch.float32, dev, 1)
+    _want(step, "step", torch.int64, dev, 1)
+    _want(lr, "lr", torch.float32, dev, 1)
     rc = lib().adamw_run(table.count, table.elems, table.bits, _ptr(table.table), _ptr(step), _ptr(lr), beta1, beta2, eps,
                          weight_decay, grad_scale, seed & 0xFFFFFFFF, _stream(dev))
     _check("adamw_run", rc)

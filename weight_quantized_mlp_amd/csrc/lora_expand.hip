@@ -24,10 +24,11 @@ using namespace lora;
 template <int NK> constexpr int kStrip = NK == 1 ? 64 : 32;
 
 // 16 bytes of a row of the output: 4 float32 or 8 16-bit elements from n on; elements at D and beyond read as 0 and are not
-// written (16-bit rows end on a whole piece: D is a multiple of 16 there).
+// written (16-bit rows end on a whole piece: D is a multiple of 16 there).  Both streams pass the caches once, and say so:
+// the adapters' weights, which every row tile reads again, stay (4099 rows x 17408: 153 -> 138 us).
 template <bool W16>
 __device__ __forceinline__ u32x4 load_piece(const uint8_t* p, int n, int D, bool aligned) {
-  if (W16 || (aligned && n + 4 <= D)) return *reinterpret_cast<const u32x4*>(p);
+  if (W16 || (aligned && n + 4 <= D)) return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
   u32x4 v = {0u, 0u, 0u, 0u};
 #pragma unroll
   for (int j = 0; j < 4; ++j)
@@ -37,7 +38,7 @@ __device__ __forceinline__ u32x4 load_piece(const uint8_t* p, int n, int D, bool
 template <bool W16>
 __device__ __forceinline__ void store_piece(uint8_t* p, int n, int D, bool aligned, u32x4 v) {
   if (W16 || (aligned && n + 4 <= D)) {
-    *reinterpret_cast<u32x4*>(p) = v;
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p));
     return;
   }
 #pragma unroll
@@ -69,11 +70,15 @@ __device__ __forceinline__ u32x4 add_piece(u32x4 v, const float* s, int ot) {
   }
 }
 
-// A wave's LDS: the sums of a strip, 32 rows of float32 padded by 16 bytes, and for transposed weights their tile.
+// A wave's LDS: the sums of a strip, 32 rows of float32 padded by 16 bytes (before the strips: a 32 x 32 piece of t), and the
+// strip's weights of one rank step, as a transposing tile or as rows of 32 ranks.  Rows are padded by 16 bytes, which spreads the
+// operand reads of 16 rows over all banks.
 template <int NK> constexpr int sum_row() { return kStrip<NK> + 4; }
+template <int T> constexpr int rank_row() { return 32 * esize<T>() + 16; }
 template <int WT, bool TRANS, int NK> constexpr int expand_wave_lds() {
-  return kRows * sum_row<NK>() * 4 + (TRANS ? terms<WT>() * tr_plane<kStrip<NK>>() : 0);
+  return kRows * sum_row<NK>() * 4 + (TRANS ? terms<WT>() * tr_plane<kStrip<NK>>() : kStrip<NK> * rank_row<WT>());
 }
+static_assert(kRows * rank_row<X_BF16>() <= kRows * sum_row<2>() * 4, "t fits the sums' space");
 
 // NK: rank steps of 32.  W16: out has 16-bit elements.
 template <int WT, bool TRANS, int NK, bool W16>
@@ -126,20 +131,25 @@ __global__ void __launch_bounds__(256) lora_expand_kernel(int M, int D, int E, i
     const int e = __builtin_amdgcn_readlane(id, __builtin_ctz(lead));
     const uint32_t mask = tile_mask(id, e);
     const uint8_t* we = w + (size_t)e * R * D * esize<WT>();
-    const bool on[2] = {(mask >> l16 & 1) != 0, (mask >> (16 + l16) & 1) != 0};
+    // a rank step's weights of a strip in whole lines.  TRANS: rows r of D elements, chunks of 8 of the 32 x strip tile; else
+    // rows n of R, 16-byte pieces of the 32 ranks
+    constexpr int WP = 16 / esize<WT>(), WL = 32 / WP, WN = TRANS ? 1 : SW * WL / 64;
     Raw<WT> raw[Q];
+    u32x4 wr[WN];
     auto load_w = [&](int n0, int k) {
+      if constexpr (TRANS) {
+        constexpr int CW = SW / 8;
 #pragma unroll
-      for (int q = 0; q < Q; ++q) {
-        if constexpr (TRANS) {                         // rows r of D elements: chunk of the 32 x strip tile
-          constexpr int CW = SW / 8;
+        for (int q = 0; q < Q; ++q) {
           const int c = lane + 64 * q, r = 32 * k + c / CW, n = n0 + 8 * (c % CW);
           if (r < R && n < D) raw_load<WT, true>(we + ((size_t)r * D + n) * esize<WT>(), raw[q]);
           else raw_zero(raw[q]);
-        } else {
-          const int r = 32 * k + 8 * g, n = n0 + 16 * q + l16;
-          if (r < R && n < D) raw_load<WT, true>(we + ((size_t)n * R + r) * esize<WT>(), raw[q]);
-          else raw_zero(raw[q]);
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < WN; ++q) {
+          const int c = lane + 64 * q, n = n0 + c / WL, r = 32 * k + WP * (c % WL);
+          wr[q] = r < R && n < D ? *reinterpret_cast<const u32x4*>(we + ((size_t)n * R + r) * esize<WT>()) : u32x4{0u, 0u, 0u, 0u};
         }
       }
     };
@@ -147,19 +157,36 @@ __global__ void __launch_bounds__(256) lora_expand_kernel(int M, int D, int E, i
       load_w(n_begin, 0);
       load_rows(mask, n_begin);
     }
-    // t of the two 16-row blocks: lane holds row l16 of the block, ranks 32 k + 8 g .. + 7
+    // t of the two 16-row blocks: lane holds row l16 of the block, ranks 32 k + 8 g .. + 7; loaded in whole lines, 2 pieces of
+    // 8 ranks per lane, and turned in LDS
     bf16x8 tf[2][NK][3];
+    uint8_t* tt = reinterpret_cast<uint8_t*>(sums);
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int k = 0; k < NK; ++k) {
+      u32x4 tr[3][2];
 #pragma unroll
-      for (int k = 0; k < NK; ++k) {
-        const int r = 32 * k + 8 * g;
-        const uint16_t* p = t + (size_t)(m0 + 16 * i + l16) * R + r;
+      for (int q = 0; q < 3; ++q)
 #pragma unroll
-        for (int q = 0; q < 3; ++q)
-          tf[i][k][q] = __builtin_bit_cast(bf16x8, on[i] && r < R ? *reinterpret_cast<const u32x4*>(p + q * (size_t)M * R)
-                                                                 : u32x4{0u, 0u, 0u, 0u});
+        for (int h = 0; h < 2; ++h) {
+          const int c = lane + 64 * h, row = c >> 2, r = 32 * k + 8 * (c & 3);
+          tr[q][h] = (mask >> row & 1) && r < R
+                         ? *reinterpret_cast<const u32x4*>(t + (size_t)q * M * R + (size_t)(m0 + row) * R + r)
+                         : u32x4{0u, 0u, 0u, 0u};
+        }
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {
+        wave_lds_fence();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int c = lane + 64 * h;
+          *reinterpret_cast<u32x4*>(tt + (c >> 2) * rank_row<X_BF16>() + (c & 3) * 16) = tr[q][h];
+        }
+        wave_lds_fence();
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          tf[i][k][q] = *reinterpret_cast<const bf16x8*>(tt + (16 * i + l16) * rank_row<X_BF16>() + 16 * g);
       }
+    }
 
     for (int n0 = n_begin; n0 < n_end; n0 += SW) {
       f32x4 acc[Q][2];
@@ -169,24 +196,35 @@ __global__ void __launch_bounds__(256) lora_expand_kernel(int M, int D, int E, i
         for (int i = 0; i < 2; ++i) acc[q][i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < NK; ++k) {
-        bf16x8 wf[Q][NW];
+        wave_lds_fence();
         if constexpr (TRANS) {
-          wave_lds_fence();
 #pragma unroll
           for (int q = 0; q < Q; ++q) tr_write<WT, SW>(tile, lane + 64 * q, raw[q]);
-          wave_lds_fence();
         } else {
 #pragma unroll
-          for (int q = 0; q < Q; ++q) raw_terms<WT>(raw[q], wf[q]);
+          for (int q = 0; q < WN; ++q) {
+            const int c = lane + 64 * q;
+            *reinterpret_cast<u32x4*>(tile + (c / WL) * rank_row<WT>() + (c % WL) * 16) = wr[q];
+          }
         }
+        wave_lds_fence();
         // the next weights (this strip's next rank step, or the next strip's first) fly during the MFMAs
         if (k + 1 < NK) load_w(n0, k + 1);
         else if (n0 + SW < n_end) load_w(n0 + SW, 0);
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
-          if constexpr (TRANS) tr_read<SW, NW>(tile, q, wf[q]);
+          bf16x8 wf[NW];
+          if constexpr (TRANS) {
+            tr_read<SW, NW>(tile, q, wf);
+          } else {
+            Raw<WT> r;
+            const uint8_t* p = tile + (16 * q + l16) * rank_row<WT>() + 8 * g * esize<WT>();
+            r.v[0] = *reinterpret_cast<const u32x4*>(p);
+            if constexpr (WT == X_F32) r.v[1] = *reinterpret_cast<const u32x4*>(p + 16);
+            raw_terms<WT>(r, wf);
+          }
 #pragma unroll
-          for (int i = 0; i < 2; ++i) acc[q][i] = mfma_terms<NW, 3>(wf[q], tf[i][k], acc[q][i]);
+          for (int i = 0; i < 2; ++i) acc[q][i] = mfma_terms<NW, 3>(wf, tf[i][k], acc[q][i]);
         }
       }
       // the sums, MFMA rows = n: lane holds columns 16 q + 4 g .. + 3 of row 16 i + l16
