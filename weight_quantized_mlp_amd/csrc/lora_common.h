@@ -170,13 +170,14 @@ __device__ __forceinline__ int tile_id(const int32_t* ids, int m0, int M, int E)
   const int e = m < M ? ids[m] : -1;
   return e >= 0 && e < E ? e : -1;
 }
-// Bit i: row i is the first of the 32 that names its adapter.
+// Bit i: row i is the first of the 32 that names its adapter.  Scalar masks throughout: written as a condition per lane, the
+// 31 comparisons became 31 nested branches.
 __device__ __forceinline__ uint32_t tile_leaders(int id) {
-  const int lane = threadIdx.x & 31;
-  bool first = id >= 0;
+  if (__ballot(id != __builtin_amdgcn_readfirstlane(id)) == 0) return id >= 0 ? 1u : 0u;   // one adapter, or none
+  uint32_t later = 0;                        // rows whose adapter an earlier row names
 #pragma unroll
-  for (int j = 0; j < 31; ++j) first = first && !(j < lane && __builtin_amdgcn_readlane(id, j) == id);
-  return (uint32_t)__ballot(first);
+  for (int j = 0; j < 31; ++j) later |= (uint32_t)__ballot(id == __builtin_amdgcn_readlane(id, j)) & (~1u << j);
+  return (uint32_t)__ballot(id >= 0) & ~later;
 }
 // Rows of the tile with adapter e.
 __device__ __forceinline__ uint32_t tile_mask(int id, int e) { return (uint32_t)__ballot(id == e); }

@@ -22,7 +22,11 @@ using namespace lora;
 constexpr int kD = 64;               // columns of a workgroup
 constexpr int kScan = 4096;          // rows whose masks are held at once
 
-template <int VT, int NR> constexpr int outer_wave_lds() { return terms<VT>() * tr_plane<kD>() + 3 * tr_plane<16 * NR>(); }
+// A wave's LDS: a block of v and of t's terms.  16-bit v is held as transposing term planes; float32 v as it is (padded rows),
+// and a lane gathers its 8 rows of a column by 4-byte reads, which needs less room than three planes.
+constexpr int kVRow = kD * 4 + 16;
+template <int VT> constexpr int outer_v_lds() { return VT == X_F32 ? kRows * kVRow : terms<VT>() * tr_plane<kD>(); }
+template <int VT, int NR> constexpr int outer_wave_lds() { return outer_v_lds<VT>() + 3 * tr_plane<16 * NR>(); }
 template <int VT, int NR> constexpr int outer_lds() {
   const int stage = 4 * outer_wave_lds<VT, NR>(), red = 4 * 16 * NR * kD * 4;
   return stage > red ? stage : red;
@@ -42,7 +46,7 @@ __global__ void __launch_bounds__(256) lora_outer_kernel(int M, int D, int E, in
   const int l16 = lane & 15, gr = lane >> 4;
   const int nd = (D + kD - 1) / kD, RC = (R + C - 1) / C;
   uint8_t* vt = lds + wave * outer_wave_lds<VT, NR>();
-  uint8_t* ut = vt + NV * tr_plane<kD>();
+  uint8_t* ut = vt + outer_v_lds<VT>();
   for (int64_t wg = blockIdx.x; wg < total; wg += gridDim.x) {
     // columns fastest, then rank chunks, parts and adapters
     const int d0 = (int)(wg % nd) * kD;
@@ -56,11 +60,17 @@ __global__ void __launch_bounds__(256) lora_outer_kernel(int M, int D, int E, in
       for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     for (int s0 = mb; s0 < me; s0 += kScan) {
       __syncthreads();                                  // the masks' and the tiles' last readers
-#pragma unroll 4
-      for (int i = wave; i < kScan / 64; i += 4) {
-        const int m = s0 + 64 * i + lane;
-        const uint64_t b = __ballot(m < me && ids[min(m, me - 1)] == e);
-        if (lane < 2) masks[2 * i + lane] = (uint32_t)(b >> (32 * lane));
+      const int groups = (min(kScan, me - s0) + 63) / 64;
+      for (int i0 = wave; i0 < groups; i0 += 32) {      // 8 groups of 64 rows in flight per wave
+        int id[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) id[q] = ids[min(s0 + 64 * (i0 + 4 * q) + lane, me - 1)];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const int i = i0 + 4 * q;
+          const uint64_t b = __ballot(s0 + 64 * i + lane < me && id[q] == e);
+          if (lane < 2 && i < groups) masks[2 * i + lane] = (uint32_t)(b >> (32 * lane));
+        }
       }
       __syncthreads();
       const int blocks = (min(kScan, me - s0) + kRows - 1) / kRows;
@@ -68,19 +78,27 @@ __global__ void __launch_bounds__(256) lora_outer_kernel(int M, int D, int E, in
         while (b < blocks && masks[b] == 0) b += 4;
         return b;
       };
-      // one block's loads, in chunks of 8 columns: 4 of v and NR of each term of t per lane
-      Raw<VT> raw[4];
+      // one block's loads, in whole lines: 16-byte pieces of v, chunks of 8 ranks of each term of t
+      constexpr int VP = 16 / esize<VT>(), VL = kD / VP, VN = kRows * VL / 64;   // 16-byte pieces of v: elements, per row, per lane
+      u32x4 raw[VN];
       u32x4 u[3][NR];
       auto load = [&](int b) {
         const uint32_t mask = masks[b];
         const int m0 = s0 + kRows * b;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int c = lane + 64 * q, row = c >> 3, d = d0 + 8 * (c & 7);
+        for (int q = 0; q < VN; ++q) {
+          const int c = lane + 64 * q, row = c / VL, d = d0 + VP * (c % VL);
           const bool on = (mask >> row & 1) != 0;
           const uint8_t* p = v + ((size_t)(m0 + row) * D + d) * esize<VT>();
-          if (on && d + 8 <= D) raw_load<VT, false>(p, raw[q]);
-          else raw_load_part<VT>(p, on ? D - d : 0, raw[q]);
+          raw[q] = u32x4{0u, 0u, 0u, 0u};
+          if (on && d + VP <= D) {
+            if constexpr (VT == X_F32) raw[q] = *reinterpret_cast<const u32x4_a4*>(p);
+            else raw[q] = *reinterpret_cast<const u32x4_a2*>(p);
+          } else if (on && d < D) {
+            Raw<VT> part;
+            raw_load_part<VT>(p, D - d, part);
+            raw[q] = part.v[0];
+          }
         }
 #pragma unroll
         for (int q = 0; q < NR; ++q) {
@@ -97,7 +115,11 @@ __global__ void __launch_bounds__(256) lora_outer_kernel(int M, int D, int E, in
       while (b < blocks) {
         wave_lds_fence();
 #pragma unroll
-        for (int q = 0; q < 4; ++q) tr_write<VT, kD>(vt, lane + 64 * q, raw[q]);
+        for (int q = 0; q < VN; ++q) {
+          const int c = lane + 64 * q;
+          if constexpr (VT == X_F32) *reinterpret_cast<u32x4*>(vt + (c / VL) * kVRow + (c % VL) * 16) = raw[q];
+          else tr_write<VT, kD>(vt, c, Raw<VT>{{raw[q]}});
+        }
 #pragma unroll
         for (int q = 0; q < NR; ++q) {
           const int c = lane + 64 * q;
@@ -114,7 +136,14 @@ __global__ void __launch_bounds__(256) lora_outer_kernel(int M, int D, int E, in
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           bf16x8 vf[NV];
-          tr_read<kD, NV>(vt, j, vf);
+          if constexpr (VT == X_F32) {
+            float x[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) x[q] = *reinterpret_cast<const float*>(vt + (8 * gr + q) * kVRow + (16 * j + l16) * 4);
+            split3<8>(x, vf);
+          } else {
+            tr_read<kD, NV>(vt, j, vf);
+          }
 #pragma unroll
           for (int i = 0; i < NR; ++i)
             acc[i][j] = RCONTIG ? mfma_terms<3, NV>(uf[i], vf, acc[i][j]) : mfma_terms<NV, 3>(vf, uf[i], acc[i][j]);
@@ -164,14 +193,21 @@ inline int64_t outer_tiles(int D, int E, int R) {
   const int C = R <= 16 ? 16 : (R <= 32 ? 32 : 64);
   return (int64_t)E * ((D + kD - 1) / kD) * ((R + C - 1) / C);
 }
-// Parts of the rows: workgroups for four per CU, each part at least 256 rows, at most 8.
+// Parts of the rows: the number, at most 8 and of at least 256 rows each, for which reading v (stretched by the last round of
+// workgroups standing partly idle, 3 per CU, which LDS allows every form) and the partial sums' way through memory take the
+// fewest bytes.
 inline int outer_parts(int M, int D, int E, int R) {
-  const int64_t tiles = outer_tiles(D, E, R);
-  int p = (int)std::min<int64_t>(8, 1024 / std::max<int64_t>(1, tiles));
-  p = std::min(p, M / 256);
-  if (p <= 1) return 1;
-  const int rows = outer_part_rows(M, p);
-  return (M + rows - 1) / rows;
+  const int64_t tiles = outer_tiles(D, E, R), slots = 768;
+  int best = 1;
+  double least = 1e30;
+  for (int p = 1; p <= 8 && (p == 1 || M / p >= 256); ++p) {
+    const int rows = outer_part_rows(std::max(M, 1), p), n = (M + rows - 1) / std::max(rows, 1);
+    if (p > 1 && n != p) continue;           // no empty part
+    const double idle = (double)((tiles * p + slots - 1) / slots * slots) / (double)(tiles * p);
+    const double cost = idle * M * 2.0 * D + (p > 1 ? p * 8.0 * E * R * D : 0.0);
+    if (cost < least) least = cost, best = p;
+  }
+  return best;
 }
 
 template <int VT, int NR, bool RCONTIG>

@@ -27,9 +27,10 @@ template <int T> constexpr int row_bytes() { return 64 * esize<T>() + 16; }
 template <int XT, int WT, bool TRANS, int NR> constexpr int shrink_wave_lds() {
   return kRows * row_bytes<XT>() + (TRANS ? terms<WT>() * tr_plane<16 * NR>() : 16 * NR * row_bytes<WT>());
 }
-// Waves of a workgroup: what fits a CU's LDS.
+// Waves of a workgroup: 8 where two workgroups then share a CU's LDS, else as many as one can have, at most 16.
 template <int XT, int WT, bool TRANS, int NR> constexpr int shrink_waves() {
-  return 8 * shrink_wave_lds<XT, WT, TRANS, NR>() <= 160 * 1024 ? 8 : 4;
+  constexpr int each = shrink_wave_lds<XT, WT, TRANS, NR>(), n = 160 * 1024 / each;
+  return 16 * each <= 160 * 1024 ? 8 : (n < 16 ? n : 16);
 }
 template <int XT, int WT, bool TRANS, int NR> constexpr int shrink_lds() {
   constexpr int waves = shrink_waves<XT, WT, TRANS, NR>();
@@ -258,13 +259,11 @@ __global__ void __launch_bounds__(256) lora_terms_kernel(int64_t plane, int E, i
   }
 }
 
-// Parts of the contraction: where fewer than a workgroup per CU would read over 512 KB of x each, as many as bring that
-// to 256 KB, at most 8 and two workgroups per CU.
+// Parts of the contraction: where fewer than a workgroup per CU would read over 512 KB of x each, two per CU, at most 8.
 int shrink_parts(int M, int D, int R, int es) {
   const int tiles = ((M + kRows - 1) / kRows) * ((R + 63) / 64);
-  const int64_t bytes = (int64_t)kRows * D * es;
-  if (tiles >= 256 || bytes <= (512 << 10)) return 1;
-  const int s = (int)std::min<int64_t>(std::min(8, 512 / tiles), (bytes + (256 << 10) - 1) / (256 << 10));
+  if (tiles >= 256 || (int64_t)kRows * D * es <= (512 << 10)) return 1;
+  const int s = std::min(8, 512 / tiles);
   if (s <= 1) return 1;
   const int nb = (D + 63) / 64, per = (nb + s - 1) / s;
   return (nb + per - 1) / per;             // no empty part
