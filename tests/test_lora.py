@@ -266,3 +266,18 @@ def test_graph_replays():
         g.replay()
         torch.cuda.synchronize()
         assert all(np.array_equal(host(t), w) for t, w in zip((out, dx, da, db), want)), i
+
+
+@pytest.mark.parametrize("xt,wt,R", [(F32, F16, 64), (F32, BF16, 64), (BF16, BF16, 64), (BF16, BF16, 32), (F32, F32, 32)])
+def test_a_row_alone_on_its_adapter(xt, wt, R):
+    """Every row of a tile in turn alone on one adapter, the others on another or on none."""
+    M, K, N, E = 70, 1040, 64, 32
+    p = problem((M, K, N, E, R, xt, wt), "one")
+    n = p["n"]
+    for rest in (-1, 3):
+        for r in range(M):
+            ids = np.full(M, rest, dtype=np.int32)
+            ids[r] = 30
+            p["ids"].copy_(torch.from_numpy(ids))
+            ref = oracle.lora_ref(n["x"], n["a"], n["b"], n["scale"], ids, n["y"])
+            assert rel2(host(forward(p)) - n["y"], ref - n["y"]) <= norm_bound(K, R) + 1e-6, (rest, r)

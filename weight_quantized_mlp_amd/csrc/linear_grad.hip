@@ -42,67 +42,53 @@ __device__ __forceinline__ int grad_row_exp(float amax) {
   return e < -126 ? -126 : e;
 }
 
-template <bool BF>
-__device__ __forceinline__ float dy_elem(const void* row, int n) {
-  if constexpr (BF) return bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(row)[n]);
-  else return reinterpret_cast<const float*>(row)[n];
-}
-
-// One workgroup per row of dy [M][N] (any N, so rows are only element-aligned): the row's largest magnitude, then
-// the scaled float16 terms, [TERMS][M][Np] with zeros from N to Np (a multiple of 64).  The second reading of the
-// row comes from the cache.
-template <bool BF, bool SC, int TERMS>
+// One workgroup per row of dy [M][N] (any N, so rows are only element-aligned): the row's largest magnitude, then the scaled
+// float16 terms, [TERMS][M][Np] with zeros from N to Np (a multiple of 64).  A thread keeps RC chunks of 8 elements in registers,
+// loaded without a branch between them so that all are in flight at once; longer rows read the rest twice.  The up to 7 elements
+// behind the last whole chunk are one thread's.
+template <bool BF, bool SC, int TERMS, int RC>
 __global__ void __launch_bounds__(256) grad_prep_kernel(int M, int N, int Np, const void* __restrict__ dy,
                                                         const float* __restrict__ scale, uint16_t* __restrict__ a16,
                                                         float* __restrict__ rowscale) {
+  typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
+  typedef uint32_t u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
   __shared__ float wmax[4];
   const int m = (int)blockIdx.x, t = (int)threadIdx.x;
-  const void* row = reinterpret_cast<const uint8_t*>(dy) + (size_t)m * N * (BF ? 2 : 4);
-  auto load8 = [&](int c, float* v) {
-    const int n0 = 8 * c;
-    if (n0 + 8 <= N) {
-      if constexpr (BF) {
-        uint16_t h[8];
-        __builtin_memcpy(h, reinterpret_cast<const uint16_t*>(row) + n0, 16);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = bf16_bits_to_f32(h[j]);
-      } else {
-        __builtin_memcpy(v, reinterpret_cast<const float*>(row) + n0, 32);
-      }
-      if constexpr (SC) {
-        const f32x4 s0 = *reinterpret_cast<const f32x4*>(scale + n0), s1 = *reinterpret_cast<const f32x4*>(scale + n0 + 4);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[j] *= s0[j];
-          v[4 + j] *= s1[j];
-        }
-      }
+  const uint8_t* row = reinterpret_cast<const uint8_t*>(dy) + (size_t)m * N * (BF ? 2 : 4);
+  const int nf = N / 8;                          // whole chunks
+  struct Chunk { u32x4 v[BF ? 1 : 2]; f32x4 s[SC ? 2 : 1]; };
+  auto load = [&](int c, Chunk& d) {             // c < nf
+    if constexpr (BF) {
+      d.v[0] = *reinterpret_cast<const u32x4_a2*>(row + 16 * (size_t)c);
     } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[j] = n0 + j < N ? dy_elem<BF>(row, n0 + j) : 0.f;
-        if constexpr (SC) v[j] = n0 + j < N ? v[j] * scale[n0 + j] : 0.f;
-      }
+      d.v[0] = *reinterpret_cast<const u32x4_a4*>(row + 32 * (size_t)c);
+      d.v[1] = *reinterpret_cast<const u32x4_a4*>(row + 32 * (size_t)c + 16);
+    }
+    if constexpr (SC) {
+      d.s[0] = reinterpret_cast<const f32x4*>(scale)[2 * c];
+      d.s[1] = reinterpret_cast<const f32x4*>(scale)[2 * c + 1];
     }
   };
-  const int nch = Np / 8;
-  float amax = 0.f;
-  for (int c = t; c < nch; c += 256) {
-    float v[8];
-    load8(c, v);
+  auto values = [&](const Chunk& d, float* v) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
-  }
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t u = d.v[0][j];
+      if constexpr (BF) {
+        v[2 * j] = __uint_as_float(u << 16);
+        v[2 * j + 1] = __uint_as_float(u & 0xFFFF0000u);
+      } else {
+        const uint32_t w = d.v[1][j];
+        v[j] = __uint_as_float(u);
+        v[4 + j] = __uint_as_float(w);
+      }
+    }
+    if constexpr (SC) {
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) amax = fmaxf(amax, __shfl_xor(amax, off, 64));
-  if ((t & 63) == 0) wmax[t >> 6] = amax;
-  __syncthreads();
-  const int e = grad_row_exp(fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3])));
-  if (t == 0) rowscale[m] = ldexpf(1.0f, e);
+      for (int j = 0; j < 8; ++j) v[j] *= d.s[j >> 2][j & 3];
+    }
+  };
   uint16_t* o = a16 + (size_t)m * Np;
-  for (int c = t; c < nch; c += 256) {
-    float v[8];
-    load8(c, v);
+  auto put = [&](int c, const float* v, int e) {
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -113,6 +99,55 @@ __global__ void __launch_bounds__(256) grad_prep_kernel(int M, int N, int Np, co
     }
     reinterpret_cast<u32x4*>(o)[c] = u32x4{hi[0], hi[1], hi[2], hi[3]};
     if constexpr (TERMS == 2) reinterpret_cast<u32x4*>(o + (size_t)M * Np)[c] = u32x4{lo[0], lo[1], lo[2], lo[3]};
+  };
+  float amax = 0.f, keep[RC][8], rest = 0.f;
+  auto maximum = [&](const float* v) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
+  };
+  if (t < N - 8 * nf) {                          // element 8 nf + t
+    const int n = 8 * nf + t;
+    rest = BF ? bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(row)[n]) : reinterpret_cast<const float*>(row)[n];
+    if constexpr (SC) rest *= scale[n];
+    amax = fabsf(rest);
+  }
+  if (nf > 0) {
+    Chunk raw[RC];
+#pragma unroll
+    for (int i = 0; i < RC; ++i) load(min(t + 256 * i, nf - 1), raw[i]);   // past the end: the last one again, not used
+#pragma unroll
+    for (int i = 0; i < RC; ++i) {
+      values(raw[i], keep[i]);
+      maximum(keep[i]);
+    }
+    for (int c = t + 256 * RC; c < nf; c += 256) {
+      float v[8];
+      load(c, raw[0]);
+      values(raw[0], v);
+      maximum(v);
+    }
+  }
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) amax = fmaxf(amax, __shfl_xor(amax, off, 64));
+  if ((t & 63) == 0) wmax[t >> 6] = amax;
+  __syncthreads();
+  const int e = grad_row_exp(fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3])));
+  if (t == 0) rowscale[m] = ldexpf(1.0f, e);
+#pragma unroll
+  for (int i = 0; i < RC; ++i)
+    if (t + 256 * i < nf) put(t + 256 * i, keep[i], e);
+  for (int c = t + 256 * RC; c < nf; c += 256) {
+    Chunk d;
+    float v[8];
+    load(c, d);
+    values(d, v);
+    put(c, v, e);
+  }
+  if (t < Np - 8 * nf) {                         // the last elements and the zeros behind them
+    const float x = ldexpf(rest, -e);
+    const _Float16 h = (_Float16)x;
+    o[8 * nf + t] = __builtin_bit_cast(uint16_t, h);
+    if constexpr (TERMS == 2) o[(size_t)M * Np + 8 * nf + t] = __builtin_bit_cast(uint16_t, (_Float16)(x - (float)h));
   }
 }
 
@@ -123,7 +158,7 @@ constexpr int kScaleRow = 72;          // float16 scales of one group: 64 n, pad
 constexpr int kABytes = 128 * 32;      // activation bytes per 32 rows and stage
 
 template <int FMT> constexpr int b_stage() { return FMT == 0 ? 64 * 256 : 64 * 128 + 16 * kScaleRow * 2; }
-template <int FMT> constexpr int grad_lds(int mb) { return 2 * (mb * kABytes + b_stage<FMT>()); }
+template <int FMT> constexpr int grad_lds(int mb) { return 2 * (mb * kABytes + b_stage<FMT>()) + 128 * 4; }   // + row scales
 
 // Work plan, a function of the shape: tiles of bm x 256; when the last round of tiles would leave many of the slots
 // idle, its tiles are cut into S parts of `per` steps of 64 n, whose float32 sums a second kernel adds in order.
@@ -358,30 +393,35 @@ __global__ void __launch_bounds__(256, 2) grad_gemm_kernel(int M, int N, int Np,
   };
 
   const int last = s1 - 1;
-  auto fetch = [&](int step, int stage) {     // copies of a step (past the end: the last one again, never used)
-    const int s = min(step, last);
-    copy_a(s, stage);
-    if constexpr (FMT == 0) copy_w(s, stage);
+  auto fetch = [&](int step, int stage) {     // copies of a step
+    copy_a(step, stage);
+    if constexpr (FMT == 0) copy_w(step, stage);
   };
-  // Prologue: steps s0 and s0 + 1 on their way, step s0 landed.
+  // Prologue: steps s0 and s0 + 1 on their way, step s0 landed.  The tile's row scales come along for the epilogue.
+  const float row_scale = tid < BM ? rowscale[min(m0 + tid, M - 1)] : 0.f;
+  if constexpr (FMT == 1) load_rec(s0);
+  fetch(s0, 0);
   if constexpr (FMT == 1) {
-    load_rec(s0);
     write_rec(0);
     load_rec(min(s0 + 1, last));
   }
-  fetch(s0, 0);
-  wait_vmem<0>();
+  if (s0 < last) fetch(s0 + 1, 1);
+  // NVFP4: the records of step s0 have been waited for, and with them everything issued before; FP8: all but the second fetch
+  if constexpr (FMT == 0) {
+    if (s0 < last) wait_vmem<MB + 4>();
+    else wait_vmem<0>();
+  } else {
+    if (s0 < last) wait_vmem<MB + 3>();
+    else wait_vmem<3>();
+  }
   wait_lds();
   __syncthreads();
-  fetch(s0 + 1, 1);
-  if constexpr (FMT == 1) write_rec(1);
   f16x8 af0[MB], af1[MB];
   Raw raw0, raw1;
   read_a(0, 0, af0);
   read_b(0, 0, raw0);
   for (int s = s0; s < s1; ++s) {
     const int st = (s - s0) & 1;
-    if constexpr (FMT == 1) load_rec(min(s + 2, last));
     read_a(st, 1, af1);
     read_b(st, 1, raw1);
     mfmas(af0, raw0);
@@ -394,18 +434,18 @@ __global__ void __launch_bounds__(256, 2) grad_gemm_kernel(int M, int N, int Np,
     read_b(st, 3, raw1);
     mfmas(af0, raw0);
     __builtin_amdgcn_sched_barrier(0);
-    wait_vmem<0>();                            // step s + 1's copies (issued a step ago) and records landed
+    // NVFP4: records of step s + 1 (its stage's last readers passed the previous barrier)
+    if constexpr (FMT == 1) write_rec(st ^ 1);
+    wait_vmem<0>();                            // step s + 1's copies (issued a step ago) landed
     wait_lds();                                // this wave's reads of stage st are in registers, its writes in LDS
     __syncthreads();
-    fetch(s + 2, st);
-    if constexpr (FMT == 1) write_rec(st);     // records of step s + 2
+    if constexpr (FMT == 1) load_rec(min(s + 2, last));
+    if (s + 2 <= last) fetch(s + 2, st);
     read_a(st ^ 1, 0, af0);
     read_b(st ^ 1, 0, raw0);
     mfmas(af1, raw1);
     __builtin_amdgcn_sched_barrier(0);
   }
-  wait_vmem<0>();                              // trailing copies land before the LDS is released
-
   if (part >= 0) {                             // raw sums [BM][256], finished by grad_finish_kernel
     float* pt = partials + (size_t)b * BM * kCols;
 #pragma unroll
@@ -423,6 +463,9 @@ __global__ void __launch_bounds__(256, 2) grad_gemm_kernel(int M, int N, int Np,
       }
     return;
   }
+  float* rscale = reinterpret_cast<float*>(lds + 2 * STAGE);
+  if (tid < BM) rscale[tid] = row_scale;
+  __syncthreads();
   const float c = FMT == 0 ? 1.0f : inv;
 #pragma unroll
   for (int i = 0; i < RB; ++i)
@@ -430,7 +473,7 @@ __global__ void __launch_bounds__(256, 2) grad_gemm_kernel(int M, int N, int Np,
     for (int r = 0; r < 16; ++r) {
       const int m = m0 + 32 * i + 8 * (r >> 2) + 4 * h + (r & 3);
       if (m >= M) continue;
-      const float rs = rowscale[m];
+      const float rs = rscale[m - m0];
       const float v0 = acc[i][0][r] * c * rs, v1 = acc[i][1][r] * c * rs;
       if constexpr (FMT == 0) {
         const int k = k0 + 64 * wave + li;
@@ -520,12 +563,18 @@ hipError_t grad_dispatch(int M, int N, int K, int terms, const GradPlan& p, cons
   return grad_gemm<FMT, 4, 1>(M, N, K, p, a16, rs, w, inv, dx, bf, partials, st);
 }
 
-template <bool BF, bool SC>
-void grad_prep(int M, int N, int Np, int terms, const void* dy, const float* scale, uint16_t* a16, float* rs, hipStream_t st) {
-  if (terms == 2)
-    hipLaunchKernelGGL((grad_prep_kernel<BF, SC, 2>), dim3(M), dim3(256), 0, st, M, N, Np, dy, scale, a16, rs);
+// 3 register chunks cover rows of 6144, 9 rows of 18432.
+template <bool BF, bool SC, int TERMS>
+void grad_prep(int M, int N, int Np, const void* dy, const float* scale, uint16_t* a16, float* rs, hipStream_t st) {
+  if (Np <= 3 * 2048)
+    hipLaunchKernelGGL((grad_prep_kernel<BF, SC, TERMS, 3>), dim3(M), dim3(256), 0, st, M, N, Np, dy, scale, a16, rs);
   else
-    hipLaunchKernelGGL((grad_prep_kernel<BF, SC, 1>), dim3(M), dim3(256), 0, st, M, N, Np, dy, scale, a16, rs);
+    hipLaunchKernelGGL((grad_prep_kernel<BF, SC, TERMS, 9>), dim3(M), dim3(256), 0, st, M, N, Np, dy, scale, a16, rs);
+}
+template <bool BF, bool SC, typename... A>
+void grad_prep_terms(int terms, A... a) {
+  if (terms == 2) grad_prep<BF, SC, 2>(a...);
+  else grad_prep<BF, SC, 1>(a...);
 }
 
 }  // namespace
@@ -544,11 +593,11 @@ hipError_t launch_linear_grad(int fmt, int M, int N, int K, const void* dy, XTyp
   const int Np = p.steps * 64;
   const bool bf = dxt == X_BF16;
   if (dyt == X_BF16) {
-    if (fmt == 0) grad_prep<true, true>(M, N, Np, terms, dy, scale, a16, rs, st);
-    else grad_prep<true, false>(M, N, Np, terms, dy, scale, a16, rs, st);
+    if (fmt == 0) grad_prep_terms<true, true>(terms, M, N, Np, dy, scale, a16, rs, st);
+    else grad_prep_terms<true, false>(terms, M, N, Np, dy, scale, a16, rs, st);
   } else {
-    if (fmt == 0) grad_prep<false, true>(M, N, Np, terms, dy, scale, a16, rs, st);
-    else grad_prep<false, false>(M, N, Np, terms, dy, scale, a16, rs, st);
+    if (fmt == 0) grad_prep_terms<false, true>(terms, M, N, Np, dy, scale, a16, rs, st);
+    else grad_prep_terms<false, false>(terms, M, N, Np, dy, scale, a16, rs, st);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;

@@ -84,6 +84,7 @@ __global__ void __launch_bounds__(256) lora_outer_kernel(int M, int D, int E, in
       u32x4 u[3][NR];
       auto load = [&](int b) {
         const uint32_t mask = masks[b];
+        const bool whole = d0 + kD <= D;                  // the same for all lanes: no branch between the loads
         const int m0 = s0 + kRows * b;
 #pragma unroll
         for (int q = 0; q < VN; ++q) {
@@ -91,12 +92,18 @@ __global__ void __launch_bounds__(256) lora_outer_kernel(int M, int D, int E, in
           const bool on = (mask >> row & 1) != 0;
           const uint8_t* p = v + ((size_t)(m0 + row) * D + d) * esize<VT>();
           raw[q] = u32x4{0u, 0u, 0u, 0u};
-          if (on && d + VP <= D) {
+          if (whole ? on : on && d + VP <= D) {
             if constexpr (VT == X_F32) raw[q] = *reinterpret_cast<const u32x4_a4*>(p);
             else raw[q] = *reinterpret_cast<const u32x4_a2*>(p);
-          } else if (on && d < D) {
+          }
+        }
+        if (!whole) {                                     // the columns' end: pieces that D cuts
+#pragma unroll
+          for (int q = 0; q < VN; ++q) {
+            const int c = lane + 64 * q, row = c / VL, d = d0 + VP * (c % VL);
+            if (!(mask >> row & 1) || d >= D || d + VP <= D) continue;
             Raw<VT> part;
-            raw_load_part<VT>(p, D - d, part);
+            raw_load_part<VT>(v + ((size_t)(m0 + row) * D + d) * esize<VT>(), D - d, part);
             raw[q] = part.v[0];
           }
         }
@@ -194,8 +201,8 @@ inline int64_t outer_tiles(int D, int E, int R) {
   return (int64_t)E * ((D + kD - 1) / kD) * ((R + C - 1) / C);
 }
 // Parts of the rows: the number, at most 8 and of at least 256 rows each, for which reading v (stretched by the last round of
-// workgroups standing partly idle, 3 per CU, which LDS allows every form) and the partial sums' way through memory take the
-// fewest bytes.
+// workgroups standing partly idle, 3 per CU, which LDS allows every form), the partial sums' way through memory and what a
+// workgroup's start and end cost (about 5 us of its share of the bandwidth, 28 KB) take the fewest bytes.
 inline int outer_parts(int M, int D, int E, int R) {
   const int64_t tiles = outer_tiles(D, E, R), slots = 768;
   int best = 1;
@@ -204,7 +211,7 @@ inline int outer_parts(int M, int D, int E, int R) {
     const int rows = outer_part_rows(std::max(M, 1), p), n = (M + rows - 1) / std::max(rows, 1);
     if (p > 1 && n != p) continue;           // no empty part
     const double idle = (double)((tiles * p + slots - 1) / slots * slots) / (double)(tiles * p);
-    const double cost = idle * M * 2.0 * D + (p > 1 ? p * 8.0 * E * R * D : 0.0);
+    const double cost = idle * M * 2.0 * D + (p > 1 ? p * 8.0 * E * R * D : 0.0) + 28672.0 * (double)(tiles * p);
     if (cost < least) least = cost, best = p;
   }
   return best;

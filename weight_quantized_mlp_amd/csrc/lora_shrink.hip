@@ -27,10 +27,12 @@ template <int T> constexpr int row_bytes() { return 64 * esize<T>() + 16; }
 template <int XT, int WT, bool TRANS, int NR> constexpr int shrink_wave_lds() {
   return kRows * row_bytes<XT>() + (TRANS ? terms<WT>() * tr_plane<16 * NR>() : 16 * NR * row_bytes<WT>());
 }
-// Waves of a workgroup: 8 where two workgroups then share a CU's LDS, else as many as one can have, at most 16.
+// Waves of a workgroup: 8 where two workgroups then share a CU's LDS or an operand is float32, else (16-bit operands of rank 64)
+// as many as one workgroup's LDS holds.
 template <int XT, int WT, bool TRANS, int NR> constexpr int shrink_waves() {
   constexpr int each = shrink_wave_lds<XT, WT, TRANS, NR>(), n = 160 * 1024 / each;
-  return 16 * each <= 160 * 1024 ? 8 : (n < 16 ? n : 16);
+  constexpr int most = 16 * each <= 160 * 1024 || XT == X_F32 || WT == X_F32 ? 8 : 16;
+  return n < most ? n : most;
 }
 template <int XT, int WT, bool TRANS, int NR> constexpr int shrink_lds() {
   constexpr int waves = shrink_waves<XT, WT, TRANS, NR>();
@@ -83,6 +85,7 @@ __global__ void __launch_bounds__((64 * shrink_waves<XT, WT, TRANS, NR>()))
     u32x4 xr[XN], wr[WN];
     Raw<WT> wtr[TRANS ? 2 : 1][NR];
     auto load = [&](int b) {
+      const bool whole = 64 * b + 64 <= D;               // the same for all lanes: no branch between the loads
 #pragma unroll
       for (int q = 0; q < XN; ++q) {
         const int c = lane + 64 * q, row = c / XL, d = 64 * b + XP * (c % XL);
@@ -90,16 +93,24 @@ __global__ void __launch_bounds__((64 * shrink_waves<XT, WT, TRANS, NR>()))
         const bool on = (mask >> row & 1) != 0;
         xr[q] = u32x4{0u, 0u, 0u, 0u};
         if constexpr (TRANS) {                         // x = dy: D may be any number
-          if (on && d + XP <= D) {
+          if (whole ? on : on && d + XP <= D) {
             if constexpr (XT == X_F32) xr[q] = *reinterpret_cast<const u32x4_a4*>(p);
             else xr[q] = *reinterpret_cast<const u32x4_a2*>(p);
-          } else if (on && d < D) {
-            Raw<XT> part;
-            raw_load_part<XT>(p, D - d, part);
-            xr[q] = part.v[0];
           }
         } else {                                       // D is a multiple of 16
           if (on && d < D) xr[q] = *reinterpret_cast<const u32x4*>(p);
+        }
+      }
+      if constexpr (TRANS) {
+        if (!whole) {                                    // the contraction's end: pieces that D cuts
+#pragma unroll
+          for (int q = 0; q < XN; ++q) {
+            const int c = lane + 64 * q, row = c / XL, d = 64 * b + XP * (c % XL);
+            if (!(mask >> row & 1) || d >= D || d + XP <= D) continue;
+            Raw<XT> part;
+            raw_load_part<XT>(x + ((size_t)(m0 + row) * D + d) * esize<XT>(), D - d, part);
+            xr[q] = part.v[0];
+          }
         }
       }
       if constexpr (TRANS) {                           // rows d, R contiguous: chunk c of the 32 x C tile of step k
