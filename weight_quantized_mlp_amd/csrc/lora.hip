@@ -40,8 +40,9 @@ hipError_t launch_lora(int M, int K, int N, int E, int R, const void* x, XType x
   const LoraWs L = lora_ws(M, K, N, E, R, false);
   uint8_t* p = reinterpret_cast<uint8_t*>(ws);
   uint16_t* t = reinterpret_cast<uint16_t*>(p);
-  hipError_t err = lora_shrink(M, K, E, R, x, xt, a, wt, false, scale, ids, t, reinterpret_cast<float*>(p + L.parts), st);
-  if (err == hipSuccess) err = lora_expand(M, N, E, R, t, b, wt, false, ids, y, out, X_F32, st);
+  const bool few = lora_few_rows(M, K, N, R, wt);
+  hipError_t err = lora_shrink(few, M, K, E, R, x, xt, a, wt, false, scale, ids, t, reinterpret_cast<float*>(p + L.parts), st);
+  if (err == hipSuccess) err = lora_expand(few, M, N, E, R, t, b, wt, false, ids, y, out, X_F32, st);
   return err;
 }
 
@@ -53,15 +54,16 @@ hipError_t launch_lora_backward(int M, int K, int N, int E, int R, const void* d
   uint16_t* t = reinterpret_cast<uint16_t*>(p);
   uint16_t* dt = reinterpret_cast<uint16_t*>(p + L.dt);
   float* parts = reinterpret_cast<float*>(p + L.parts);
+  const bool few = lora_few_rows(M, K, N, R, wt);
   hipError_t err = hipSuccess;
   if (db != nullptr) {
-    if (M > 0) err = lora_shrink(M, K, E, R, x, xt, a, wt, false, scale, ids, t, parts, st);
+    if (M > 0) err = lora_shrink(few, M, K, E, R, x, xt, a, wt, false, scale, ids, t, parts, st);
     if (err == hipSuccess) err = lora_outer(M, N, E, R, t, dy, dyt, true, ids, db, parts, st);
   }
   if (da == nullptr && dx == nullptr) return err;
-  if (err == hipSuccess && M > 0) err = lora_shrink(M, N, E, R, dy, dyt, b, wt, true, scale, ids, dt, parts, st);
+  if (err == hipSuccess && M > 0) err = lora_shrink(few, M, N, E, R, dy, dyt, b, wt, true, scale, ids, dt, parts, st);
   if (err == hipSuccess && da != nullptr) err = lora_outer(M, K, E, R, dt, x, xt, false, ids, da, parts, st);
-  if (err == hipSuccess && dx != nullptr && M > 0) err = lora_expand(M, K, E, R, dt, a, wt, true, ids, dx0, dx, dxt, st);
+  if (err == hipSuccess && dx != nullptr && M > 0) err = lora_expand(few, M, K, E, R, dt, a, wt, true, ids, dx0, dx, dxt, st);
   return err;
 }
 

@@ -184,18 +184,25 @@ __device__ __forceinline__ uint32_t tile_mask(int id, int e) { return (uint32_t)
 
 }  // namespace lora
 
-// Whether a batch takes the row kernels (one row at a time, every row reading its adapter) instead of the tiles.
-inline bool lora_few_rows(int M, int R) { return (int64_t)M * R <= 2048; }
+// Whether a batch takes the row kernels (one row at a time, every row reading its adapter) instead of the tiles: while what
+// all rows read of their adapters, from L2, stays below 300 MB and the work small.  At 5120 -> 17408 in bfloat16, all rows on one
+// adapter (the tiles' best case), rank 16: 256 rows 24 us against 28, 512 rows 43 against 35; rank 64: 64 rows 17 against 25,
+// 128 rows 29 against 26; on random adapters 512 rows of rank 16 take 44 us against 177.
+inline bool lora_few_rows(int M, int K, int N, int R, XType wt) {
+  const int64_t mr = (int64_t)M * (R < 16 ? 16 : R);
+  return mr <= 16384 && mr * ((int64_t)K + N) * (wt == X_F32 ? 4 : 2) <= 300000000;
+}
 
 // Launchers of the three products (internal to the lora files).  The rank-R intermediate is held as its operand
 // terms, t [3][M][R] bfloat16 of scale[e] * sum, so that the many workgroups that read it neither add nor split it;
 // rows without an adapter are not written.
-// t = scale[e] * sum_d x[m,d] w[e][r,d] (trans: w[e][d,r]), e = ids[m]; parts: scratch of lora_shrink_bytes.
-hipError_t lora_shrink(int M, int D, int E, int R, const void* x, XType xt, const void* w, XType wt, bool trans,
+// t = scale[e] * sum_d x[m,d] w[e][r,d] (trans: w[e][d,r]), e = ids[m]; few: by rows (lora_few_rows); parts: scratch of
+// lora_shrink_bytes.
+hipError_t lora_shrink(bool few, int M, int D, int E, int R, const void* x, XType xt, const void* w, XType wt, bool trans,
                        const float* scale, const int32_t* ids, uint16_t* t, float* parts, hipStream_t st);
 size_t lora_shrink_bytes(int M, int D, int R, XType xt);
 // out[m,n] = base[m,n] + sum_r t[m,r] w[e][n,r] (trans: w[e][r,n]); base may be null or out.
-hipError_t lora_expand(int M, int D, int E, int R, const uint16_t* t, const void* w, XType wt, bool trans,
+hipError_t lora_expand(bool few, int M, int D, int E, int R, const uint16_t* t, const void* w, XType wt, bool trans,
                        const int32_t* ids, const void* base, void* out, XType ot, hipStream_t st);
 // g[e][r,d] (rcontig: g[e][d,r]) = sum_{m: ids[m] = e} t[m,r] v[m,d]; parts: scratch of lora_outer_bytes.
 hipError_t lora_outer(int M, int D, int E, int R, const uint16_t* t, const void* v, XType vt, bool rcontig,

@@ -23,32 +23,35 @@ using namespace lora;
 // Columns a wave takes at a time, by rank steps: half as many where the operand t takes more registers.
 template <int NK> constexpr int kStrip = NK == 1 ? 64 : 32;
 
-// 16 bytes of a row of the output: 4 float32 or 8 16-bit elements from n on; elements at D and beyond read as 0 and are not
-// written (16-bit rows end on a whole piece: D is a multiple of 16 there).  Both streams pass the caches once, and say so:
-// the adapters' weights, which every row tile reads again, stay (4099 rows x 17408: 153 -> 138 us).
+// 16 bytes of a row of the output: 4 float32 (rows of any length: element-aligned) or 8 16-bit elements (rows of a multiple of
+// 16) from n on; elements at D and beyond read as 0 and are not written.  Both streams pass the caches once, and say so: the
+// adapters' weights, which every row tile reads again, stay (4099 rows x 17408: 153 -> 138 us).
 template <bool W16>
-__device__ __forceinline__ u32x4 load_piece(const uint8_t* p, int n, int D, bool aligned) {
-  if (W16 || (aligned && n + 4 <= D)) return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+__device__ __forceinline__ u32x4 load_piece(const uint8_t* p, int n, int D) {
+  if (W16) return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
+  if (n + 4 <= D) return __builtin_nontemporal_load(reinterpret_cast<const u32x4_a4*>(p));
   u32x4 v = {0u, 0u, 0u, 0u};
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
+  for (int j = 0; j < 3; ++j)
     if (n + j < D) v[j] = reinterpret_cast<const uint32_t*>(p)[j];
   return v;
 }
 template <bool W16>
-__device__ __forceinline__ void store_piece(uint8_t* p, int n, int D, bool aligned, u32x4 v) {
-  if (W16 || (aligned && n + 4 <= D)) {
+__device__ __forceinline__ void store_piece(uint8_t* p, int n, int D, u32x4 v) {
+  if (W16) {
     __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p));
-    return;
-  }
+  } else if (n + 4 <= D) {
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x4_a4*>(p));
+  } else {
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (n + j < D) reinterpret_cast<uint32_t*>(p)[j] = v[j];
+    for (int j = 0; j < 3; ++j)
+      if (n + j < D) reinterpret_cast<uint32_t*>(p)[j] = v[j];
+  }
 }
-// piece + the sums at s (4 or 8 float32 in LDS), rounded to the output's type
+// piece + the sums at s (4 or 8 float32), rounded to the output's type
 template <bool W16>
 __device__ __forceinline__ u32x4 add_piece(u32x4 v, const float* s, int ot) {
-  const f32x4 a = *reinterpret_cast<const f32x4*>(s);
+  const f32x4 a = {s[0], s[1], s[2], s[3]};
   if constexpr (!W16) {
     u32x4 o;
 #pragma unroll
@@ -58,7 +61,7 @@ __device__ __forceinline__ u32x4 add_piece(u32x4 v, const float* s, int ot) {
     }
     return o;
   } else {
-    const f32x4 b = *reinterpret_cast<const f32x4*>(s + 4);
+    const f32x4 b = {s[4], s[5], s[6], s[7]};
     uint32_t h[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -98,7 +101,6 @@ __global__ void __launch_bounds__(256) lora_expand_kernel(int M, int D, int E, i
   const int n_begin = (((int)blockIdx.x - rt * nx) * 4 + wave) * SW * strips, n_end = min(n_begin + SW * strips, D);
   const int id = tile_id(ids, m0, M, E);
   uint32_t lead = tile_leaders(id);
-  const bool aligned = (D & 3) == 0;
   float* sums = reinterpret_cast<float*>(lds + wave * expand_wave_lds<WT, TRANS, NK>());
   uint8_t* tile = reinterpret_cast<uint8_t*>(sums + kRows * sum_row<NK>());
 
@@ -110,7 +112,7 @@ __global__ void __launch_bounds__(256) lora_expand_kernel(int M, int D, int E, i
       const int c = lane + 64 * q, row = c / PL, n = n0 + PE * (c % PL);
       y[q] = u32x4{0u, 0u, 0u, 0u};
       if (base != nullptr && (rows >> row & 1) && n < n_end)
-        y[q] = load_piece<W16>(base + ((size_t)(m0 + row) * D + n) * ES, n, D, aligned);
+        y[q] = load_piece<W16>(base + ((size_t)(m0 + row) * D + n) * ES, n, D);
     }
   };
   // rows without an adapter: out = base
@@ -121,7 +123,7 @@ __global__ void __launch_bounds__(256) lora_expand_kernel(int M, int D, int E, i
 #pragma unroll
       for (int q = 0; q < PN; ++q) {
         const int c = lane + 64 * q, row = c / PL, n = n0 + PE * (c % PL);
-        if ((bare >> row & 1) && n < n_end) store_piece<W16>(out + ((size_t)(m0 + row) * D + n) * ES, n, D, aligned, y[q]);
+        if ((bare >> row & 1) && n < n_end) store_piece<W16>(out + ((size_t)(m0 + row) * D + n) * ES, n, D, y[q]);
       }
     }
   }
@@ -244,7 +246,7 @@ __global__ void __launch_bounds__(256) lora_expand_kernel(int M, int D, int E, i
 #pragma unroll
       for (int q = 0; q < PN; ++q) {
         const int c = lane + 64 * q, row = c / PL, n = n0 + PE * (c % PL);
-        if ((mask >> row & 1) && n < n_end) store_piece<W16>(out + ((size_t)(m0 + row) * D + n) * ES, n, D, aligned, o[q]);
+        if ((mask >> row & 1) && n < n_end) store_piece<W16>(out + ((size_t)(m0 + row) * D + n) * ES, n, D, o[q]);
       }
     }
   }
@@ -317,6 +319,54 @@ __global__ void __launch_bounds__(256) lora_expand_rows_kernel(int M, int N, int
   }
 }
 
+// Few rows, backward: a workgroup takes one row and 2048 columns, a thread 8 of them: all ranks' pieces of a, read in whole
+// lines, times t from LDS.
+template <int WT>
+__global__ void __launch_bounds__(256) lora_expand_rows_t_kernel(int M, int D, int E, int R, int nx, const uint16_t* __restrict__ t,
+                                                                 const uint8_t* __restrict__ w, const int32_t* __restrict__ ids,
+                                                                 const uint8_t* base, uint8_t* out, int ot) {
+  __shared__ float tr[256];
+  const int m = (int)blockIdx.x / nx, n = (((int)blockIdx.x - m * nx) * 256 + (int)threadIdx.x) * 8;
+  const int e = ids[m];
+  const int es = ot == X_F32 ? 4 : 2;
+  const size_t at = ((size_t)m * D + n) * es;
+  u32x4 y[2] = {u32x4{0u, 0u, 0u, 0u}, u32x4{0u, 0u, 0u, 0u}};
+  if (base != nullptr && n < D) {              // D is a multiple of 16
+    y[0] = *reinterpret_cast<const u32x4*>(base + at);
+    if (ot == X_F32) y[1] = *reinterpret_cast<const u32x4*>(base + at + 16);
+  }
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (e >= 0 && e < E) {
+    if ((int)threadIdx.x < R) {
+      const uint16_t* p = t + (size_t)m * R + threadIdx.x;
+      tr[threadIdx.x] = (bf16_bits_to_f32(p[2 * (size_t)M * R]) + bf16_bits_to_f32(p[(size_t)M * R])) + bf16_bits_to_f32(p[0]);
+    }
+    __syncthreads();
+    if (n < D) {
+      const uint8_t* we = w + ((size_t)e * R * D + n) * esize<WT>();
+      for (int r = 0; r < R; r += 8) {         // R is a multiple of 8
+        Raw<WT> raw[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) raw_load<WT, true>(we + (size_t)(r + q) * D * esize<WT>(), raw[q]);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          float v[8];
+          raw_f32<WT>(raw[q], v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) acc[j] = fmaf(tr[r + q], v[j], acc[j]);
+        }
+      }
+    }
+  }
+  if (n >= D) return;
+  if (ot == X_F32) {
+    *reinterpret_cast<u32x4*>(out + at) = add_piece<false>(y[0], acc, ot);
+    *reinterpret_cast<u32x4*>(out + at + 16) = add_piece<false>(y[1], acc + 4, ot);
+  } else {
+    *reinterpret_cast<u32x4*>(out + at) = add_piece<true>(y[0], acc, ot);
+  }
+}
+
 template <int WT, bool TRANS, int NK, bool W16>
 hipError_t go(int M, int D, int E, int R, const uint16_t* t, const void* w, const int32_t* ids, const void* base, void* out,
               int ot, hipStream_t st) {
@@ -369,9 +419,20 @@ hipError_t rows_by_rank(int M, int N, int E, int R, A... a) {
 }  // namespace
 
 // Forward (not trans) the output is float32, backward any type.
-hipError_t lora_expand(int M, int D, int E, int R, const uint16_t* t, const void* w, XType wt, bool trans,
+hipError_t lora_expand(bool few, int M, int D, int E, int R, const uint16_t* t, const void* w, XType wt, bool trans,
                        const int32_t* ids, const void* base, void* out, XType ot, hipStream_t st) {
-  if (!trans && ot == X_F32 && lora_few_rows(M, R)) {
+  if (trans && few) {
+    const int nx = (D + 2047) / 2048;
+    auto launch = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, dim3((unsigned)(M * nx)), dim3(256), 0, st, M, D, E, R, nx, t, reinterpret_cast<const uint8_t*>(w),
+                         ids, reinterpret_cast<const uint8_t*>(base), reinterpret_cast<uint8_t*>(out), (int)ot);
+      return hipGetLastError();
+    };
+    if (wt == X_F32) return launch(lora_expand_rows_t_kernel<X_F32>);
+    if (wt == X_BF16) return launch(lora_expand_rows_t_kernel<X_BF16>);
+    return launch(lora_expand_rows_t_kernel<X_F16>);
+  }
+  if (!trans && ot == X_F32 && few) {
     if (wt == X_F32) return rows_by_rank<X_F32>(M, D, E, R, t, w, ids, base, out, st);
     if (wt == X_BF16) return rows_by_rank<X_BF16>(M, D, E, R, t, w, ids, base, out, st);
     return rows_by_rank<X_F16>(M, D, E, R, t, w, ids, base, out, st);

@@ -257,6 +257,62 @@ __global__ void __launch_bounds__(256) lora_shrink_rows_kernel(int M, int D, int
   if (lane == 0) put_terms(t + (size_t)m * R + r, (size_t)M * R, acc * scale[e]);
 }
 
+// Few rows, w's rows along the contraction: one workgroup per row.  The ranks of one d lie next to each other; G lanes (a power of
+// two covering R / 8) share a d, each holding the sums of its 8 ranks, so a wave reads w in whole lines; the lanes' and the 16
+// waves' sums are added at the end, in a fixed order.
+template <int XT, int WT, int G>
+__global__ void __launch_bounds__(1024) lora_shrink_rows_t_kernel(int M, int D, int E, int R, const uint8_t* __restrict__ x,
+                                                                  const uint8_t* __restrict__ w, const float* __restrict__ scale,
+                                                                  const int32_t* __restrict__ ids, uint16_t* __restrict__ t) {
+  constexpr int DPW = 64 / G, STEP = 16 * DPW;   // d of a wave's and of the workgroup's step
+  __shared__ float sums[16][8 * G];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int m = (int)blockIdx.x;
+  const int e = ids[m];
+  if (e < 0 || e >= E) return;
+  const int c = lane % G;
+  const bool on = 8 * c < R;
+  const uint8_t* xr = x + (size_t)m * D * esize<XT>();
+  const uint8_t* we = w + ((size_t)e * D * R + 8 * c) * esize<WT>();
+  float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int d0 = wave * DPW + lane / G; d0 < D; d0 += 4 * STEP) {
+    Raw<WT> raw[4];
+    float xv[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int d = d0 + q * STEP;
+      raw_zero(raw[q]);
+      xv[q] = 0.f;
+      if (on && d < D) {
+        raw_load<WT, true>(we + (size_t)d * R * esize<WT>(), raw[q]);
+        xv[q] = XT == X_F32 ? reinterpret_cast<const float*>(xr)[d] : bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(xr)[d]);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      float v[8];
+      raw_f32<WT>(raw[q], v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j] = fmaf(xv[q], v[j], acc[j]);
+    }
+  }
+#pragma unroll
+  for (int off = 32; off >= G; off >>= 1)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j] += __shfl_xor(acc[j], off, 64);
+  if (lane < G) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sums[wave][8 * lane + j] = acc[j];
+  }
+  __syncthreads();
+  const int r = threadIdx.x;
+  if (r >= R) return;
+  float v = sums[0][r];
+#pragma unroll
+  for (int q = 1; q < 16; ++q) v += sums[q][r];
+  put_terms(t + (size_t)m * R + r, (size_t)M * R, v * scale[e]);
+}
+
 // Terms of the sums of S parts, in order: one thread per element.
 __global__ void __launch_bounds__(256) lora_terms_kernel(int64_t plane, int E, int R, int S, const float* __restrict__ parts,
                                                          const float* __restrict__ scale, const int32_t* __restrict__ ids,
@@ -311,6 +367,28 @@ hipError_t rows_by_weight(XType wt, A... a) {
   if (wt == X_BF16) return go_rows<XT, X_BF16>(a...);
   return go_rows<XT, X_F16>(a...);
 }
+template <int XT, int WT, int G>
+hipError_t go_rows_t(int M, int D, int E, int R, const void* x, const void* w, const float* scale, const int32_t* ids,
+                     uint16_t* t, hipStream_t st) {
+  hipLaunchKernelGGL((lora_shrink_rows_t_kernel<XT, WT, G>), dim3(M), dim3(1024), 0, st, M, D, E, R,
+                     reinterpret_cast<const uint8_t*>(x), reinterpret_cast<const uint8_t*>(w), scale, ids, t);
+  return hipGetLastError();
+}
+template <int XT, int WT, typename... A>
+hipError_t rows_t_by_rank(int M, int D, int E, int R, A... a) {
+  if (R <= 8) return go_rows_t<XT, WT, 1>(M, D, E, R, a...);
+  if (R <= 16) return go_rows_t<XT, WT, 2>(M, D, E, R, a...);
+  if (R <= 32) return go_rows_t<XT, WT, 4>(M, D, E, R, a...);
+  if (R <= 64) return go_rows_t<XT, WT, 8>(M, D, E, R, a...);
+  if (R <= 128) return go_rows_t<XT, WT, 16>(M, D, E, R, a...);
+  return go_rows_t<XT, WT, 32>(M, D, E, R, a...);
+}
+template <int XT, typename... A>
+hipError_t rows_t_by_weight(XType wt, A... a) {
+  if (wt == X_F32) return rows_t_by_rank<XT, X_F32>(a...);
+  if (wt == X_BF16) return rows_t_by_rank<XT, X_BF16>(a...);
+  return rows_t_by_rank<XT, X_F16>(a...);
+}
 template <int XT, bool TRANS, typename... A>
 hipError_t by_weight(XType wt, A... a) {
   if (wt == X_F32) return by_rank<XT, X_F32, TRANS>(a...);
@@ -325,9 +403,14 @@ size_t lora_shrink_bytes(int M, int D, int R, XType xt) {
   return s > 1 ? (size_t)s * M * R * 4 : 0;
 }
 
-hipError_t lora_shrink(int M, int D, int E, int R, const void* x, XType xt, const void* w, XType wt, bool trans,
+hipError_t lora_shrink(bool few, int M, int D, int E, int R, const void* x, XType xt, const void* w, XType wt, bool trans,
                        const float* scale, const int32_t* ids, uint16_t* t, float* parts, hipStream_t st) {
-  if (!trans && lora_few_rows(M, R)) {
+  // transposed: a workgroup reads a whole adapter matrix, at some 150 GB/s
+  if (few && trans && (int64_t)D * R * (wt == X_F32 ? 4 : 2) <= (512 << 10)) {
+    if (xt == X_F32) return rows_t_by_weight<X_F32>(wt, M, D, E, R, x, w, scale, ids, t, st);
+    return rows_t_by_weight<X_BF16>(wt, M, D, E, R, x, w, scale, ids, t, st);
+  }
+  if (few && !trans) {
     if (xt == X_F32) return rows_by_weight<X_F32>(wt, M, D, E, R, x, w, scale, ids, t, st);
     if (xt == X_BF16) return rows_by_weight<X_BF16>(wt, M, D, E, R, x, w, scale, ids, t, st);
     return rows_by_weight<X_F16>(wt, M, D, E, R, x, w, scale, ids, t, st);
