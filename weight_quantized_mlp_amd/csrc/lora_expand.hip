@@ -378,7 +378,7 @@ hipError_t go(int M, int D, int E, int R, const uint16_t* t, const void* w, cons
   int strips = 1;
   while (strips < 256 / kStrip<NK> && (int64_t)tiles * ((D + 2 * strips * kGroup - 1) / (2 * strips * kGroup)) > 2048) strips *= 2;
   const int nx = (D + strips * kGroup - 1) / (strips * kGroup);
-  const int dz = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(E, kRows), 4096 / ((int64_t)tiles * nx)));
+  const int dz = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(E, kRows), 2048 / ((int64_t)tiles * nx)));
   hipLaunchKernelGGL((lora_expand_kernel<WT, TRANS, NK, W16>), dim3((unsigned)(tiles * nx), 1, dz), dim3(256), lds, st, M, D, E, R,
                      strips, nx, t, reinterpret_cast<const uint8_t*>(w), ids, reinterpret_cast<const uint8_t*>(base),
                      reinterpret_cast<uint8_t*>(out), ot);

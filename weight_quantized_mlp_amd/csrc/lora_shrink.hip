@@ -341,8 +341,8 @@ hipError_t go(int M, int D, int E, int R, int S, const void* x, const void* w, c
               uint16_t* t, float* parts, hipStream_t st) {
   if (!raise_lds_limit<lora_shrink_kernel<XT, WT, TRANS, NR>>()) return hipErrorInvalidValue;
   const int tiles = (M + kRows - 1) / kRows, RC = (R + 16 * NR - 1) / (16 * NR);
-  // workgroups for further adapters of a tile: up to one per possible adapter while the launch stays small
-  const int dz = std::max(1, std::min(std::min(E, kRows), 2048 / std::max(1, tiles * S * RC)));
+  // workgroups for further adapters of a tile, at least two; what they leave, each does in turn
+  const int dz = std::min(std::min(E, kRows), std::max(2, 512 / std::max(1, tiles * S * RC)));
   hipLaunchKernelGGL((lora_shrink_kernel<XT, WT, TRANS, NR>), dim3(tiles, S * RC, dz),
                      dim3(64 * shrink_waves<XT, WT, TRANS, NR>()), (shrink_lds<XT, WT, TRANS, NR>()), st, M, D, E, R, S, RC,
                      reinterpret_cast<const uint8_t*>(x), reinterpret_cast<const uint8_t*>(w), scale, ids, t, parts);
