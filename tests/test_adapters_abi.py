@@ -35,7 +35,7 @@ def test_every_declared_symbol_is_exported(L):
 
 
 def lora_args(**kw):
-    a = dict(M=4, K=64, N=48, E=2, R=8, x=A, xt=1, a=A + MB, b=A + 2 * MB, wt=1, sc=A + 3 * MB, ids=A + 4 * MB,
+    a = dict(M=4, K=2048, N=48, E=2, R=8, x=A, xt=1, a=A + MB, b=A + 2 * MB, wt=1, sc=A + 3 * MB, ids=A + 4 * MB,
              y=A + 5 * MB, ws=A + 6 * MB, wsb=MB, out=A + 7 * MB)
     a.update(kw)
     return [a[k] for k in ("M", "K", "N", "E", "R", "x", "xt", "a", "b", "wt", "sc", "ids", "y", "ws", "wsb", "out")] + [None]
@@ -61,7 +61,8 @@ def test_lora_empty_calls(L):
     assert L.lora_run(*lora_args(M=0, a=None)) == EINVAL
     assert L.lora_workspace_bytes(0, 64, 48, 2, 9, 0) == 0
     assert L.lora_workspace_bytes(4, 64, 48, 2, 8, 2) == 0
-    assert L.lora_workspace_bytes(4, 64, 48, 2, 8, 0) >= 4 * 8 * 4
+    assert L.lora_workspace_bytes(4, 2048, 48, 2, 8, 0) >= 4 * 8 * 4
+    assert L.lora_workspace_bytes(4, 64, 48, 2, 8, 0) == 0              # a small adapter: one launch, no intermediate
     assert L.lora_workspace_bytes(4, 64, 48, 2, 8, 1) >= 2 * 4 * 8 * 4
 
 

@@ -422,9 +422,10 @@ def lora_run(x, a, b, scale, ids, y, out=None, workspace=None):
         out = torch.empty((M, N), dtype=torch.float32, device=dev)
     else:
         _want(out, "out", torch.float32, dev, M * N)
-    ws = _workspace(lora_workspace_bytes(M, K, N, E, R), dev, workspace)
+    nb = lora_workspace_bytes(M, K, N, E, R)
+    ws = _workspace(nb, dev, workspace) if nb else None
     rc = lib().lora_run(M, K, N, E, R, _ptr(x), xt, _ptr(a), _ptr(b), wt, _ptr(scale), _ptr(ids), _ptr(y), _ptr(ws),
-                        ws.numel(), _ptr(out), _stream(dev))
+                        0 if ws is None else ws.numel(), _ptr(out), _stream(dev))
     _check("lora_run", rc)
     return out
 
@@ -483,9 +484,10 @@ def qlinear_backward(fmt, dy, w, scale=None, global_scale=1.0, dtype=None, out=N
         out = torch.empty((M, K), dtype=want, device=dev)
     else:
         _want(out, "out", want, dev, M * K)
-    ws = _workspace(qlinear_backward_workspace_bytes(fmt, M, N, K, want), dev, workspace)
-    rc = lib().qlinear_backward(fmt, M, N, K, _ptr(dy), dyt, _ptr(w), _ptr(scale), float(global_scale), _ptr(ws), ws.numel(),
-                                _ptr(out), dxt, _stream(dev))
+    nb = qlinear_backward_workspace_bytes(fmt, M, N, K, want)
+    ws = _workspace(nb, dev, workspace) if nb else None
+    rc = lib().qlinear_backward(fmt, M, N, K, _ptr(dy), dyt, _ptr(w), _ptr(scale), float(global_scale), _ptr(ws),
+                                0 if ws is None else ws.numel(), _ptr(out), dxt, _stream(dev))
     _check("qlinear_backward", rc)
     return out
 

@@ -158,7 +158,13 @@ constexpr int kScaleRow = 72;          // float16 scales of one group: 64 n, pad
 constexpr int kABytes = 128 * 32;      // activation bytes per 32 rows and stage
 
 template <int FMT> constexpr int b_stage() { return FMT == 0 ? 64 * 256 : 64 * 128 + 16 * kScaleRow * 2; }
-template <int FMT> constexpr int grad_lds(int mb) { return 2 * (mb * kABytes + b_stage<FMT>()) + 128 * 4; }   // + row scales
+// The epilogue reuses the stages: 32 x 64 float32 per wave, rows padded by 16 bytes; the tile's row scales lie behind both.
+constexpr int kEpiRow = 64 + 4, kEpiBytes = 32 * kEpiRow * 4;
+template <int FMT> constexpr int grad_scale_at(int mb) {
+  const int stages = 2 * (mb * kABytes + b_stage<FMT>());
+  return stages > 4 * kEpiBytes ? stages : 4 * kEpiBytes;
+}
+template <int FMT> constexpr int grad_lds(int mb) { return grad_scale_at<FMT>(mb) + 128 * 4; }
 
 // Work plan, a function of the shape: tiles of bm x 256; when the last round of tiles would leave many of the slots
 // idle, its tiles are cut into S parts of `per` steps of 64 n, whose float32 sums a second kernel adds in order.
@@ -196,9 +202,10 @@ inline int grad_mb(int M, int terms) {
   return rows <= 32 ? (terms == 2 ? 2 : 1) : (rows <= 64 ? 2 : 4);
 }
 
-__device__ __forceinline__ void store_dx(void* dx, bool bf, size_t i, float v) {
-  if (bf) reinterpret_cast<uint16_t*>(dx)[i] = __builtin_bit_cast(uint16_t, (__bf16)v);
-  else reinterpret_cast<float*>(dx)[i] = v;
+// LDS written by other lanes of the wave is read next (or the reverse): order them.
+__device__ __forceinline__ void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
 }
 
 typedef __attribute__((address_space(3))) const uint8_t lds_u8;
@@ -446,52 +453,60 @@ __global__ void __launch_bounds__(256, 2) grad_gemm_kernel(int M, int N, int Np,
     mfmas(af1, raw1);
     __builtin_amdgcn_sched_barrier(0);
   }
-  if (part >= 0) {                             // raw sums [BM][256], finished by grad_finish_kernel
-    float* pt = partials + (size_t)b * BM * kCols;
-#pragma unroll
-    for (int i = 0; i < RB; ++i)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int row = 32 * i + 8 * (r >> 2) + 4 * h + (r & 3);
-        if (m0 + row >= M) continue;
-        if constexpr (FMT == 0) {
-          pt[row * kCols + 64 * wave + li] = acc[i][0][r];
-          pt[row * kCols + 64 * wave + 32 + li] = acc[i][1][r];
-        } else {
-          *reinterpret_cast<f32x2*>(pt + row * kCols + 64 * wave + 2 * li) = f32x2{acc[i][0][r], acc[i][1][r]};
-        }
-      }
-    return;
-  }
-  float* rscale = reinterpret_cast<float*>(lds + 2 * STAGE);
-  if (tid < BM) rscale[tid] = row_scale;
+  // Epilogue, 32 rows at a time through LDS of the wave's own (every wave is done with the stages), so that rows leave in 16-byte
+  // pieces: stored from the MFMA layout, element by element with its own address, a 128-row tile took 6 us by itself.
+  const float rsc = row_scale;
+  float* rscale = reinterpret_cast<float*>(lds + grad_scale_at<FMT>(MB));
+  if (tid < BM) rscale[tid] = rsc;
   __syncthreads();
+  float* ep = reinterpret_cast<float*>(lds + wave * kEpiBytes);
   const float c = FMT == 0 ? 1.0f : inv;
+  float* pt = partials + (size_t)b * BM * kCols + 64 * wave;            // split tile: raw sums [BM][256] for grad_finish_kernel
 #pragma unroll
-  for (int i = 0; i < RB; ++i)
+  for (int i = 0; i < RB; ++i) {
+    wave_order();
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
-      const int m = m0 + 32 * i + 8 * (r >> 2) + 4 * h + (r & 3);
-      if (m >= M) continue;
-      const float rs = rscale[m - m0];
-      const float v0 = acc[i][0][r] * c * rs, v1 = acc[i][1][r] * c * rs;
+      float* e = ep + (8 * (r >> 2) + 4 * h + (r & 3)) * kEpiRow;
       if constexpr (FMT == 0) {
-        const int k = k0 + 64 * wave + li;
-        const size_t o = (size_t)m * K + k;
-        if (k < K) store_dx(dx, dx_bf, o, v0);
-        if (k + 32 < K) store_dx(dx, dx_bf, o + 32, v1);
+        e[li] = acc[i][0][r];
+        e[32 + li] = acc[i][1][r];
       } else {
-        const int k = k0 + 64 * wave + 2 * li;
-        if (k >= K) continue;
-        const size_t o = (size_t)m * K + k;
-        if (dx_bf) {
-          const uint32_t lo = __builtin_bit_cast(uint16_t, (__bf16)v0), hi = __builtin_bit_cast(uint16_t, (__bf16)v1);
-          *reinterpret_cast<uint32_t*>(reinterpret_cast<uint16_t*>(dx) + o) = lo | (hi << 16);
-        } else {
-          *reinterpret_cast<f32x2*>(reinterpret_cast<float*>(dx) + o) = f32x2{v0, v1};
+        *reinterpret_cast<f32x2*>(e + 2 * li) = f32x2{acc[i][0][r], acc[i][1][r]};
+      }
+    }
+    wave_order();
+    if (part < 0 && dx_bf) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int p = lane + 64 * q, row = 32 * i + (p >> 3), col = 8 * (p & 7), m = m0 + row, k = k0 + 64 * wave + col;
+        const float* e = ep + (p >> 3) * kEpiRow + col;
+        const f32x4 u = *reinterpret_cast<const f32x4*>(e), v = *reinterpret_cast<const f32x4*>(e + 4);
+        const float rs = rscale[row];
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float x0 = (j < 2 ? u[2 * j] : v[2 * j - 4]) * c * rs, x1 = (j < 2 ? u[2 * j + 1] : v[2 * j - 3]) * c * rs;
+          o[j] = (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x0) | ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)x1) << 16);
+        }
+        if (m < M && k < K)
+          *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(dx) + (size_t)m * K + k) = u32x4{o[0], o[1], o[2], o[3]};
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const int p = lane + 64 * q, row = 32 * i + (p >> 4), col = 4 * (p & 15), m = m0 + row, k = k0 + 64 * wave + col;
+        const f32x4 v = *reinterpret_cast<const f32x4*>(ep + (p >> 4) * kEpiRow + col);
+        if (part >= 0) {
+          if (m < M) *reinterpret_cast<f32x4*>(pt + row * kCols + col) = v;
+        } else if (m < M && k < K) {
+          const float rs = rscale[row];
+          *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(dx) + (size_t)m * K + k) =
+              f32x4{v[0] * c * rs, v[1] * c * rs, v[2] * c * rs, v[3] * c * rs};
         }
       }
     }
+  }
 }
 
 // dx of the split tiles: the S parts of every element added in order.  A thread takes 4 columns (K is a multiple
@@ -579,7 +594,9 @@ void grad_prep_terms(int terms, A... a) {
 
 }  // namespace
 
-size_t linear_grad_scratch_bytes(int fmt, int M, int N, int K, XType dxt) { return grad_ws(M, N, K, terms_of(dxt)).total; }
+size_t linear_grad_scratch_bytes(int fmt, int M, int N, int K, XType dxt) {
+  return grad_ws(M, N, K, terms_of(dxt)).total;
+}
 
 hipError_t launch_linear_grad(int fmt, int M, int N, int K, const void* dy, XType dyt, const uint8_t* w, const float* scale,
                               float inv, void* ws, void* dx, XType dxt, hipStream_t st) {

@@ -32,11 +32,12 @@ LoraWs lora_ws(int M, int K, int N, int E, int R, bool backward) {
 }  // namespace
 
 size_t lora_scratch_bytes(int M, int K, int N, int E, int R, bool backward) {
-  return lora_ws(M, K, N, E, R, backward).total;
+  return !backward && lora_one_launch(M, K, N, R) ? 0 : lora_ws(M, K, N, E, R, backward).total;
 }
 
 hipError_t launch_lora(int M, int K, int N, int E, int R, const void* x, XType xt, const void* a, const void* b, XType wt,
                        const float* scale, const int32_t* ids, const float* y, void* ws, float* out, hipStream_t st) {
+  if (lora_one_launch(M, K, N, R)) return lora_rows(M, K, N, E, R, x, xt, a, b, wt, scale, ids, y, out, st);
   const LoraWs L = lora_ws(M, K, N, E, R, false);
   uint8_t* p = reinterpret_cast<uint8_t*>(ws);
   uint16_t* t = reinterpret_cast<uint16_t*>(p);

@@ -204,6 +204,10 @@ size_t lora_shrink_bytes(int M, int D, int R, XType xt);
 // out[m,n] = base[m,n] + sum_r t[m,r] w[e][n,r] (trans: w[e][r,n]); base may be null or out.
 hipError_t lora_expand(bool few, int M, int D, int E, int R, const uint16_t* t, const void* w, XType wt, bool trans,
                        const int32_t* ids, const void* base, void* out, XType ot, hipStream_t st);
+// Both forward products in one launch, for small adapters.
+bool lora_one_launch(int M, int K, int N, int R);
+hipError_t lora_rows(int M, int K, int N, int E, int R, const void* x, XType xt, const void* a, const void* b, XType wt,
+                     const float* scale, const int32_t* ids, const float* y, float* out, hipStream_t st);
 // g[e][r,d] (rcontig: g[e][d,r]) = sum_{m: ids[m] = e} t[m,r] v[m,d]; parts: scratch of lora_outer_bytes.
 hipError_t lora_outer(int M, int D, int E, int R, const uint16_t* t, const void* v, XType vt, bool rcontig,
                       const int32_t* ids, float* g, float* parts, hipStream_t st);

@@ -12,6 +12,7 @@
 // Few rows (decode): see lora_expand_rows_kernel.
 #include <algorithm>
 
+#include "../../include/wqmlp_adapters.h"
 #include "lora_common.h"
 
 namespace wq {
@@ -319,6 +320,67 @@ __global__ void __launch_bounds__(256) lora_expand_rows_kernel(int M, int N, int
   }
 }
 
+// Few rows of a small adapter, forward in one launch: every workgroup computes its row's t for itself (a wave per rank, as
+// lora_shrink_rows_kernel does), which costs less than a second launch while the adapter's K x R matrix is small.
+template <int XT, int WT>
+__global__ void __launch_bounds__(256) lora_rows_kernel(int M, int K, int N, int E, int R, int nx, const uint8_t* __restrict__ x,
+                                                        const uint8_t* __restrict__ a, const uint8_t* __restrict__ b,
+                                                        const float* __restrict__ scale, const int32_t* __restrict__ ids,
+                                                        const float* base, float* out) {
+  __shared__ float t[WQ_LORA_MAX_RANK];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int m = (int)blockIdx.x / nx, n = ((int)blockIdx.x - m * nx) * 256 + (int)threadIdx.x;
+  const int e = ids[m];
+  float y = 0.f;
+  if (base != nullptr && n < N) y = base[(size_t)m * N + n];
+  if (e >= 0 && e < E) {
+    const uint8_t* xr = x + (size_t)m * K * esize<XT>();
+    const float f = scale[e];
+    for (int r = wave; r < R; r += 8) {        // two ranks at a time (R is a multiple of 8)
+      const uint8_t* a0 = a + ((size_t)e * R + r) * K * esize<WT>();
+      const uint8_t* a1 = a0 + (size_t)4 * K * esize<WT>();
+      float s0 = 0.f, s1 = 0.f;
+      for (int k = 8 * lane; k < K; k += 512) {
+        Raw<XT> rx;
+        Raw<WT> r0, r1;
+        raw_load<XT, true>(xr + (size_t)k * esize<XT>(), rx);
+        raw_load<WT, true>(a0 + (size_t)k * esize<WT>(), r0);
+        raw_load<WT, true>(a1 + (size_t)k * esize<WT>(), r1);
+        float u[8], v[8], w[8];
+        raw_f32<XT>(rx, u);
+        raw_f32<WT>(r0, v);
+        raw_f32<WT>(r1, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          s0 = fmaf(u[j], v[j], s0);
+          s1 = fmaf(u[j], w[j], s1);
+        }
+      }
+      s0 = wave64_sum(s0);
+      s1 = wave64_sum(s1);
+      if (lane == 0) {
+        t[r] = s0 * f;
+        t[r + 4] = s1 * f;
+      }
+    }
+    __syncthreads();
+    if (n < N) {
+      const uint8_t* br = b + ((size_t)e * N + n) * R * esize<WT>();
+      float acc = 0.f;
+      for (int r = 0; r < R; r += 8) {
+        Raw<WT> raw;
+        raw_load<WT, true>(br + (size_t)r * esize<WT>(), raw);
+        float v[8];
+        raw_f32<WT>(raw, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc = fmaf(t[r + j], v[j], acc);
+      }
+      y += acc;
+    }
+  }
+  if (n < N) out[(size_t)m * N + n] = y;
+}
+
 // Few rows, backward: a workgroup takes one row and 2048 columns, a thread 8 of them: all ranks' pieces of a, read in whole
 // lines, times t from LDS.
 template <int WT>
@@ -417,6 +479,32 @@ hipError_t rows_by_rank(int M, int N, int E, int R, A... a) {
 }
 
 }  // namespace
+
+// One launch while an adapter's a has at most 8192 elements and all workgroups together read at most 4 Mi of them.
+bool lora_one_launch(int M, int K, int N, int R) {
+  const int64_t each = (int64_t)K * R;
+  return each <= 8192 && each * M * ((N + 255) / 256) <= (4 << 20);
+}
+hipError_t lora_rows(int M, int K, int N, int E, int R, const void* x, XType xt, const void* a, const void* b, XType wt,
+                     const float* scale, const int32_t* ids, const float* y, float* out, hipStream_t st) {
+  const int nx = (N + 255) / 256;
+  auto launch = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(M * nx)), dim3(256), 0, st, M, K, N, E, R, nx, reinterpret_cast<const uint8_t*>(x),
+                       reinterpret_cast<const uint8_t*>(a), reinterpret_cast<const uint8_t*>(b), scale, ids, y, out);
+    return hipGetLastError();
+  };
+  switch (3 * (int)xt + (int)wt) {
+    case 0: return launch(lora_rows_kernel<X_F32, X_F32>);
+    case 1: return launch(lora_rows_kernel<X_F32, X_BF16>);
+    case 2: return launch(lora_rows_kernel<X_F32, X_F16>);
+    case 3: return launch(lora_rows_kernel<X_BF16, X_F32>);
+    case 4: return launch(lora_rows_kernel<X_BF16, X_BF16>);
+    case 5: return launch(lora_rows_kernel<X_BF16, X_F16>);
+    case 6: return launch(lora_rows_kernel<X_F16, X_F32>);
+    case 7: return launch(lora_rows_kernel<X_F16, X_BF16>);
+    default: return launch(lora_rows_kernel<X_F16, X_F16>);
+  }
+}
 
 // Forward (not trans) the output is float32, backward any type.
 hipError_t lora_expand(bool few, int M, int D, int E, int R, const uint16_t* t, const void* w, XType wt, bool trans,
