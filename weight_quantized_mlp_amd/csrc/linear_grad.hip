@@ -166,40 +166,52 @@ template <int FMT> constexpr int grad_scale_at(int mb) {
 }
 template <int FMT> constexpr int grad_lds(int mb) { return grad_scale_at<FMT>(mb) + 128 * 4; }
 
-// Work plan, a function of the shape: tiles of bm x 256; when the last round of tiles would leave many of the slots
-// idle, its tiles are cut into S parts of `per` steps of 64 n, whose float32 sums a second kernel adds in order.
+// Work plan, a function of the shape: tiles of bm x 256, of which the last round may be cut into S parts of `per` steps of 64 n,
+// whose float32 sums a second kernel adds in order.
 struct GradPlan {
-  int bm, ntm, ntk, tiles, steps;
+  int mb, bm, ntm, ntk, tiles, steps;  // mb: activation blocks of 32 rows (of one term) per tile
   int full, S, per, units;             // tiles [0, full) run whole; units = (tiles - full) * S parts
 };
-inline GradPlan grad_plan(int M, int N, int K, int mb, int terms) {
-  GradPlan p{};
-  p.bm = 32 * mb / terms;
-  p.ntm = (M + p.bm - 1) / p.bm;
-  p.ntk = (K + kCols - 1) / kCols;
-  p.tiles = p.ntm * p.ntk;
-  p.steps = (N + 63) / 64;
-  int tail = p.tiles % kSlots;
-  if (tail * 10 >= kSlots * 9) tail = 0;
-  p.S = 1;
-  if (tail > 0) {
-    // parts of at least 4 steps, all parts in one round of slots; scratch of at most 64 MiB
-    int s = std::min(kSlots / tail, std::max(1, p.steps / 4));
-    while (s > 1 && (size_t)tail * s * p.bm * kCols * 4 > ((size_t)64 << 20)) --s;
-    if (s > 1) {
-      p.per = (p.steps + s - 1) / s;
-      p.S = (p.steps + p.per - 1) / p.per;
+// The plan is the one of least estimated time, in us: a step of a 128-row tile takes 0.55 us of its CU (a quarter of that does not
+// shrink with the rows: weights and their decoding) and never less than 0.9 (a copy's way through memory); a tile's rows take 1.2
+// per 32 of them to leave; split tiles write and read their sums at 4.5 TB/s and take a further launch of 2.5.  At 512 x 1024 -> 8192 four parts per tile cost 35 us and whole
+// tiles 17; at 512 x 17408 -> 5120 six parts take 98 us and whole tiles, on 80 of 256 CUs, 190.
+inline GradPlan grad_plan(int M, int N, int K, int terms) {
+  GradPlan best{};
+  double least = 1e30;
+  for (int mb = 4; mb >= terms; mb /= 2) {
+    GradPlan p{};
+    p.mb = mb;
+    p.bm = 32 * mb / terms;
+    if (mb > terms && M <= p.bm / 2) continue;   // half the tile would stay empty
+    p.ntm = (M + p.bm - 1) / p.bm;
+    p.ntk = (K + kCols - 1) / kCols;
+    p.tiles = p.ntm * p.ntk;
+    p.steps = (N + 63) / 64;
+    auto step_us = [&](int64_t wgs) {            // of one workgroup, with wgs of them (at most two per CU at once) on the chip
+      const double share = (double)std::min<int64_t>(2, (wgs + 255) / 256);
+      return std::max(0.9, 0.55 * share * (0.25 + 0.1875 * mb));
+    };
+    for (int split = 0; split < 2; ++split) {    // whole tiles only, or the last round in parts
+      const int tail = split ? p.tiles % kSlots : 0;
+      if (split && tail == 0) continue;
+      const int full = p.tiles - tail;
+      const double body = full == 0 ? 0 : (double)((full + kSlots - 1) / kSlots) * (p.steps * step_us(full) + 1.2 * mb);
+      const int most = split ? std::min(p.steps, std::max(1, kSlots / tail)) : 1;
+      for (int s = split ? 2 : 1; s <= most; ++s) {
+        GradPlan q = p;
+        q.full = full;
+        q.per = (p.steps + s - 1) / s;
+        q.S = split ? (p.steps + q.per - 1) / q.per : 1;
+        q.units = tail * q.S;
+        const double bytes = (double)q.units * p.bm * kCols * 4;
+        if (bytes > (double)((size_t)64 << 20)) break;
+        const double us = body + (split ? q.per * step_us(q.units) + 1.2 * mb + 2.5 + bytes * 2 / 4.5e6 : 0.0);
+        if (us < least) least = us, best = q;
+      }
     }
   }
-  if (p.S == 1) tail = 0;
-  p.full = p.tiles - tail;
-  p.units = tail * p.S;
-  return p;
-}
-// Activation blocks of 32 rows (times terms) per tile.
-inline int grad_mb(int M, int terms) {
-  const int rows = M * terms;
-  return rows <= 32 ? (terms == 2 ? 2 : 1) : (rows <= 64 ? 2 : 4);
+  return best;
 }
 
 // LDS written by other lanes of the wave is read next (or the reverse): order them.
@@ -548,7 +560,7 @@ struct GradWs {
   size_t rs, partials, total;
 };
 inline GradWs grad_ws(int M, int N, int K, int terms) {
-  const GradPlan p = grad_plan(M, N, K, grad_mb(M, terms), terms);
+  const GradPlan p = grad_plan(M, N, K, terms);
   GradWs w;
   w.rs = up256((size_t)terms * M * p.steps * 64 * 2);
   w.partials = w.rs + up256((size_t)M * 4);
@@ -569,7 +581,7 @@ hipError_t grad_gemm(int M, int N, int K, const GradPlan& p, const uint16_t* a16
 template <int FMT>
 hipError_t grad_dispatch(int M, int N, int K, int terms, const GradPlan& p, const uint16_t* a16, const float* rs,
                          const uint8_t* w, float inv, void* dx, bool bf, float* partials, hipStream_t st) {
-  const int mb = grad_mb(M, terms);
+  const int mb = p.mb;
   if (terms == 2)
     return mb == 2 ? grad_gemm<FMT, 2, 2>(M, N, K, p, a16, rs, w, inv, dx, bf, partials, st)
                    : grad_gemm<FMT, 4, 2>(M, N, K, p, a16, rs, w, inv, dx, bf, partials, st);
@@ -601,7 +613,7 @@ size_t linear_grad_scratch_bytes(int fmt, int M, int N, int K, XType dxt) {
 hipError_t launch_linear_grad(int fmt, int M, int N, int K, const void* dy, XType dyt, const uint8_t* w, const float* scale,
                               float inv, void* ws, void* dx, XType dxt, hipStream_t st) {
   const int terms = terms_of(dxt);
-  const GradPlan p = grad_plan(M, N, K, grad_mb(M, terms), terms);
+  const GradPlan p = grad_plan(M, N, K, terms);
   const GradWs L = grad_ws(M, N, K, terms);
   uint8_t* base = reinterpret_cast<uint8_t*>(ws);
   uint16_t* a16 = reinterpret_cast<uint16_t*>(base);
