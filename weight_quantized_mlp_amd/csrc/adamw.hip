@@ -4,9 +4,12 @@
 // element with float32 states and gradients (p, m, v read and written, g read), 16 with 8-bit states, plus
 // 2 for a 16-bit copy, against some 30 (8-bit states: 80) ALU operations, so HBM bounds it and one pass
 // over every array is the whole plan.  The tensors are cut into chunks of kChunk elements, numbered through
-// all tensors; a workgroup takes a contiguous run of chunks, finds its first tensor with one parallel
-// compare against the table's chunk starts and walks on from there, so one launch serves any number of
-// tensors of any sizes.  A wave takes 256 consecutive elements at a time, 4 per lane: 16-byte accesses to
+// all tensors; a workgroup takes a chunk (in huge tables a run of them), finds its tensor with one
+// parallel compare against the table's chunk starts and walks on from there, so one launch serves any
+// number of tensors of any sizes.  Tables beyond the last-level cache stream with the non-temporal hint
+// (178M elements, float32 states: 801 us = 5.8 TB/s against 825 without it and 837 for 2048 workgroups
+// with a run of chunks each; 83M elements, 8-bit states: 264, 276 and 285 us = 5.6 TB/s at best); small
+// ones do without, since what backward just wrote is still cached (1M elements: 9.0 us against 9.8).  A wave takes 256 consecutive elements at a time, 4 per lane: 16-byte accesses to
 // the float32 arrays, 4-byte accesses to the codes, and a block's scale is one wave maximum.
 #include "dev_common.h"
 #include "launch.h"
@@ -109,13 +112,22 @@ struct AdamwHyper {
   uint32_t seed;
 };
 
+// One vector load or store, NT: with the non-temporal hint.
+template <bool NT, typename T>
+__device__ __forceinline__ T vload(const T* p) {
+  if constexpr (NT) return __builtin_nontemporal_load(p);
+  else return *p;
+}
+template <bool NT, typename T>
+__device__ __forceinline__ void vstore(T v, T* p) {
+  if constexpr (NT) __builtin_nontemporal_store(v, p);
+  else *p = v;
+}
 // Four consecutive elements at index i (i a multiple of 4); elements at n and beyond read as 0 / not written.
-template <typename T>
-__device__ __forceinline__ void load4(const T* a, int64_t i, int64_t n, float* v);
-template <>
-__device__ __forceinline__ void load4<float>(const float* a, int64_t i, int64_t n, float* v) {
+template <bool NT>
+__device__ __forceinline__ void load4(const float* a, int64_t i, int64_t n, float* v) {
   if (i + 4 <= n) {
-    const f32x4 t = *reinterpret_cast<const f32x4*>(a + i);
+    const f32x4 t = vload<NT>(reinterpret_cast<const f32x4*>(a + i));
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = t[j];
   } else {
@@ -123,10 +135,10 @@ __device__ __forceinline__ void load4<float>(const float* a, int64_t i, int64_t 
     for (int j = 0; j < 4; ++j) v[j] = i + j < n ? a[i + j] : 0.f;
   }
 }
-template <>
-__device__ __forceinline__ void load4<uint16_t>(const uint16_t* a, int64_t i, int64_t n, float* v) {   // bfloat16
+template <bool NT>
+__device__ __forceinline__ void load4(const uint16_t* a, int64_t i, int64_t n, float* v) {   // bfloat16
   if (i + 4 <= n) {
-    const u32x2 t = *reinterpret_cast<const u32x2*>(a + i);
+    const u32x2 t = vload<NT>(reinterpret_cast<const u32x2*>(a + i));
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       v[2 * j] = __uint_as_float(t[j] << 16);
@@ -137,26 +149,29 @@ __device__ __forceinline__ void load4<uint16_t>(const uint16_t* a, int64_t i, in
     for (int j = 0; j < 4; ++j) v[j] = i + j < n ? bf16_bits_to_f32(a[i + j]) : 0.f;
   }
 }
+template <bool NT>
 __device__ __forceinline__ uint32_t load_codes(const uint8_t* a, int64_t i, int64_t n) {
-  if (i + 4 <= n) return *reinterpret_cast<const uint32_t*>(a + i);
+  if (i + 4 <= n) return vload<NT>(reinterpret_cast<const uint32_t*>(a + i));
   uint32_t w = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     if (i + j < n) w |= (uint32_t)a[i + j] << (8 * j);
   return w;
 }
+template <bool NT>
 __device__ __forceinline__ void store4(float* a, int64_t i, int64_t n, const float* v) {
   if (i + 4 <= n) {
-    *reinterpret_cast<f32x4*>(a + i) = f32x4{v[0], v[1], v[2], v[3]};
+    vstore<NT>(f32x4{v[0], v[1], v[2], v[3]}, reinterpret_cast<f32x4*>(a + i));
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       if (i + j < n) a[i + j] = v[j];
   }
 }
+template <bool NT>
 __device__ __forceinline__ void store_codes(uint8_t* a, int64_t i, int64_t n, uint32_t w) {
   if (i + 4 <= n) {
-    *reinterpret_cast<uint32_t*>(a + i) = w;
+    vstore<NT>(w, reinterpret_cast<uint32_t*>(a + i));
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -164,7 +179,7 @@ __device__ __forceinline__ void store_codes(uint8_t* a, int64_t i, int64_t n, ui
   }
 }
 
-template <int BITS>
+template <int BITS, bool NT>
 __global__ void __launch_bounds__(256) adamw_kernel(const uint8_t* __restrict__ table, const int64_t* __restrict__ step_p,
                                                     const float* __restrict__ lr_p, AdamwHyper h) {
   const int64_t* head = reinterpret_cast<const int64_t*>(table);
@@ -201,15 +216,15 @@ __global__ void __launch_bounds__(256) adamw_kernel(const uint8_t* __restrict__ 
       if (b0 >= n) break;
       const int64_t i = b0 + 4 * lane;
       float p[4], g[4], m[4], v[4];
-      load4<float>(e.p, i, n, p);
-      if (e.g_dtype == 0) load4<float>(reinterpret_cast<const float*>(e.g), i, n, g);
-      else load4<uint16_t>(reinterpret_cast<const uint16_t*>(e.g), i, n, g);
+      load4<NT>(e.p, i, n, p);
+      if (e.g_dtype == 0) load4<NT>(reinterpret_cast<const float*>(e.g), i, n, g);
+      else load4<NT>(reinterpret_cast<const uint16_t*>(e.g), i, n, g);
       if constexpr (BITS == 32) {
-        load4<float>(reinterpret_cast<const float*>(e.m), i, n, m);
-        load4<float>(reinterpret_cast<const float*>(e.v), i, n, v);
+        load4<NT>(reinterpret_cast<const float*>(e.m), i, n, m);
+        load4<NT>(reinterpret_cast<const float*>(e.v), i, n, v);
       } else {
-        const uint32_t mc = load_codes(reinterpret_cast<const uint8_t*>(e.m), i, n);
-        const uint32_t vc = load_codes(reinterpret_cast<const uint8_t*>(e.v), i, n);
+        const uint32_t mc = load_codes<NT>(reinterpret_cast<const uint8_t*>(e.m), i, n);
+        const uint32_t vc = load_codes<NT>(reinterpret_cast<const uint8_t*>(e.v), i, n);
         const float ms = e.m_scale[b0 >> 8], vs = e.v_scale[b0 >> 8];
         const f32x2 m0 = e4m3x2_f32<false>(mc), m1 = e4m3x2_f32<true>(mc);
         const f32x2 v0 = __builtin_amdgcn_cvt_pk_f32_bf8(vc, false), v1 = __builtin_amdgcn_cvt_pk_f32_bf8(vc, true);
@@ -235,14 +250,14 @@ __global__ void __launch_bounds__(256) adamw_kernel(const uint8_t* __restrict__ 
         const float d = __builtin_amdgcn_sqrtf(v[j] * ibc2) + h.eps;
         p[j] = p[j] * keep - lr * ((m[j] * ibc1) * __builtin_amdgcn_rcpf(d));
       }
-      store4(e.p, i, n, p);
+      store4<NT>(e.p, i, n, p);
       if (e.copy != nullptr) {
         uint32_t w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[j] = e.copy_dtype == 1 ? round_bf16(p[j]) : round_f16(p[j]);
         uint16_t* o = reinterpret_cast<uint16_t*>(e.copy);
         if (i + 4 <= n) {
-          *reinterpret_cast<u32x2*>(o + i) = u32x2{w[0] | (w[1] << 16), w[2] | (w[3] << 16)};
+          vstore<NT>(u32x2{w[0] | (w[1] << 16), w[2] | (w[3] << 16)}, reinterpret_cast<u32x2*>(o + i));
         } else {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
@@ -250,8 +265,8 @@ __global__ void __launch_bounds__(256) adamw_kernel(const uint8_t* __restrict__ 
         }
       }
       if constexpr (BITS == 32) {
-        store4(reinterpret_cast<float*>(e.m), i, n, m);
-        store4(reinterpret_cast<float*>(e.v), i, n, v);
+        store4<NT>(reinterpret_cast<float*>(e.m), i, n, m);
+        store4<NT>(reinterpret_cast<float*>(e.v), i, n, v);
       } else {
         float am = fmaxf(fmaxf(fabsf(m[0]), fabsf(m[1])), fmaxf(fabsf(m[2]), fabsf(m[3])));
         float av = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
@@ -272,8 +287,8 @@ __global__ void __launch_bounds__(256) adamw_kernel(const uint8_t* __restrict__ 
         cm = __builtin_amdgcn_cvt_pk_fp8_f32(qm[2], qm[3], cm, true);
         int cv = __builtin_amdgcn_cvt_pk_bf8_f32(qv[0], qv[1], 0, false);
         cv = __builtin_amdgcn_cvt_pk_bf8_f32(qv[2], qv[3], cv, true);
-        store_codes(reinterpret_cast<uint8_t*>(e.m), i, n, (uint32_t)cm);
-        store_codes(reinterpret_cast<uint8_t*>(e.v), i, n, (uint32_t)cv);
+        store_codes<NT>(reinterpret_cast<uint8_t*>(e.m), i, n, (uint32_t)cm);
+        store_codes<NT>(reinterpret_cast<uint8_t*>(e.v), i, n, (uint32_t)cv);
       }
     }
   }
@@ -298,11 +313,13 @@ hipError_t launch_adamw(int64_t count, int64_t elems, int bits, const void* tabl
   const AdamwHyper h{(float)beta1, (float)(1.0 - beta1), (float)beta2, (float)(1.0 - beta2), (float)eps, grad_scale,
                      beta1, beta2, (float)weight_decay, seed};
   const int64_t chunks = adamw_chunks(elems) + count;   // at least the table's number
-  const int grid = (int)(chunks < 2048 ? chunks : 2048);
-  if (bits == 8)
-    hipLaunchKernelGGL(adamw_kernel<8>, dim3(grid), dim3(256), 0, st, reinterpret_cast<const uint8_t*>(table), step, lr, h);
-  else
-    hipLaunchKernelGGL(adamw_kernel<32>, dim3(grid), dim3(256), 0, st, reinterpret_cast<const uint8_t*>(table), step, lr, h);
+  const unsigned grid = (unsigned)(chunks < (1 << 22) ? chunks : (1 << 22));
+  const bool nt = elems >= ((int64_t)1 << 23);           // 134 MB and more
+  auto launch = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), 0, st, reinterpret_cast<const uint8_t*>(table), step, lr, h);
+  };
+  if (bits == 8) nt ? launch(adamw_kernel<8, true>) : launch(adamw_kernel<8, false>);
+  else nt ? launch(adamw_kernel<32, true>) : launch(adamw_kernel<32, false>);
   return hipGetLastError();
 }
 
