@@ -187,6 +187,38 @@ def test_a_tensor_past_4_GiB():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("gt,copy", [(BF16, F16), (F32, BF16)])
+def test_tensors_of_a_large_table_step_as_in_a_small_one(bits, gt, copy):
+    """Large tables take other access hints; the same tensors at the same places step to the same bits."""
+    sizes = [100003, 1, 257, 4099, 300]
+    small, large = states(sizes, bits, gt, copy), states(sizes, bits, gt, copy)
+    n = 21 << 20
+    z = lambda d: torch.zeros(n, dtype=d, device=DEV)
+    big = dict(p=z(F32), g=torch.ones(n, dtype=gt, device=DEV), m=z(F32 if bits == 32 else torch.uint8),
+               v=z(F32 if bits == 32 else torch.uint8), copy=z(copy))
+    if bits == 8:
+        big.update(ms=torch.zeros(n // 256, device=DEV), vs=torch.zeros(n // 256, device=DEV))
+    if bits == 8:
+        large["m"], large["v"] = [[t.view(torch.uint8) for t in large[k]] for k in ("m", "v")]
+    for k, t in big.items():
+        large[k].append(t)
+    large["table"] = wq.adamw_table(large["p"], large["g"], large["m"], large["v"], large["copy"], large["ms"] or None,
+                                    large["vs"] or None)
+    step, lr = scalars(1, 1e-3)
+    for s in (small, large):
+        wq.adamw_run(s["table"], step, lr, seed=9, **HYPER)
+    a, b = snapshot(small), snapshot(large)
+    for k in a:
+        for u, w in zip(a[k], b[k][:-1] if b[k] else []):
+            assert np.array_equal(u, w), k
+    assert all(torch.equal(u, w) for u, w in zip(small["copy"], large["copy"]))
+    # unit gradients from zero states: the update (of the states before their rounding) is lr, up to eps = 1e-8 and
+    # some eight float32 roundings of 2^-24 each
+    assert float((big["p"] + 1e-3).abs().max()) <= 1e-3 * 1e-6
+
+
+@pytest.mark.gpu
 def test_a_table_of_the_other_form_is_left_alone():
     s = states([1000], 32, F32, None)
     before = snapshot(s)

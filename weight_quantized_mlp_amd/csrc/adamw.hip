@@ -6,11 +6,10 @@
 // over every array is the whole plan.  The tensors are cut into chunks of kChunk elements, numbered through
 // all tensors; a workgroup takes a chunk (in huge tables a run of them), finds its tensor with one
 // parallel compare against the table's chunk starts and walks on from there, so one launch serves any
-// number of tensors of any sizes.  Tables beyond the last-level cache stream with the non-temporal hint
-// (178M elements, float32 states: 801 us = 5.8 TB/s against 825 without it and 837 for 2048 workgroups
-// with a run of chunks each; 83M elements, 8-bit states: 264, 276 and 285 us = 5.6 TB/s at best); small
-// ones do without, since what backward just wrote is still cached (1M elements: 9.0 us against 9.8).  A wave takes 256 consecutive elements at a time, 4 per lane: 16-byte accesses to
-// the float32 arrays, 4-byte accesses to the codes, and a block's scale is one wave maximum.
+// number of tensors of any sizes.  178M elements with float32 states take 800 us (5.8 TB/s; 837 us with
+// 2048 workgroups and a run of chunks each), 83M with 8-bit states 263 us (285 us).  A wave takes 256
+// consecutive elements at a time, 4 per lane: 16-byte accesses to the float32 arrays, 4-byte accesses to
+// the codes, and a block's scale is one wave maximum.
 #include "dev_common.h"
 #include "launch.h"
 
@@ -314,7 +313,10 @@ hipError_t launch_adamw(int64_t count, int64_t elems, int bits, const void* tabl
                      beta1, beta2, (float)weight_decay, seed};
   const int64_t chunks = adamw_chunks(elems) + count;   // at least the table's number
   const unsigned grid = (unsigned)(chunks < (1 << 22) ? chunks : (1 << 22));
-  const bool nt = elems >= ((int64_t)1 << 23);           // 134 MB and more
+  // Tables beyond the last-level cache stream with the non-temporal hint, smaller ones find last step's
+  // states there.  us with and without it, a bfloat16 gradient written just before: float32 states 16M
+  // elements 92 and 77, 24M 134 and 143, 64M 332 and 370; 8-bit 53 and 46, 78 and 81, 193 and 221.
+  const bool nt = elems >= ((int64_t)20 << 20);
   auto launch = [&](auto kernel) {
     hipLaunchKernelGGL(kernel, dim3(grid), dim3(256), 0, st, reinterpret_cast<const uint8_t*>(table), step, lr, h);
   };
