@@ -11,21 +11,21 @@ namespace {
 
 inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 
-// Workspace: the terms of t, backward also those of dt, [3][M][R] bfloat16 each; then the parts of a split contraction or
-// of a weight gradient's rows, whichever is largest (each is done with before the next begins).  x's type is not known
-// here: the float32 need covers it.
+// Workspace: the terms of t, backward also those of dt, [3][M][R] bfloat16 each; then the parts of a split contraction, of
+// either product in turn; then, backward, those of db's and of da's rows.  x's type is not known here: the float32 need covers it.
 struct LoraWs {
-  size_t dt, parts, total;
+  size_t dt, parts, db_parts, da_parts, total;
 };
 LoraWs lora_ws(int M, int K, int N, int E, int R, bool backward) {
   const size_t terms = up256((size_t)3 * M * R * 2);
-  LoraWs w{terms, terms * (backward ? 2 : 1), 0};
+  LoraWs w{};
+  w.dt = terms;
+  w.parts = terms * (backward ? 2 : 1);
   size_t p = std::max(lora_shrink_bytes(M, K, R, X_F32), lora_shrink_bytes(M, K, R, X_BF16));
-  if (backward) {
-    p = std::max({p, lora_shrink_bytes(M, N, R, X_F32), lora_shrink_bytes(M, N, R, X_BF16), lora_outer_bytes(M, K, E, R),
-                  lora_outer_bytes(M, N, E, R)});
-  }
-  w.total = w.parts + up256(p);
+  if (backward) p = std::max({p, lora_shrink_bytes(M, N, R, X_F32), lora_shrink_bytes(M, N, R, X_BF16)});
+  w.db_parts = w.parts + up256(p);
+  w.da_parts = w.db_parts + (backward ? up256(lora_outer_bytes(M, N, E, R)) : 0);
+  w.total = w.da_parts + (backward ? up256(lora_outer_bytes(M, K, E, R)) : 0);
   return w;
 }
 
@@ -56,14 +56,22 @@ hipError_t launch_lora_backward(int M, int K, int N, int E, int R, const void* d
   uint16_t* dt = reinterpret_cast<uint16_t*>(p + L.dt);
   float* parts = reinterpret_cast<float*>(p + L.parts);
   const bool few = lora_few_rows(M, K, N, R, wt);
+  // Each pass over dy (or x) follows the other one directly, so that it finds a part of it in the last-level cache (4096 x 17408
+  // float32: 47 us instead of 57); da and db in one launch, for operands of one type, come after both products instead.
+  const bool together = da != nullptr && db != nullptr && xt == dyt;
+  const OuterJob jobs[2] = {{N, t, dy, dyt, true, db, reinterpret_cast<float*>(p + L.db_parts)},
+                            {K, dt, x, xt, false, da, reinterpret_cast<float*>(p + L.da_parts)}};
   hipError_t err = hipSuccess;
   if (db != nullptr) {
     if (M > 0) err = lora_shrink(few, M, K, E, R, x, xt, a, wt, false, scale, ids, t, parts, st);
-    if (err == hipSuccess) err = lora_outer(M, N, E, R, t, dy, dyt, true, ids, db, parts, st);
+    if (err == hipSuccess && !together) err = lora_outer(M, E, R, jobs, 1, ids, st);
   }
-  if (da == nullptr && dx == nullptr) return err;
-  if (err == hipSuccess && M > 0) err = lora_shrink(few, M, N, E, R, dy, dyt, b, wt, true, scale, ids, dt, parts, st);
-  if (err == hipSuccess && da != nullptr) err = lora_outer(M, K, E, R, dt, x, xt, false, ids, da, parts, st);
+  if (err == hipSuccess && (da != nullptr || dx != nullptr) && M > 0)
+    err = lora_shrink(few, M, N, E, R, dy, dyt, b, wt, true, scale, ids, dt, parts, st);
+  if (err == hipSuccess && together) err = lora_outer(M, E, R, jobs, 2, ids, st);
+  else if (err == hipSuccess && da != nullptr) err = lora_outer(M, E, R, jobs + 1, 1, ids, st);
+  if (err == hipSuccess && (da != nullptr || db != nullptr))
+    err = lora_outer_join(M, E, R, db != nullptr ? jobs : jobs + 1, (db != nullptr) + (da != nullptr), st);
   if (err == hipSuccess && dx != nullptr && M > 0) err = lora_expand(few, M, K, E, R, dt, a, wt, true, ids, dx0, dx, dxt, st);
   return err;
 }

@@ -208,9 +208,19 @@ hipError_t lora_expand(bool few, int M, int D, int E, int R, const uint16_t* t, 
 bool lora_one_launch(int M, int K, int N, int R);
 hipError_t lora_rows(int M, int K, int N, int E, int R, const void* x, XType xt, const void* a, const void* b, XType wt,
                      const float* scale, const int32_t* ids, const float* y, float* out, hipStream_t st);
-// g[e][r,d] (rcontig: g[e][d,r]) = sum_{m: ids[m] = e} t[m,r] v[m,d]; parts: scratch of lora_outer_bytes.
-hipError_t lora_outer(int M, int D, int E, int R, const uint16_t* t, const void* v, XType vt, bool rcontig,
-                      const int32_t* ids, float* g, float* parts, hipStream_t st);
+// g[e][r,d] (rcontig: g[e][d,r]) = sum_{m: ids[m] = e} t[m,r] v[m,d], one or two such sums over v of one type; parts: scratch
+// of lora_outer_bytes, which lora_outer_join (with any one or two jobs run before) adds up.
+struct OuterJob {
+  int D;
+  const uint16_t* t;
+  const void* v;
+  XType vt;
+  bool rcontig;
+  float* g;
+  float* parts;
+};
+hipError_t lora_outer(int M, int E, int R, const OuterJob* jobs, int count, const int32_t* ids, hipStream_t st);
+hipError_t lora_outer_join(int M, int E, int R, const OuterJob* jobs, int count, hipStream_t st);
 size_t lora_outer_bytes(int M, int D, int E, int R);
 
 }  // namespace wq

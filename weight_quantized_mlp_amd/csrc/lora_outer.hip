@@ -6,9 +6,10 @@
 // between blocks, and add them through LDS at the end.  Which blocks hold rows of the adapter is found first, from
 // the ids, as one 32-bit mask per block; other blocks are never loaded, and rows of other adapters enter as zeros
 // (in v as well, so that nothing a foreign row holds can reach the sum).  Both operands have the contraction (rows)
-// as their slow index, so both go through the wave's transposing LDS tiles; the next block's loads are issued before
-// this block's MFMAs.  Long batches with few adapters split the rows over up to 8 workgroups, joined in order by a
-// second kernel.
+// as their slow index, so both go through the wave's transposing LDS tiles, t's three terms one after the other through
+// the same one (a tile per term left room for two workgroups on a CU at rank 32, one at rank 64); the next block's loads
+// are issued before this block's MFMAs.  Long batches with few adapters split the rows over up to 8 workgroups, joined in
+// order by a second kernel.  da and db of a backward pass share a launch where x and dy have one type, and the second kernel's.
 #include <algorithm>
 
 #include "lora_common.h"
@@ -21,43 +22,61 @@ using namespace lora;
 
 constexpr int kD = 64;               // columns of a workgroup
 constexpr int kScan = 4096;          // rows whose masks are held at once
+constexpr int kParts = 8;            // most parts of the rows
 
 // A wave's LDS: a block of v and of t's terms.  16-bit v is held as transposing term planes; float32 v as it is (padded rows),
 // and a lane gathers its 8 rows of a column by 4-byte reads, which needs less room than three planes.
 constexpr int kVRow = kD * 4 + 16;
 template <int VT> constexpr int outer_v_lds() { return VT == X_F32 ? kRows * kVRow : terms<VT>() * tr_plane<kD>(); }
-template <int VT, int NR> constexpr int outer_wave_lds() { return outer_v_lds<VT>() + 3 * tr_plane<16 * NR>(); }
+template <int VT, int NR> constexpr int outer_wave_lds() { return outer_v_lds<VT>() + tr_plane<16 * NR>(); }
 template <int VT, int NR> constexpr int outer_lds() {
-  const int stage = 4 * outer_wave_lds<VT, NR>(), red = 4 * 16 * NR * kD * 4;
+  const int stage = 4 * outer_wave_lds<VT, NR>(), red = 4 * 16 * kD * 4;
   return stage > red ? stage : red;
 }
 
 // Rows of one workgroup's part: a multiple of kRows.
 inline int outer_part_rows(int M, int parts) { return ((M + parts - 1) / parts + kRows - 1) / kRows * kRows; }
 
-template <int VT, int NR, bool RCONTIG>
-__global__ void __launch_bounds__(256) lora_outer_kernel(int M, int D, int E, int R, int parts, int part_rows, int64_t total,
-                                                         const uint16_t* __restrict__ t, const uint8_t* __restrict__ v,
-                                                         const int32_t* __restrict__ ids, float* __restrict__ g) {
-  constexpr int C = 16 * NR, NV = terms<VT>();
+// One of a launch's sums: its operands, the workgroups of its (columns, rank chunks, parts, adapters) and where they write
+// (g itself, or the parts' arrays one after the other).
+struct OuterSum {
+  const uint16_t* t;
+  const uint8_t* v;
+  float* g;
+  int64_t wgs;
+  int D, parts, part_rows;
+  bool rcontig;                      // g's rank index is contiguous, else its columns are
+};
+
+template <int VT, int NR>
+__global__ void __launch_bounds__(256) lora_outer_kernel(int M, int E, int R, int64_t total, OuterSum first, OuterSum second,
+                                                         const int32_t* __restrict__ ids) {
+  constexpr int C = 16 * NR, NV = terms<VT>(), J = kD / 16;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   __shared__ uint32_t masks[kScan / kRows];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l16 = lane & 15, gr = lane >> 4;
-  const int nd = (D + kD - 1) / kD, RC = (R + C - 1) / C;
+  const int RC = (R + C - 1) / C;
   uint8_t* vt = lds + wave * outer_wave_lds<VT, NR>();
   uint8_t* ut = vt + outer_v_lds<VT>();
   for (int64_t wg = blockIdx.x; wg < total; wg += gridDim.x) {
+    const bool two = wg >= first.wgs;
+    const uint16_t* t = two ? second.t : first.t;
+    const uint8_t* v = two ? second.v : first.v;
+    const int D = two ? second.D : first.D, parts = two ? second.parts : first.parts;
     // columns fastest, then rank chunks, parts and adapters
-    const int d0 = (int)(wg % nd) * kD;
-    const int64_t w1 = wg / nd, w2 = w1 / RC;
+    const int64_t w0 = two ? wg - first.wgs : wg;
+    const int nd = (D + kD - 1) / kD;
+    const int d0 = (int)(w0 % nd) * kD;
+    const int64_t w1 = w0 / nd, w2 = w1 / RC;
     const int r0 = (int)(w1 % RC) * C, part = (int)(w2 % parts), e = (int)(w2 / parts);
+    const int part_rows = two ? second.part_rows : first.part_rows;
     const int mb = part * part_rows, me = min(mb + part_rows, M);
-    f32x4 acc[NR][4];
+    f32x4 acc[NR][J];
 #pragma unroll
     for (int i = 0; i < NR; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int j = 0; j < J; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     for (int s0 = mb; s0 < me; s0 += kScan) {
       __syncthreads();                                  // the masks' and the tiles' last readers
       const int groups = (min(kScan, me - s0) + 63) / 64;
@@ -82,7 +101,7 @@ __global__ void __launch_bounds__(256) lora_outer_kernel(int M, int D, int E, in
       constexpr int VP = 16 / esize<VT>(), VL = kD / VP, VN = kRows * VL / 64;   // 16-byte pieces of v: elements, per row, per lane
       u32x4 raw[VN];
       u32x4 u[3][NR];
-      auto load = [&](int b) {
+      auto load_v = [&](int b) {
         const uint32_t mask = masks[b];
         const bool whole = d0 + kD <= D;                  // the same for all lanes: no branch between the loads
         const int m0 = s0 + kRows * b;
@@ -107,6 +126,10 @@ __global__ void __launch_bounds__(256) lora_outer_kernel(int M, int D, int E, in
             raw[q] = part.v[0];
           }
         }
+      };
+      auto load_u = [&](int b) {
+        const uint32_t mask = masks[b];
+        const int m0 = s0 + kRows * b;
 #pragma unroll
         for (int q = 0; q < NR; ++q) {
           const int c = lane + 64 * q, row = c / (C / 8), r = r0 + 8 * (c % (C / 8));
@@ -117,8 +140,15 @@ __global__ void __launch_bounds__(256) lora_outer_kernel(int M, int D, int E, in
             u[i][q] = on ? *reinterpret_cast<const u32x4*>(p + i * (size_t)M * R) : u32x4{0u, 0u, 0u, 0u};
         }
       };
+      auto put_u = [&](int i, const u32x4 (&v)[NR]) {    // term i of t
+#pragma unroll
+        for (int q = 0; q < NR; ++q) {
+          const int c = lane + 64 * q;
+          *reinterpret_cast<u32x4*>(ut + (c / (C / 8)) * tr_stride<C>() + (c % (C / 8)) * 16) = v[q];
+        }
+      };
       int b = next(wave);
-      if (b < blocks) load(b);
+      if (b < blocks) load_v(b), load_u(b);
       while (b < blocks) {
         wave_lds_fence();
 #pragma unroll
@@ -127,72 +157,95 @@ __global__ void __launch_bounds__(256) lora_outer_kernel(int M, int D, int E, in
           if constexpr (VT == X_F32) *reinterpret_cast<u32x4*>(vt + (c / VL) * kVRow + (c % VL) * 16) = raw[q];
           else tr_write<VT, kD>(vt, c, Raw<VT>{{raw[q]}});
         }
-#pragma unroll
-        for (int q = 0; q < NR; ++q) {
-          const int c = lane + 64 * q;
-          uint8_t* p = ut + (c / (C / 8)) * tr_stride<C>() + (c % (C / 8)) * 16;
-#pragma unroll
-          for (int i = 0; i < 3; ++i) *reinterpret_cast<u32x4*>(p + i * tr_plane<C>()) = u[i][q];
-        }
+        put_u(2, u[2]);
         wave_lds_fence();
         b = next(b + 4);
-        if (b < blocks) load(b);
-        bf16x8 uf[NR][3];
+        if (b < blocks) load_v(b);
+        bf16x8 vf[J][NV];
 #pragma unroll
-        for (int i = 0; i < NR; ++i) tr_read<C, 3>(ut, i, uf[i]);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          bf16x8 vf[NV];
+        for (int j = 0; j < J; ++j) {
           if constexpr (VT == X_F32) {
             float x[8];
 #pragma unroll
             for (int q = 0; q < 8; ++q) x[q] = *reinterpret_cast<const float*>(vt + (8 * gr + q) * kVRow + (16 * j + l16) * 4);
-            split3<8>(x, vf);
+            split3<8>(x, vf[j]);
           } else {
-            tr_read<kD, NV>(vt, j, vf);
+            tr_read<kD, NV>(vt, j, vf[j]);
           }
+        }
+        u32x4 u1[NR], u0[NR];
 #pragma unroll
-          for (int i = 0; i < NR; ++i)
-            acc[i][j] = RCONTIG ? mfma_terms<3, NV>(uf[i], vf, acc[i][j]) : mfma_terms<NV, 3>(vf, uf[i], acc[i][j]);
+        for (int q = 0; q < NR; ++q) u1[q] = u[1][q], u0[q] = u[0][q];
+        if (b < blocks) load_u(b);
+#pragma unroll
+        for (int i = 2; i >= 0; --i) {
+          if (i < 2) {
+            wave_lds_fence();
+            put_u(i, i == 1 ? u1 : u0);
+            wave_lds_fence();
+          }
+          bf16x8 uf[NR];
+#pragma unroll
+          for (int r = 0; r < NR; ++r) tr_read<C, 1>(ut, r, &uf[r]);
+#pragma unroll
+          for (int j = 0; j < J; ++j)
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+#pragma unroll
+              for (int k = NV - 1; k >= 0; --k)           // small products first
+                if (i + k <= 2) acc[r][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(uf[r], vf[j][k], acc[r][j], 0, 0, 0);
         }
       }
     }
 
-    // the waves' sums in wave order; fragment (i, j), lane: RCONTIG ranks 16 i + 4 gr .. + 3 of column 16 j + l16,
-    // else columns 16 j + 4 gr .. + 3 of rank 16 i + l16
-    __syncthreads();
+    // the waves' sums in wave order, 16 ranks at a time; fragment (i, j), lane: ranks 16 i + 4 gr .. + 3 of column 16 j + l16
     f32x4* red = reinterpret_cast<f32x4*>(lds);
+    float* ge = (two ? second.g : first.g) + ((size_t)part * E + e) * (size_t)R * D;
+    const bool rcontig = two ? second.rcontig : first.rcontig;
 #pragma unroll
-    for (int i = 0; i < NR; ++i)
+    for (int i = 0; i < NR; ++i) {
+      __syncthreads();
 #pragma unroll
-      for (int j = 0; j < 4; ++j) red[(wave * 4 * NR + 4 * i + j) * 64 + lane] = acc[i][j];
-    __syncthreads();
-    float* ge = g + ((size_t)part * E + e) * (size_t)R * D;
+      for (int j = 0; j < J; ++j) red[(wave * J + j) * 64 + lane] = acc[i][j];
+      __syncthreads();
+      f32x4 s = red[wave * 64 + lane];
 #pragma unroll
-    for (int fr = 0; fr < NR; ++fr) {
-      const int k = 4 * fr + wave, i = k >> 2, j = k & 3;
-      f32x4 s = red[k * 64 + lane];
-#pragma unroll
-      for (int q = 1; q < 4; ++q) s += red[(q * 4 * NR + k) * 64 + lane];
-      if constexpr (RCONTIG) {
-        const int d = d0 + 16 * j + l16, r = r0 + 16 * i + 4 * gr;
-        if (d < D && r < R) *reinterpret_cast<f32x4*>(ge + (size_t)d * R + r) = s;
+      for (int q = 1; q < 4; ++q) s += red[(q * J + wave) * 64 + lane];
+      const int d = d0 + 16 * wave + l16, r = r0 + 16 * i + 4 * gr;
+      if (d >= D || r >= R) continue;                     // R is a multiple of 8
+      if (rcontig) {
+        *reinterpret_cast<f32x4*>(ge + (size_t)d * R + r) = s;
       } else {
-        const int d = d0 + 16 * j + 4 * gr, r = r0 + 16 * i + l16;
-        if (d < D && r < R) *reinterpret_cast<f32x4*>(ge + (size_t)r * D + d) = s;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) ge[(size_t)(r + q) * D + d] = s[q];
       }
     }
     __syncthreads();
   }
 }
 
-// out[i] = the sum of `parts` arrays of n float32 (a multiple of 4), in order.
-__global__ void __launch_bounds__(256) lora_join_kernel(int64_t n4, int parts, const f32x4* __restrict__ p,
-                                                        f32x4* __restrict__ out) {
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (int64_t)gridDim.x * 256) {
-    f32x4 s = p[i];
-    for (int q = 1; q < parts; ++q) s += p[(int64_t)q * n4 + i];
-    out[i] = s;
+// out[i] = the sum of `parts` arrays of 4 n4 float32, in order; two such sums, the second behind the first.
+struct JoinSum {
+  const f32x4* p;
+  f32x4* out;
+  int64_t n4;
+  int parts;
+};
+__global__ void __launch_bounds__(256) lora_join_kernel(JoinSum a, JoinSum b) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < a.n4 + b.n4; i += (int64_t)gridDim.x * 256) {
+    const bool two = i >= a.n4;
+    const int64_t at = two ? i - a.n4 : i, n4 = two ? b.n4 : a.n4;
+    const f32x4* p = two ? b.p : a.p;
+    const int parts = two ? b.parts : a.parts;
+    f32x4 v[kParts];                       // all loads in flight together
+#pragma unroll
+    for (int q = 0; q < kParts; ++q)
+      if (q < parts) v[q] = p[(int64_t)q * n4 + at];
+    f32x4 s = v[0];
+#pragma unroll
+    for (int q = 1; q < kParts; ++q)
+      if (q < parts) s += v[q];
+    (two ? b.out : a.out)[at] = s;
   }
 }
 
@@ -207,7 +260,7 @@ inline int outer_parts(int M, int D, int E, int R) {
   const int64_t tiles = outer_tiles(D, E, R), slots = 768;
   int best = 1;
   double least = 1e30;
-  for (int p = 1; p <= 8 && (p == 1 || M / p >= 256); ++p) {
+  for (int p = 1; p <= kParts && (p == 1 || M / p >= 256); ++p) {
     const int rows = outer_part_rows(std::max(M, 1), p), n = (M + rows - 1) / std::max(rows, 1);
     if (p > 1 && n != p) continue;           // no empty part
     const double idle = (double)((tiles * p + slots - 1) / slots * slots) / (double)(tiles * p);
@@ -217,32 +270,31 @@ inline int outer_parts(int M, int D, int E, int R) {
   return best;
 }
 
-template <int VT, int NR, bool RCONTIG>
-hipError_t go(int M, int D, int E, int R, const uint16_t* t, const void* v, const int32_t* ids, float* g, float* ws,
-              hipStream_t st) {
-  if (!raise_lds_limit<lora_outer_kernel<VT, NR, RCONTIG>>()) return hipErrorInvalidValue;
-  const int parts = outer_parts(M, D, E, R);
-  const int64_t total = outer_tiles(D, E, R) * parts;
-  float* dst = parts > 1 ? ws : g;
-  hipLaunchKernelGGL((lora_outer_kernel<VT, NR, RCONTIG>), dim3((unsigned)std::min<int64_t>(total, 1 << 20)), dim3(256),
-                     (outer_lds<VT, NR>()), st, M, D, E, R, parts, outer_part_rows(std::max(M, 1), parts), total, t,
-                     reinterpret_cast<const uint8_t*>(v), ids, dst);
-  if (parts > 1) {
-    const int64_t n4 = (int64_t)E * R * D / 4;
-    hipLaunchKernelGGL(lora_join_kernel, dim3((unsigned)std::min<int64_t>((n4 + 255) / 256, 2048)), dim3(256), 0, st, n4,
-                       parts, reinterpret_cast<const f32x4*>(ws), reinterpret_cast<f32x4*>(g));
-  }
+OuterSum outer_sum(const OuterJob& j, int M, int E, int R) {
+  const int parts = outer_parts(M, j.D, E, R);
+  return {j.t, reinterpret_cast<const uint8_t*>(j.v), parts > 1 ? j.parts : j.g, outer_tiles(j.D, E, R) * parts, j.D, parts,
+          outer_part_rows(std::max(M, 1), parts), j.rcontig};
+}
+
+template <int VT, int NR>
+hipError_t go(int M, int E, int R, const OuterSum& a, const OuterSum& b, const int32_t* ids, hipStream_t st) {
+  if (!raise_lds_limit<lora_outer_kernel<VT, NR>>()) return hipErrorInvalidValue;
+  const int64_t total = a.wgs + b.wgs;
+  hipLaunchKernelGGL((lora_outer_kernel<VT, NR>), dim3((unsigned)std::min<int64_t>(total, 1 << 20)), dim3(256),
+                     (outer_lds<VT, NR>()), st, M, E, R, total, a, b, ids);
   return hipGetLastError();
 }
-template <int VT, bool RCONTIG, typename... A>
-hipError_t by_rank(int M, int D, int E, int R, A... a) {
-  if (R <= 16) return go<VT, 1, RCONTIG>(M, D, E, R, a...);
-  if (R <= 32) return go<VT, 2, RCONTIG>(M, D, E, R, a...);
-  return go<VT, 4, RCONTIG>(M, D, E, R, a...);
-}
 template <int VT, typename... A>
-hipError_t by_layout(bool rcontig, A... a) {
-  return rcontig ? by_rank<VT, true>(a...) : by_rank<VT, false>(a...);
+hipError_t by_rank(int M, int E, int R, const A&... a) {
+  if (R <= 16) return go<VT, 1>(M, E, R, a...);
+  if (R <= 32) return go<VT, 2>(M, E, R, a...);
+  return go<VT, 4>(M, E, R, a...);
+}
+template <typename... A>
+hipError_t by_type(XType vt, const A&... a) {
+  if (vt == X_F32) return by_rank<X_F32>(a...);
+  if (vt == X_BF16) return by_rank<X_BF16>(a...);
+  return by_rank<X_F16>(a...);
 }
 
 }  // namespace
@@ -252,11 +304,24 @@ size_t lora_outer_bytes(int M, int D, int E, int R) {
   return parts > 1 ? (size_t)parts * E * R * D * 4 : 0;
 }
 
-hipError_t lora_outer(int M, int D, int E, int R, const uint16_t* t, const void* v, XType vt, bool rcontig,
-                      const int32_t* ids, float* g, float* parts, hipStream_t st) {
-  if (vt == X_F32) return by_layout<X_F32>(rcontig, M, D, E, R, t, v, ids, g, parts, st);
-  if (vt == X_BF16) return by_layout<X_BF16>(rcontig, M, D, E, R, t, v, ids, g, parts, st);
-  return by_layout<X_F16>(rcontig, M, D, E, R, t, v, ids, g, parts, st);
+hipError_t lora_outer(int M, int E, int R, const OuterJob* jobs, int count, const int32_t* ids, hipStream_t st) {
+  const OuterSum none{nullptr, nullptr, nullptr, 0, 1, 1, kRows, false};
+  return by_type(jobs[0].vt, M, E, R, outer_sum(jobs[0], M, E, R), count > 1 ? outer_sum(jobs[1], M, E, R) : none, ids, st);
+}
+
+hipError_t lora_outer_join(int M, int E, int R, const OuterJob* jobs, int count, hipStream_t st) {
+  JoinSum join[2] = {{nullptr, nullptr, 0, 1}, {nullptr, nullptr, 0, 1}};
+  for (int i = 0; i < count; ++i) {
+    const int parts = outer_parts(M, jobs[i].D, E, R);
+    if (parts > 1)
+      join[i] = {reinterpret_cast<const f32x4*>(jobs[i].parts), reinterpret_cast<f32x4*>(jobs[i].g),
+                 (int64_t)E * R * jobs[i].D / 4, parts};
+  }
+  const int64_t n4 = join[0].n4 + join[1].n4;
+  if (n4 == 0) return hipSuccess;
+  hipLaunchKernelGGL(lora_join_kernel, dim3((unsigned)std::min<int64_t>((n4 + 255) / 256, 2048)), dim3(256), 0, st, join[0],
+                     join[1]);
+  return hipGetLastError();
 }
 
 }  // namespace wq

@@ -21,6 +21,8 @@ namespace {
 
 using namespace lora;
 
+constexpr int kParts = 8;            // most parts of the contraction
+
 // A wave's LDS: 32 rows of x and, as rows (16 NR of them) or as a transposing tile, w; a row of 64 elements is padded by
 // 16 bytes, which spreads the operand reads of 16 rows over all banks.
 template <int T> constexpr int row_bytes() { return 64 * esize<T>() + 16; }
@@ -320,8 +322,14 @@ __global__ void __launch_bounds__(256) lora_terms_kernel(int64_t plane, int E, i
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < plane; i += (int64_t)gridDim.x * 256) {
     const int e = ids[i / R];
     if (e < 0 || e >= E) continue;
-    float v = parts[i];
-    for (int s = 1; s < S; ++s) v += parts[s * plane + i];
+    float p[kParts];                       // all loads in flight together
+#pragma unroll
+    for (int s = 0; s < kParts; ++s)
+      if (s < S) p[s] = parts[s * plane + i];
+    float v = p[0];
+#pragma unroll
+    for (int s = 1; s < kParts; ++s)
+      if (s < S) v += p[s];
     put_terms(t + i, plane, v * scale[e]);
   }
 }
@@ -330,7 +338,7 @@ __global__ void __launch_bounds__(256) lora_terms_kernel(int64_t plane, int E, i
 int shrink_parts(int M, int D, int R, int es) {
   const int tiles = ((M + kRows - 1) / kRows) * ((R + 63) / 64);
   if (tiles >= 256 || (int64_t)kRows * D * es <= (512 << 10)) return 1;
-  const int s = std::min(8, 512 / tiles);
+  const int s = std::min(kParts, 512 / tiles);
   if (s <= 1) return 1;
   const int nb = (D + 63) / 64, per = (nb + s - 1) / s;
   return (nb + per - 1) / per;             // no empty part
