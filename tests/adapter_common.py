@@ -4,7 +4,7 @@ Bounds.  u = 2^-24 is half a float32 step.  A float32 sum of n products in any o
 (n + 1) u sum |products| to first order; an n-term matrix-core sum may round or truncate each step, which at most
 doubles that.  `dot_bound` is that worst case for a chain of two products.  For inputs of random sign the
 rounding errors add like a random walk, so the error of a whole matrix in the 2-norm stays near sqrt(n) u times its
-norm; `norm_bound` is 8 times that, which a rounding of any operand to 16 bits (2^-9 relative or 2^-12) exceeds.
+norm; `norm_bound` is 8 times that, which a rounding of any operand to 16 bits (up to 2^-8 relative or 2^-11) exceeds.
 """
 import numpy as np
 import torch

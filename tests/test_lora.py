@@ -10,7 +10,6 @@ from adapter_common import DEV, U, host, norm_bound, randn, rel2, runs
 pytestmark = pytest.mark.gpu
 
 F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
-HALF = {F32: U, BF16: 2.0 ** -9, F16: 2.0 ** -12}   # half a step, relative to a value's power of two: eps / 4
 
 # M, K, N, E, R, x, w: one token to several tiles, odd N, every rank class, every pair of types
 SHAPES = [
@@ -232,6 +231,26 @@ def test_rows_past_4_GiB():
     t = x[on].double() @ a[1].double().T.contiguous()
     rdb = 2.0 * (y[on].double().T.contiguous() @ t)
     assert rel2(host(db[1]), rdb.cpu().numpy()) <= norm_bound(K, M // 3)
+
+
+def test_many_rows_that_end_inside_a_line():
+    """N odd and 2^25 outputs or more: rows share lines, which large outputs write through the caches."""
+    M, K, N, R = 2113, 32, 16001, 24
+    x, xd = randn(1, (M, K), F16)
+    a, ad = randn(2, (3, R, K), BF16)
+    b, bd = randn(3, (3, N, R), BF16)
+    y, yd = randn(4, (M, N), F32)
+    ids = ids_for("runs", M, 3, 8)
+    scale = np.array([0.5, 2.0, 1.25], dtype=np.float32)
+    at = np.r_[0:40, 1000:1040, M - 40:M]
+    ref = oracle.lora_ref(xd[at], ad, bd, scale, ids[at], yd[at])
+    args = (x, a, b, torch.from_numpy(scale).to(DEV), torch.from_numpy(ids).to(DEV))
+    got = wq.lora_run(*args, y)
+    part = np.linalg.norm(ref - yd[at]) / np.linalg.norm(ref)
+    assert rel2(host(got)[at], ref) <= norm_bound(K, R) * part + 2 * U
+    off = ids < 0
+    assert np.array_equal(host(got)[off], host(y)[off])
+    assert torch.equal(wq.lora_run(*args, y, out=y), got)              # in place: the same bits
 
 
 def test_graph_replays():

@@ -25,30 +25,45 @@ using namespace lora;
 template <int NK> constexpr int kStrip = NK == 1 ? 64 : 32;
 
 // 16 bytes of a row of the output: 4 float32 (rows of any length: element-aligned) or 8 16-bit elements (rows of a multiple of
-// 16) from n on; elements at D and beyond read as 0 and are not written.  Both streams pass the caches once, and say so: the
-// adapters' weights, which every row tile reads again, stay (4099 rows x 17408: 153 -> 138 us).
-template <bool W16>
+// 16) from n on; elements at D and beyond read as 0 and are not written.  Both streams pass the caches once, and say so (ONCE):
+// the adapters' weights, which every row tile reads again, stay (4099 rows x 17408: 153 -> 138 us).  See expand_once for rows that
+// end inside a line.
+template <bool ONCE, typename V>
+__device__ __forceinline__ V load_as(const uint8_t* p) {
+  if constexpr (ONCE) return __builtin_nontemporal_load(reinterpret_cast<const V*>(p));
+  else return *reinterpret_cast<const V*>(p);
+}
+template <bool ONCE, typename V>
+__device__ __forceinline__ void store_as(uint8_t* p, V v) {
+  if constexpr (ONCE) __builtin_nontemporal_store(v, reinterpret_cast<V*>(p));
+  else *reinterpret_cast<V*>(p) = v;
+}
+template <bool W16, bool ONCE>
 __device__ __forceinline__ u32x4 load_piece(const uint8_t* p, int n, int D) {
-  if (W16) return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
-  if (n + 4 <= D) return __builtin_nontemporal_load(reinterpret_cast<const u32x4_a4*>(p));
+  if (W16) return load_as<ONCE, u32x4>(p);
+  if (n + 4 <= D) return load_as<ONCE, u32x4_a4>(p);
   u32x4 v = {0u, 0u, 0u, 0u};
 #pragma unroll
   for (int j = 0; j < 3; ++j)
     if (n + j < D) v[j] = reinterpret_cast<const uint32_t*>(p)[j];
   return v;
 }
-template <bool W16>
+template <bool W16, bool ONCE>
 __device__ __forceinline__ void store_piece(uint8_t* p, int n, int D, u32x4 v) {
   if (W16) {
-    __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(p));
+    store_as<ONCE, u32x4>(p, v);
   } else if (n + 4 <= D) {
-    __builtin_nontemporal_store(v, reinterpret_cast<u32x4_a4*>(p));
+    store_as<ONCE, u32x4_a4>(p, v);
   } else {
 #pragma unroll
     for (int j = 0; j < 3; ++j)
       if (n + j < D) reinterpret_cast<uint32_t*>(p)[j] = v[j];
   }
 }
+// Whether the streams carry the non-temporal hint.  Lines that two rows share are written in two parts, which large outputs
+// then send to memory separately: 4096 rows x 17407 211 us with the hint, 164 without; 2048 rows 95 and 87; 1536 rows 71 and 73;
+// 4096 rows x 17408 117 and 128.
+inline bool expand_once(int M, int D) { return D % 4 == 0 || (int64_t)M * D < ((int64_t)1 << 25); }
 // piece + the sums at s (4 or 8 float32), rounded to the output's type
 template <bool W16>
 __device__ __forceinline__ u32x4 add_piece(u32x4 v, const float* s, int ot) {
@@ -84,8 +99,8 @@ template <int WT, bool TRANS, int NK> constexpr int expand_wave_lds() {
 }
 static_assert(kRows * rank_row<X_BF16>() <= kRows * sum_row<2>() * 4, "t fits the sums' space");
 
-// NK: rank steps of 32.  W16: out has 16-bit elements.
-template <int WT, bool TRANS, int NK, bool W16>
+// NK: rank steps of 32.  W16: out has 16-bit elements.  ONCE: the streams' hint.
+template <int WT, bool TRANS, int NK, bool W16, bool ONCE>
 __global__ void __launch_bounds__(256) lora_expand_kernel(int M, int D, int E, int R, int strips, int nx,
                                                           const uint16_t* __restrict__ t, const uint8_t* __restrict__ w,
                                                           const int32_t* __restrict__ ids, const uint8_t* base, uint8_t* out,
@@ -113,7 +128,14 @@ __global__ void __launch_bounds__(256) lora_expand_kernel(int M, int D, int E, i
       const int c = lane + 64 * q, row = c / PL, n = n0 + PE * (c % PL);
       y[q] = u32x4{0u, 0u, 0u, 0u};
       if (base != nullptr && (rows >> row & 1) && n < n_end)
-        y[q] = load_piece<W16>(base + ((size_t)(m0 + row) * D + n) * ES, n, D);
+        y[q] = load_piece<W16, ONCE>(base + ((size_t)(m0 + row) * D + n) * ES, n, D);
+    }
+  };
+  auto store_rows = [&](uint32_t rows, int n0, const u32x4* v) {
+#pragma unroll
+    for (int q = 0; q < PN; ++q) {
+      const int c = lane + 64 * q, row = c / PL, n = n0 + PE * (c % PL);
+      if ((rows >> row & 1) && n < n_end) store_piece<W16, ONCE>(out + ((size_t)(m0 + row) * D + n) * ES, n, D, v[q]);
     }
   };
   // rows without an adapter: out = base
@@ -121,11 +143,7 @@ __global__ void __launch_bounds__(256) lora_expand_kernel(int M, int D, int E, i
   if (blockIdx.z == 0 && bare != 0 && base != out) {
     for (int n0 = n_begin; n0 < n_end; n0 += SW) {
       load_rows(bare, n0);
-#pragma unroll
-      for (int q = 0; q < PN; ++q) {
-        const int c = lane + 64 * q, row = c / PL, n = n0 + PE * (c % PL);
-        if ((bare >> row & 1) && n < n_end) store_piece<W16>(out + ((size_t)(m0 + row) * D + n) * ES, n, D, y[q]);
-      }
+      store_rows(bare, n0, y);
     }
   }
 
@@ -244,11 +262,7 @@ __global__ void __launch_bounds__(256) lora_expand_kernel(int M, int D, int E, i
         o[q] = add_piece<W16>(y[q], sums + (c / PL) * sum_row<NK>() + PE * (c % PL), ot);
       }
       if (n0 + SW < n_end) load_rows(mask, n0 + SW);
-#pragma unroll
-      for (int q = 0; q < PN; ++q) {
-        const int c = lane + 64 * q, row = c / PL, n = n0 + PE * (c % PL);
-        if ((mask >> row & 1) && n < n_end) store_piece<W16>(out + ((size_t)(m0 + row) * D + n) * ES, n, D, o[q]);
-      }
+      store_rows(mask, n0, o);
     }
   }
 }
@@ -429,11 +443,14 @@ __global__ void __launch_bounds__(256) lora_expand_rows_t_kernel(int M, int D, i
   }
 }
 
-template <int WT, bool TRANS, int NK, bool W16>
+template <int WT, bool TRANS, int NK, bool W16, bool ONCE = true>
 hipError_t go(int M, int D, int E, int R, const uint16_t* t, const void* w, const int32_t* ids, const void* base, void* out,
               int ot, hipStream_t st) {
+  if constexpr (!TRANS && ONCE) {                        // transposed: D is a multiple of 16
+    if (!expand_once(M, D)) return go<WT, TRANS, NK, W16, false>(M, D, E, R, t, w, ids, base, out, ot, st);
+  }
   constexpr int lds = 4 * expand_wave_lds<WT, TRANS, NK>();
-  if (!raise_lds_limit<lora_expand_kernel<WT, TRANS, NK, W16>>()) return hipErrorInvalidValue;
+  if (!raise_lds_limit<lora_expand_kernel<WT, TRANS, NK, W16, ONCE>>()) return hipErrorInvalidValue;
   const int tiles = (M + kRows - 1) / kRows;
   // strips per wave: more while the launch keeps over 2048 workgroups (t is loaded once per wave)
   constexpr int kGroup = 4 * kStrip<NK>;
@@ -441,7 +458,7 @@ hipError_t go(int M, int D, int E, int R, const uint16_t* t, const void* w, cons
   while (strips < 256 / kStrip<NK> && (int64_t)tiles * ((D + 2 * strips * kGroup - 1) / (2 * strips * kGroup)) > 2048) strips *= 2;
   const int nx = (D + strips * kGroup - 1) / (strips * kGroup);
   const int dz = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(E, kRows), 2048 / ((int64_t)tiles * nx)));
-  hipLaunchKernelGGL((lora_expand_kernel<WT, TRANS, NK, W16>), dim3((unsigned)(tiles * nx), 1, dz), dim3(256), lds, st, M, D, E, R,
+  hipLaunchKernelGGL((lora_expand_kernel<WT, TRANS, NK, W16, ONCE>), dim3((unsigned)(tiles * nx), 1, dz), dim3(256), lds, st, M, D, E, R,
                      strips, nx, t, reinterpret_cast<const uint8_t*>(w), ids, reinterpret_cast<const uint8_t*>(base),
                      reinterpret_cast<uint8_t*>(out), ot);
   return hipGetLastError();
