@@ -186,8 +186,9 @@ __device__ __forceinline__ uint32_t tile_mask(int id, int e) { return (uint32_t)
 
 // Whether a batch takes the row kernels (one row at a time, every row reading its adapter) instead of the tiles: while what
 // all rows read of their adapters, from L2, stays below 300 MB and the work small.  At 5120 -> 17408 in bfloat16, all rows on one
-// adapter (the tiles' best case), rank 16: 256 rows 24 us against 28, 512 rows 43 against 35; rank 64: 64 rows 17 against 25,
-// 128 rows 29 against 26; on random adapters 512 rows of rank 16 take 44 us against 177.
+// adapter (the tiles' best case), rank 16: 128 rows 14 us against 19, 256 rows 24 against 21, 512 rows 42 against 30; rank 64: 64
+// rows 16 against 21, 128 rows 27 against 24; each row on a random adapter, rank 16: 256 rows 26 against 101, 512 rows 43
+// against 172.
 inline bool lora_few_rows(int M, int K, int N, int R, XType wt) {
   const int64_t mr = (int64_t)M * (R < 16 ? 16 : R);
   return mr <= 16384 && mr * ((int64_t)K + N) * (wt == X_F32 ? 4 : 2) <= 300000000;
