@@ -219,6 +219,35 @@ def test_tensors_of_a_large_table_step_as_in_a_small_one(bits, gt, copy):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("count", [255, 256, 257, 513, 65535, 65537, 70000])
+def test_many_small_tensors(count):
+    """Every tensor of a long table is found: one, two and three steps of the search, empty tensors among them."""
+    r = np.random.default_rng(count)
+    sizes = r.integers(0, 9, count)
+    sizes[r.random(count) < 0.3] = 0
+    if count > 60000:
+        sizes[1000:2000] = 0                                           # a long empty run, and a tensor of many chunks
+        sizes[2000] = 3 * 4096 + 5
+    at = np.concatenate(([0], np.cumsum((sizes + 7) // 8 * 8)))          # 16-byte aligned places in flat buffers
+    p, pd = torch.zeros(at[-1] + 8, device=DEV), r.standard_normal(at[-1] + 8).astype(np.float32)
+    p.copy_(torch.from_numpy(pd))
+    g = torch.from_numpy(r.standard_normal(at[-1] + 8)).to(BF16).to(DEV)
+    m, v = torch.zeros_like(p), torch.zeros_like(p)
+    cut = lambda b: [b[a:a + n] for a, n in zip(at.tolist(), sizes.tolist())]
+    step, lr = scalars(1, 1e-3)
+    wq.adamw_run(wq.adamw_table(cut(p), cut(g), cut(m), cut(v)), step, lr, **HYPER)
+    want, wm, wv = oracle.adamw_ref(pd, host(g), 0 * pd, 0 * pd, 1, float(np.float32(1e-3)), HYPER["beta1"], HYPER["beta2"],
+                                    HYPER["eps"], HYPER["weight_decay"])
+    on = np.zeros(at[-1] + 8, dtype=bool)
+    for a, n in zip(at, sizes):
+        on[a:a + n] = True
+    # as in check_step; from zero states the step is lr itself, up to eps
+    assert np.all(np.abs(host(p) - want)[on] <= 4 * U * np.abs(pd[on]) + 32 * U * 1e-3)
+    assert np.all(np.abs(host(m) - wm)[on] <= 4 * U * np.abs(wm[on])) and np.all(np.abs(host(v) - wv)[on] <= 5 * U * np.abs(wv[on]))
+    assert np.array_equal(host(p)[~on], pd[~on]) and not host(m)[~on].any() and not host(v)[~on].any()
+
+
+@pytest.mark.gpu
 def test_a_table_of_the_other_form_is_left_alone():
     s = states([1000], 32, F32, None)
     before = snapshot(s)

@@ -4,9 +4,9 @@
 // element with float32 states and gradients (p, m, v read and written, g read), 16 with 8-bit states, plus
 // 2 for a 16-bit copy, against some 30 (8-bit states: 80) ALU operations, so HBM bounds it and one pass
 // over every array is the whole plan.  The tensors are cut into chunks of kChunk elements, numbered through
-// all tensors; a workgroup takes a chunk (in huge tables a run of them), finds its tensor with one
-// parallel compare against the table's chunk starts and walks on from there, so one launch serves any
-// number of tensors of any sizes.  178M elements with float32 states take 800 us (5.8 TB/s; 837 us with
+// all tensors; a workgroup takes a chunk (in huge tables a run of them), finds its tensor with a 256-way
+// search of the table's chunk starts and walks on from there, so one launch serves any number of tensors
+// of any sizes.  178M elements with float32 states take 800 us (5.8 TB/s; 837 us with
 // 2048 workgroups and a run of chunks each), 83M with 8-bit states 263 us (285 us).  A wave takes 256
 // consecutive elements at a time, 4 per lane: 16-byte accesses to the float32 arrays, 4-byte accesses to
 // the codes, and a block's scale is one wave maximum.
@@ -190,11 +190,15 @@ __global__ void __launch_bounds__(256) adamw_kernel(const uint8_t* __restrict__ 
   int64_t c = (int64_t)blockIdx.x * per;
   const int64_t c1 = c + per < total ? c + per : total;
   if (c >= c1) return;
-  // tensor of chunk c: the last with chunk0 <= c (empty tensors share a start with their successor)
-  int64_t t = -1;
-  for (int64_t s = 0; s < count; s += 256) {
-    const int64_t i = s + threadIdx.x;
-    t += __syncthreads_count(i < count && chunk0[i] <= c);
+  // tensor of chunk c: the last with chunk0 <= c (empty tensors share a start with their successor), by 256-way steps: one for
+  // up to 256 tensors, three for the most a table holds
+  int64_t t = 0;
+  for (int64_t span = count;;) {
+    const int64_t stride = (span + 255) / 256, i = threadIdx.x * stride;
+    const int64_t below = __syncthreads_count(i < span && chunk0[t + i] <= c) - 1;   // the first always is
+    t += below * stride;
+    if (stride == 1) break;
+    span = min(stride, span - below * stride);
   }
   const int64_t step = *step_p;
   const float lr = *lr_p;
