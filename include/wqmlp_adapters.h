@@ -38,8 +38,8 @@ extern "C" {
  *   out   [M, N]     float32; may be y itself
  * The result is that of float32 arithmetic: operands enter the matrix cores as sums of bfloat16 terms that
  * hold all their bits, the rank-R intermediate is float32.  An adapter's values reach only the rows that
- * name it, whatever they are (NaN and infinities included); where a row's own operands hold an infinity
- * its result may be NaN.  K: a multiple of 16; N: any; R: a multiple of 8 up to WQ_LORA_MAX_RANK.
+ * name it, whatever they are (NaN and infinities included); where a row's own operands hold an infinity,
+ * or a float32 above 3.38e38, its result may be NaN.  K: a multiple of 16; N: any; R: a multiple of 8 up to WQ_LORA_MAX_RANK.
  * M == 0 is a valid empty call (x, ids, y, out and the workspace may then be NULL).
  */
 size_t lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t E, int64_t R, int backward);
@@ -96,7 +96,8 @@ int qlinear_backward(int fmt, int64_t M, int64_t N, int64_t K, const void* dy, i
  *       floor(x' 2^9 + r 2^-16) 2^-9 (v: 2^16, 2^-16).  r are the low (m) and high (v) 16 bits of
  *       mix(key + 0x9E3779B9 i) for element i of tensor j, key = mix(mix(seed + 0x9E3779B9 t) + j), with
  *       mix(h): h ^= h>>16; h *= 0x7FEB352D; h ^= h>>15; h *= 0x846CA68B; h ^= h>>16 on 32 bits.
- *       p takes the step with m and v before their rounding.  A state that is not finite gets a NaN code.
+ *       p takes the step with m and v before their rounding.  A state that is not finite gets a NaN code
+ *       and does not count for its block's scale.
  *
  * The tensors' addresses live in a table in device memory that is built once:
  *   adamw_table_build fills `table` (adamw_table_bytes(count) bytes) from `tensors`, a HOST array of count

@@ -131,6 +131,30 @@ def test_values_that_are_not_finite():
 
 
 @pytest.mark.gpu
+def test_a_state_that_is_not_finite_leaves_its_block_alone():
+    """The other elements of the block get the codes and scales that they get beside zeros."""
+    s, c = (states([700], 8, F32, None, seed=6) for _ in range(2))
+    at = [256, 300, 301, 511, 699]
+    for u in (s, c):
+        u["m"][0].view(torch.uint8)[at] = 0
+        u["v"][0].view(torch.uint8)[at] = 0
+        u["g"][0][at] = 0
+    s["g"][0][at] = torch.tensor([float("inf"), float("nan"), float("-inf"), 3e38, float("inf")], device=DEV)  # 3e38: v infinite
+    step, lr = scalars(5, 1e-3)
+    for u in (s, c):
+        wq.adamw_run(u["table"], step, lr, seed=3, **HYPER)
+    bad, clean = snapshot(s), snapshot(c)
+    keep = np.delete(np.arange(700), at)
+    for k in ("p", "v"):
+        assert np.array_equal(bad[k][0][keep], clean[k][0][keep]), k
+    # m: 0.1 * 3e38 is finite and rules its block (256 .. 511), at the largest scale
+    assert np.array_equal(bad["m"][0][:256], clean["m"][0][:256]) and np.array_equal(bad["m"][0][512:699], clean["m"][0][512:699])
+    assert np.array_equal(bad["vs"][0], clean["vs"][0]) and bad["ms"][0][1] == 2.0 ** 100
+    assert np.array_equal(bad["ms"][0][[0, 2]], clean["ms"][0][[0, 2]])
+    assert np.all((bad["v"][0][at] & 0x7F) > 0x7B) and np.all((bad["m"][0][[256, 300, 301, 699]] & 0x7F) == 0x7F)
+
+
+@pytest.mark.gpu
 def test_eight_bit_states_follow_the_moving_average():
     """Over many steps on one gradient v approaches g^2, which rounding to nearest would not: a step moves v by
     0.1% where codes are 25% apart.  The mean over n elements of the stochastic walk is off by its spread / sqrt(n);

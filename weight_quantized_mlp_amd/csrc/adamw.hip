@@ -71,9 +71,12 @@ __device__ __forceinline__ float wave_max(float v) {
   return fmaxf(fmaxf(r0, r1), fmaxf(r2, r3));
 }
 
-// Smallest e in [-100, 100] with amax <= 0.875 * 2^half * 2^e; 0 for a zero or non-finite amax.
+// |x|, 0 where x is not finite: such a state has no say in its block's scale.
+__device__ __forceinline__ float finite_abs(float x) { return fabsf(x) <= 3.4028235e38f ? fabsf(x) : 0.f; }
+
+// Smallest e in [-100, 100] with amax <= 0.875 * 2^half * 2^e; 0 for a zero amax.
 __device__ __forceinline__ int block_exp(float amax, int half) {
-  if (!(amax > 0.f) || !(amax <= 3.0e38f)) return 0;
+  if (!(amax > 0.f)) return 0;
   int p;
   const float f = frexpf(amax, &p);
   const int e = p - half + (f > 0.875f ? 1 : 0);
@@ -271,8 +274,8 @@ __global__ void __launch_bounds__(256) adamw_kernel(const uint8_t* __restrict__ 
         store4<NT>(reinterpret_cast<float*>(e.m), i, n, m);
         store4<NT>(reinterpret_cast<float*>(e.v), i, n, v);
       } else {
-        float am = fmaxf(fmaxf(fabsf(m[0]), fabsf(m[1])), fmaxf(fabsf(m[2]), fabsf(m[3])));
-        float av = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+        const float am = fmaxf(fmaxf(finite_abs(m[0]), finite_abs(m[1])), fmaxf(finite_abs(m[2]), finite_abs(m[3])));
+        const float av = fmaxf(fmaxf(finite_abs(v[0]), finite_abs(v[1])), fmaxf(finite_abs(v[2]), finite_abs(v[3])));
         const int em = block_exp(wave_max(am), 9), ev = block_exp(wave_max(av), 16);
         const float im = ldexpf(1.0f, -em), iv = ldexpf(1.0f, -ev);
         if (lane == 0) {
