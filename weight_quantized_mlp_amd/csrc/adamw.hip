@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(256) adamw_kernel(const uint8_t* __restrict__ 
   if (head[2] != BITS) return;   // a table of the other state form: nothing is touched
   const int64_t* chunk0 = head + kAdamwHead;
   const AdamwEntry* entries = reinterpret_cast<const AdamwEntry*>(table + adamw_entries_offset(count));
-  const int64_t per = (total + gridDim.x - 1) / gridDim.x;
+  const int64_t per = total <= gridDim.x ? 1 : (total + gridDim.x - 1) / gridDim.x;   // a 64-bit division is 140 instructions
   int64_t c = (int64_t)blockIdx.x * per;
   const int64_t c1 = c + per < total ? c + per : total;
   if (c >= c1) return;

@@ -45,13 +45,12 @@ struct OuterSum {
   const uint16_t* t;
   const uint8_t* v;
   float* g;
-  int64_t wgs;
-  int D, parts, part_rows;
+  int wgs, D, parts, part_rows;
   bool rcontig;                      // g's rank index is contiguous, else its columns are
 };
 
 template <int VT, int NR>
-__global__ void __launch_bounds__(256) lora_outer_kernel(int M, int E, int R, int64_t total, OuterSum first, OuterSum second,
+__global__ void __launch_bounds__(256) lora_outer_kernel(int M, int E, int R, int total, OuterSum first, OuterSum second,
                                                          const int32_t* __restrict__ ids) {
   constexpr int C = 16 * NR, NV = terms<VT>(), J = kD / 16;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -61,17 +60,14 @@ __global__ void __launch_bounds__(256) lora_outer_kernel(int M, int E, int R, in
   const int RC = (R + C - 1) / C;
   uint8_t* vt = lds + wave * outer_wave_lds<VT, NR>();
   uint8_t* ut = vt + outer_v_lds<VT>();
-  for (int64_t wg = blockIdx.x; wg < total; wg += gridDim.x) {
+  for (int wg = blockIdx.x; wg < total; wg += gridDim.x) {
     const bool two = wg >= first.wgs;
     const uint16_t* t = two ? second.t : first.t;
     const uint8_t* v = two ? second.v : first.v;
     const int D = two ? second.D : first.D, parts = two ? second.parts : first.parts;
-    // columns fastest, then rank chunks, parts and adapters
-    const int64_t w0 = two ? wg - first.wgs : wg;
-    const int nd = (D + kD - 1) / kD;
-    const int d0 = (int)(w0 % nd) * kD;
-    const int64_t w1 = w0 / nd, w2 = w1 / RC;
-    const int r0 = (int)(w1 % RC) * C, part = (int)(w2 % parts), e = (int)(w2 / parts);
+    // columns fastest, then rank chunks, parts and adapters; in 32 bits (three 64-bit divisions were 450 instructions)
+    const int w0 = two ? wg - first.wgs : wg, nd = (D + kD - 1) / kD, w1 = w0 / nd, w2 = w1 / RC;
+    const int d0 = (w0 - w1 * nd) * kD, r0 = (w1 - w2 * RC) * C, e = w2 / parts, part = w2 - e * parts;
     const int part_rows = two ? second.part_rows : first.part_rows;
     const int mb = part * part_rows, me = min(mb + part_rows, M);
     f32x4 acc[NR][J];
@@ -105,27 +101,33 @@ __global__ void __launch_bounds__(256) lora_outer_kernel(int M, int E, int R, in
       u32x4 u[3][NR];
       auto load_v = [&](int b) {
         const uint32_t mask = masks[b];
-        const bool whole = d0 + kD <= D;                  // the same for all lanes: no branch between the loads
         const int m0 = s0 + kRows * b;
+        if (d0 + kD <= D) {                               // the same for all lanes: no branch between the loads
 #pragma unroll
-        for (int q = 0; q < VN; ++q) {
-          const int c = lane + 64 * q, row = c / VL, d = d0 + VP * (c % VL);
-          const bool on = (mask >> row & 1) != 0;
-          const uint8_t* p = v + ((size_t)(m0 + row) * D + d) * esize<VT>();
-          raw[q] = u32x4{0u, 0u, 0u, 0u};
-          if (whole ? on : on && d + VP <= D) {
-            if constexpr (VT == X_F32) raw[q] = *reinterpret_cast<const u32x4_a4*>(p);
-            else raw[q] = *reinterpret_cast<const u32x4_a2*>(p);
+          for (int q = 0; q < VN; ++q) {
+            const int c = lane + 64 * q, row = c / VL;
+            const uint8_t* p = v + ((size_t)(m0 + row) * D + d0 + VP * (c % VL)) * esize<VT>();
+            raw[q] = u32x4{0u, 0u, 0u, 0u};
+            if (mask >> row & 1) {
+              if constexpr (VT == X_F32) raw[q] = *reinterpret_cast<const u32x4_a4*>(p);
+              else raw[q] = *reinterpret_cast<const u32x4_a2*>(p);
+            }
           }
-        }
-        if (!whole) {                                     // the columns' end: pieces that D cuts
+        } else {                                          // the columns' end: pieces that D cuts
 #pragma unroll
           for (int q = 0; q < VN; ++q) {
             const int c = lane + 64 * q, row = c / VL, d = d0 + VP * (c % VL);
-            if (!(mask >> row & 1) || d >= D || d + VP <= D) continue;
-            Raw<VT> part;
-            raw_load_part<VT>(v + ((size_t)(m0 + row) * D + d) * esize<VT>(), D - d, part);
-            raw[q] = part.v[0];
+            raw[q] = u32x4{0u, 0u, 0u, 0u};
+            if (!(mask >> row & 1) || d >= D) continue;
+            const uint8_t* p = v + ((size_t)(m0 + row) * D + d) * esize<VT>();
+            if (d + VP <= D) {
+              if constexpr (VT == X_F32) raw[q] = *reinterpret_cast<const u32x4_a4*>(p);
+              else raw[q] = *reinterpret_cast<const u32x4_a2*>(p);
+            } else {
+              Raw<VT> part;
+              raw_load_part<VT>(p, D - d, part);
+              raw[q] = part.v[0];
+            }
           }
         }
       };
@@ -274,15 +276,15 @@ inline int outer_parts(int M, int D, int E, int R) {
 
 OuterSum outer_sum(const OuterJob& j, int M, int E, int R) {
   const int parts = outer_parts(M, j.D, E, R);
-  return {j.t, reinterpret_cast<const uint8_t*>(j.v), parts > 1 ? j.parts : j.g, outer_tiles(j.D, E, R) * parts, j.D, parts,
-          outer_part_rows(std::max(M, 1), parts), j.rcontig};
+  return {j.t, reinterpret_cast<const uint8_t*>(j.v), parts > 1 ? j.parts : j.g, (int)(outer_tiles(j.D, E, R) * parts), j.D,
+          parts, outer_part_rows(std::max(M, 1), parts), j.rcontig};
 }
 
 template <int VT, int NR>
 hipError_t go(int M, int E, int R, const OuterSum& a, const OuterSum& b, const int32_t* ids, hipStream_t st) {
   if (!raise_lds_limit<lora_outer_kernel<VT, NR>>()) return hipErrorInvalidValue;
-  const int64_t total = a.wgs + b.wgs;
-  hipLaunchKernelGGL((lora_outer_kernel<VT, NR>), dim3((unsigned)std::min<int64_t>(total, 1 << 20)), dim3(256),
+  const int total = a.wgs + b.wgs;
+  hipLaunchKernelGGL((lora_outer_kernel<VT, NR>), dim3((unsigned)std::min(total, 1 << 20)), dim3(256),
                      (outer_lds<VT, NR>()), st, M, E, R, total, a, b, ids);
   return hipGetLastError();
 }
@@ -307,7 +309,10 @@ size_t lora_outer_bytes(int M, int D, int E, int R) {
 }
 
 hipError_t lora_outer(int M, int E, int R, const OuterJob* jobs, int count, const int32_t* ids, hipStream_t st) {
-  const OuterSum none{nullptr, nullptr, nullptr, 0, 1, 1, kRows, false};
+  const OuterSum none{nullptr, nullptr, nullptr, 0, 0, 1, kRows, false};
+  int64_t tiles = 0;
+  for (int i = 0; i < count; ++i) tiles += outer_tiles(jobs[i].D, E, R);
+  if (tiles > (1 << 27)) return hipErrorInvalidValue;     // gradients beyond any memory; workgroups (up to 8 a tile) are counted in int
   return by_type(jobs[0].vt, M, E, R, outer_sum(jobs[0], M, E, R), count > 1 ? outer_sum(jobs[1], M, E, R) : none, ids, st);
 }
 
