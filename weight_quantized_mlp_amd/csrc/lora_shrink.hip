@@ -320,10 +320,10 @@ __global__ void __launch_bounds__(1024) lora_shrink_rows_t_kernel(int M, int D, 
 }
 
 // Terms of the sums of S parts, in order: one thread per element.
-__global__ void __launch_bounds__(256) lora_terms_kernel(int64_t plane, int E, int R, int S, const float* __restrict__ parts,
+__global__ void __launch_bounds__(256) lora_terms_kernel(int plane, int E, int R, int S, const float* __restrict__ parts,
                                                          const float* __restrict__ scale, const int32_t* __restrict__ ids,
                                                          uint16_t* __restrict__ t) {
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < plane; i += (int64_t)gridDim.x * 256) {
+  for (int i = blockIdx.x * 256 + threadIdx.x; i < plane; i += gridDim.x * 256) {
     const int e = ids[i / R];
     if (e < 0 || e >= E) continue;
     float p[kParts];                       // all loads in flight together
@@ -438,8 +438,8 @@ hipError_t lora_shrink(bool few, int M, int D, int E, int R, const void* x, XTyp
                          : by_weight<X_F16, false>(wt, M, D, E, R, S, x, w, scale, ids, t, parts, st);
   }
   if (err != hipSuccess || S == 1) return err;
-  const int64_t plane = (int64_t)M * R;
-  hipLaunchKernelGGL(lora_terms_kernel, dim3((unsigned)std::min<int64_t>((plane + 255) / 256, 4096)), dim3(256), 0, st, plane, E,
+  const int plane = M * R;                 // parts are for less than 256 tiles of 32 rows
+  hipLaunchKernelGGL(lora_terms_kernel, dim3((unsigned)std::min((plane + 255) / 256, 4096)), dim3(256), 0, st, plane, E,
                      R, S, parts, scale, ids, t);
   return hipGetLastError();
 }
