@@ -152,6 +152,20 @@ def test_backward(shape, dyt, dxt, kind):
     assert np.all(np.abs(host(db) - rb) <= 2 * (K + c + 8) * U * sb)
 
 
+@pytest.mark.parametrize("dyt", [F32, BF16])
+def test_columns_that_end_inside_a_piece(dyt):
+    """Every remainder of N by the 4 or 8 elements of a 16-byte piece, and rows shorter than one."""
+    for N in list(range(1, 18)) + list(range(121, 129)):
+        print("[lora_backward] N", N, dyt, flush=True)
+        p = problem((70, 48, N, 2, 8, BF16, BF16), "runs", seed=N)
+        dy, dyd = randn(N, (70, N), dyt, 1e-3)
+        dx, da, db = wq.lora_backward(dy, p["x"], p["a"], p["b"], p["scale"], p["ids"], dx_dtype=F32)
+        rx, ra, rb = backward_refs(p, dyd, np.zeros((70, 48)))
+        assert rel2(host(db), rb) <= norm_bound(48, 70), N
+        assert rel2(host(da), ra) <= norm_bound(N, 70), N
+        assert rel2(host(dx), rx) <= norm_bound(N, 8) + 2 * U, N
+
+
 def test_backward_in_place_and_parts():
     p = problem((150, 192, 140, 3, 16, BF16, BF16), "runs")
     dy, _ = randn(1, (150, 140), F32, 1e-3)

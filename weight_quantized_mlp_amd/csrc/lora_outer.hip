@@ -39,6 +39,19 @@ template <int VT, int NR> constexpr int outer_lds() {
 // Rows of one workgroup's part: a multiple of kRows.
 inline int outer_part_rows(int M, int parts) { return ((M + parts - 1) / parts + kRows - 1) / kRows * kRows; }
 
+// A 16-byte piece without its first s elements, zeros behind the rest (s beyond the piece: of a piece of zeros).
+template <int VT>
+__device__ __forceinline__ u32x4 drop_first(u32x4 v, int s) {
+  constexpr int D2 = VT == X_F32 ? 2 : 4, D1 = D2 / 2;    // elements of two dwords, of one
+  if (s & D2) v = u32x4{v.z, v.w, 0u, 0u};
+  if (s & D1) v = u32x4{v.y, v.z, v.w, 0u};
+  if constexpr (VT != X_F32) {
+    if (s & 1)
+      v = u32x4{v.x >> 16 | v.y << 16, v.y >> 16 | v.z << 16, v.z >> 16 | v.w << 16, v.w >> 16};
+  }
+  return v;
+}
+
 // One of a launch's sums: its operands, the workgroups of its (columns, rank chunks, parts, adapters) and where they write
 // (g itself, or the parts' arrays one after the other).
 struct OuterSum {
@@ -99,35 +112,31 @@ __global__ void __launch_bounds__(256) lora_outer_kernel(int M, int E, int R, in
       constexpr int VP = 16 / esize<VT>(), VL = kD / VP, VN = kRows * VL / 64;   // 16-byte pieces of v: elements, per row, per lane
       u32x4 raw[VN];
       u32x4 u[3][NR];
+      // a lane's pieces are of one column; the one that the rows' end cuts is loaded further left, whole, and shifted into place
+      const int dv = d0 + VP * (lane % VL), dl = max(min(dv, D - VP), 0), cut = D >= VP ? dv - dl : 0;
       auto load_v = [&](int b) {
         const uint32_t mask = masks[b];
         const int m0 = s0 + kRows * b;
-        if (d0 + kD <= D) {                               // the same for all lanes: no branch between the loads
+        if (D >= VP) {                                    // the same for all lanes: no branch between the loads
 #pragma unroll
           for (int q = 0; q < VN; ++q) {
-            const int c = lane + 64 * q, row = c / VL;
-            const uint8_t* p = v + ((size_t)(m0 + row) * D + d0 + VP * (c % VL)) * esize<VT>();
+            const int row = (lane + 64 * q) / VL;
+            const uint8_t* p = v + ((size_t)(m0 + row) * D + dl) * esize<VT>();
             raw[q] = u32x4{0u, 0u, 0u, 0u};
-            if (mask >> row & 1) {
+            if ((mask >> row & 1) && dv < D) {
               if constexpr (VT == X_F32) raw[q] = *reinterpret_cast<const u32x4_a4*>(p);
               else raw[q] = *reinterpret_cast<const u32x4_a2*>(p);
             }
           }
-        } else {                                          // the columns' end: pieces that D cuts
+        } else {                                          // a row is less than a piece
 #pragma unroll
           for (int q = 0; q < VN; ++q) {
-            const int c = lane + 64 * q, row = c / VL, d = d0 + VP * (c % VL);
+            const int row = (lane + 64 * q) / VL;
             raw[q] = u32x4{0u, 0u, 0u, 0u};
-            if (!(mask >> row & 1) || d >= D) continue;
-            const uint8_t* p = v + ((size_t)(m0 + row) * D + d) * esize<VT>();
-            if (d + VP <= D) {
-              if constexpr (VT == X_F32) raw[q] = *reinterpret_cast<const u32x4_a4*>(p);
-              else raw[q] = *reinterpret_cast<const u32x4_a2*>(p);
-            } else {
-              Raw<VT> part;
-              raw_load_part<VT>(p, D - d, part);
-              raw[q] = part.v[0];
-            }
+            if (!(mask >> row & 1) || dv > 0) continue;
+            Raw<VT> part;
+            raw_load_part<VT>(v + (size_t)(m0 + row) * D * esize<VT>(), D, part);
+            raw[q] = part.v[0];
           }
         }
       };
@@ -154,6 +163,10 @@ __global__ void __launch_bounds__(256) lora_outer_kernel(int M, int E, int R, in
       int b = next(wave);
       if (b < blocks) load_v(b), load_u(b);
       while (b < blocks) {
+        if (d0 + kD > D) {
+#pragma unroll
+          for (int q = 0; q < VN; ++q) raw[q] = drop_first<VT>(raw[q], cut);
+        }
         wave_lds_fence();
 #pragma unroll
         for (int q = 0; q < VN; ++q) {
