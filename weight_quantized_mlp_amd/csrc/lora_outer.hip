@@ -2,8 +2,8 @@
 // (db from t = scale x a^T and v = dy, da from t = scale dy b and v = x).
 //
 // v is the bytes, read once per adapter that a block of rows names.  A workgroup owns one adapter, 64 columns d and
-// up to 64 ranks; its 4 waves take blocks of 32 rows in turn, each with its own accumulators, so no barrier stands
-// between blocks, and add them through LDS at the end.  Which blocks hold rows of the adapter is found first, from
+// up to 64 ranks; its 4 waves (or its one, see outer_one_wave) take blocks of 32 rows in turn, each with its own accumulators, so
+// no barrier stands between blocks, and add them through LDS at the end.  Which blocks hold rows of the adapter is found first, from
 // the ids, as one 32-bit mask per block; other blocks are never loaded, and rows of other adapters enter as zeros
 // (in v as well, so that nothing a foreign row holds can reach the sum).  Both operands have the contraction (rows)
 // as their slow index, so both go through the wave's transposing LDS tiles, t's three terms one after the other through
@@ -31,8 +31,8 @@ constexpr int kParts = 8;            // most parts of the rows
 constexpr int kVRow = kD * 4 + 16;
 template <int VT> constexpr int outer_v_lds() { return VT == X_F32 ? kRows * kVRow : terms<VT>() * tr_plane<kD>(); }
 template <int VT, int NR> constexpr int outer_wave_lds() { return outer_v_lds<VT>() + tr_plane<16 * NR>(); }
-template <int VT, int NR> constexpr int outer_lds() {
-  const int stage = 4 * outer_wave_lds<VT, NR>(), red = 4 * 16 * kD * 4;
+template <int VT, int NR, int WAVES> constexpr int outer_lds() {
+  const int stage = WAVES * outer_wave_lds<VT, NR>(), red = WAVES == 1 ? 0 : WAVES * 16 * kD * 4;
   return stage > red ? stage : red;
 }
 
@@ -62,8 +62,8 @@ struct OuterSum {
   bool rcontig;                      // g's rank index is contiguous, else its columns are
 };
 
-template <int VT, int NR>
-__global__ void __launch_bounds__(256) lora_outer_kernel(int M, int E, int R, int total, OuterSum first, OuterSum second,
+template <int VT, int NR, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES) lora_outer_kernel(int M, int E, int R, int total, OuterSum first, OuterSum second,
                                                          const int32_t* __restrict__ ids) {
   constexpr int C = 16 * NR, NV = terms<VT>(), J = kD / 16;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -91,13 +91,13 @@ __global__ void __launch_bounds__(256) lora_outer_kernel(int M, int E, int R, in
     for (int s0 = mb; s0 < me; s0 += kScan) {
       __syncthreads();                                  // the masks' and the tiles' last readers
       const int groups = (min(kScan, me - s0) + 63) / 64;
-      for (int i0 = wave; i0 < groups; i0 += 32) {      // 8 groups of 64 rows in flight per wave
+      for (int i0 = wave; i0 < groups; i0 += 8 * WAVES) {   // 8 groups of 64 rows in flight per wave
         int id[8];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) id[q] = ids[min(s0 + 64 * (i0 + 4 * q) + lane, me - 1)];
+        for (int q = 0; q < 8; ++q) id[q] = ids[min(s0 + 64 * (i0 + WAVES * q) + lane, me - 1)];
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          const int i = i0 + 4 * q;
+          const int i = i0 + WAVES * q;
           const uint64_t b = __ballot(s0 + 64 * i + lane < me && id[q] == e);
           if (lane < 2 && i < groups) masks[2 * i + lane] = (uint32_t)(b >> (32 * lane));
         }
@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(256) lora_outer_kernel(int M, int E, int R, in
       __syncthreads();
       const int blocks = (min(kScan, me - s0) + kRows - 1) / kRows;
       auto next = [&](int b) {
-        while (b < blocks && masks[b] == 0) b += 4;
+        while (b < blocks && masks[b] == 0) b += WAVES;
         return b;
       };
       // one block's loads, in whole lines: 16-byte pieces of v, chunks of 8 ranks of each term of t
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(256) lora_outer_kernel(int M, int E, int R, in
         }
         put_u(2, u[2]);
         wave_lds_fence();
-        b = next(b + 4);
+        b = next(b + WAVES);
         if (b < blocks) load_v(b);
         bf16x8 vf[J][NV];
 #pragma unroll
@@ -215,26 +215,36 @@ __global__ void __launch_bounds__(256) lora_outer_kernel(int M, int E, int R, in
       }
     }
 
-    // the waves' sums in wave order, 16 ranks at a time; fragment (i, j), lane: ranks 16 i + 4 gr .. + 3 of column 16 j + l16
-    f32x4* red = reinterpret_cast<f32x4*>(lds);
+    // fragment (i, j), lane: ranks 16 i + 4 gr .. + 3 of column 16 j + l16
     float* ge = (two ? second.g : first.g) + ((size_t)part * E + e) * (size_t)R * D;
     const bool rcontig = two ? second.rcontig : first.rcontig;
-#pragma unroll
-    for (int i = 0; i < NR; ++i) {
-      __syncthreads();
-#pragma unroll
-      for (int j = 0; j < J; ++j) red[(wave * J + j) * 64 + lane] = acc[i][j];
-      __syncthreads();
-      f32x4 s = red[wave * 64 + lane];
-#pragma unroll
-      for (int q = 1; q < 4; ++q) s += red[(q * J + wave) * 64 + lane];
-      const int d = d0 + 16 * wave + l16, r = r0 + 16 * i + 4 * gr;
-      if (d >= D || r >= R) continue;                     // R is a multiple of 8
+    auto store = [&](int i, int j, f32x4 s) {
+      const int d = d0 + 16 * j + l16, r = r0 + 16 * i + 4 * gr;
+      if (d >= D || r >= R) return;                       // R is a multiple of 8
       if (rcontig) {
         *reinterpret_cast<f32x4*>(ge + (size_t)d * R + r) = s;
       } else {
 #pragma unroll
         for (int q = 0; q < 4; ++q) ge[(size_t)(r + q) * D + d] = s[q];
+      }
+    };
+    if constexpr (WAVES == 1) {
+#pragma unroll
+      for (int i = 0; i < NR; ++i)
+#pragma unroll
+        for (int j = 0; j < J; ++j) store(i, j, acc[i][j]);
+    } else {                                              // the four waves' sums in wave order, 16 ranks at a time
+      f32x4* red = reinterpret_cast<f32x4*>(lds);
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < J; ++j) red[(wave * J + j) * 64 + lane] = acc[i][j];
+        __syncthreads();
+        f32x4 s = red[wave * 64 + lane];
+#pragma unroll
+        for (int q = 1; q < 4; ++q) s += red[(q * J + wave) * 64 + lane];
+        store(i, wave, s);
       }
     }
     __syncthreads();
@@ -287,19 +297,32 @@ inline int outer_parts(int M, int D, int E, int R) {
   return best;
 }
 
+// Whether a workgroup has one wave instead of four: where workgroups with little to sum (their fixed part counts then) are more
+// than stand on the card at once, as four times as many of one wave do.  da and db at 5120 x 5120 in float32 on 16 adapters in 32 runs, rank 16:
+// 128 rows 23 us with one and 34 with four, 256 rows 29 and 38 (all rows on one adapter: 28 and 30), 1024 rows on one adapter 78
+// and 51; at 512 x 512, 256 rows 17 and 14.
+inline bool outer_one_wave(int wgs, int rows, int E) {
+  return wgs > 768 && rows <= std::max(kRows, 16 * std::min(E, 16));
+}
+
 OuterSum outer_sum(const OuterJob& j, int M, int E, int R) {
   const int parts = outer_parts(M, j.D, E, R);
   return {j.t, reinterpret_cast<const uint8_t*>(j.v), parts > 1 ? j.parts : j.g, (int)(outer_tiles(j.D, E, R) * parts), j.D,
           parts, outer_part_rows(std::max(M, 1), parts), j.rcontig};
 }
 
+template <int VT, int NR, int WAVES>
+hipError_t go_waves(int M, int E, int R, const OuterSum& a, const OuterSum& b, const int32_t* ids, hipStream_t st) {
+  if (!raise_lds_limit<lora_outer_kernel<VT, NR, WAVES>>()) return hipErrorInvalidValue;
+  const int total = a.wgs + b.wgs;
+  hipLaunchKernelGGL((lora_outer_kernel<VT, NR, WAVES>), dim3((unsigned)std::min(total, 1 << 20)), dim3(64 * WAVES),
+                     (outer_lds<VT, NR, WAVES>()), st, M, E, R, total, a, b, ids);
+  return hipGetLastError();
+}
 template <int VT, int NR>
 hipError_t go(int M, int E, int R, const OuterSum& a, const OuterSum& b, const int32_t* ids, hipStream_t st) {
-  if (!raise_lds_limit<lora_outer_kernel<VT, NR>>()) return hipErrorInvalidValue;
-  const int total = a.wgs + b.wgs;
-  hipLaunchKernelGGL((lora_outer_kernel<VT, NR>), dim3((unsigned)std::min(total, 1 << 20)), dim3(256),
-                     (outer_lds<VT, NR>()), st, M, E, R, total, a, b, ids);
-  return hipGetLastError();
+  if (outer_one_wave(a.wgs + b.wgs, std::max(a.part_rows, b.part_rows), E)) return go_waves<VT, NR, 1>(M, E, R, a, b, ids, st);
+  return go_waves<VT, NR, 4>(M, E, R, a, b, ids, st);
 }
 template <int VT, typename... A>
 hipError_t by_rank(int M, int E, int R, const A&... a) {
