@@ -338,10 +338,14 @@ __global__ void __launch_bounds__(256) lora_terms_kernel(int plane, int E, int R
   }
 }
 
-// Parts of the contraction: where fewer than a workgroup per CU would read over 512 KB of x each, two per CU, at most 8.
-int shrink_parts(int M, int D, int R, int es) {
+// Parts of the contraction, at most 8, two workgroups per CU: where fewer than a workgroup per CU would read over 512 KB of x each,
+// or much of x and w together.  512 KB of both with at most 32 workgroups (64 rows of 7007 bfloat16, rank 64: 15 us instead of 27;
+// one row, rank 128, float32 w: 19 instead of 57), else 1.5 MB, below which the parts' own launch takes what they gain (2048 rows,
+// rank 64, of 7007: float32 w 42 instead of 62, bfloat16 w 33 instead of 31).
+int shrink_parts(int M, int D, int R, int es, int ws) {
   const int tiles = ((M + kRows - 1) / kRows) * ((R + 63) / 64);
-  if (tiles >= 256 || (int64_t)kRows * D * es <= (512 << 10)) return 1;
+  const int64_t xb = (int64_t)kRows * D * es, wb = (int64_t)std::min(R, 64) * D * ws;
+  if (tiles >= 256 || (xb <= (512 << 10) && xb + wb <= (tiles <= 32 ? 512 << 10 : 1536 << 10))) return 1;
   const int s = std::min(kParts, 512 / tiles);
   if (s <= 1) return 1;
   const int nb = (D + 63) / 64, per = (nb + s - 1) / s;
@@ -411,7 +415,7 @@ hipError_t by_weight(XType wt, A... a) {
 }  // namespace
 
 size_t lora_shrink_bytes(int M, int D, int R, XType xt) {
-  const int s = shrink_parts(M, D, R, xt == X_F32 ? 4 : 2);
+  const int s = shrink_parts(M, D, R, xt == X_F32 ? 4 : 2, 4);      // of any weights
   return s > 1 ? (size_t)s * M * R * 4 : 0;
 }
 
@@ -427,7 +431,7 @@ hipError_t lora_shrink(bool few, int M, int D, int E, int R, const void* x, XTyp
     if (xt == X_BF16) return rows_by_weight<X_BF16>(wt, M, D, E, R, x, w, scale, ids, t, st);
     return rows_by_weight<X_F16>(wt, M, D, E, R, x, w, scale, ids, t, st);
   }
-  const int S = shrink_parts(M, D, R, xt == X_F32 ? 4 : 2);
+  const int S = shrink_parts(M, D, R, xt == X_F32 ? 4 : 2, wt == X_F32 ? 4 : 2);
   hipError_t err;
   if (trans) {
     err = xt == X_F32 ? by_weight<X_F32, true>(wt, M, D, E, R, S, x, w, scale, ids, t, parts, st)
