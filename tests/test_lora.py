@@ -166,6 +166,19 @@ def test_columns_that_end_inside_a_piece(dyt):
         assert rel2(host(dx), rx) <= norm_bound(N, 8) + 2 * U, N
 
 
+@pytest.mark.parametrize("M,K,N,E,R", [(33, 5120, 1280, 16, 16), (70, 5120, 5120, 8, 8), (300, 640, 512, 3, 24),
+                                       (61, 1040, 7007, 32, 64)])
+def test_each_gradient_is_the_same_without_the_others(M, K, N, E, R):
+    p = problem((M, K, N, E, R, BF16, BF16), "runs", seed=3)
+    dy, _ = randn(M, (M, N), BF16, 1e-3)
+    args = (dy, p["x"], p["a"], p["b"], p["scale"], p["ids"])
+    whole = wq.lora_backward(*args)
+    for i in range(1, 7):
+        need = tuple(bool(i >> j & 1) for j in range(3))
+        for got, want, on in zip(wq.lora_backward(*args, need=need), whole, need):
+            assert (got is not None) == on and (not on or torch.equal(got, want)), need
+
+
 def test_backward_in_place_and_parts():
     p = problem((150, 192, 140, 3, 16, BF16, BF16), "runs")
     dy, _ = randn(1, (150, 140), F32, 1e-3)

@@ -9,8 +9,8 @@
 // as their slow index, so both go through the wave's transposing LDS tiles, t's three terms one after the other through
 // the same one (a tile per term left room for two workgroups on a CU at rank 32, one at rank 64); the next block's loads
 // are issued before this block's MFMAs.  Long batches with few adapters split the rows over up to 8 workgroups, joined in
-// order by a second kernel.  da and db of a backward pass share a launch where x and dy have one type, and always the second
-// kernel's.  4096 x 17408 float32 (db, rank 16): 62 us (4.6 TB/s); da and db of 2047 x (17408 + 5120) bfloat16, rank 32 on 5
+// order by a second kernel.  da and db of a backward pass share a launch where x and dy have one type and both take as many waves,
+// and always the second kernel's.  4096 x 17408 float32 (db, rank 16): 62 us (4.6 TB/s); da and db of 2047 x (17408 + 5120) bfloat16, rank 32 on 5
 // adapters: 32 us, and 31 with all operands cached: its 2112 short workgroups bound it, not memory.
 #include <algorithm>
 
@@ -319,9 +319,17 @@ hipError_t go_waves(int M, int E, int R, const OuterSum& a, const OuterSum& b, c
                      (outer_lds<VT, NR, WAVES>()), st, M, E, R, total, a, b, ids);
   return hipGetLastError();
 }
+// The choice is each sum's own, so that its order of additions does not depend on the other's being computed.
 template <int VT, int NR>
 hipError_t go(int M, int E, int R, const OuterSum& a, const OuterSum& b, const int32_t* ids, hipStream_t st) {
-  if (outer_one_wave(a.wgs + b.wgs, std::max(a.part_rows, b.part_rows), E)) return go_waves<VT, NR, 1>(M, E, R, a, b, ids, st);
+  const bool one = outer_one_wave(a.wgs, a.part_rows, E);
+  if (b.wgs > 0 && outer_one_wave(b.wgs, b.part_rows, E) != one) {
+    OuterSum none = b;
+    none.wgs = 0;
+    const hipError_t err = go<VT, NR>(M, E, R, a, none, ids, st);
+    return err != hipSuccess ? err : go<VT, NR>(M, E, R, b, none, ids, st);
+  }
+  if (one) return go_waves<VT, NR, 1>(M, E, R, a, b, ids, st);
   return go_waves<VT, NR, 4>(M, E, R, a, b, ids, st);
 }
 template <int VT, typename... A>
