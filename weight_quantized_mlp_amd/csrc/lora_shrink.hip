@@ -344,6 +344,7 @@ __global__ void __launch_bounds__(256) lora_terms_kernel(int plane, int E, int R
 // rank 64, of 7007: float32 w 42 instead of 62, bfloat16 w 33 instead of 31).
 int shrink_parts(int M, int D, int R, int es, int ws) {
   const int tiles = ((M + kRows - 1) / kRows) * ((R + 63) / 64);
+  if (tiles == 0) return 1;                // no rows: the size queries and the weight gradients (zeros) still come here
   const int64_t xb = (int64_t)kRows * D * es, wb = (int64_t)std::min(R, 64) * D * ws;
   if (tiles >= 256 || (xb <= (512 << 10) && xb + wb <= (tiles <= 32 ? 512 << 10 : 1536 << 10))) return 1;
   const int s = std::min(kParts, 512 / tiles);
