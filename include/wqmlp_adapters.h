@@ -57,7 +57,8 @@ int lora_run(int64_t M, int64_t K, int64_t N, int64_t E, int64_t R, const void* 
  * WQ_F16 (dx rounded once from float32); dx0 NULL stands for zeros and may be dx itself (the gradient that
  * qlinear_backward left there); da [E,R,K] and db [E,N,R] float32, written whole (zeros for an adapter
  * that no row names).  Each of dx, da and db may be NULL and is then not computed, at least one is not.
- * The workspace is lora_workspace_bytes(..., backward = 1).  M == 0 writes da and db with zeros.
+ * The workspace is lora_workspace_bytes(..., backward = 1).  M == 0 writes da and db, where given, with
+ * zeros (dy, x, ids, dx0 and dx may then be NULL).
  */
 int lora_backward(int64_t M, int64_t K, int64_t N, int64_t E, int64_t R, const void* dy, int dy_dtype,
                   const void* x, int x_dtype, const void* a, const void* b, int w_dtype, const float* scale,

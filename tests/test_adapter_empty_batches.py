@@ -36,3 +36,22 @@ def test_calls_of_no_rows(K, N, E, R):
     da, db = torch.full((E, R, K), 7.0, device=dev), torch.full((E, N, R), 7.0, device=dev)
     dx, da, db = wq.lora_backward(y, x, a, b, scale, ids, da=da, db=db)
     assert dx.shape == (0, K) and not da.any() and not db.any()
+
+
+def test_empty_dx_alone_on_the_host():
+    """An empty dx may be NULL, so a call that asks for dx alone passes no output at all."""
+    A, MB = 1 << 40, 1 << 20
+    for M, rc in ((0, 0), (1, -1)):
+        x = None if M == 0 else A + 4 * MB
+        assert wq.lib().lora_backward(M, 64, 48, 2, 8, x, 1, x, 1, A, A + MB, 1, A + 2 * MB, x, None, 1, None, 0, None, None, None,
+                                      None) == rc
+
+
+@pytest.mark.gpu
+def test_empty_dx_alone():
+    import torch
+    dev = torch.device("cuda:0")
+    a, b, scale = torch.ones((2, 8, 64), device=dev), torch.ones((2, 48, 8), device=dev), torch.ones(2, device=dev)
+    dx, da, db = wq.lora_backward(torch.empty((0, 48), device=dev), torch.empty((0, 64), device=dev), a, b, scale,
+                                  torch.empty(0, dtype=torch.int32, device=dev), need=(True, False, False))
+    assert dx.shape == (0, 64) and da is None and db is None

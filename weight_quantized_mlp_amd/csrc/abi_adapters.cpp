@@ -71,8 +71,8 @@ int lora_backward(int64_t M, int64_t K, int64_t N, int64_t E, int64_t R, const v
     return WQ_EINVAL;
   if (!lora_shape_ok(M, K, N, E, R)) return WQ_EINVAL;
   if (any_null({a, b, scale})) return WQ_EINVAL;
-  if (dx == nullptr && da == nullptr && db == nullptr) return WQ_EINVAL;
-  if (M == 0) {   // no rows: dx is empty, the weight gradients are zero
+  if (M > 0 && dx == nullptr && da == nullptr && db == nullptr) return WQ_EINVAL;
+  if (M == 0) {   // no rows: dx is empty (and may be NULL, as an empty tensor's address is), the weight gradients are zero
     dx = nullptr;
     if (da == nullptr && db == nullptr) return WQ_OK;
     dy = x = dx0 = nullptr;
