@@ -71,7 +71,7 @@ int lora_backward(int64_t M, int64_t K, int64_t N, int64_t E, int64_t R, const v
  * fmt, w, scale and global_scale as for qlinear_run.  dy [M,N]: WQ_F32 or WQ_BF16; dx [M,K]: dx_dtype,
  * WQ_F32 or WQ_BF16.  K: a multiple of 16 (FP8) or 64 (NVFP4); N: any.
  * Each row of dy (FP8: times scale[n], one float32 rounding) is scaled by a power of two so that its
- * largest magnitude lies in [2^14, 2^15) and enters float16 MFMAs: rounded once to float16 where dx is
+ * largest finite magnitude lies in [2^14, 2^15) and enters float16 MFMAs: rounded once to float16 where dx is
  * bfloat16 (relative error at most 2^-11 per element, below the 2^-8 of dx's own rounding), as the sum of
  * two float16 terms (2^-22) where dx is float32.  Weights decode exactly; sums are float32.
  * M == 0 is a valid empty call.

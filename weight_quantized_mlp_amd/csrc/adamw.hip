@@ -71,9 +71,6 @@ __device__ __forceinline__ float wave_max(float v) {
   return fmaxf(fmaxf(r0, r1), fmaxf(r2, r3));
 }
 
-// |x|, 0 where x is not finite: such a state has no say in its block's scale.
-__device__ __forceinline__ float finite_abs(float x) { return fabsf(x) <= 3.4028235e38f ? fabsf(x) : 0.f; }
-
 // Smallest e in [-100, 100] with amax <= 0.875 * 2^half * 2^e; 0 for a zero amax.
 __device__ __forceinline__ int block_exp(float amax, int half) {
   if (!(amax > 0.f)) return 0;
@@ -274,6 +271,7 @@ __global__ void __launch_bounds__(256) adamw_kernel(const uint8_t* __restrict__ 
         store4<NT>(reinterpret_cast<float*>(e.m), i, n, m);
         store4<NT>(reinterpret_cast<float*>(e.v), i, n, v);
       } else {
+        // a state that is not finite has no say in its block's scale
         const float am = fmaxf(fmaxf(finite_abs(m[0]), finite_abs(m[1])), fmaxf(finite_abs(m[2]), finite_abs(m[3])));
         const float av = fmaxf(fmaxf(finite_abs(v[0]), finite_abs(v[1])), fmaxf(finite_abs(v[2]), finite_abs(v[3])));
         const int em = block_exp(wave_max(am), 9), ev = block_exp(wave_max(av), 16);

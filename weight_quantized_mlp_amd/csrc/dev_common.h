@@ -171,6 +171,9 @@ __device__ __forceinline__ float wave64_sum(float v) {
 
 __device__ __forceinline__ float silu_f32(float z) { return z / (1.0f + expf(-z)); }
 
+// |x|, 0 where x is not finite (a maximum that infinities and NaN have no say in).
+__device__ __forceinline__ float finite_abs(float x) { return fabsf(x) <= 3.4028235e38f ? fabsf(x) : 0.f; }
+
 __device__ __forceinline__ float bf16_bits_to_f32(uint32_t b) { return __uint_as_float(b << 16); }
 
 }  // namespace wq

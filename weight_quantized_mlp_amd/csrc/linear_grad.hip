@@ -24,7 +24,7 @@
 // with them.
 //
 // Numerics: dy (times s[n] for FP8, one float32 rounding) is scaled per row by a power of two so that its largest
-// magnitude lies in [2^14, 2^15).  TERMS = 1 (bfloat16 dx): rounded once to float16, 2^-11 at most per element,
+// finite magnitude lies in [2^14, 2^15).  TERMS = 1 (bfloat16 dx): rounded once to float16, 2^-11 at most per element,
 // where dx's own rounding is 2^-8.  TERMS = 2 (float32 dx): the float16 value and the float16 of what it left,
 // 2^-22, two MFMAs into one float32 accumulator.
 #include <algorithm>
@@ -37,17 +37,23 @@ namespace wq {
 namespace {
 
 // ---- dy -> float16 terms ---------------------------------------------------------------------------------------
-// Power-of-two exponent e of a row: amax * 2^-e in [2^14, 2^15); 0 for a zero or non-finite amax.  The clamp keeps
+// Power-of-two exponent e of a row: amax * 2^-e in [2^14, 2^15); 0 for a zero amax.  The clamp keeps
 // 2^e and 2^-e normal float32 numbers.
 __device__ __forceinline__ int grad_row_exp(float amax) {
-  if (!(amax > 0.f) || !(amax <= 3.4028235e38f)) return 0;
+  if (!(amax > 0.f)) return 0;
   int ex;
   (void)frexpf(amax, &ex);
   const int e = ex - 15;
   return e < -126 ? -126 : e;
 }
 
-// One workgroup per row of dy [M][N] (any N, so rows are only element-aligned): the row's largest magnitude, then the scaled
+// What float16 h left of x; nothing where h is infinite (x - h would be NaN, and the row's infinities lose their sign) or NaN.
+__device__ __forceinline__ _Float16 second_term(float x, _Float16 h) {
+  const float r = x - (float)h;
+  return r == r ? (_Float16)r : (_Float16)0.f;
+}
+
+// One workgroup per row of dy [M][N] (any N, so rows are only element-aligned): the row's largest finite magnitude, then the scaled
 // float16 terms, [TERMS][M][Np] with zeros from N to Np (a multiple of 64).  A thread keeps RC chunks of 8 elements in registers,
 // loaded without a branch between them so that all are in flight at once; longer rows read the rest twice.  The up to 7 elements
 // behind the last whole chunk are one thread's.
@@ -100,7 +106,7 @@ __global__ void __launch_bounds__(256) grad_prep_kernel(int M, int N, int Np, co
       const float x0 = ldexpf(v[2 * j], -e), x1 = ldexpf(v[2 * j + 1], -e);
       const _Float16 h0 = (_Float16)x0, h1 = (_Float16)x1;
       hi[j] = as_u32(f16x2{h0, h1});
-      if constexpr (TERMS == 2) lo[j] = as_u32(f16x2{(_Float16)(x0 - (float)h0), (_Float16)(x1 - (float)h1)});
+      if constexpr (TERMS == 2) lo[j] = as_u32(f16x2{second_term(x0, h0), second_term(x1, h1)});
     }
     reinterpret_cast<u32x4*>(o)[c] = u32x4{hi[0], hi[1], hi[2], hi[3]};
     if constexpr (TERMS == 2) reinterpret_cast<u32x4*>(o + (size_t)M * Np)[c] = u32x4{lo[0], lo[1], lo[2], lo[3]};
@@ -108,13 +114,13 @@ __global__ void __launch_bounds__(256) grad_prep_kernel(int M, int N, int Np, co
   float amax = 0.f, keep[RC][8], rest = 0.f;
   auto maximum = [&](const float* v) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
+    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, finite_abs(v[j]));
   };
   if (t < N - 8 * nf) {                          // element 8 nf + t
     const int n = 8 * nf + t;
     rest = BF ? bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(row)[n]) : reinterpret_cast<const float*>(row)[n];
     if constexpr (SC) rest *= scale[n];
-    amax = fabsf(rest);
+    amax = finite_abs(rest);
   }
   if (nf > 0) {
     Chunk raw[RC];
@@ -152,7 +158,7 @@ __global__ void __launch_bounds__(256) grad_prep_kernel(int M, int N, int Np, co
     const float x = ldexpf(rest, -e);
     const _Float16 h = (_Float16)x;
     o[8 * nf + t] = __builtin_bit_cast(uint16_t, h);
-    if constexpr (TERMS == 2) o[(size_t)M * Np + 8 * nf + t] = __builtin_bit_cast(uint16_t, (_Float16)(x - (float)h));
+    if constexpr (TERMS == 2) o[(size_t)M * Np + 8 * nf + t] = __builtin_bit_cast(uint16_t, second_term(x, h));
   }
 }
 
