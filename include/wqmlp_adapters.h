@@ -71,9 +71,12 @@ int lora_backward(int64_t M, int64_t K, int64_t N, int64_t E, int64_t R, const v
  * fmt, w, scale and global_scale as for qlinear_run.  dy [M,N]: WQ_F32 or WQ_BF16; dx [M,K]: dx_dtype,
  * WQ_F32 or WQ_BF16.  K: a multiple of 16 (FP8) or 64 (NVFP4); N: any.
  * Each row of dy (FP8: times scale[n], one float32 rounding) is scaled by a power of two so that its
- * largest finite magnitude lies in [2^14, 2^15) and enters float16 MFMAs: rounded once to float16 where dx is
- * bfloat16 (relative error at most 2^-11 per element, below the 2^-8 of dx's own rounding), as the sum of
- * two float16 terms (2^-22) where dx is float32.  Weights decode exactly; sums are float32.
+ * largest finite magnitude lies in [2^14, 2^15) (a row below 2^-112: by 2^126) and enters float16 MFMAs.
+ * dx bfloat16: rounded once to float16; an element is off by at most 2^-11 of itself (dx's own rounding is
+ * 2^-8) or 2^-39 of its row's largest, whichever is more.  dx float32: as two float16 terms; 2^-22 of the
+ * element or 2^-51 of the row's largest.  A caller who wants more than float16 holds of dy in a bfloat16 dx
+ * asks for float32 and rounds it.  Weights decode exactly; sums are float32.  NaN and infinities of dy stay in
+ * their row and act there as float32 products would.
  * M == 0 is a valid empty call.
  */
 size_t qlinear_backward_workspace_bytes(int fmt, int64_t M, int64_t N, int64_t K, int dx_dtype);

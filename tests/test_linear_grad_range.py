@@ -48,3 +48,29 @@ def test_an_infinity_keeps_its_sign_beside_large_values(fmt, dxt, M):
         want = np.inf * dq[3] - np.inf * dq[4]
     assert np.array_equal(got[2], want.astype(np.float32), equal_nan=True)
     assert np.isfinite(got[3:]).all()
+
+
+@pytest.mark.parametrize("M", [5, 200])
+@pytest.mark.parametrize("dxt", [F32, BF16])
+@pytest.mark.parametrize("fmt", [FP8, NV], ids=["fp8", "nvfp4"])
+def test_small_elements_beside_a_large_one(fmt, dxt, M):
+    """A large element in every row, the others 2^-14 to 2^-40 of it.  Where the large one meets a zero weight dx is made
+    of the small ones alone, and is as exact as they were taken: within 2^-22 (bfloat16 dx: 2^-11) of each, or 2^-51
+    (2^-39) of the row's largest."""
+    N, K = 150, 320
+    w, s, gs, dq = weights(fmt, N, K)
+    r = np.random.default_rng(M)
+    for bits in (14, 20, 28, 40):
+        dyn = (r.standard_normal((M, N)) * 2.0 ** -bits).astype(np.float32)
+        at = r.integers(0, N, M)
+        dyn[np.arange(M), at] = np.where(r.random(M) < 0.5, -1.0, 1.0)
+        got = host(wq.qlinear_backward(fmt, torch.from_numpy(dyn).to(DEV), w, s, gs, dtype=dxt)).astype(np.float64)
+        dyd = dyn.astype(np.float64)
+        ref, size = dyd @ dq, np.abs(dyd) @ np.abs(dq)
+        each, floor = (2.0 ** -22, 2.0 ** -51) if dxt == F32 else (2.0 ** -11, 2.0 ** -39)
+        # the elements as they are taken (FP8: and scaled; NVFP4: 1 / global scale and its product), the sums, dx's rounding
+        bound = (each + 4 * U + 2 * (N + 8) * U) * size + floor * np.abs(dyd).max(1, keepdims=True) * np.abs(dq).sum(0) + \
+            torch.finfo(dxt).eps / 2 * np.abs(ref)
+        assert np.all(np.abs(got - ref) <= bound), bits
+        zero = dq[at] == 0
+        assert zero.any() and np.all(size[zero] < 1.5 * N * 2.0 ** -bits * np.abs(dq).max())    # those columns see no large one

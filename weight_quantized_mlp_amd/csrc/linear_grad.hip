@@ -24,9 +24,12 @@
 // with them.
 //
 // Numerics: dy (times s[n] for FP8, one float32 rounding) is scaled per row by a power of two so that its largest
-// finite magnitude lies in [2^14, 2^15).  TERMS = 1 (bfloat16 dx): rounded once to float16, 2^-11 at most per element,
-// where dx's own rounding is 2^-8.  TERMS = 2 (float32 dx): the float16 value and the float16 of what it left,
-// 2^-22, two MFMAs into one float32 accumulator.
+// finite magnitude lies in [2^14, 2^15).  TERMS = 1 (bfloat16 dx): rounded once to float16, off by at most 2^-11 of the
+// element, where dx's own rounding is 2^-8, or by half of float16's smallest step, 2^-39 of the row's largest.  TERMS = 2
+// (float32 dx): the float16 value and, as another float16, 2^12 times what it left, so that the second term of a small
+// element beside a large one is not lost among the subnormals: off by at most 2^-22 of the element or 2^-51 of the row's
+// largest.  The second terms' products have float32 accumulators of their own (a tile of two terms has half the rows, so
+// both kinds of tile hold as many), which join the others' at the end.
 #include <algorithm>
 
 #include "dev_common.h"
@@ -47,9 +50,11 @@ __device__ __forceinline__ int grad_row_exp(float amax) {
   return e < -126 ? -126 : e;
 }
 
-// What float16 h left of x; nothing where h is infinite (x - h would be NaN, and the row's infinities lose their sign) or NaN.
+// What float16 h left of x, times 2^12; nothing where h is infinite (x - h would be NaN, and the row's infinities lose their
+// sign) or NaN.  |x| < 2^15, so h is off by at most 8.
+constexpr float kSecond = 4096.f;
 __device__ __forceinline__ _Float16 second_term(float x, _Float16 h) {
-  const float r = x - (float)h;
+  const float r = (x - (float)h) * kSecond;
   return r == r ? (_Float16)r : (_Float16)0.f;
 }
 
@@ -342,9 +347,9 @@ __global__ void __launch_bounds__(256, 2) grad_gemm_kernel(int M, int N, int Np,
     sc[3 * kScaleRow] = (uint16_t)(d1 >> 16);
   };
 
-  f32x16 acc[RB][2];
+  f32x16 acc[MB][2];                         // block i: rows 32 (i % RB) .. of the tile, term i / RB
 #pragma unroll
-  for (int i = 0; i < RB; ++i)
+  for (int i = 0; i < MB; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -413,7 +418,7 @@ __global__ void __launch_bounds__(256, 2) grad_gemm_kernel(int M, int N, int Np,
     for (int i = 0; i < MB; ++i)
 #pragma unroll
       for (int j = 0; j < 2; ++j)
-        acc[i % RB][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(af[i], bf[j], acc[i % RB][j], 0, 0, 0);
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(af[i], bf[j], acc[i][j], 0, 0, 0);
 #pragma unroll
     for (int i = 0; i < 2 * MB; ++i) {       // one MFMA, one fragment read, two ALU operations at a time
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
@@ -484,6 +489,14 @@ __global__ void __launch_bounds__(256, 2) grad_gemm_kernel(int M, int N, int Np,
   __syncthreads();
   float* ep = reinterpret_cast<float*>(lds + wave * kEpiBytes);
   const float c = FMT == 0 ? 1.0f : inv;
+  if constexpr (TERMS == 2) {
+#pragma unroll
+    for (int i = 0; i < RB; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = fmaf(acc[i + RB][j][r], 1.0f / kSecond, acc[i][j][r]);
+  }
   float* pt = partials + (size_t)b * BM * kCols + 64 * wave;            // split tile: raw sums [BM][256] for grad_finish_kernel
 #pragma unroll
   for (int i = 0; i < RB; ++i) {
