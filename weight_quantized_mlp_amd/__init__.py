@@ -470,6 +470,8 @@ def qlinear_backward(fmt, dy, w, scale=None, global_scale=1.0, dtype=None, out=N
     global_scale as for qlinear_run; dx [M,K] f32/bf16 (out's type, or dtype, default dy's)."""
     dev = dy.device
     M, N = dy.shape
+    if N == 0:
+        raise ValueError("dy must have at least one column")
     dyt = _float_code(dy.dtype, "dy", (torch.float32, torch.bfloat16))
     _want(dy, "dy", dy.dtype, dev, M * N)
     if w.shape[0] != N:
