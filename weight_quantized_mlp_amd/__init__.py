@@ -430,16 +430,27 @@ def lora_run(x, a, b, scale, ids, y, out=None, workspace=None):
     return out
 
 
+def _result_dtype(name, asked, default, **given):
+    """The result's type: that of the given tensors, else the one asked for by name, else the default; TypeError where they differ."""
+    want = asked
+    for key, t in given.items():
+        if t is not None:
+            if want is not None and t.dtype != want:
+                raise TypeError(f"{key} is {t.dtype}, where {name} or another tensor says {want}")
+            want = t.dtype
+    return default if want is None else want
+
+
 def lora_backward(dy, x, a, b, scale, ids, dx0=None, dx=None, da=None, db=None, workspace=None, dx_dtype=None,
                   need=(True, True, True)):
     """Gradients of lora_run: (dx, da, db).  dx = dx0 (None: zeros) + the adapters' part, of dx0's type (or dx_dtype,
-    default x's); da, db float32, summed over each adapter's rows.  need: which of (dx, da, db) to compute (others
+    default x's; a TypeError where they differ); da, db float32, summed over each adapter's rows.  need: which of (dx, da, db) to compute (others
     None).  dx may be dx0 (in place)."""
+    want = _result_dtype("dx_dtype", dx_dtype, x.dtype, dx=dx, dx0=dx0)
     M, K, N, E, R, xt, wt = _lora_args(x, a, b, scale, ids)
     dev = x.device
     dyt = _float_code(dy.dtype, "dy", (torch.float32, torch.bfloat16))
     _want(dy, "dy", dy.dtype, dev, M * N)
-    want = dx.dtype if dx is not None else dx0.dtype if dx0 is not None else dx_dtype or x.dtype
     dxt = _float_code(want, "dx")
     if dx0 is not None:
         _want(dx0, "dx0", want, dev, M * K)
@@ -467,7 +478,9 @@ def qlinear_backward_workspace_bytes(fmt, M, N, K, dx_dtype=torch.float32):
 
 def qlinear_backward(fmt, dy, w, scale=None, global_scale=1.0, dtype=None, out=None, workspace=None):
     """dx = dy dq(W): the gradient of qlinear_run with respect to its input.  dy [M,N] f32/bf16; w, scale and
-    global_scale as for qlinear_run; dx [M,K] f32/bf16 (out's type, or dtype, default dy's)."""
+    global_scale as for qlinear_run; dx [M,K] f32/bf16 (out's type, or dtype, default dy's;
+    a TypeError where they differ)."""
+    want = _result_dtype("dtype", dtype, dy.dtype, out=out)
     dev = dy.device
     M, N = dy.shape
     if N == 0:
@@ -480,7 +493,6 @@ def qlinear_backward(fmt, dy, w, scale=None, global_scale=1.0, dtype=None, out=N
     _want(w, "w", torch.uint8, dev, N * (K // 64) * 36 if fmt == WQ_FMT_NVFP4 else N * K)
     if scale is not None:
         _want(scale, "scale", torch.float32, dev, N)
-    want = out.dtype if out is not None else dtype or dy.dtype
     dxt = _float_code(want, "dx", (torch.float32, torch.bfloat16))
     if out is None:
         out = torch.empty((M, K), dtype=want, device=dev)
