@@ -58,6 +58,13 @@ __device__ __forceinline__ double pow_int(double b, int64_t t) {
   return r;
 }
 
+// Square root within one unit.  The instruction takes subnormal operands as zero, whose roots are ordinary numbers: small
+// operands go through it scaled.
+__device__ __forceinline__ float root(float x) {
+  const bool small = x < 0x1p-96f;
+  return __builtin_amdgcn_sqrtf(small ? x * 0x1p64f : x) * (small ? 0x1p-32f : 1.0f);
+}
+
 __device__ __forceinline__ float wave_max(float v) {
   v = fmaxf(v, dpp_f32<0xB1>(v));
   v = fmaxf(v, dpp_f32<0x4E>(v));
@@ -250,7 +257,7 @@ __global__ void __launch_bounds__(256) adamw_kernel(const uint8_t* __restrict__ 
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float d = __builtin_amdgcn_sqrtf(v[j] * ibc2) + h.eps;
+        const float d = root(v[j] * ibc2) + h.eps;
         p[j] = p[j] * keep - lr * ((m[j] * ibc1) * __builtin_amdgcn_rcpf(d));
       }
       store4<NT>(e.p, i, n, p);
