@@ -89,6 +89,7 @@ int qlinear_backward(int fmt, int64_t M, int64_t N, int64_t K, const void* dy, i
  *   m = beta1 m + (1 - beta1) g            v = beta2 v + (1 - beta2) g^2
  *   p = p (1 - lr weight_decay) - lr (m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
  *   copy = p rounded to copy_dtype (the adapter weights that lora_run reads), where a copy is kept
+ * eps: 0, or taken as at least 2^-126.
  * p is float32 (master weights), g float32 or bfloat16.  State forms (state_bits):
  *   32  m, v float32
  *    8  blocks of WQ_ADAMW_BLOCK consecutive elements (the last may be short) with one power-of-two float32

@@ -32,7 +32,7 @@ def test_small_second_moments(eps, t):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("eps", [2.0 ** -126, 1e-30, 1e-8])
+@pytest.mark.parametrize("eps", [1e-60, 1e-45, 1e-40, 2.0 ** -126, 1e-30, 1e-8])
 @pytest.mark.parametrize("bits", [32, 8])
 def test_elements_without_gradients_stay(bits, eps):
     n = 700

@@ -10,6 +10,8 @@
 // 2048 workgroups and a run of chunks each), 83M with 8-bit states 263 us (285 us).  A wave takes 256
 // consecutive elements at a time, 4 per lane: 16-byte accesses to the float32 arrays, 4-byte accesses to
 // the codes, and a block's scale is one wave maximum.
+#include <algorithm>
+
 #include "dev_common.h"
 #include "launch.h"
 
@@ -323,7 +325,10 @@ hipError_t launch_adamw_table(int64_t count, int64_t first, int n, int64_t total
 hipError_t launch_adamw(int64_t count, int64_t elems, int bits, const void* table, const int64_t* step, const float* lr,
                         double beta1, double beta2, double eps, double weight_decay, float grad_scale, uint32_t seed,
                         hipStream_t st) {
-  const AdamwHyper h{(float)beta1, (float)(1.0 - beta1), (float)beta2, (float)(1.0 - beta2), (float)eps, grad_scale,
+  // The root of any v is 0 or above 2^-75, so a positive eps below 2^-126 matters only where v is 0: there it keeps
+  // 0 / eps at 0, which a subnormal would not (the reciprocal instruction takes one as zero).
+  const float eps32 = eps > 0.0 ? std::max((float)eps, 0x1p-126f) : 0.f;
+  const AdamwHyper h{(float)beta1, (float)(1.0 - beta1), (float)beta2, (float)(1.0 - beta2), eps32, grad_scale,
                      beta1, beta2, (float)weight_decay, seed};
   const int64_t chunks = adamw_chunks(elems) + count;   // at least the table's number
   const unsigned grid = (unsigned)(chunks < (1 << 22) ? chunks : (1 << 22));
