@@ -37,7 +37,8 @@ extern "C" {
  *   y     [M, N]     float32: the projection's result (qlinear_run); NULL stands for zeros
  *   out   [M, N]     float32; may be y itself
  * The result is that of float32 arithmetic: operands enter the matrix cores as sums of bfloat16 terms that
- * hold all their bits, the rank-R intermediate is float32.  An adapter's values reach only the rows that
+ * hold all their bits down to 2^-133, bfloat16's smallest step (a float32 operand is off by at most 2^-134), and
+ * so does the rank-R intermediate, which is float32.  An adapter's values reach only the rows that
  * name it, whatever they are (NaN and infinities included); where a row's own operands hold an infinity,
  * or a float32 above 3.38e38, its result may be NaN.  K: a multiple of 16; N: any; R: a multiple of 8 up to WQ_LORA_MAX_RANK.
  * M == 0 is a valid empty call (x, ids, y, out and the workspace may then be NULL).

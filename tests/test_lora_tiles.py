@@ -249,3 +249,22 @@ def test_graph_replays_streams_and_in_place(shape):
     wq.lora_run(p["x"], p["a"], p["b"], p["scale"], p["ids"], y, out=y)
     wq.lora_backward(*args(), d, dx=d, need=(True, False, False))
     assert np.array_equal(host(y), want[0]) and np.array_equal(host(d), want[1])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("power", [-100, -112, -124])
+@pytest.mark.parametrize("shape", [(300, 208, 150, 3, 64, F32, F32), (300, 208, 150, 3, 64, F32, BF16), (320, 5120, 131, 3, 64, F32, F16)], ids=name)
+def test_operands_near_the_smallest_bfloat16_step(shape, power):
+    """A float32 operand keeps its bits down to 2^-133: each is off by 2^-134 at most, beside float32's own roundings."""
+    M, K, N, E, R = shape[:5]
+    assert tiled(shape)
+    p = problem(shape, "random", seed=5)
+    p["x"] = p["x"] * 2.0 ** power                                     # exact
+    n = dict(p["n"], x=p["x"].double().cpu().numpy(), y=np.zeros((M, N)))
+    got = host(wq.lora_run(p["x"], p["a"], p["b"], p["scale"], p["ids"], None)).astype(np.float64)
+    ref = oracle.lora_ref(n["x"], n["a"], n["b"], n["scale"], n["ids"], n["y"])
+    size = oracle.lora_ref(abs(n["x"]), abs(n["a"]), abs(n["b"]), n["scale"], n["ids"], n["y"])
+    # an error of 2^-134 in every x against a, and in every element of the scaled intermediate against b; float32 subnormals
+    off = oracle.lora_ref(np.full((M, K), 2.0 ** -134), abs(n["a"]), abs(n["b"]), n["scale"], n["ids"], n["y"])
+    off += 2.0 ** -134 * np.abs(n["b"]).sum(2).max() + 2.0 ** -149 * (K + R)
+    assert np.all(np.abs(got - ref) <= 2 * (K + R + 8) * U * size + 2 * U * np.abs(ref) + off)

@@ -1,8 +1,8 @@
 // Device-side pieces shared by the low-rank adapter kernels (lora_*.hip).
 //
 // Operand terms.  The adapters' products run on bfloat16 MFMAs but are to be float32 products: every operand is
-// taken as a sum of bfloat16 terms that holds all its bits -- bfloat16 is 1 term, float16 2, float32 (and the float32
-// intermediates) 3 -- and a product is the sum of the term products that reach above 2^-25 of it (term indices i + j
+// taken as a sum of bfloat16 terms that holds all its bits (down to 2^-133, bfloat16's smallest step) -- bfloat16 is 1 term,
+// float16 2, float32 (and the float32 intermediates) 3 -- and a product is the sum of the term products that reach above 2^-25 of it (term indices i + j
 // <= 2).  The kernels move far more bytes than they multiply, so the extra MFMAs hide behind the loads.
 //
 // Transposed operands.  An MFMA 16x16x32 operand wants 8 consecutive contraction indices per lane.  Where memory
