@@ -42,6 +42,8 @@ extern "C" {
  * name it, whatever they are (NaN and infinities included); where a row's own operands hold an infinity,
  * or a float32 above 3.38e38, its result may be NaN.  K: a multiple of 16; N: any; R: a multiple of 8 up to WQ_LORA_MAX_RANK.
  * M == 0 is a valid empty call (x, ids, y, out and the workspace may then be NULL).
+ * The fused MLP calls take no adapters: an MLP with adapters is qlinear_run and lora_run for each of its
+ * projections, with the activation (and its gradient) between them the caller's.
  */
 size_t lora_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t E, int64_t R, int backward);
 int lora_run(int64_t M, int64_t K, int64_t N, int64_t E, int64_t R, const void* x, int x_dtype,
