@@ -61,7 +61,8 @@ int lora_run(int64_t M, int64_t K, int64_t N, int64_t E, int64_t R, const void* 
  * qlinear_backward left there); da [E,R,K] and db [E,N,R] float32, written whole (zeros for an adapter
  * that no row names).  Each of dx, da and db may be NULL and is then not computed, at least one is not.
  * The workspace is lora_workspace_bytes(..., backward = 1).  M == 0 writes da and db, where given, with
- * zeros (dy, x, ids, dx0 and dx may then be NULL).
+ * zeros (dy, x, ids, dx0 and dx may then be NULL).  Precision and infinities as for lora_run: where a row of dy
+ * or x holds an infinity, its dx and its adapter's da and db may be NaN.
  */
 int lora_backward(int64_t M, int64_t K, int64_t N, int64_t E, int64_t R, const void* dy, int dy_dtype,
                   const void* x, int x_dtype, const void* a, const void* b, int w_dtype, const float* scale,
@@ -105,7 +106,8 @@ int qlinear_backward(int fmt, int64_t M, int64_t N, int64_t K, const void* dy, i
  *       element whose gradients stay below 2^-16 of its block's largest takes shorter steps than float32
  *       states give it, never longer ones (a v of zero beside an m that is not would).  r are the low (m) and high (v) 16 bits of
  *       mix(key + 0x9E3779B9 i) for element i of tensor j, key = mix(mix(seed + 0x9E3779B9 t) + j), with
- *       mix(h): h ^= h>>16; h *= 0x7FEB352D; h ^= h>>15; h *= 0x846CA68B; h ^= h>>16 on 32 bits.
+ *       mix(h): h ^= h>>16; h *= 0x7FEB352D; h ^= h>>15; h *= 0x846CA68B; h ^= h>>16 on 32 bits (constants:
+ *       C. Wellons, "Prospecting for Hash Functions", 2018).
  *       p takes the step with m and v before their rounding.  A state that is not finite gets a NaN code
  *       and does not count for its block's scale.
  *
@@ -115,7 +117,7 @@ int qlinear_backward(int fmt, int64_t M, int64_t N, int64_t K, const void* dy, i
  *   in use, must not overlap, and n == 0 is allowed.  Rebuild it when a gradient buffer moves.
  *   adamw_run takes one step over the table's tensors.  step (int64, >= 1) and lr (float32) are read from
  *   device memory, so that a captured graph can be replayed over many steps.  elems: the sum of n, which
- *   sizes the launch and nothing else.  A table built for the other state_bits is left untouched.  Steps
+ *   sizes the launch (0: an empty call) and nothing else.  A table built for the other state_bits is left untouched.  Steps
  *   over the same tensors must not run at the same time, nor before the build that wrote the table.
  */
 typedef struct {

@@ -444,8 +444,8 @@ def _result_dtype(name, asked, default, **given):
 def lora_backward(dy, x, a, b, scale, ids, dx0=None, dx=None, da=None, db=None, workspace=None, dx_dtype=None,
                   need=(True, True, True)):
     """Gradients of lora_run: (dx, da, db).  dx = dx0 (None: zeros) + the adapters' part, of dx0's type (or dx_dtype,
-    default x's; a TypeError where they differ); da, db float32, summed over each adapter's rows.  need: which of (dx, da, db) to compute (others
-    None).  dx may be dx0 (in place)."""
+    default x's; a TypeError where they differ); da, db float32, summed over each adapter's rows.  need: which of
+    (dx, da, db) to compute (others None).  dx may be dx0 (in place)."""
     want = _result_dtype("dx_dtype", dx_dtype, x.dtype, dx=dx, dx0=dx0)
     M, K, N, E, R, xt, wt = _lora_args(x, a, b, scale, ids)
     dev = x.device

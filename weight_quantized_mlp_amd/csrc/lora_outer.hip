@@ -281,8 +281,12 @@ inline int64_t outer_tiles(int D, int E, int R) {
   return (int64_t)E * ((D + kD - 1) / kD) * ((R + C - 1) / C);
 }
 // Parts of the rows: the number, at most 8 and of at least 256 rows each, for which reading v (stretched by the last round of
-// workgroups standing partly idle, 3 per CU, which LDS allows every form), the partial sums' way through memory and what a
-// workgroup's start and end cost (about 5 us of its share of the bandwidth, 28 KB) take the fewest bytes.
+// workgroups standing partly idle), the partial sums' way through memory and what a workgroup's start and end cost (about 5 us
+// of its share of the bandwidth, 28 KB) take the fewest bytes.  A round is taken as 768 workgroups, 3 per CU, for every form;
+// their registers let 4 stand on one (bfloat16 up to rank 16), 3 (bfloat16 up to rank 32, float16 up to 16), 2, or 1 (float32
+// above rank 32).  Rounds of 512, 768 and 1024, da and db of a call: 4096 rows of 4096 x 4096, rank 128, float32 dy 145, 164 and
+// 157 us; 4096 rows of 5120 x 5120 bfloat16, rank 64 on 4 adapters 97, 89 and 94; 2048 rows of 5120 x 5120 float32, rank 32 on 2
+// adapters 73, 75 and 75; 2047 rows of 17408 x 5120 bfloat16, rank 32 on 6 adapters 66 with each.
 inline int outer_parts(int M, int D, int E, int R) {
   const int64_t tiles = outer_tiles(D, E, R), slots = 768;
   int best = 1;
@@ -298,7 +302,7 @@ inline int outer_parts(int M, int D, int E, int R) {
 }
 
 // Whether a workgroup has one wave instead of four: where workgroups with little to sum (their fixed part counts then) are more
-// than stand on the card at once, as four times as many of one wave do.  da and db at 5120 x 5120 in float32 on 16 adapters in 32 runs, rank 16:
+// than a round of 768, as four times as many of one wave do.  da and db at 5120 x 5120 in float32 on 16 adapters in 32 runs, rank 16:
 // 128 rows 23 us with one and 34 with four, 256 rows 29 and 38 (all rows on one adapter: 28 and 30), 1024 rows on one adapter 78
 // and 51; at 512 x 512, 256 rows 17 and 14.
 inline bool outer_one_wave(int wgs, int rows, int E) {
