@@ -8,9 +8,12 @@
 #include <mutex>
 
 #include "../../include/wqmlp.h"
+#include "launch.h"
 
 namespace wq {
 namespace abi {
+
+using wq::align256;
 
 // hipError_t of the last WQ_ELAUNCH / WQ_EDEVICE on this host thread.
 inline thread_local int g_last_hip = 0;
@@ -48,8 +51,6 @@ inline bool any_null(std::initializer_list<const void*> ps) {
     if (p == nullptr) return true;
   return false;
 }
-
-inline size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
 // ---- device checks (phase 2) ---------------------------------------------------------------------
 constexpr int kMaxDev = 64;

@@ -133,6 +133,12 @@ __device__ __forceinline__ void wait_vmem() {
 }
 __device__ __forceinline__ void wait_lds() { __builtin_amdgcn_s_waitcnt(0xC07F); }   // lgkmcnt(0)
 
+// LDS written by other lanes of the wave is read next (or the reverse): order them.
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 // ---- reductions -----------------------------------------------------------------------------
 // Butterfly sum over groups of W lanes (W = 16 or 64): xor offsets W/2, ..., 1.
 // The order is fixed, so the result is bitwise reproducible and equal in all lanes.

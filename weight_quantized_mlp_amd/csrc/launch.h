@@ -32,6 +32,9 @@ inline bool raise_lds_limit() {
   return true;
 }
 
+// Regions of a workspace start at multiples of 256 bytes.
+inline size_t align256(size_t v) { return (v + 255) / 256 * 256; }
+
 enum XType { X_F32 = 0, X_BF16 = 1, X_F16 = 2 };
 
 // ---- M < 128: split-K GEMV family -------------------------------------------------------------

@@ -230,12 +230,6 @@ inline GradPlan grad_plan(int M, int N, int K, int terms) {
   return best;
 }
 
-// LDS written by other lanes of the wave is read next (or the reverse): order them.
-__device__ __forceinline__ void wave_order() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 typedef __attribute__((address_space(3))) const uint8_t lds_u8;
 typedef int i32x2 __attribute__((ext_vector_type(2)));
 
@@ -500,7 +494,7 @@ __global__ void __launch_bounds__(256, 2) grad_gemm_kernel(int M, int N, int Np,
   float* pt = partials + (size_t)b * BM * kCols + 64 * wave;            // split tile: raw sums [BM][256] for grad_finish_kernel
 #pragma unroll
   for (int i = 0; i < RB; ++i) {
-    wave_order();
+    wave_lds_fence();
 #pragma unroll
     for (int r = 0; r < 16; ++r) {
       float* e = ep + (8 * (r >> 2) + 4 * h + (r & 3)) * kEpiRow;
@@ -511,7 +505,7 @@ __global__ void __launch_bounds__(256, 2) grad_gemm_kernel(int M, int N, int Np,
         *reinterpret_cast<f32x2*>(e + 2 * li) = f32x2{acc[i][0][r], acc[i][1][r]};
       }
     }
-    wave_order();
+    wave_lds_fence();
     if (part < 0 && dx_bf) {
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -578,7 +572,6 @@ __global__ void __launch_bounds__(256) grad_finish_kernel(int M, int K, GradPlan
 }
 
 inline int terms_of(XType dxt) { return dxt == X_F32 ? 2 : 1; }
-inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 // Workspace: float16 terms [TERMS][M][Np], row scales [M], split tiles' sums.
 struct GradWs {
   size_t rs, partials, total;
@@ -586,9 +579,9 @@ struct GradWs {
 inline GradWs grad_ws(int M, int N, int K, int terms) {
   const GradPlan p = grad_plan(M, N, K, terms);
   GradWs w;
-  w.rs = up256((size_t)terms * M * p.steps * 64 * 2);
-  w.partials = w.rs + up256((size_t)M * 4);
-  w.total = w.partials + up256((size_t)p.units * p.bm * kCols * 4);
+  w.rs = align256((size_t)terms * M * p.steps * 64 * 2);
+  w.partials = w.rs + align256((size_t)M * 4);
+  w.total = w.partials + align256((size_t)p.units * p.bm * kCols * 4);
   return w;
 }
 

@@ -9,23 +9,21 @@ namespace wq {
 
 namespace {
 
-inline size_t up256(size_t v) { return (v + 255) / 256 * 256; }
-
 // Workspace: the terms of t, backward also those of dt, [3][M][R] bfloat16 each; then the parts of a split contraction, of
 // either product in turn; then, backward, those of db's and of da's rows.  x's type is not known here: the float32 need covers it.
 struct LoraWs {
   size_t dt, parts, db_parts, da_parts, total;
 };
 LoraWs lora_ws(int M, int K, int N, int E, int R, bool backward) {
-  const size_t terms = up256((size_t)3 * M * R * 2);
+  const size_t terms = align256((size_t)3 * M * R * 2);
   LoraWs w{};
   w.dt = terms;
   w.parts = terms * (backward ? 2 : 1);
   size_t p = std::max(lora_shrink_bytes(M, K, R, X_F32), lora_shrink_bytes(M, K, R, X_BF16));
   if (backward) p = std::max({p, lora_shrink_bytes(M, N, R, X_F32), lora_shrink_bytes(M, N, R, X_BF16)});
-  w.db_parts = w.parts + up256(p);
-  w.da_parts = w.db_parts + (backward ? up256(lora_outer_bytes(M, N, E, R)) : 0);
-  w.total = w.da_parts + (backward ? up256(lora_outer_bytes(M, K, E, R)) : 0);
+  w.db_parts = w.parts + align256(p);
+  w.da_parts = w.db_parts + (backward ? align256(lora_outer_bytes(M, N, E, R)) : 0);
+  w.total = w.da_parts + (backward ? align256(lora_outer_bytes(M, K, E, R)) : 0);
   return w;
 }
 

@@ -132,12 +132,6 @@ __device__ __forceinline__ f32x4 mfma_terms(const bf16x8* a, const bf16x8* b, f3
 template <int C> constexpr int tr_stride() { return C == 16 ? 32 : 2 * C + 32; }
 template <int C> constexpr int tr_plane() { return 32 * tr_stride<C>(); }
 
-// LDS written by other lanes of the wave is read next (or the reverse): order them.
-__device__ __forceinline__ void wave_lds_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 // Columns 16 c .. 16 c + 15 as an operand: lane holds column lane % 16, rows 8 (lane / 16) .. + 7.
 template <int C, int NT>
 __device__ __forceinline__ void tr_read(const uint8_t* tile, int c, bf16x8* t) {
