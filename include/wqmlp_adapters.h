@@ -102,9 +102,7 @@ int qlinear_backward(int fmt, int64_t M, int64_t N, int64_t K, const void* dy, i
  *       block.  Codes are rounded stochastically: beta2 = 0.999 moves v by far less than half a code step,
  *       which rounding to nearest would drop in every step.  x' = |x| / scale keeps its 3 (v: 2) mantissa
  *       bits after 16 random bits r are added right below them, or below 2^-6 (v: 2^-14) becomes
- *       floor(x' 2^9 + r 2^-16) 2^-9 (v: 2^16, 2^-16), but a positive v at least the smallest code, 2^-16: an
- *       element whose gradients stay below 2^-16 of its block's largest takes shorter steps than float32
- *       states give it, never longer ones (a v of zero beside an m that is not would).  r are the low (m) and high (v) 16 bits of
+ *       floor(x' 2^9 + r 2^-16) 2^-9 (v: 2^16, 2^-16).  r are the low (m) and high (v) 16 bits of
  *       mix(key + 0x9E3779B9 i) for element i of tensor j, key = mix(mix(seed + 0x9E3779B9 t) + j), with
  *       mix(h): h ^= h>>16; h *= 0x7FEB352D; h ^= h>>15; h *= 0x846CA68B; h ^= h>>16 on 32 bits (constants:
  *       C. Wellons, "Prospecting for Hash Functions", 2018).

@@ -105,7 +105,5 @@ def adamw8_states(mc, ms, vc, vs, g, t, beta1, beta2, seed, tensor, grad_scale=1
         e[pos & (amax <= most * 2.0 ** (e - 1)) & (e > -100)] -= 1
         sc = 2.0 ** e
         code = stochastic_code(np.abs(x).astype(np.float64) / sc[at], r, grid)
-        if grid is E5M2_GRID:
-            code = np.where(x > 0, np.maximum(code, 1), code)          # a positive v keeps a positive code
         out += [(code | np.where(np.signbit(x), 0x80, 0)).astype(np.uint8), sc.astype(f)]
     return out[0], out[1], out[2], out[3], m, v
