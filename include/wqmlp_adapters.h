@@ -22,6 +22,8 @@ extern "C" {
 #define WQ_LORA_MAX_RANK 256
 /* Elements per scale of the 8-bit optimizer states. */
 #define WQ_ADAMW_BLOCK 256
+/* With 8-bit optimizer states (in adamw_table_build's state_bits): a positive v keeps a positive code. */
+#define WQ_ADAMW_KEEP_V 256
 /* Tensors one AdamW table can hold. */
 #define WQ_ADAMW_MAX_TENSORS (1 << 20)
 
@@ -106,6 +108,13 @@ int qlinear_backward(int fmt, int64_t M, int64_t N, int64_t K, const void* dy, i
  *       mix(key + 0x9E3779B9 i) for element i of tensor j, key = mix(mix(seed + 0x9E3779B9 t) + j), with
  *       mix(h): h ^= h>>16; h *= 0x7FEB352D; h ^= h>>15; h *= 0x846CA68B; h ^= h>>16 on 32 bits (constants:
  *       C. Wellons, "Prospecting for Hash Functions", 2018).
+ *       A code of m reaches down to 2^-18 of its block's largest m, one of v to 2^-32 of the largest v, which is
+ *       2^-16 in gradient: below that v becomes 0 beside an m that does not, and the next step divides by
+ *       sqrt((1 - beta2) g^2) alone, many times lr where g is small.  Blocks whose gradients lie that far apart
+ *       want float32 states, or WQ_ADAMW_KEEP_V:
+ *    8 | WQ_ADAMW_KEEP_V  the same, but a v that is positive before its rounding gets at least the smallest code,
+ *       2^-16.  Elements below 2^-16 of their block's largest gradient then take shorter steps than float32 states
+ *       give them, never longer ones than those ever do.  (To adamw_run such a table is one of 8-bit states.)
  *       p takes the step with m and v before their rounding.  A state that is not finite gets a NaN code
  *       and does not count for its block's scale.
  *

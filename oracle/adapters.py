@@ -80,9 +80,9 @@ def stochastic_code(x, r, grid):
     return np.where(pos + r >= 65536, hi, lo)
 
 
-def adamw8_states(mc, ms, vc, vs, g, t, beta1, beta2, seed, tensor, grad_scale=1.0, block=256):
+def adamw8_states(mc, ms, vc, vs, g, t, beta1, beta2, seed, tensor, grad_scale=1.0, block=256, keep_v=False):
     """New 8-bit states: (m codes, m scales, v codes, v scales, m, v), m and v the float32 states before rounding.
-    The state updates are float32 operations, each rounded by itself."""
+    The state updates are float32 operations, each rounded by itself.  keep_v: a positive v keeps a positive code."""
     f = np.float32
     n = mc.size
     at = np.arange(n) // block
@@ -105,5 +105,7 @@ def adamw8_states(mc, ms, vc, vs, g, t, beta1, beta2, seed, tensor, grad_scale=1
         e[pos & (amax <= most * 2.0 ** (e - 1)) & (e > -100)] -= 1
         sc = 2.0 ** e
         code = stochastic_code(np.abs(x).astype(np.float64) / sc[at], r, grid)
+        if keep_v and grid is E5M2_GRID:
+            code = np.where(x > 0, np.maximum(code, 1), code)
         out += [(code | np.where(np.signbit(x), 0x80, 0)).astype(np.uint8), sc.astype(f)]
     return out[0], out[1], out[2], out[3], m, v

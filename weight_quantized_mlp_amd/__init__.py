@@ -20,7 +20,7 @@ __all__ = [
     "WQ_STATIC_SCRATCH_BYTES", "mlp_workspace_bytes", "mlp_fp8w_run", "mlp_fp8w_run_noalloc", "mlp_nvfp4_run", "awq_bank_bytes", "moe_awq_m1_run",
     "nvfp4_pack_block64", "awq_pack_bank", "fp8w_dequant_f32", "nvfp4_dequant_f32", "awq_dequant_f16",
     "qlinear_workspace_bytes", "qlinear_run", "wq_read_probe",
-    "WQ_LORA_MAX_RANK", "WQ_ADAMW_BLOCK", "lora_workspace_bytes", "lora_run", "lora_backward",
+    "WQ_LORA_MAX_RANK", "WQ_ADAMW_BLOCK", "WQ_ADAMW_KEEP_V", "lora_workspace_bytes", "lora_run", "lora_backward",
     "qlinear_backward_workspace_bytes", "qlinear_backward", "adamw_table_bytes", "AdamWTable", "adamw_table", "adamw_run",
 ]
 
@@ -32,6 +32,7 @@ WQ_ACT_E4M3 = 16
 WQ_STATIC_SCRATCH_BYTES = 32 << 20
 WQ_LORA_MAX_RANK = 256
 WQ_ADAMW_BLOCK = 256
+WQ_ADAMW_KEEP_V = 256
 _PATHS = {"auto": WQ_PATH_AUTO, "gemv": WQ_PATH_GEMV, "mfma": WQ_PATH_MFMA}
 _STAGES = {None: 0, "gateup": WQ_STAGE_GATEUP_ONLY, "down": WQ_STAGE_DOWN_ONLY}
 _ACTS = {None: 0, "e4m3": WQ_ACT_E4M3}
@@ -517,15 +518,18 @@ class AdamWTable:
         self.table, self.count, self.elems, self.bits, self.tensors = table, count, elems, bits, tensors
 
 
-def adamw_table(params, grads, m, v, copies=None, m_scales=None, v_scales=None):
+def adamw_table(params, grads, m, v, copies=None, m_scales=None, v_scales=None, keep_v=False):
     """Table of the tensors adamw_run steps over (lists of equal length): params f32, grads f32/bf16, states m and v
     f32, or, with m_scales and v_scales (f32, one per WQ_ADAMW_BLOCK elements), 8-bit codes (float8_e4m3fn and
     float8_e5m2, or their uint8 views); copies: bf16/f16 tensors that receive the rounded parameters (entries may be
-    None).  The table holds addresses: rebuild it when a tensor is replaced.  Waits for the current stream."""
+    None).  keep_v (8-bit states): a positive v keeps a positive code, for blocks whose gradients lie further apart than
+    2^16.  The table holds addresses: rebuild it when a tensor is replaced.  Waits for the current stream."""
     count = len(params)
     bits = 8 if m_scales is not None else 32
     if (m_scales is None) != (v_scales is None):
         raise ValueError("m_scales and v_scales come together")
+    if keep_v and bits != 8:
+        raise ValueError("keep_v is for 8-bit states")
     lists = {"grads": grads, "m": m, "v": v, "copies": copies, "m_scales": m_scales, "v_scales": v_scales}
     for name, ts in lists.items():
         if ts is not None and len(ts) != count:
@@ -555,7 +559,7 @@ def adamw_table(params, grads, m, v, copies=None, m_scales=None, v_scales=None):
             t.copy_dtype = _float_code(c.dtype, f"copies[{i}]", (torch.bfloat16, torch.float16))
             t.copy = _ptr(_need(c, f"copies[{i}]", c.dtype, dev, n))
     table = torch.empty(max(adamw_table_bytes(count), 1), dtype=torch.uint8, device=dev)
-    _check("adamw_table_build", lib().adamw_table_build(count, arr, bits, _ptr(table), table.numel(), _stream(dev)))
+    _check("adamw_table_build", lib().adamw_table_build(count, arr, bits | (WQ_ADAMW_KEEP_V if keep_v else 0), _ptr(table), table.numel(), _stream(dev)))
     torch.cuda.current_stream(dev).synchronize()      # built once: steps on any stream may follow
     keep = (list(params), list(grads), list(m), list(v), copies and list(copies), m_scales and list(m_scales),
             v_scales and list(v_scales))

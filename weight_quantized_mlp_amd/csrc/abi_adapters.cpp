@@ -17,6 +17,8 @@ namespace {
 
 using namespace wq::abi;
 
+static_assert(wq::kAdamwKeepV == WQ_ADAMW_KEEP_V, "one flag");
+
 bool is_float(int dt) { return dt == WQ_F32 || dt == WQ_BF16 || dt == WQ_F16; }
 wq::XType xtype(int dt) { return dt == WQ_F32 ? wq::X_F32 : (dt == WQ_BF16 ? wq::X_BF16 : wq::X_F16); }
 
@@ -132,12 +134,12 @@ size_t adamw_table_bytes(int64_t count) {
 
 int adamw_table_build(int64_t count, const wq_adamw_tensor* tensors, int state_bits, void* table, size_t table_bytes,
                       void* stream) try {
-  if (count <= 0 || count > WQ_ADAMW_MAX_TENSORS || (state_bits != 8 && state_bits != 32)) return WQ_EINVAL;
+  const bool b8 = state_bits == 8 || state_bits == (8 | WQ_ADAMW_KEEP_V);
+  if (count <= 0 || count > WQ_ADAMW_MAX_TENSORS || (!b8 && state_bits != 32)) return WQ_EINVAL;
   if (tensors == nullptr || table == nullptr) return WQ_EINVAL;
   const size_t need = adamw_table_bytes(count);
   if (!all_aligned({table})) return WQ_EALIGN;
   if (table_bytes < need) return WQ_EWORKSPACE;
-  const bool b8 = state_bits == 8;
   struct Span {
     uintptr_t p, end;
     bool out;

@@ -92,9 +92,9 @@ __device__ __forceinline__ int block_exp(float amax, int half) {
 }
 
 // |x| already divided by the block scale -> stochastically rounded magnitude on the code's grid (MANT mantissa
-// bits, smallest normal 2^EMIN, at most MAXV), NaN if x is not finite.  r: 16 random bits.
+// bits, smallest normal 2^EMIN, from `least` to MAXV), NaN if x is not finite.  r: 16 random bits.
 template <int MANT, int EMIN>
-__device__ __forceinline__ float round_code(float x, uint32_t r, float maxv) {
+__device__ __forceinline__ float round_code(float x, uint32_t r, float least, float maxv) {
   constexpr int DROP = 23 - MANT;
   const float mag = fabsf(x);
   const uint32_t up = ((__float_as_uint(mag) + (r << (DROP - 16))) >> DROP) << DROP;
@@ -103,7 +103,7 @@ __device__ __forceinline__ float round_code(float x, uint32_t r, float maxv) {
   const uint32_t fixed = (uint32_t)(fminf(mag, kMin) * (65536.0f / kStep));   // below 2^20: exact multiples of 2^-16 steps
   const float sub = (float)((fixed + r) >> 16) * kStep;
   float q = mag < kMin ? sub : __uint_as_float(up);
-  q = fminf(q, maxv);
+  q = fminf(fmaxf(q, least), maxv);
   q = mag <= 3.4028235e38f ? q : __uint_as_float(0x7FC00000u);
   return copysignf(q, x);
 }
@@ -194,7 +194,8 @@ __global__ void __launch_bounds__(256) adamw_kernel(const uint8_t* __restrict__ 
                                                     const float* __restrict__ lr_p, AdamwHyper h) {
   const int64_t* head = reinterpret_cast<const int64_t*>(table);
   const int64_t count = head[0], total = head[1];
-  if (head[2] != BITS) return;   // a table of the other state form: nothing is touched
+  if ((head[2] & 255) != BITS) return;   // a table of the other state form: nothing is touched
+  const float least_v = (head[2] & kAdamwKeepV) != 0 ? 0x1p-16f : 0.f;   // v's smallest code, where a positive v keeps one
   const int64_t* chunk0 = head + kAdamwHead;
   const AdamwEntry* entries = reinterpret_cast<const AdamwEntry*>(table + adamw_entries_offset(count));
   const int64_t per = total <= gridDim.x ? 1 : (total + gridDim.x - 1) / gridDim.x;   // a 64-bit division is 140 instructions
@@ -295,8 +296,8 @@ __global__ void __launch_bounds__(256) adamw_kernel(const uint8_t* __restrict__ 
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint32_t r = mix32(key + 0x9E3779B9u * (uint32_t)(i + j));
-          qm[j] = round_code<3, -6>(m[j] * im, r & 0xFFFFu, 448.f);
-          qv[j] = round_code<2, -14>(v[j] * iv, r >> 16, 57344.f);
+          qm[j] = round_code<3, -6>(m[j] * im, r & 0xFFFFu, 0.f, 448.f);
+          qv[j] = round_code<2, -14>(v[j] * iv, r >> 16, v[j] > 0.f ? least_v : 0.f, 57344.f);
         }
         int cm = __builtin_amdgcn_cvt_pk_fp8_f32(qm[0], qm[1], 0, false);
         cm = __builtin_amdgcn_cvt_pk_fp8_f32(qm[2], qm[3], cm, true);

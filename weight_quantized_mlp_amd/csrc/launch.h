@@ -125,6 +125,7 @@ struct AdamwEntry {
   void* copy;
   int32_t g_dtype, copy_dtype;
 };
+constexpr int kAdamwKeepV = 256;  // in a table's state bits: a positive 8-bit v keeps a positive code (WQ_ADAMW_KEEP_V)
 constexpr int kAdamwBatch = 32;   // entries one table launch writes (they travel as kernel arguments)
 // table: int64 {count, total chunks, state bits}, int64 chunk0[count + 1], entries
 constexpr int64_t kAdamwHead = 3;
