@@ -6,8 +6,9 @@
 // over every array is the whole plan.  The tensors are cut into chunks of kChunk elements, numbered through
 // all tensors; a workgroup takes a chunk (in huge tables a run of them), finds its tensor with a 256-way
 // search of the table's chunk starts and walks on from there, so one launch serves any number of tensors
-// of any sizes.  178M elements with float32 states take 800 us (5.8 TB/s; 837 us with
-// 2048 workgroups and a run of chunks each), 83M with 8-bit states 263 us (285 us).  A wave takes 256
+// of any sizes (chosen against 2048 workgroups with a run of chunks each at 800 us to 837 for 178M
+// elements with float32 states, 264 to 285 for 83M with 8-bit states; over several cards 800-863, 5.4-5.8
+// TB/s, and 263-282).  A wave takes 256
 // consecutive elements at a time, 4 per lane: 16-byte accesses to the float32 arrays, 4-byte accesses to
 // the codes, and a block's scale is one wave maximum.
 #include <algorithm>

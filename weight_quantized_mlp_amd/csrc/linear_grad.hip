@@ -18,8 +18,10 @@
 // stage, the copies for two steps ahead follow it, and the first fragments of the next step are read behind the
 // last MFMAs of this one.  Two workgroups share a CU.
 //
-// The matrix cores bound it: NVFP4 4096 x 5120 -> 17408 takes 690 us (1.06 PFLOP/s; a float16 product of those sizes in the
-// library 635), FP8 512 x 17408 -> 5120 85 us (1.07 PFLOP/s) and 20 for the kernels before and after it.  MFMAs are busy in
+// The matrix cores bound it.  Calls in a row, bfloat16 dx: NVFP4 4096 x 5120 -> 17408 690-720 us (1.01-1.06 PFLOP/s; a float16
+// product of those sizes in the library 635), FP8 512 x 17408 -> 5120 107-110 us, of which the GEMM 85-87 (1.05-1.07 PFLOP/s) and
+// the kernels before and after it 20.  float32 dx, twice the MFMAs: NVFP4 2048 x 5120 -> 17408 685 us (1.07 PFLOP/s in MFMAs), FP8
+// 512 x 17408 -> 5120 193 us.  In the first two MFMAs are busy in
 // 55% and 59% of the busy CUs' cycles; 5.9 and 3.3 VALU instructions per MFMA (the decode) and the weights' LDS reads take turns
 // with them.
 //

@@ -7,8 +7,9 @@
 // next strip in flight during this strip's MFMAs; there is no barrier.  The sums leave the MFMAs a row per lane; adding
 // and storing them that way would touch a cache line per lane, so they pass through LDS of the wave's own and meet base
 // in whole lines (16 lanes on 256 consecutive bytes of a row).  A tile whose rows name several adapters is computed once
-// per adapter, each storing its own rows; rows without an adapter are copied by the first.  4099 rows x 17408, rank 64: 129 us
-// (571 MB, 4.4 TB/s; with the products taken out 113); 2047 rows x 17408 bfloat16 (dx), rank 32: 41 us.
+// per adapter, each storing its own rows; rows without an adapter are copied by the first.  Shortest and mean of 20 calls:
+// 4099 rows x 17408, rank 64: 129 and 137 us (571 MB, 4.2-4.4 TB/s; with the products taken out 113); 2047 rows x 17408 bfloat16
+// (dx), rank 32: 41 and 44 us.
 //
 // Few rows (decode): see lora_expand_rows_kernel.
 #include <algorithm>

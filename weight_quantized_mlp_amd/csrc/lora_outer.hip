@@ -10,8 +10,9 @@
 // the same one (a tile per term left room for two workgroups on a CU at rank 32, one at rank 64); the next block's loads
 // are issued before this block's MFMAs.  Long batches with few adapters split the rows over up to 8 workgroups, joined in
 // order by a second kernel.  da and db of a backward pass share a launch where x and dy have one type and both take as many waves,
-// and always the second kernel's.  4096 x 17408 float32 (db, rank 16): 62 us (4.6 TB/s); da and db of 2047 x (17408 + 5120) bfloat16, rank 32 on 5
-// adapters: 32 us, and 31 with all operands cached: its 2112 short workgroups bound it, not memory.
+// and always the second kernel's.  Shortest and mean of 20 calls: 4096 x 17408 float32 (db,
+// rank 16) 62 and 66 us (4.3-4.6 TB/s); da and db of 2047 x (17408 + 5120) bfloat16, rank 32 on 5 adapters 32 and 34 us, and 31
+// with all operands cached: its 2112 short workgroups bound it, not memory.
 #include <algorithm>
 
 #include "lora_common.h"
