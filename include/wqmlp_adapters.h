@@ -77,7 +77,7 @@ int lora_backward(int64_t M, int64_t K, int64_t N, int64_t E, int64_t R, const v
  * fmt, w, scale and global_scale as for qlinear_run.  dy [M,N]: WQ_F32 or WQ_BF16; dx [M,K]: dx_dtype,
  * WQ_F32 or WQ_BF16.  K: a multiple of 16 (FP8) or 64 (NVFP4); N: any.
  * Each row of dy (FP8: times scale[n], one float32 rounding) is scaled by a power of two so that its
- * largest finite magnitude lies in [2^14, 2^15) (a row below 2^-112: by 2^126) and enters float16 MFMAs.
+ * largest finite magnitude lies in [2^14, 2^15) and enters float16 MFMAs (a row below 2^-112 as one of 2^-112).
  * dx bfloat16: rounded once to float16; an element is off by at most 2^-11 of itself (dx's own rounding is
  * 2^-8) or 2^-39 of its row's largest, whichever is more.  dx float32: as two float16 terms; 2^-22 of the
  * element or 2^-51 of the row's largest.  A caller who wants more than float16 holds of dy in a bfloat16 dx
@@ -101,7 +101,7 @@ int qlinear_backward(int fmt, int64_t M, int64_t N, int64_t K, const void* dy, i
  *    8  blocks of WQ_ADAMW_BLOCK consecutive elements (the last may be short) with one power-of-two float32
  *       scale each: m = m_scale * E4M3 code, v = v_scale * E5M2 code, sign bit unused.  The new block scale
  *       is the smallest 2^e (e in [-100, 100]) with max |m| <= 448 * 2^e (v: 57344 * 2^e), 1 for a zero
- *       block.  Codes are rounded stochastically: beta2 = 0.999 moves v by far less than half a code step,
+ *       block; what even 2^100 leaves above the largest code takes that code.  Codes are rounded stochastically: beta2 = 0.999 moves v by far less than half a code step,
  *       which rounding to nearest would drop in every step.  x' = |x| / scale keeps its 3 (v: 2) mantissa
  *       bits after 16 random bits r are added right below them, or below 2^-6 (v: 2^-14) becomes
  *       floor(x' 2^9 + r 2^-16) 2^-9 (v: 2^16, 2^-16).  r are the low (m) and high (v) 16 bits of
@@ -115,8 +115,8 @@ int qlinear_backward(int fmt, int64_t M, int64_t N, int64_t K, const void* dy, i
  *    8 | WQ_ADAMW_KEEP_V  the same, but a v that is positive before its rounding gets at least the smallest code,
  *       2^-16.  Elements below 2^-16 of their block's largest gradient then take shorter steps than float32 states
  *       give them, never longer ones than those ever do.  (To adamw_run such a table is one of 8-bit states.)
- *       p takes the step with m and v before their rounding.  A state that is not finite gets a NaN code
- *       and does not count for its block's scale.
+ * In both 8-bit forms p takes the step with m and v before their rounding, and a state that is not finite gets
+ * a NaN code and does not count for its block's scale.
  *
  * The tensors' addresses live in a table in device memory that is built once:
  *   adamw_table_build fills `table` (adamw_table_bytes(count) bytes) from `tensors`, a HOST array of count
@@ -124,8 +124,9 @@ int qlinear_backward(int fmt, int64_t M, int64_t N, int64_t K, const void* dy, i
  *   in use, must not overlap, and n == 0 is allowed.  Rebuild it when a gradient buffer moves.
  *   adamw_run takes one step over the table's tensors.  step (int64, >= 1) and lr (float32) are read from
  *   device memory, so that a captured graph can be replayed over many steps.  elems: the sum of n, which
- *   sizes the launch (0: an empty call) and nothing else.  A table built for the other state_bits is left untouched.  Steps
- *   over the same tensors must not run at the same time, nor before the build that wrote the table.
+ *   sizes the launch (0: an empty call) and nothing else.  A table built for the other state_bits is left
+ *   untouched.  Steps over the same tensors must not run at the same time, nor before the build that wrote
+ *   the table.
  */
 typedef struct {
   int64_t n;        /* elements */

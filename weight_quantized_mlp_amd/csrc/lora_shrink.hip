@@ -10,7 +10,8 @@
 // the adapter's rows are loaded and written).  Where few tiles have a long contraction, it is split over up to 8
 // workgroups and lora_terms_kernel adds their parts in order.  Shortest and mean of 20 calls: 4096 x 17408 float32, rank 16: 46
 // and 48 us (6.0-6.2 TB/s, a part of it from the last-level cache); 4099 x 5120 bfloat16, rank 64: 18 and 20 us; 2047 x 17408
-// bfloat16, rank 32: 21 and 24 us (3.0-3.3 TB/s).  Short ones are a launch's latency (5 us at 256 columns) and the few CUs that 32-row tiles occupy.
+// bfloat16, rank 32: 21 and 24 us (3.0-3.3 TB/s).  Short ones are a launch's latency (5 us at 256 columns) and the few CUs that
+// 32-row tiles occupy.
 //
 // Few rows (decode): one wave per row and rank, plain float32 products; see lora_shrink_rows_kernel.
 #include <algorithm>
