@@ -1,0 +1,66 @@
+/*
+ * wqmlp_blocks.h -- C ABI of libwqmlp, third part: what stands around the MLP in a block.  The norms before and
+ * after it with its gate and residual, forward and backward.
+ *
+ * The conventions of wqmlp.h hold for every call here: device pointers of the current device, 16-byte
+ * aligned, dense row-major; nothing is allocated or synchronised and every call can be captured into a
+ * hipGraph; argument errors are found before anything is enqueued; the same return codes.  Calls that may
+ * run at the same time (streams, threads, captured graphs) need workspaces of their own.  Sums are float32
+ * (float64 where said) in an order fixed by the shape, so a call's results are reproducible bit for bit.
+ */
+#ifndef WQMLP_BLOCKS_H
+#define WQMLP_BLOCKS_H
+
+#include "wqmlp.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/*
+ * What stands between one block (an MLP, say) and the next: the norm of the block's result, its gate and
+ * residual scale, the residual stream and the norm before the next block, row by row:
+ *   norm(t; w)[m,i] = t[m,i] / sqrt(mean_i t[m,i]^2 + eps) * (offset + w[i])
+ *   p = norm(y; post), or y where post is NULL
+ *   h_out[m,i] = h[m,i] + alpha * gate[m / (M/G), i] * p[m,i]         (h itself where y is NULL)
+ *   x[m,i] = norm(h_out; pre), of h_out as it is stored (rounded to h_dtype)
+ *   h, h_out [M, H]  h_dtype: the residual stream; h_out may be h itself, and is NULL where y is
+ *   y        [M, H]  y_dtype: the block's result, or NULL (only the norm before a block)
+ *   post, pre [H]    w_dtype: the norms' weights (offset 1: weights stored as their distance from one); pre NULL:
+ *                    no second norm (x is then NULL, too)
+ *   gate     [G, H]  g_dtype, or NULL for one; G divides M, and gate row j serves the M/G rows from j M/G on:
+ *                    G = 1 a gate per channel, G = M one for every element, between them one per sequence
+ *   x        [M, H]  x_dtype: the next block's input
+ * All types: WQ_F32, WQ_BF16 or WQ_F16 (the type of an absent tensor is ignored).  H: a multiple of 8.  eps >= 0.  Arithmetic is float32, rounded once to h_out
+ * and once to x.  M == 0 is a valid empty call.
+ */
+int block_norm_run(int64_t M, int64_t H, const void* h, int h_dtype, const void* y, int y_dtype, const void* post,
+                   const void* pre, int w_dtype, const void* gate, int64_t G, int g_dtype, float alpha, float offset,
+                   float eps, void* h_out, void* x, int x_dtype, void* stream);
+
+/*
+ * The gradients of block_norm_run.  h is the stream after the block (h_out as block_norm_run stored it), y as there;
+ * dh = dL/dh_out from later uses of the stream [M, H] h_dtype (NULL: zeros), dx = dL/dx [M, H] x_dtype (NULL with
+ * pre NULL).  With r(t) = 1 / sqrt(mean t^2 + eps), n(t) = t r(t), w+ = offset + w:
+ *   du = dh + r(h) (dn - n(h) mean_i(dn n(h))),  dn = dx pre+            dh_in = du   (h_dtype)
+ *   dpre = sum_m dx n(h)                                                (float32 [H])
+ *   dgate[g] = sum over the gate row's rows of alpha du p               (float32 [G, H])
+ *   dp = alpha gate du;  dpost = sum_m dp n(y)                          (float32 [H])
+ *   dy = r(y) (dp post+ - n(y) mean_i(dp post+ n(y))), or dp where post is NULL     (y_dtype)
+ * Each output may be NULL and is then not written; at least one is not.  dh_in may be dh itself.  An output whose
+ * input is NULL (dy, dgate, dpost without y; dpost without post; dgate without gate; dpre without pre) is
+ * WQ_EINVAL.  Sums over rows are float32, in an order fixed by M, H and G.
+ * M == 0 writes the weights' gradients, where given, with zeros.
+ */
+size_t block_norm_backward_workspace_bytes(int64_t M, int64_t H, int64_t G);
+int block_norm_backward(int64_t M, int64_t H, const void* h, int h_dtype, const void* y, int y_dtype, const void* dh,
+                        const void* dx, int x_dtype, const void* post, const void* pre, int w_dtype, const void* gate,
+                        int64_t G, int g_dtype, float alpha, float offset, float eps, void* workspace,
+                        size_t workspace_bytes, void* dh_in, void* dy, float* dpost, float* dgate, float* dpre,
+                        void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* WQMLP_BLOCKS_H */

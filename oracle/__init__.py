@@ -37,5 +37,6 @@ from .moe import moe_awq_m1_ref, moe_w13_stage_ref, moe_w2_stage_ref, moe_brutef
 from .metric import normwise_rel_err
 from .adapters import (lora_ref, lora_backward_ref, adamw_ref, adamw8_states, adamw_random_bits, stochastic_code,
                        E4M3_GRID, E5M2_GRID)
+from .blocks import block_norm_ref, block_norm_backward_ref, gate_rows, norm_ref
 
 __all__ = [n for n in dir() if not n.startswith("_")]

@@ -1,4 +1,4 @@
-"""Python binding of libwqmlp (the C ABI declared in include/wqmlp.h and include/wqmlp_adapters.h).
+"""Python binding of libwqmlp (the C ABI declared in include/wqmlp.h, include/wqmlp_adapters.h and include/wqmlp_blocks.h).
 
 Argument marshalling only: torch tensors provide device memory and the
 current HIP stream; every step of the computation runs in the library's
@@ -22,6 +22,7 @@ __all__ = [
     "qlinear_workspace_bytes", "qlinear_run", "wq_read_probe",
     "WQ_LORA_MAX_RANK", "WQ_ADAMW_BLOCK", "WQ_ADAMW_KEEP_V", "lora_workspace_bytes", "lora_run", "lora_backward",
     "qlinear_backward_workspace_bytes", "qlinear_backward", "adamw_table_bytes", "AdamWTable", "adamw_table", "adamw_run",
+    "block_norm_run", "block_norm_backward_workspace_bytes", "block_norm_backward",
 ]
 
 WQ_F32, WQ_BF16, WQ_F16 = 0, 1, 2
@@ -74,6 +75,10 @@ _SIGS = {
     "adamw_table_bytes": (_SZ, [_I64]),
     "adamw_table_build": (_INT, [_I64, _P, _INT, _P, _SZ, _P]),
     "adamw_run": (_INT, [_I64, _I64, _INT, _P, _P, _P, _D, _D, _D, _D, _F, ctypes.c_uint32, _P]),
+    "block_norm_run": (_INT, [_I64, _I64, _P, _INT, _P, _INT, _P, _P, _INT, _P, _I64, _INT, _F, _F, _F, _P, _P, _INT, _P]),
+    "block_norm_backward_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
+    "block_norm_backward": (_INT, [_I64, _I64, _P, _INT, _P, _INT, _P, _P, _INT, _P, _P, _INT, _P, _I64, _INT, _F, _F, _F,
+                                   _P, _SZ, _P, _P, _P, _P, _P, _P]),
 }
 
 
@@ -575,3 +580,118 @@ def adamw_run(table, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.
     rc = lib().adamw_run(table.count, table.elems, table.bits, _ptr(table.table), _ptr(step), _ptr(lr), beta1, beta2, eps,
                          weight_decay, grad_scale, seed & 0xFFFFFFFF, _stream(dev))
     _check("adamw_run", rc)
+
+
+def _norm_args(h, y, post, gate, pre):
+    """Checks shared by block_norm_run and its backward call; (M, H, G, h code, y code, weight code, gate code)."""
+    dev = h.device
+    if h.dim() != 2:
+        raise ValueError("h must be [M, H]")
+    M, H = h.shape
+    ht = _float_code(h.dtype, "h")
+    _want(h, "h", h.dtype, dev, M * H)
+    yt = wt = gt = 0
+    G = 1
+    if y is None:
+        if post is not None or gate is not None:
+            raise ValueError("post and gate need y")
+        if pre is None:
+            raise ValueError("neither y nor pre: nothing to do")
+    else:
+        yt = _float_code(y.dtype, "y")
+        _want(y, "y", y.dtype, dev, M * H)
+    if post is not None or pre is not None:
+        first = post if post is not None else pre
+        wt = _float_code(first.dtype, "post and pre")
+        for t, name in ((post, "post"), (pre, "pre")):
+            if t is not None:
+                _want(t, name, first.dtype, dev, H)
+    if gate is not None:
+        gt = _float_code(gate.dtype, "gate")
+        if gate.dim() == 2:
+            G = gate.shape[0]
+        if G == 0 or M % G:
+            raise ValueError(f"gate must be [G, H] with G a divisor of the {M} rows, has {G} rows")
+        _want(gate, "gate", gate.dtype, dev, G * H)
+    return M, H, G, ht, yt, wt, gt
+
+
+def block_norm_run(h, y=None, post=None, gate=None, alpha=1.0, pre=None, eps=1e-6, offset=0.0, x_dtype=None, h_out=None,
+                   x=None):
+    """h_out = h + alpha * gate * norm(y; post) and x = norm(h_out; pre), what stands between one block and the next;
+    norm(t; w) = t / sqrt(mean(t^2) + eps) * (offset + w).
+
+    h [M,H] (the residual stream) and y [M,H] (a block's result) f32/bf16/f16; post and pre [H] of one float type; gate
+    [G,H], G a divisor of M (row j for the M/G rows from j M/G on), or [H].  Without post, y enters as it is; without y
+    only the norm before a block is taken (h_out is h); without pre no x (None).  x of x_dtype (default h's type), h_out of
+    h's type (may be h: in place).  Returns (h_out, x)."""
+    M, H, G, ht, yt, wt, gt = _norm_args(h, y, post, gate, pre)
+    dev = h.device
+    xt = 0
+    if pre is not None:
+        want = _result_dtype("x_dtype", x_dtype, h.dtype, x=x)
+        xt = _float_code(want, "x")
+        if x is None:
+            x = torch.empty((M, H), dtype=want, device=dev)
+        else:
+            _want(x, "x", want, dev, M * H)
+    elif x is not None or x_dtype is not None:
+        raise ValueError("x and x_dtype need pre")
+    if y is not None:
+        if h_out is None:
+            h_out = torch.empty((M, H), dtype=h.dtype, device=dev)
+        else:
+            _want(h_out, "h_out", h.dtype, dev, M * H)
+    elif h_out is not None:
+        raise ValueError("h_out needs y")
+    rc = lib().block_norm_run(M, H, _ptr(h), ht, _ptr(y), yt, _ptr(post), _ptr(pre), wt, _ptr(gate), G, gt, alpha, offset, eps,
+                              _ptr(h_out), _ptr(x), xt, _stream(dev))
+    _check("block_norm_run", rc)
+    return (h if y is None else h_out), x
+
+
+def block_norm_backward_workspace_bytes(M, H, G=1):
+    return lib().block_norm_backward_workspace_bytes(M, H, G)
+
+
+def block_norm_backward(h, y=None, dh=None, dx=None, post=None, gate=None, alpha=1.0, pre=None, eps=1e-6, offset=0.0,
+                        dh_in=None, dy=None, dpost=None, dgate=None, dpre=None, workspace=None,
+                        need=(True, True, True, True, True)):
+    """Gradients of block_norm_run: (dh, dy, dpost, dgate, dpre).  h: the stream after the block (h_out of the forward call,
+    or h itself without y); dh: the gradient of h_out from its later uses (None: zeros), of h's type; dx: that of x (with
+    pre).  The first result is the gradient of the stream before the block, of h's type (dh_in may be dh: in place); dy of
+    y's type; dpost, dpre [H] and dgate [G,H] (or [H] like gate) float32.  need: which of them to compute, where their
+    inputs are there (others None)."""
+    M, H, G, ht, yt, wt, gt = _norm_args(h, y, post, gate, pre)
+    dev = h.device
+    if dh is not None:
+        _want(dh, "dh", h.dtype, dev, M * H)
+    if (dx is None) != (pre is None):
+        raise ValueError("dx and pre come together")
+    xt = 0
+    if dx is not None:
+        xt = _float_code(dx.dtype, "dx")
+        _want(dx, "dx", dx.dtype, dev, M * H)
+    f32 = torch.float32
+    outs = []
+    for t, name, src, shape, dtype, wanted in (
+            (dh_in, "dh_in", h, (M, H), h.dtype, need[0]), (dy, "dy", y, (M, H), y is not None and y.dtype, need[1]),
+            (dpost, "dpost", post, (H,), f32, need[2]), (dgate, "dgate", gate, gate is not None and gate.shape, f32, need[3]),
+            (dpre, "dpre", pre, (H,), f32, need[4])):
+        if src is None or not wanted:
+            if t is not None:
+                raise ValueError(f"{name} is given, but not computed")
+            outs.append(None)
+            continue
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=dev)
+        else:
+            _want(t, name, dtype, dev, src.numel())
+        outs.append(t)
+    nb = block_norm_backward_workspace_bytes(M, H, G)
+    ws = _workspace(nb, dev, workspace) if nb else None
+    rc = lib().block_norm_backward(M, H, _ptr(h), ht, _ptr(y), yt, _ptr(dh), _ptr(dx), xt, _ptr(post), _ptr(pre), wt,
+                                   _ptr(gate), G, gt, alpha, offset, eps, _ptr(ws), 0 if ws is None else ws.numel(),
+                                   *(_ptr(t) for t in outs), _stream(dev))
+    _check("block_norm_backward", rc)
+    return tuple(outs)

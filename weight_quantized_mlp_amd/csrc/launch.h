@@ -140,6 +140,19 @@ hipError_t launch_adamw(int64_t count, int64_t elems, int bits, const void* tabl
                         double beta1, double beta2, double eps, double weight_decay, float grad_scale, uint32_t seed,
                         hipStream_t st);
 
+// ---- norms around a block (include/wqmlp_blocks.h) --------------------------------------------------
+struct BlockNorm {
+  const void *h, *y, *post, *pre, *gate;   // y, post, pre, gate: null where absent
+  XType ht, yt, wt, gt;
+  int G;                                   // gate rows, a divisor of M (1 without a gate)
+  float alpha, offset, eps;
+};
+hipError_t launch_block_norm(int M, int H, const BlockNorm& n, void* h_out, void* x, XType xt, hipStream_t st);
+size_t block_norm_grad_scratch_bytes(int M, int H, int G);
+// dh may be null (zeros); every output may be null.  M may be 0 (the weights' gradients become zeros).
+hipError_t launch_block_norm_grad(int M, int H, const BlockNorm& n, const void* dh, const void* dx, XType xt, void* ws,
+                                  void* dh_in, void* dy, float* dpost, float* dgate, float* dpre, hipStream_t st);
+
 // ---- packers and debug decoders -------------------------------------------------------------
 hipError_t launch_nvfp4_pack(int64_t N, int64_t K, const uint8_t* wp, const uint8_t* ws, uint8_t* blk,
                              hipStream_t st);
