@@ -1,6 +1,7 @@
 /*
- * wqmlp_blocks.h -- C ABI of libwqmlp, third part: what stands around the MLP in a block.  The norms before and
- * after it with its gate and residual, forward and backward.
+ * wqmlp_blocks.h -- C ABI of libwqmlp, third part: blocks with 4-bit weights and what stands around them.  The
+ * linear with AWQ int4 group-32 weights, and the norms before and after a block with its gate and residual,
+ * forward and backward.
  *
  * The conventions of wqmlp.h hold for every call here: device pointers of the current device, 16-byte
  * aligned, dense row-major; nothing is allocated or synchronised and every call can be captured into a
@@ -16,6 +17,24 @@
 #ifdef __cplusplus
 extern "C" {
 #endif
+
+/*
+ * Linear with AWQ int4 group-32 weights:
+ *   y[m,n] = sum_k x[m,k] dq[n,k],   dq = RN_f16(fma(q, scale, RN_f16(-zero * scale))) as in moe_awq_m1_run
+ *   x     [M, K]  WQ_F32, WQ_BF16 or WQ_F16
+ *   bank          one expert's [N, K] weights: awq_pack_bank / awq_bank_bytes with E = 1 (an expert of a larger
+ *                 bank starts at a multiple of awq_bank_bytes(1, N, K, meta_layout)); meta_layout 3 or 4
+ *   y     [M, N]  float32
+ * K: a multiple of 32; N and M: any.  The products are exact in float32 and summed there: weights are float16
+ * values, float16 x enters as it is, bfloat16 and float32 rows are scaled by a power of two so that their
+ * largest finite magnitude lies in [2^14, 2^15) and enter as one (bfloat16) or two (float32) float16 terms: a
+ * bfloat16 element is off by at most 2^-39 of its row's largest, a float32 one by 2^-22 of itself or 2^-39 of its
+ * row's largest, whichever is more.  A row's result does not depend on the other rows' values; NaN and infinities
+ * stay in their row.  M == 0 is a valid empty call.
+ */
+size_t awq_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int x_dtype);
+int awq_linear_run(int64_t M, int64_t N, int64_t K, const void* x, int x_dtype, const void* bank, int meta_layout,
+                   void* workspace, size_t workspace_bytes, float* y, void* stream);
 
 /*
  * What stands between one block (an MLP, say) and the next: the norm of the block's result, its gate and

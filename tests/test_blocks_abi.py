@@ -95,3 +95,32 @@ def test_norm_backward_without_rows(L):
     none = dict(M=0, h=None, y=None, dh=None, dx=None, dhi=None, dy=None, ws=None, wsb=0)
     assert L.block_norm_backward(*ngrad_args(**none, dpost=None, dgate=None, dpre=None)) == 0
     assert L.block_norm_backward(*ngrad_args(**none, pre=None)) == EINVAL
+
+
+LIN = ("M", "N", "K", "x", "xt", "bank", "layout", "ws", "wsb", "y")
+
+
+def lin_args(**kw):
+    a = dict(M=4, N=48, K=64, x=A, xt=1, bank=A + MB, layout=3, ws=A + 2 * MB, wsb=MB, y=A + 3 * MB)
+    a.update(kw)
+    return [a[k] for k in LIN] + [None]
+
+
+@pytest.mark.parametrize("kw,rc", [
+    (dict(x=None), EINVAL), (dict(bank=None), EINVAL), (dict(y=None), EINVAL), (dict(xt=3), EINVAL), (dict(xt=-1), EINVAL),
+    (dict(layout=2), EINVAL), (dict(M=-1), EINVAL), (dict(N=0), EINVAL), (dict(K=48), EINVAL), (dict(K=0), EINVAL),
+    (dict(M=(1 << 23) + 1), EINVAL), (dict(N=(1 << 23) + 1), EINVAL), (dict(M=1 << 23, N=1 << 14), EINVAL),
+    (dict(x=A + 8), EALIGN), (dict(bank=A + MB + 4), EALIGN), (dict(y=A + 3 * MB + 4), EALIGN), (dict(ws=A + 2 * MB + 1), EALIGN),
+    (dict(ws=None), EWORKSPACE), (dict(wsb=64), EWORKSPACE),
+    (dict(y=A), EOVERLAP), (dict(y=A + MB + 1024), EOVERLAP), (dict(ws=A), EOVERLAP), (dict(ws=A + 3 * MB), EOVERLAP),
+])
+def test_awq_linear_refusals(L, kw, rc):
+    assert L.awq_linear_run(*lin_args(**kw)) == rc
+
+
+def test_awq_linear_empty_calls(L):
+    assert L.awq_linear_run(*lin_args(M=0, x=None, y=None, ws=None, wsb=0)) == 0
+    assert L.awq_linear_run(*lin_args(M=0, bank=None)) == EINVAL
+    assert L.awq_linear_workspace_bytes(0, 48, 64, 0) == 0
+    assert L.awq_linear_workspace_bytes(4, 48, 48, 0) == 0
+    assert L.awq_linear_workspace_bytes(4, 48, 64, 3) == 0

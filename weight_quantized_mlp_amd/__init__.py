@@ -22,7 +22,7 @@ __all__ = [
     "qlinear_workspace_bytes", "qlinear_run", "wq_read_probe",
     "WQ_LORA_MAX_RANK", "WQ_ADAMW_BLOCK", "WQ_ADAMW_KEEP_V", "lora_workspace_bytes", "lora_run", "lora_backward",
     "qlinear_backward_workspace_bytes", "qlinear_backward", "adamw_table_bytes", "AdamWTable", "adamw_table", "adamw_run",
-    "block_norm_run", "block_norm_backward_workspace_bytes", "block_norm_backward",
+    "awq_linear_workspace_bytes", "awq_linear_run", "block_norm_run", "block_norm_backward_workspace_bytes", "block_norm_backward",
 ]
 
 WQ_F32, WQ_BF16, WQ_F16 = 0, 1, 2
@@ -75,6 +75,8 @@ _SIGS = {
     "adamw_table_bytes": (_SZ, [_I64]),
     "adamw_table_build": (_INT, [_I64, _P, _INT, _P, _SZ, _P]),
     "adamw_run": (_INT, [_I64, _I64, _INT, _P, _P, _P, _D, _D, _D, _D, _F, ctypes.c_uint32, _P]),
+    "awq_linear_workspace_bytes": (_SZ, [_I64, _I64, _I64, _INT]),
+    "awq_linear_run": (_INT, [_I64, _I64, _I64, _P, _INT, _P, _INT, _P, _SZ, _P, _P]),
     "block_norm_run": (_INT, [_I64, _I64, _P, _INT, _P, _INT, _P, _P, _INT, _P, _I64, _INT, _F, _F, _F, _P, _P, _INT, _P]),
     "block_norm_backward_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
     "block_norm_backward": (_INT, [_I64, _I64, _P, _INT, _P, _INT, _P, _P, _INT, _P, _P, _INT, _P, _I64, _INT, _F, _F, _F,
@@ -580,6 +582,32 @@ def adamw_run(table, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.
     rc = lib().adamw_run(table.count, table.elems, table.bits, _ptr(table.table), _ptr(step), _ptr(lr), beta1, beta2, eps,
                          weight_decay, grad_scale, seed & 0xFFFFFFFF, _stream(dev))
     _check("adamw_run", rc)
+
+
+def awq_linear_workspace_bytes(M, N, K, x_dtype=torch.float32):
+    return lib().awq_linear_workspace_bytes(M, N, K, _FLOATS[x_dtype])
+
+
+def awq_linear_run(x, bank, N, meta_layout=3, out=None, workspace=None):
+    """y = x dq(W)^T with AWQ int4 group-32 weights.  x [M,K] f32/bf16/f16; bank: the [N,K] weights as awq_pack_bank lays
+    them out (E = 1); y [M,N] f32."""
+    dev = x.device
+    if x.dim() != 2:
+        raise ValueError("x must be [M, K]")
+    M, K = x.shape
+    xt = _float_code(x.dtype, "x")
+    _want(x, "x", x.dtype, dev, M * K)
+    _want(bank, "bank", torch.uint8, dev, awq_bank_bytes(1, N, K, meta_layout))
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.float32, device=dev)
+    else:
+        _want(out, "out", torch.float32, dev, M * N)
+    nb = awq_linear_workspace_bytes(M, N, K, x.dtype)
+    ws = _workspace(nb, dev, workspace) if nb else None
+    rc = lib().awq_linear_run(M, N, K, _ptr(x), xt, _ptr(bank), meta_layout, _ptr(ws), 0 if ws is None else ws.numel(),
+                              _ptr(out), _stream(dev))
+    _check("awq_linear_run", rc)
+    return out
 
 
 def _norm_args(h, y, post, gate, pre):

@@ -16,6 +16,11 @@ using namespace wq::abi;
 bool is_float(int dt) { return dt == WQ_F32 || dt == WQ_BF16 || dt == WQ_F16; }
 wq::XType xtype(int dt) { return dt == WQ_F32 ? wq::X_F32 : (dt == WQ_BF16 ? wq::X_BF16 : wq::X_F16); }
 
+bool awq_shape_ok(int64_t M, int64_t N, int64_t K) {
+  return M >= 0 && M <= kMaxDim && N > 0 && N <= kMaxDim && K > 0 && K <= kMaxDim && K % 32 == 0 &&
+         M * (N > K ? N : K) <= kMaxElems;
+}
+
 bool norm_shape_ok(int64_t M, int64_t H, int64_t G) {
   return M >= 0 && M <= kMaxDim && H > 0 && H <= kMaxDim && H % 8 == 0 && G > 0 && G <= kMaxDim && M % G == 0 &&
          M * H <= kMaxElems && G * H <= kMaxElems;
@@ -43,6 +48,29 @@ size_t bytes_of(const void* p, int64_t n, int dt) { return p == nullptr ? 0 : (s
 }  // namespace
 
 extern "C" {
+
+size_t awq_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int x_dtype) {
+  if (!awq_shape_ok(M, N, K) || !is_float(x_dtype)) return 0;
+  return wq::awq_linear_scratch_bytes((int)M, (int)N, (int)K, xtype(x_dtype));
+}
+
+int awq_linear_run(int64_t M, int64_t N, int64_t K, const void* x, int x_dtype, const void* bank, int meta_layout,
+                   void* workspace, size_t workspace_bytes, float* y, void* stream) {
+  if (!awq_shape_ok(M, N, K) || !is_float(x_dtype) || (meta_layout != 3 && meta_layout != 4)) return WQ_EINVAL;
+  if (bank == nullptr) return WQ_EINVAL;
+  if (M == 0) return WQ_OK;
+  if (any_null({x, y})) return WQ_EINVAL;
+  if (!all_aligned({x, bank, workspace, y})) return WQ_EALIGN;
+  const size_t need = awq_linear_workspace_bytes(M, N, K, x_dtype);
+  if (need && (workspace == nullptr || workspace_bytes < need)) return WQ_EWORKSPACE;
+  if (any_overlap({{y, (size_t)M * N * 4}, {workspace, need}},
+                  {{x, (size_t)M * K * xsize(x_dtype)}, {bank, awq_bank_bytes(1, N, K, meta_layout)}}))
+    return WQ_EOVERLAP;
+  const int rc = check_device({x, bank, need ? workspace : nullptr, y});
+  if (rc != WQ_OK) return rc;
+  return launched(wq::launch_awq_linear((int)M, (int)N, (int)K, x, xtype(x_dtype), static_cast<const uint8_t*>(bank), meta_layout,
+                                        workspace, y, reinterpret_cast<hipStream_t>(stream)));
+}
 
 int block_norm_run(int64_t M, int64_t H, const void* h, int h_dtype, const void* y, int y_dtype, const void* post,
                    const void* pre, int w_dtype, const void* gate, int64_t G, int g_dtype, float alpha, float offset,

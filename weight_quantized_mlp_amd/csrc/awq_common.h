@@ -1,0 +1,110 @@
+// Shared by the kernels that multiply rows with AWQ int4 group-32 weights on the matrix cores (awq_linear.hip,
+// moe_layer.hip).
+//
+// One MFMA (16 x 16 x 32, float16) takes 8 contraction elements from each lane: lane l holds row l % 16 of the weights and
+// the octet l / 16 of the step.  Which k an octet's place stands for is free as long as both operands agree, so the weights
+// stay as they are packed: a step is 4 groups of 32 k, lane quarter l / 16 holds one whole group (16 bytes of codes, one
+// scale, one zero), and MFMA i of the step takes the group's dword i.  A dword decodes into the pairs (k, k + 4), so the
+// activations' octets are stored in the order 0 4 1 5 2 6 3 7.
+#pragma once
+#include "dev_common.h"
+#include "launch.h"
+
+namespace wq {
+
+constexpr int kStepK = 128;             // contraction elements of a step: 4 groups
+
+
+// 8 weights of one dword, in the order above.
+__device__ __forceinline__ f16x8 awq_frag(uint32_t w, f16x2 s2, f16x2 b2, const AwqDecode& dc) {
+  f16x2 p[4];
+  awq_quad(w, s2, b2, dc, p);
+  return f16x8{p[0].x, p[0].y, p[1].x, p[1].y, p[2].x, p[2].y, p[3].x, p[3].y};
+}
+
+// A lane's share of one step of 16 weight rows: raw, so that every load is issued before any is used.
+struct AwqStep {
+  u32x4 c;
+  uint32_t s, z;
+};
+// Row `row` (clamped by the caller), group g; groups past the row's end read its last one and count as zero weights.
+template <int ML>
+__device__ __forceinline__ AwqStep awq_load(const uint8_t* codes, const uint8_t* expert, const AwqLayout& L, int64_t row, int g) {
+  const int gc = min(g, (int)L.G - 1);
+  AwqStep r;
+  r.c = *reinterpret_cast<const u32x4*>(codes + 16 * gc);
+  const int64_t at = row * L.G + gc;
+  r.s = reinterpret_cast<const uint16_t*>(expert + L.scale_off)[at];
+  if constexpr (ML == 3) r.z = expert[L.meta2_off + at];
+  else r.z = reinterpret_cast<const uint16_t*>(expert + L.meta2_off)[at];
+  return r;
+}
+template <int ML>
+__device__ __forceinline__ void awq_meta(const AwqStep& r, bool live, f16x2& s2, f16x2& b2) {
+  const _Float16 s = f16_from_bits((uint16_t)r.s);
+  _Float16 b;
+  if constexpr (ML == 3) b = awq_bias(r.z, s);
+  else b = f16_from_bits((uint16_t)r.z);
+  const _Float16 sv = live ? s : (_Float16)0.f, bv = live ? b : (_Float16)0.f;
+  s2 = f16x2{sv, sv};
+  b2 = f16x2{bv, bv};
+}
+
+// What float16 h left of x; nothing where h is infinite or NaN (x - h would be NaN and the infinity lose its sign).
+__device__ __forceinline__ _Float16 f16_rest(float x, _Float16 h) {
+  const float r = x - (float)h;
+  return r == r ? (_Float16)r : (_Float16)0.f;
+}
+
+// 8 values of x -> float16 terms in octet order (0 4 1 5 2 6 3 7), scaled by 2^-e.
+template <int TERMS>
+__device__ __forceinline__ void octet_terms(const float* v, int e, u32x4 (&o)[TERMS]) {
+  float x[8];
+  _Float16 h[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    x[j] = ldexpf(v[j], -e);
+    h[j] = (_Float16)x[j];
+  }
+  const u32x4 hi = {as_u32(f16x2{h[0], h[4]}), as_u32(f16x2{h[1], h[5]}), as_u32(f16x2{h[2], h[6]}), as_u32(f16x2{h[3], h[7]})};
+  o[0] = hi;
+  if constexpr (TERMS == 2) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] = f16_rest(x[j], h[j]);
+    const u32x4 lo = {as_u32(f16x2{h[0], h[4]}), as_u32(f16x2{h[1], h[5]}), as_u32(f16x2{h[2], h[6]}), as_u32(f16x2{h[3], h[7]})};
+    o[1] = lo;
+  }
+}
+// 8 elements of a row of x at element `at` (16-byte aligned).
+template <int XT>
+__device__ __forceinline__ void load_octet(const void* x, size_t at, float* v) {
+  if constexpr (XT == X_F32) {
+    const f32x4* p = reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(x) + at);
+    const f32x4 a = p[0], b = p[1];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = a[j];
+      v[4 + j] = b[j];
+    }
+  } else {
+    const u32x4 a = *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(x) + at);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t u = a[j];
+      if constexpr (XT == X_BF16) {
+        v[2 * j] = __uint_as_float(u << 16);
+        v[2 * j + 1] = __uint_as_float(u & 0xFFFF0000u);
+      } else {
+        const f16x2 p = as_f16x2(u);
+        v[2 * j] = (float)p.x;
+        v[2 * j + 1] = (float)p.y;
+      }
+    }
+  }
+}
+
+// float32 rows take two float16 terms (their products' sum is off by 2^-22 of an element or 2^-39 of its row's largest), bfloat16
+// ones fit into one after the scaling (down to 2^-39 of the row's largest), float16 ones are taken as they are.
+inline int awq_terms(XType xt) { return xt == X_F32 ? 2 : 1; }
+
+}  // namespace wq

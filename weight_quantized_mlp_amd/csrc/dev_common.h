@@ -180,6 +180,16 @@ __device__ __forceinline__ float silu_f32(float z) { return z / (1.0f + expf(-z)
 // |x|, 0 where x is not finite (a maximum that infinities and NaN have no say in).
 __device__ __forceinline__ float finite_abs(float x) { return fabsf(x) <= 3.4028235e38f ? fabsf(x) : 0.f; }
 
+// Power-of-two exponent e of a row: amax * 2^-e in [2^14, 2^15), which float16 holds; 0 for a zero amax.  The clamp keeps
+// 2^e and 2^-e normal float32 numbers.
+__device__ __forceinline__ int f16_row_exp(float amax) {
+  if (!(amax > 0.f)) return 0;
+  int ex;
+  (void)frexpf(amax, &ex);
+  const int e = ex - 15;
+  return e < -126 ? -126 : e;
+}
+
 __device__ __forceinline__ float bf16_bits_to_f32(uint32_t b) { return __uint_as_float(b << 16); }
 
 }  // namespace wq

@@ -140,6 +140,11 @@ hipError_t launch_adamw(int64_t count, int64_t elems, int bits, const void* tabl
                         double beta1, double beta2, double eps, double weight_decay, float grad_scale, uint32_t seed,
                         hipStream_t st);
 
+// ---- linear with AWQ weights (include/wqmlp_blocks.h) ------------------------------------------------
+size_t awq_linear_scratch_bytes(int M, int N, int K, XType xt);
+hipError_t launch_awq_linear(int M, int N, int K, const void* x, XType xt, const uint8_t* bank, int meta_layout, void* ws, float* y,
+                             hipStream_t st);
+
 // ---- norms around a block (include/wqmlp_blocks.h) --------------------------------------------------
 struct BlockNorm {
   const void *h, *y, *post, *pre, *gate;   // y, post, pre, gate: null where absent

@@ -42,16 +42,6 @@ namespace wq {
 namespace {
 
 // ---- dy -> float16 terms ---------------------------------------------------------------------------------------
-// Power-of-two exponent e of a row: amax * 2^-e in [2^14, 2^15); 0 for a zero amax.  The clamp keeps
-// 2^e and 2^-e normal float32 numbers.
-__device__ __forceinline__ int grad_row_exp(float amax) {
-  if (!(amax > 0.f)) return 0;
-  int ex;
-  (void)frexpf(amax, &ex);
-  const int e = ex - 15;
-  return e < -126 ? -126 : e;
-}
-
 // What float16 h left of x, times 2^12; nothing where h is infinite (x - h would be NaN, and the row's infinities lose their
 // sign) or NaN.  |x| < 2^15, so h is off by at most 8.
 constexpr float kSecond = 4096.f;
@@ -149,7 +139,7 @@ __global__ void __launch_bounds__(256) grad_prep_kernel(int M, int N, int Np, co
   for (int off = 32; off >= 1; off >>= 1) amax = fmaxf(amax, __shfl_xor(amax, off, 64));
   if ((t & 63) == 0) wmax[t >> 6] = amax;
   __syncthreads();
-  const int e = grad_row_exp(fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3])));
+  const int e = f16_row_exp(fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3])));
   if (t == 0) rowscale[m] = ldexpf(1.0f, e);
 #pragma unroll
   for (int i = 0; i < RC; ++i)
