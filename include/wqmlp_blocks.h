@@ -1,6 +1,6 @@
 /*
  * wqmlp_blocks.h -- C ABI of libwqmlp, third part: blocks with 4-bit weights and what stands around them.  The
- * linear with AWQ int4 group-32 weights, and the norms before and after a block with its gate and residual,
+ * linear with AWQ int4 group-32 weights and the gradient through it, and the norms before and after a block with its gate and residual,
  * forward and backward.
  *
  * The conventions of wqmlp.h hold for every call here: device pointers of the current device, 16-byte
@@ -35,6 +35,20 @@ extern "C" {
 size_t awq_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int x_dtype);
 int awq_linear_run(int64_t M, int64_t N, int64_t K, const void* x, int x_dtype, const void* bank, int meta_layout,
                    void* workspace, size_t workspace_bytes, float* y, void* stream);
+
+/*
+ * The gradient of awq_linear_run with respect to its input, through the frozen packed weights:
+ *   dx[m,k] = sum_n dy[m,n] dq[n,k]
+ * dy [M,N]: WQ_F32 or WQ_BF16; dx [M,K]: dx_dtype, WQ_F32 or WQ_BF16; bank and meta_layout as above.  K: a
+ * multiple of 32; N and M: any.  Numerics as for qlinear_backward: each row of dy is scaled by a power of two so that
+ * its largest finite magnitude lies in [2^14, 2^15) and enters float16 MFMAs.  bfloat16 dy: one float16 term, off
+ * by at most 2^-39 of the row's largest.  float32 dy into a float32 dx: two terms, 2^-22 of the element or 2^-51 of the
+ * row's largest; into a bfloat16 dx: rounded once to float16, 2^-11 of the element (dx's own rounding is 2^-8) or 2^-39
+ * of the row's largest.  NaN and infinities of dy stay in their row.  M == 0 is a valid empty call.
+ */
+size_t awq_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int dy_dtype, int dx_dtype);
+int awq_linear_backward(int64_t M, int64_t N, int64_t K, const void* dy, int dy_dtype, const void* bank, int meta_layout,
+                        void* workspace, size_t workspace_bytes, void* dx, int dx_dtype, void* stream);
 
 /*
  * What stands between one block (an MLP, say) and the next: the norm of the block's result, its gate and

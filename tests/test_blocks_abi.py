@@ -124,3 +124,32 @@ def test_awq_linear_empty_calls(L):
     assert L.awq_linear_workspace_bytes(0, 48, 64, 0) == 0
     assert L.awq_linear_workspace_bytes(4, 48, 48, 0) == 0
     assert L.awq_linear_workspace_bytes(4, 48, 64, 3) == 0
+
+
+LGRAD = ("M", "N", "K", "dy", "dyt", "bank", "layout", "ws", "wsb", "dx", "dxt")
+
+
+def lgrad_args(**kw):
+    a = dict(M=4, N=48, K=64, dy=A, dyt=1, bank=A + MB, layout=3, ws=A + 2 * MB, wsb=MB, dx=A + 3 * MB, dxt=0)
+    a.update(kw)
+    return [a[k] for k in LGRAD] + [None]
+
+
+@pytest.mark.parametrize("kw,rc", [
+    (dict(dy=None), EINVAL), (dict(bank=None), EINVAL), (dict(dx=None), EINVAL), (dict(dyt=2), EINVAL), (dict(dxt=2), EINVAL),
+    (dict(layout=5), EINVAL), (dict(M=-1), EINVAL), (dict(N=0), EINVAL), (dict(K=48), EINVAL), (dict(K=0), EINVAL),
+    (dict(M=(1 << 23) + 1), EINVAL), (dict(N=(1 << 23) + 1), EINVAL), (dict(M=1 << 23, K=1 << 14), EINVAL),
+    (dict(dy=A + 8), EALIGN), (dict(bank=A + MB + 4), EALIGN), (dict(dx=A + 3 * MB + 4), EALIGN), (dict(ws=A + 2 * MB + 1), EALIGN),
+    (dict(ws=None), EWORKSPACE), (dict(wsb=64), EWORKSPACE),
+    (dict(dx=A), EOVERLAP), (dict(dx=A + MB + 1024), EOVERLAP), (dict(ws=A), EOVERLAP), (dict(ws=A + 3 * MB), EOVERLAP),
+])
+def test_awq_linear_backward_refusals(L, kw, rc):
+    assert L.awq_linear_backward(*lgrad_args(**kw)) == rc
+
+
+def test_awq_linear_backward_empty_calls(L):
+    assert L.awq_linear_backward(*lgrad_args(M=0, dy=None, dx=None, ws=None, wsb=0)) == 0
+    assert L.awq_linear_backward(*lgrad_args(M=0, bank=None)) == EINVAL
+    assert L.awq_linear_backward_workspace_bytes(0, 48, 64, 0, 0) == 0
+    assert L.awq_linear_backward_workspace_bytes(4, 48, 48, 0, 0) == 0
+    assert L.awq_linear_backward_workspace_bytes(4, 48, 64, 2, 0) == 0

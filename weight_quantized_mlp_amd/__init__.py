@@ -22,7 +22,8 @@ __all__ = [
     "qlinear_workspace_bytes", "qlinear_run", "wq_read_probe",
     "WQ_LORA_MAX_RANK", "WQ_ADAMW_BLOCK", "WQ_ADAMW_KEEP_V", "lora_workspace_bytes", "lora_run", "lora_backward",
     "qlinear_backward_workspace_bytes", "qlinear_backward", "adamw_table_bytes", "AdamWTable", "adamw_table", "adamw_run",
-    "awq_linear_workspace_bytes", "awq_linear_run", "block_norm_run", "block_norm_backward_workspace_bytes", "block_norm_backward",
+    "awq_linear_workspace_bytes", "awq_linear_run", "awq_linear_backward_workspace_bytes", "awq_linear_backward",
+    "block_norm_run", "block_norm_backward_workspace_bytes", "block_norm_backward",
 ]
 
 WQ_F32, WQ_BF16, WQ_F16 = 0, 1, 2
@@ -77,6 +78,8 @@ _SIGS = {
     "adamw_run": (_INT, [_I64, _I64, _INT, _P, _P, _P, _D, _D, _D, _D, _F, ctypes.c_uint32, _P]),
     "awq_linear_workspace_bytes": (_SZ, [_I64, _I64, _I64, _INT]),
     "awq_linear_run": (_INT, [_I64, _I64, _I64, _P, _INT, _P, _INT, _P, _SZ, _P, _P]),
+    "awq_linear_backward_workspace_bytes": (_SZ, [_I64, _I64, _I64, _INT, _INT]),
+    "awq_linear_backward": (_INT, [_I64, _I64, _I64, _P, _INT, _P, _INT, _P, _SZ, _P, _INT, _P]),
     "block_norm_run": (_INT, [_I64, _I64, _P, _INT, _P, _INT, _P, _P, _INT, _P, _I64, _INT, _F, _F, _F, _P, _P, _INT, _P]),
     "block_norm_backward_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
     "block_norm_backward": (_INT, [_I64, _I64, _P, _INT, _P, _INT, _P, _P, _INT, _P, _P, _INT, _P, _I64, _INT, _F, _F, _F,
@@ -607,6 +610,34 @@ def awq_linear_run(x, bank, N, meta_layout=3, out=None, workspace=None):
     rc = lib().awq_linear_run(M, N, K, _ptr(x), xt, _ptr(bank), meta_layout, _ptr(ws), 0 if ws is None else ws.numel(),
                               _ptr(out), _stream(dev))
     _check("awq_linear_run", rc)
+    return out
+
+
+def awq_linear_backward_workspace_bytes(M, N, K, dy_dtype=torch.float32, dx_dtype=torch.float32):
+    return lib().awq_linear_backward_workspace_bytes(M, N, K, _FLOATS[dy_dtype], _FLOATS[dx_dtype])
+
+
+def awq_linear_backward(dy, bank, K, meta_layout=3, dtype=None, out=None, workspace=None):
+    """dx = dy dq(W): the gradient of awq_linear_run with respect to its input.  dy [M,N] f32/bf16; bank as for
+    awq_linear_run; dx [M,K] f32/bf16 (out's type, or dtype, default dy's; a TypeError where they differ)."""
+    want = _result_dtype("dtype", dtype, dy.dtype, out=out)
+    dev = dy.device
+    if dy.dim() != 2:
+        raise ValueError("dy must be [M, N]")
+    M, N = dy.shape
+    dyt = _float_code(dy.dtype, "dy", (torch.float32, torch.bfloat16))
+    dxt = _float_code(want, "dx", (torch.float32, torch.bfloat16))
+    _want(dy, "dy", dy.dtype, dev, M * N)
+    _want(bank, "bank", torch.uint8, dev, awq_bank_bytes(1, N, K, meta_layout))
+    if out is None:
+        out = torch.empty((M, K), dtype=want, device=dev)
+    else:
+        _want(out, "out", want, dev, M * K)
+    nb = awq_linear_backward_workspace_bytes(M, N, K, dy.dtype, want)
+    ws = _workspace(nb, dev, workspace) if nb else None
+    rc = lib().awq_linear_backward(M, N, K, _ptr(dy), dyt, _ptr(bank), meta_layout, _ptr(ws), 0 if ws is None else ws.numel(),
+                                   _ptr(out), dxt, _stream(dev))
+    _check("awq_linear_backward", rc)
     return out
 
 

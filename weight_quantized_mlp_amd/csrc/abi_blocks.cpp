@@ -16,6 +16,8 @@ using namespace wq::abi;
 bool is_float(int dt) { return dt == WQ_F32 || dt == WQ_BF16 || dt == WQ_F16; }
 wq::XType xtype(int dt) { return dt == WQ_F32 ? wq::X_F32 : (dt == WQ_BF16 ? wq::X_BF16 : wq::X_F16); }
 
+bool is_grad(int dt) { return dt == WQ_F32 || dt == WQ_BF16; }
+
 bool awq_shape_ok(int64_t M, int64_t N, int64_t K) {
   return M >= 0 && M <= kMaxDim && N > 0 && N <= kMaxDim && K > 0 && K <= kMaxDim && K % 32 == 0 &&
          M * (N > K ? N : K) <= kMaxElems;
@@ -70,6 +72,29 @@ int awq_linear_run(int64_t M, int64_t N, int64_t K, const void* x, int x_dtype, 
   if (rc != WQ_OK) return rc;
   return launched(wq::launch_awq_linear((int)M, (int)N, (int)K, x, xtype(x_dtype), static_cast<const uint8_t*>(bank), meta_layout,
                                         workspace, y, reinterpret_cast<hipStream_t>(stream)));
+}
+
+size_t awq_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int dy_dtype, int dx_dtype) {
+  if (!awq_shape_ok(M, N, K) || !is_grad(dy_dtype) || !is_grad(dx_dtype)) return 0;
+  return wq::awq_linear_grad_scratch_bytes((int)M, (int)N, (int)K, xtype(dy_dtype), xtype(dx_dtype));
+}
+
+int awq_linear_backward(int64_t M, int64_t N, int64_t K, const void* dy, int dy_dtype, const void* bank, int meta_layout,
+                        void* workspace, size_t workspace_bytes, void* dx, int dx_dtype, void* stream) {
+  if (!awq_shape_ok(M, N, K) || !is_grad(dy_dtype) || !is_grad(dx_dtype) || (meta_layout != 3 && meta_layout != 4)) return WQ_EINVAL;
+  if (bank == nullptr) return WQ_EINVAL;
+  if (M == 0) return WQ_OK;
+  if (any_null({dy, dx})) return WQ_EINVAL;
+  if (!all_aligned({dy, bank, workspace, dx})) return WQ_EALIGN;
+  const size_t need = awq_linear_backward_workspace_bytes(M, N, K, dy_dtype, dx_dtype);
+  if (need && (workspace == nullptr || workspace_bytes < need)) return WQ_EWORKSPACE;
+  if (any_overlap({{dx, (size_t)M * K * xsize(dx_dtype)}, {workspace, need}},
+                  {{dy, (size_t)M * N * xsize(dy_dtype)}, {bank, awq_bank_bytes(1, N, K, meta_layout)}}))
+    return WQ_EOVERLAP;
+  const int rc = check_device({dy, bank, need ? workspace : nullptr, dx});
+  if (rc != WQ_OK) return rc;
+  return launched(wq::launch_awq_linear_grad((int)M, (int)N, (int)K, dy, xtype(dy_dtype), static_cast<const uint8_t*>(bank),
+                                             meta_layout, workspace, dx, xtype(dx_dtype), reinterpret_cast<hipStream_t>(stream)));
 }
 
 int block_norm_run(int64_t M, int64_t H, const void* h, int h_dtype, const void* y, int y_dtype, const void* post,

@@ -145,6 +145,11 @@ size_t awq_linear_scratch_bytes(int M, int N, int K, XType xt);
 hipError_t launch_awq_linear(int M, int N, int K, const void* x, XType xt, const uint8_t* bank, int meta_layout, void* ws, float* y,
                              hipStream_t st);
 
+// The gradient with respect to x (linear_grad.hip).
+size_t awq_linear_grad_scratch_bytes(int M, int N, int K, XType dyt, XType dxt);
+hipError_t launch_awq_linear_grad(int M, int N, int K, const void* dy, XType dyt, const uint8_t* bank, int meta_layout, void* ws,
+                                  void* dx, XType dxt, hipStream_t st);
+
 // ---- norms around a block (include/wqmlp_blocks.h) --------------------------------------------------
 struct BlockNorm {
   const void *h, *y, *post, *pre, *gate;   // y, post, pre, gate: null where absent

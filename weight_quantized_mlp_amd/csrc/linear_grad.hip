@@ -1,5 +1,5 @@
 // Gradient of a quantised linear with respect to its input (gfx950): qlinear_backward in
-// include/wqmlp_adapters.h,  dx[m,k] = sum_n dy[m,n] dq(W[n,k]).
+// include/wqmlp_adapters.h and awq_linear_backward in include/wqmlp_blocks.h,  dx[m,k] = sum_n dy[m,n] dq(W[n,k]).
 //
 // A GEMM whose contraction runs over the weight's rows, while the weights are packed along their columns (k), so
 // the matrix cores need each lane to hold 8 consecutive n of one column: the transpose of what is stored.  The
@@ -11,6 +11,9 @@
 //   NVFP4: a byte column holds the k pair (2c, 2c+1), so one read gives both column blocks of a wave, the even
 //     and the odd k.  The E4M3 group scales (one per n and 16 k) are held in LDS as float16, [group][n], so a
 //     lane's 8 scales are one 16-byte read; E2M1 x E4M3 products are exact float16 values.
+//   AWQ: byte columns as NVFP4; scales and biases (one each per n and 32 k) are held the same way.  A transposed dword
+//     holds the nibbles of n, n + 1, n + 2, n + 3, of which masks give the pairs (n, n + 2) and (n + 1, n + 3): each
+//     8 n of dy and of the scales are stored in the order 0 2 1 3 4 6 5 7, and no nibble has to move.
 //
 // Tile: 4 waves compute (32 MB / TERMS) rows x 256 columns, 64 columns per wave; the waves share the activation
 // tile (64 n of float16 = 128-byte rows, moved by global->LDS copies), each decodes only its own columns.  n is
@@ -33,6 +36,7 @@
 // largest.  The second terms' products have float32 accumulators of their own (a tile of two terms has half the rows, so
 // both kinds of tile hold as many), which join the others' at the end.
 #include <algorithm>
+#include <type_traits>
 
 #include "dev_common.h"
 #include "launch.h"
@@ -50,11 +54,15 @@ __device__ __forceinline__ _Float16 second_term(float x, _Float16 h) {
   return r == r ? (_Float16)r : (_Float16)0.f;
 }
 
+// Place of element t in the order 0 2 1 3 4 6 5 7: its two low bits change places.
+__device__ __forceinline__ int awq_place(int t) { return (t & ~3) | ((t & 1) << 1) | ((t >> 1) & 1); }
+
 // One workgroup per row of dy [M][N] (any N, so rows are only element-aligned): the row's largest finite magnitude, then the scaled
 // float16 terms, [TERMS][M][Np] with zeros from N to Np (a multiple of 64).  A thread keeps RC chunks of 8 elements in registers,
 // loaded without a branch between them so that all are in flight at once; longer rows read the rest twice.  The up to 7 elements
 // behind the last whole chunk are one thread's.
-template <bool BF, bool SC, int TERMS, int RC>
+// PERM: each 8 elements in the order 0 2 1 3 4 6 5 7 (AWQ).
+template <bool BF, bool SC, bool PERM, int TERMS, int RC>
 __global__ void __launch_bounds__(256) grad_prep_kernel(int M, int N, int Np, const void* __restrict__ dy,
                                                         const float* __restrict__ scale, uint16_t* __restrict__ a16,
                                                         float* __restrict__ rowscale) {
@@ -100,7 +108,8 @@ __global__ void __launch_bounds__(256) grad_prep_kernel(int M, int N, int Np, co
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float x0 = ldexpf(v[2 * j], -e), x1 = ldexpf(v[2 * j + 1], -e);
+      const int a = PERM ? 4 * (j >> 1) + (j & 1) : 2 * j, b = PERM ? a + 2 : a + 1;
+      const float x0 = ldexpf(v[a], -e), x1 = ldexpf(v[b], -e);
       const _Float16 h0 = (_Float16)x0, h1 = (_Float16)x1;
       hi[j] = as_u32(f16x2{h0, h1});
       if constexpr (TERMS == 2) lo[j] = as_u32(f16x2{second_term(x0, h0), second_term(x1, h1)});
@@ -154,8 +163,9 @@ __global__ void __launch_bounds__(256) grad_prep_kernel(int M, int N, int Np, co
   if (t < Np - 8 * nf) {                         // the last elements and the zeros behind them
     const float x = ldexpf(rest, -e);
     const _Float16 h = (_Float16)x;
-    o[8 * nf + t] = __builtin_bit_cast(uint16_t, h);
-    if constexpr (TERMS == 2) o[(size_t)M * Np + 8 * nf + t] = __builtin_bit_cast(uint16_t, second_term(x, h));
+    const int at = 8 * nf + (PERM ? awq_place(t) : t);
+    o[at] = __builtin_bit_cast(uint16_t, h);
+    if constexpr (TERMS == 2) o[(size_t)M * Np + at] = __builtin_bit_cast(uint16_t, second_term(x, h));
   }
 }
 
@@ -165,6 +175,9 @@ constexpr int kSlots = 512;            // workgroups the chip runs at once
 constexpr int kScaleRow = 72;          // float16 scales of one group: 64 n, padded so that the 4 records' writes spread over the banks
 constexpr int kABytes = 128 * 32;      // activation bytes per 32 rows and stage
 
+// Formats: 0 FP8, 1 NVFP4, 2 and 3 AWQ with metadata layout 3 and 4.  NVFP4 has 16 rows of group scales per stage, AWQ 8 of
+// scales and 8 of biases.
+constexpr bool is_awq(int fmt) { return fmt >= 2; }
 template <int FMT> constexpr int b_stage() { return FMT == 0 ? 64 * 256 : 64 * 128 + 16 * kScaleRow * 2; }
 // The epilogue reuses the stages: 32 x 64 float32 per wave, rows padded by 16 bytes; the tile's row scales lie behind both.
 constexpr int kEpiRow = 64 + 4, kEpiBytes = 32 * kEpiRow * 4;
@@ -229,8 +242,8 @@ template <int FMT, int MB, int TERMS>
 __global__ void __launch_bounds__(256, 2) grad_gemm_kernel(int M, int N, int Np, int K, GradPlan plan,
                                                            const uint16_t* __restrict__ a16,
                                                            const float* __restrict__ rowscale,
-                                                           const uint8_t* __restrict__ w, float inv, void* __restrict__ dx,
-                                                           bool dx_bf, float* __restrict__ partials) {
+                                                           const uint8_t* __restrict__ w, AwqLayout L, float inv,
+                                                           void* __restrict__ dx, bool dx_bf, float* __restrict__ partials) {
   constexpr int RB = MB / TERMS;               // 32-row blocks of the output tile
   constexpr int BM = 32 * RB;
   constexpr int ASTAGE = MB * kABytes, BSTAGE = b_stage<FMT>(), STAGE = ASTAGE + BSTAGE;
@@ -238,6 +251,7 @@ __global__ void __launch_bounds__(256, 2) grad_gemm_kernel(int M, int N, int Np,
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 31, h = lane >> 5;
+  const AwqDecode dc = awq_decode_consts();     // (AWQ only; dead elsewhere)
 
   // Parts of the split tiles first, then whole tiles: workgroup b runs on XCD b % 8, and each XCD gets a contiguous
   // run of tiles, ordered in bands of 8 tile rows so that the tiles in flight share rows and columns in its L2.
@@ -284,7 +298,7 @@ __global__ void __launch_bounds__(256, 2) grad_gemm_kernel(int M, int N, int Np,
 
   // FP8 weight copies: rows of 256 bytes, 16 rows per wave, 4 rows per copy; chunk c of row r at c ^ (r & 15).  Rows
   // past N and columns past K repeat the last ones (their products meet zeros of dy or are not stored).
-  const int rb = FMT == 0 ? K : (K >> 6) * 36;       // bytes of a weight row
+  const int rb = FMT == 0 ? K : (FMT == 1 ? (K >> 6) * 36 : K >> 1);   // bytes of a weight row
   uint32_t woff[4];
   // NVFP4: thread t loads record t % 4 of row t / 4 of a step into registers and writes it to LDS a step later.
   const uint8_t* nvbase = nullptr;
@@ -294,7 +308,7 @@ __global__ void __launch_bounds__(256, 2) grad_gemm_kernel(int M, int N, int Np,
       const int r = 16 * wave + 4 * i + (lane >> 4), c = (lane & 15) ^ (r & 15);
       woff[i] = (uint32_t)min(16 * c, K - 16 - k0);
     }
-  } else {
+  } else if constexpr (FMT == 1) {
     nvbase = w + (size_t)min((k0 >> 6) + (tid & 3), (K >> 6) - 1) * 36;
   }
   auto copy_w = [&](int step, int stage) {          // FP8
@@ -313,24 +327,57 @@ __global__ void __launch_bounds__(256, 2) grad_gemm_kernel(int M, int N, int Np,
     lds_copy16_run<4>(v, bases, sb);
   };
   struct Rec { u32x3_a4 a, b, c; };                  // 36 bytes: scale dword, 8 nibble dwords
-  Rec rec;
-  auto load_rec = [&](int step) {                    // NVFP4
-    const uint8_t* p = nvbase + (size_t)min(64 * step + (tid >> 2), N - 1) * rb;
-    rec.a = *reinterpret_cast<const u32x3_a4*>(p);
-    rec.b = *reinterpret_cast<const u32x3_a4*>(p + 12);
-    rec.c = *reinterpret_cast<const u32x3_a4*>(p + 24);
+  struct AwqRec { u32x4 c[2]; uint32_t s[2], z[2]; };  // two groups of a row: codes, scales, zeros or biases
+  std::conditional_t<is_awq(FMT), AwqRec, Rec> rec;
+  // AWQ: thread t loads groups 2 (t % 4) and the next of row t / 4 of a step (past K the last one again, not stored)
+  const int g0 = min((k0 >> 5) + 2 * (tid & 3), (int)L.G - 1), g1 = min(g0 + 1, (int)L.G - 1);
+  auto load_rec = [&](int step) {                    // NVFP4, AWQ
+    const size_t n = (size_t)min(64 * step + (tid >> 2), N - 1);
+    if constexpr (is_awq(FMT)) {
+      const size_t at = n * (size_t)L.G;
+      const uint16_t* sc = reinterpret_cast<const uint16_t*>(w + L.scale_off) + at;
+      rec.c[0] = *reinterpret_cast<const u32x4*>(w + n * rb + 16 * g0);
+      rec.c[1] = *reinterpret_cast<const u32x4*>(w + n * rb + 16 * g1);
+      rec.s[0] = sc[g0];
+      rec.s[1] = sc[g1];
+      if constexpr (FMT == 2) {
+        const uint8_t* z = w + L.meta2_off + at;
+        rec.z[0] = z[g0];
+        rec.z[1] = z[g1];
+      } else {
+        const uint16_t* z = reinterpret_cast<const uint16_t*>(w + L.meta2_off) + at;
+        rec.z[0] = z[g0];
+        rec.z[1] = z[g1];
+      }
+    } else {
+      const uint8_t* p = nvbase + n * rb;
+      rec.a = *reinterpret_cast<const u32x3_a4*>(p);
+      rec.b = *reinterpret_cast<const u32x3_a4*>(p + 12);
+      rec.c = *reinterpret_cast<const u32x3_a4*>(p + 24);
+    }
   };
   auto write_rec = [&](int stage) {
     uint8_t* bs = lds + stage * STAGE + ASTAGE;
     const int r = tid >> 2, q = tid & 3, sw = (r >> 1) & 7;
-    *reinterpret_cast<u32x4*>(bs + r * 128 + (((2 * q) ^ sw) * 16)) = u32x4{rec.a.y, rec.a.z, rec.b.x, rec.b.y};
-    *reinterpret_cast<u32x4*>(bs + r * 128 + (((2 * q + 1) ^ sw) * 16)) = u32x4{rec.b.z, rec.c.x, rec.c.y, rec.c.z};
-    const uint32_t d0 = as_u32(e4m3x2_f16<false>(rec.a.x)), d1 = as_u32(e4m3x2_f16<true>(rec.a.x));
-    uint16_t* sc = reinterpret_cast<uint16_t*>(bs + 64 * 128) + 4 * q * kScaleRow + r;
-    sc[0] = (uint16_t)d0;
-    sc[kScaleRow] = (uint16_t)(d0 >> 16);
-    sc[2 * kScaleRow] = (uint16_t)d1;
-    sc[3 * kScaleRow] = (uint16_t)(d1 >> 16);
+    if constexpr (is_awq(FMT)) {
+      uint16_t* sc = reinterpret_cast<uint16_t*>(bs + 64 * 128) + 2 * q * kScaleRow + awq_place(r);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        *reinterpret_cast<u32x4*>(bs + r * 128 + (((2 * q + j) ^ sw) * 16)) = rec.c[j];
+        const _Float16 sv = f16_from_bits((uint16_t)rec.s[j]);
+        sc[j * kScaleRow] = (uint16_t)rec.s[j];
+        sc[(8 + j) * kScaleRow] = FMT == 2 ? __builtin_bit_cast(uint16_t, awq_bias(rec.z[j], sv)) : (uint16_t)rec.z[j];
+      }
+    } else {
+      *reinterpret_cast<u32x4*>(bs + r * 128 + (((2 * q) ^ sw) * 16)) = u32x4{rec.a.y, rec.a.z, rec.b.x, rec.b.y};
+      *reinterpret_cast<u32x4*>(bs + r * 128 + (((2 * q + 1) ^ sw) * 16)) = u32x4{rec.b.z, rec.c.x, rec.c.y, rec.c.z};
+      const uint32_t d0 = as_u32(e4m3x2_f16<false>(rec.a.x)), d1 = as_u32(e4m3x2_f16<true>(rec.a.x));
+      uint16_t* sc = reinterpret_cast<uint16_t*>(bs + 64 * 128) + 4 * q * kScaleRow + r;
+      sc[0] = (uint16_t)d0;
+      sc[kScaleRow] = (uint16_t)(d0 >> 16);
+      sc[2 * kScaleRow] = (uint16_t)d1;
+      sc[3 * kScaleRow] = (uint16_t)(d1 >> 16);
+    }
   };
 
   f32x16 acc[MB][2];                         // block i: rows 32 (i % RB) .. of the tile, term i / RB
@@ -342,7 +389,7 @@ __global__ void __launch_bounds__(256, 2) grad_gemm_kernel(int M, int N, int Np,
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
 
   // Fragments of sub-step s (16 n): activations chunk 2 s + h of each row; weights raw, 8 bytes along n per column.
-  struct Raw { i32x2 q[FMT == 0 ? 2 : 1]; u32x4 d; };
+  struct Raw { i32x2 q[FMT == 0 ? 2 : 1]; u32x4 d, z; };
   auto read_a = [&](int stage, int s, f16x8* af) {
     const uint8_t* ast = lds + stage * STAGE;
 #pragma unroll
@@ -366,9 +413,11 @@ __global__ void __launch_bounds__(256, 2) grad_gemm_kernel(int M, int N, int Np,
       const int c = 2 * wave + tr_chunk;
       raw.q[0] = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
           (__attribute__((address_space(3))) i32x2*)(bs + r * 128 + ((c ^ ((r >> 1) & 7)) * 16) + tr_half));
-      // the lane's byte column li lies in group li / 8 of record `wave`; its 8 n
-      raw.d = *reinterpret_cast<const u32x4*>(lds + stage * STAGE + ASTAGE + 64 * 128 +
-                                              ((4 * wave + (li >> 3)) * kScaleRow + 16 * s + 8 * h) * 2);
+      // the lane's byte column li lies in group li / 8 of record `wave` (AWQ: in group 2 wave + li / 16); its 8 n
+      const int group = is_awq(FMT) ? 2 * wave + (li >> 4) : 4 * wave + (li >> 3);
+      const uint8_t* meta = lds + stage * STAGE + ASTAGE + 64 * 128 + (group * kScaleRow + 16 * s + 8 * h) * 2;
+      raw.d = *reinterpret_cast<const u32x4*>(meta);
+      if constexpr (is_awq(FMT)) raw.z = *reinterpret_cast<const u32x4*>(meta + 8 * kScaleRow * 2);
     }
   };
   auto decode = [&](const Raw& raw, f16x8* bf) {
@@ -379,6 +428,19 @@ __global__ void __launch_bounds__(256, 2) grad_gemm_kernel(int M, int N, int Np,
         const f16x2 p2 = e4m3x2_f16<false>(raw.q[j].y), p3 = e4m3x2_f16<true>(raw.q[j].y);
         bf[j] = f16x8{p0.x, p0.y, p1.x, p1.y, p2.x, p2.y, p3.x, p3.y};
       }
+    } else if constexpr (is_awq(FMT)) {
+      // low nibbles: even k, high nibbles: odd k; dword j holds 4 n, pairs (n, n + 2) below and (n + 1, n + 3) 8 bits up
+      f16x2 ev[4], od[4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t wd = (uint32_t)(j ? raw.q[0].y : raw.q[0].x);
+        const uint32_t s0 = j ? raw.d.z : raw.d.x, s1 = j ? raw.d.w : raw.d.y;
+        const uint32_t z0 = j ? raw.z.z : raw.z.x, z1 = j ? raw.z.w : raw.z.y;
+        awq_pairs(wd, as_f16x2(s0), as_f16x2(z0), dc, ev[2 * j], od[2 * j]);
+        awq_pairs(wd >> 8, as_f16x2(s1), as_f16x2(z1), dc, ev[2 * j + 1], od[2 * j + 1]);
+      }
+      bf[0] = f16x8{ev[0].x, ev[0].y, ev[1].x, ev[1].y, ev[2].x, ev[2].y, ev[3].x, ev[3].y};
+      bf[1] = f16x8{od[0].x, od[0].y, od[1].x, od[1].y, od[2].x, od[2].y, od[3].x, od[3].y};
     } else {
       // low nibbles: even k, high nibbles: odd k; the pairs (n, n + 1) of one k are put into one byte for the decoder
       const uint32_t wd[2] = {(uint32_t)raw.q[0].x, (uint32_t)raw.q[0].y};
@@ -420,9 +482,9 @@ __global__ void __launch_bounds__(256, 2) grad_gemm_kernel(int M, int N, int Np,
   };
   // Prologue: steps s0 and s0 + 1 on their way, step s0 landed.  The tile's row scales come along for the epilogue.
   const float row_scale = tid < BM ? rowscale[min(m0 + tid, M - 1)] : 0.f;
-  if constexpr (FMT == 1) load_rec(s0);
+  if constexpr (FMT != 0) load_rec(s0);
   fetch(s0, 0);
-  if constexpr (FMT == 1) {
+  if constexpr (FMT != 0) {
     write_rec(0);
     load_rec(min(s0 + 1, last));
   }
@@ -430,6 +492,10 @@ __global__ void __launch_bounds__(256, 2) grad_gemm_kernel(int M, int N, int Np,
   // NVFP4: the records of step s0 have been waited for, and with them everything issued before; FP8: all but the second fetch
   if constexpr (FMT == 0) {
     if (s0 < last) wait_vmem<MB + 4>();
+    else wait_vmem<0>();
+  } else if constexpr (is_awq(FMT)) {
+    // how many instructions a record's loads become is the compiler's choice: only the copies behind them stay out
+    if (s0 < last) wait_vmem<MB>();
     else wait_vmem<0>();
   } else {
     if (s0 < last) wait_vmem<MB + 3>();
@@ -456,11 +522,11 @@ __global__ void __launch_bounds__(256, 2) grad_gemm_kernel(int M, int N, int Np,
     mfmas(af0, raw0);
     __builtin_amdgcn_sched_barrier(0);
     // NVFP4: records of step s + 1 (its stage's last readers passed the previous barrier)
-    if constexpr (FMT == 1) write_rec(st ^ 1);
+    if constexpr (FMT != 0) write_rec(st ^ 1);
     wait_vmem<0>();                            // step s + 1's copies (issued a step ago) landed
     wait_lds();                                // this wave's reads of stage st are in registers, its writes in LDS
     __syncthreads();
-    if constexpr (FMT == 1) load_rec(min(s + 2, last));
+    if constexpr (FMT != 0) load_rec(min(s + 2, last));
     if (s + 2 <= last) fetch(s + 2, st);
     read_a(st ^ 1, 0, af0);
     read_b(st ^ 1, 0, raw0);
@@ -578,39 +644,39 @@ inline GradWs grad_ws(int M, int N, int K, int terms) {
 }
 
 template <int FMT, int MB, int TERMS>
-hipError_t grad_gemm(int M, int N, int K, const GradPlan& p, const uint16_t* a16, const float* rs, const uint8_t* w, float inv,
-                     void* dx, bool bf, float* partials, hipStream_t st) {
+hipError_t grad_gemm(int M, int N, int K, const GradPlan& p, const uint16_t* a16, const float* rs, const uint8_t* w,
+                     const AwqLayout& L, float inv, void* dx, bool bf, float* partials, hipStream_t st) {
   if (!raise_lds_limit<grad_gemm_kernel<FMT, MB, TERMS>>()) return hipErrorInvalidValue;
   const int grid = ((p.units + 7) & ~7) + (p.full + 7) / 8 * 8;
   hipLaunchKernelGGL((grad_gemm_kernel<FMT, MB, TERMS>), dim3(grid), dim3(256), grad_lds<FMT>(MB), st, M, N, p.steps * 64, K,
-                     p, a16, rs, w, inv, dx, bf, partials);
+                     p, a16, rs, w, L, inv, dx, bf, partials);
   return hipGetLastError();
 }
 
 template <int FMT>
 hipError_t grad_dispatch(int M, int N, int K, int terms, const GradPlan& p, const uint16_t* a16, const float* rs,
-                         const uint8_t* w, float inv, void* dx, bool bf, float* partials, hipStream_t st) {
+                         const uint8_t* w, const AwqLayout& L, float inv, void* dx, bool bf, float* partials, hipStream_t st) {
   const int mb = p.mb;
   if (terms == 2)
-    return mb == 2 ? grad_gemm<FMT, 2, 2>(M, N, K, p, a16, rs, w, inv, dx, bf, partials, st)
-                   : grad_gemm<FMT, 4, 2>(M, N, K, p, a16, rs, w, inv, dx, bf, partials, st);
-  if (mb == 1) return grad_gemm<FMT, 1, 1>(M, N, K, p, a16, rs, w, inv, dx, bf, partials, st);
-  if (mb == 2) return grad_gemm<FMT, 2, 1>(M, N, K, p, a16, rs, w, inv, dx, bf, partials, st);
-  return grad_gemm<FMT, 4, 1>(M, N, K, p, a16, rs, w, inv, dx, bf, partials, st);
+    return mb == 2 ? grad_gemm<FMT, 2, 2>(M, N, K, p, a16, rs, w, L, inv, dx, bf, partials, st)
+                   : grad_gemm<FMT, 4, 2>(M, N, K, p, a16, rs, w, L, inv, dx, bf, partials, st);
+  if (mb == 1) return grad_gemm<FMT, 1, 1>(M, N, K, p, a16, rs, w, L, inv, dx, bf, partials, st);
+  if (mb == 2) return grad_gemm<FMT, 2, 1>(M, N, K, p, a16, rs, w, L, inv, dx, bf, partials, st);
+  return grad_gemm<FMT, 4, 1>(M, N, K, p, a16, rs, w, L, inv, dx, bf, partials, st);
 }
 
 // 3 register chunks cover rows of 6144, 9 rows of 18432.
-template <bool BF, bool SC, int TERMS>
+template <bool BF, bool SC, bool PERM, int TERMS>
 void grad_prep(int M, int N, int Np, const void* dy, const float* scale, uint16_t* a16, float* rs, hipStream_t st) {
   if (Np <= 3 * 2048)
-    hipLaunchKernelGGL((grad_prep_kernel<BF, SC, TERMS, 3>), dim3(M), dim3(256), 0, st, M, N, Np, dy, scale, a16, rs);
+    hipLaunchKernelGGL((grad_prep_kernel<BF, SC, PERM, TERMS, 3>), dim3(M), dim3(256), 0, st, M, N, Np, dy, scale, a16, rs);
   else
-    hipLaunchKernelGGL((grad_prep_kernel<BF, SC, TERMS, 9>), dim3(M), dim3(256), 0, st, M, N, Np, dy, scale, a16, rs);
+    hipLaunchKernelGGL((grad_prep_kernel<BF, SC, PERM, TERMS, 9>), dim3(M), dim3(256), 0, st, M, N, Np, dy, scale, a16, rs);
 }
-template <bool BF, bool SC, typename... A>
+template <bool BF, bool SC, bool PERM, typename... A>
 void grad_prep_terms(int terms, A... a) {
-  if (terms == 2) grad_prep<BF, SC, 2>(a...);
-  else grad_prep<BF, SC, 1>(a...);
+  if (terms == 2) grad_prep<BF, SC, PERM, 2>(a...);
+  else grad_prep<BF, SC, PERM, 1>(a...);
 }
 
 }  // namespace
@@ -619,32 +685,59 @@ size_t linear_grad_scratch_bytes(int fmt, int M, int N, int K, XType dxt) {
   return grad_ws(M, N, K, terms_of(dxt)).total;
 }
 
-hipError_t launch_linear_grad(int fmt, int M, int N, int K, const void* dy, XType dyt, const uint8_t* w, const float* scale,
-                              float inv, void* ws, void* dx, XType dxt, hipStream_t st) {
-  const int terms = terms_of(dxt);
+namespace {
+
+hipError_t linear_grad(int fmt, int terms, int M, int N, int K, const void* dy, XType dyt, const uint8_t* w, const float* scale,
+                       const AwqLayout& L, float inv, void* ws, void* dx, XType dxt, hipStream_t st) {
   const GradPlan p = grad_plan(M, N, K, terms);
-  const GradWs L = grad_ws(M, N, K, terms);
+  const GradWs W = grad_ws(M, N, K, terms);
   uint8_t* base = reinterpret_cast<uint8_t*>(ws);
   uint16_t* a16 = reinterpret_cast<uint16_t*>(base);
-  float* rs = reinterpret_cast<float*>(base + L.rs);
-  float* partials = reinterpret_cast<float*>(base + L.partials);
+  float* rs = reinterpret_cast<float*>(base + W.rs);
+  float* partials = reinterpret_cast<float*>(base + W.partials);
   const int Np = p.steps * 64;
   const bool bf = dxt == X_BF16;
   if (dyt == X_BF16) {
-    if (fmt == 0) grad_prep_terms<true, true>(terms, M, N, Np, dy, scale, a16, rs, st);
-    else grad_prep_terms<true, false>(terms, M, N, Np, dy, scale, a16, rs, st);
+    if (fmt == 0) grad_prep_terms<true, true, false>(terms, M, N, Np, dy, scale, a16, rs, st);
+    else if (fmt == 1) grad_prep_terms<true, false, false>(terms, M, N, Np, dy, scale, a16, rs, st);
+    else grad_prep<true, false, true, 1>(M, N, Np, dy, scale, a16, rs, st);
   } else {
-    if (fmt == 0) grad_prep_terms<false, true>(terms, M, N, Np, dy, scale, a16, rs, st);
-    else grad_prep_terms<false, false>(terms, M, N, Np, dy, scale, a16, rs, st);
+    if (fmt == 0) grad_prep_terms<false, true, false>(terms, M, N, Np, dy, scale, a16, rs, st);
+    else if (fmt == 1) grad_prep_terms<false, false, false>(terms, M, N, Np, dy, scale, a16, rs, st);
+    else grad_prep_terms<false, false, true>(terms, M, N, Np, dy, scale, a16, rs, st);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  e = fmt == 0 ? grad_dispatch<0>(M, N, K, terms, p, a16, rs, w, inv, dx, bf, partials, st)
-               : grad_dispatch<1>(M, N, K, terms, p, a16, rs, w, inv, dx, bf, partials, st);
+  switch (fmt) {
+    case 0: e = grad_dispatch<0>(M, N, K, terms, p, a16, rs, w, L, inv, dx, bf, partials, st); break;
+    case 1: e = grad_dispatch<1>(M, N, K, terms, p, a16, rs, w, L, inv, dx, bf, partials, st); break;
+    case 2: e = grad_dispatch<2>(M, N, K, terms, p, a16, rs, w, L, inv, dx, bf, partials, st); break;
+    default: e = grad_dispatch<3>(M, N, K, terms, p, a16, rs, w, L, inv, dx, bf, partials, st); break;
+  }
   if (e != hipSuccess || p.units == 0) return e;
   hipLaunchKernelGGL(grad_finish_kernel, dim3((unsigned)(p.tiles - p.full) * (p.bm / 4)), dim3(256), 0, st, M, K, p,
                      partials, rs, fmt == 0 ? 1.0f : inv, dx, bf);
   return hipGetLastError();
+}
+
+// bfloat16 dy fits into one float16 term after the scaling, whatever dx's type.
+inline int awq_grad_terms(XType dyt, XType dxt) { return dyt == X_F32 && dxt == X_F32 ? 2 : 1; }
+
+}  // namespace
+
+hipError_t launch_linear_grad(int fmt, int M, int N, int K, const void* dy, XType dyt, const uint8_t* w, const float* scale,
+                              float inv, void* ws, void* dx, XType dxt, hipStream_t st) {
+  return linear_grad(fmt, terms_of(dxt), M, N, K, dy, dyt, w, scale, AwqLayout{}, inv, ws, dx, dxt, st);
+}
+
+size_t awq_linear_grad_scratch_bytes(int M, int N, int K, XType dyt, XType dxt) {
+  return M == 0 ? 0 : grad_ws(M, N, K, awq_grad_terms(dyt, dxt)).total;
+}
+
+hipError_t launch_awq_linear_grad(int M, int N, int K, const void* dy, XType dyt, const uint8_t* bank, int meta_layout, void* ws,
+                                  void* dx, XType dxt, hipStream_t st) {
+  return linear_grad(meta_layout == 3 ? 2 : 3, awq_grad_terms(dyt, dxt), M, N, K, dy, dyt, bank, nullptr,
+                     awq_layout(N, K, meta_layout), 1.f, ws, dx, dxt, st);
 }
 
 }  // namespace wq
