@@ -1,7 +1,7 @@
 /*
  * wqmlp_blocks.h -- C ABI of libwqmlp, third part: blocks with 4-bit weights and what stands around them.  The
- * linear with AWQ int4 group-32 weights and the gradient through it, and the norms before and after a block with its gate and residual,
- * forward and backward.
+ * linear with AWQ int4 group-32 weights and the gradient through it, a whole mixture-of-experts layer for a few
+ * tokens, and the norms before and after a block with its gate and residual, forward and backward.
  *
  * The conventions of wqmlp.h hold for every call here: device pointers of the current device, 16-byte
  * aligned, dense row-major; nothing is allocated or synchronised and every call can be captured into a
@@ -49,6 +49,33 @@ int awq_linear_run(int64_t M, int64_t N, int64_t K, const void* x, int x_dtype, 
 size_t awq_linear_backward_workspace_bytes(int64_t M, int64_t N, int64_t K, int dy_dtype, int dx_dtype);
 int awq_linear_backward(int64_t M, int64_t N, int64_t K, const void* dy, int dy_dtype, const void* bank, int meta_layout,
                         void* workspace, size_t workspace_bytes, void* dx, int dx_dtype, void* stream);
+
+/*
+ * A mixture-of-experts layer with AWQ int4 group-32 experts for M tokens at once (moe_awq_m1_run is its step for
+ * one token and ready-made ids, in float16):
+ *   logits[m,e] = RN_f32(sum_h x[m,h] router[e,h]), summed in float64
+ *   ids[m,:]    the topk largest logits, largest first; equal ones by the lower index; NaN below all others
+ *   weights     softmax of the chosen logits (flags with WQ_MOE_RENORM) or their share in the softmax of all E
+ *   out[m,o]  = sum over k, in order, of weights[m,k] * sum_i act[m,k,i] dq2[e][o,i],  e = ids[m,k]
+ *   act[m,k,i] = silu(g) * u,  g = sum_h x[m,h] dq13[e][i,h],  u = the same with row i + I
+ *   x       [M, H]    WQ_F32, WQ_BF16 or WQ_F16
+ *   router  [E, H]    router_dtype (any of the three); NULL: ids and weights are inputs (flags is then 0), where an
+ *                     id outside [0, E) contributes nothing and repeated ids keep their weights
+ *   ids, weights [M, topk]  int32, float32
+ *   w13_bank, w2_bank as for moe_awq_m1_run; meta_layout 3 or 4
+ *   out     [M, H]    out_dtype (any of the three), rounded once
+ * 0 <= M <= WQ_MOE_MAX_TOKENS, 1 <= topk <= min(E, WQ_MOE_MAX_TOPK) (given ids: topk may exceed E), H and I
+ * multiples of 32.  Numerics as for awq_linear_run: products and sums are float32, float32 x and act enter as two
+ * float16 terms; no intermediate is rounded to 16 bits (moe_awq_m1_run rounds g, u, act and each route's result to
+ * float16).  A token's result is the same bits whatever the other tokens are and however many.  Where x holds an infinity or NaN its row's ids are those of the order above, and its out may be NaN.  An expert is
+ * read once for up to 16 of its tokens.
+ */
+#define WQ_MOE_MAX_TOKENS 256
+enum { WQ_MOE_RENORM = 1 };
+size_t moe_awq_workspace_bytes(int64_t M, int64_t E, int64_t topk, int64_t H, int64_t I);
+int moe_awq_run(int64_t M, int64_t E, int64_t topk, int64_t H, int64_t I, const void* x, int x_dtype, const void* router,
+                int router_dtype, int32_t* ids, float* weights, const void* w13_bank, const void* w2_bank, int meta_layout,
+                void* workspace, size_t workspace_bytes, void* out, int out_dtype, int flags, void* stream);
 
 /*
  * What stands between one block (an MLP, say) and the next: the norm of the block's result, its gate and

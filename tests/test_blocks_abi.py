@@ -153,3 +153,37 @@ def test_awq_linear_backward_empty_calls(L):
     assert L.awq_linear_backward_workspace_bytes(0, 48, 64, 0, 0) == 0
     assert L.awq_linear_backward_workspace_bytes(4, 48, 48, 0, 0) == 0
     assert L.awq_linear_backward_workspace_bytes(4, 48, 64, 2, 0) == 0
+
+
+MOE = ("M", "E", "topk", "H", "I", "x", "xt", "router", "rt", "ids", "w", "w13", "w2", "layout", "ws", "wsb", "out", "ot", "flags")
+
+
+def moe_args(**kw):
+    a = dict(M=4, E=8, topk=2, H=64, I=32, x=A, xt=1, router=A + MB, rt=0, ids=A + 2 * MB, w=A + 3 * MB, w13=A + 4 * MB, w2=A + 5 * MB, layout=3,
+             ws=A + 6 * MB, wsb=MB, out=A + 7 * MB, ot=2, flags=1)
+    a.update(kw)
+    return [a[k] for k in MOE] + [None]
+
+
+@pytest.mark.parametrize("kw,rc", [
+    (dict(x=None), EINVAL), (dict(ids=None), EINVAL), (dict(w=None), EINVAL), (dict(w13=None), EINVAL), (dict(w2=None), EINVAL),
+    (dict(out=None), EINVAL), (dict(xt=3), EINVAL), (dict(rt=3), EINVAL), (dict(ot=-1), EINVAL), (dict(layout=5), EINVAL),
+    (dict(M=-1), EINVAL), (dict(M=257), EINVAL), (dict(E=0), EINVAL), (dict(topk=0), EINVAL), (dict(topk=17, E=32), EINVAL),
+    (dict(topk=9), EINVAL), (dict(H=48), EINVAL), (dict(I=16), EINVAL), (dict(H=0), EINVAL), (dict(I=(1 << 22) + 32), EINVAL),
+    (dict(E=1 << 23, H=1 << 14), EINVAL), (dict(flags=2), EINVAL), (dict(router=None), EINVAL), (dict(router=None, flags=4), EINVAL),
+    (dict(x=A + 8), EALIGN), (dict(ids=A + 2 * MB + 4), EALIGN), (dict(w2=A + 5 * MB + 8), EALIGN), (dict(router=A + MB + 2), EALIGN),
+    (dict(ws=None), EWORKSPACE), (dict(wsb=256), EWORKSPACE),
+    (dict(out=A), EOVERLAP), (dict(out=A + 4 * MB), EOVERLAP), (dict(ids=A + 3 * MB), EOVERLAP), (dict(ids=A + 7 * MB), EOVERLAP),
+    (dict(w=A + 6 * MB), EOVERLAP), (dict(ws=A + MB), EOVERLAP), (dict(router=None, flags=0, out=A + 2 * MB), EOVERLAP),
+    (dict(router=None, flags=0, ws=A + 3 * MB), EOVERLAP),
+])
+def test_moe_refusals(L, kw, rc):
+    assert L.moe_awq_run(*moe_args(**kw)) == rc
+
+
+def test_moe_empty_calls(L):
+    assert L.moe_awq_run(*moe_args(M=0, x=None, ids=None, w=None, out=None, ws=None, wsb=0)) == 0
+    assert L.moe_awq_run(*moe_args(M=0, w13=None)) == EINVAL
+    assert L.moe_awq_workspace_bytes(0, 8, 2, 64, 32) == 0
+    assert L.moe_awq_workspace_bytes(257, 8, 2, 64, 32) == 0
+    assert L.moe_awq_workspace_bytes(4, 8, 2, 48, 32) == 0

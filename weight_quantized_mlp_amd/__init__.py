@@ -23,6 +23,7 @@ __all__ = [
     "WQ_LORA_MAX_RANK", "WQ_ADAMW_BLOCK", "WQ_ADAMW_KEEP_V", "lora_workspace_bytes", "lora_run", "lora_backward",
     "qlinear_backward_workspace_bytes", "qlinear_backward", "adamw_table_bytes", "AdamWTable", "adamw_table", "adamw_run",
     "awq_linear_workspace_bytes", "awq_linear_run", "awq_linear_backward_workspace_bytes", "awq_linear_backward",
+    "WQ_MOE_MAX_TOKENS", "WQ_MOE_RENORM", "moe_awq_workspace_bytes", "moe_awq_run",
     "block_norm_run", "block_norm_backward_workspace_bytes", "block_norm_backward",
 ]
 
@@ -35,6 +36,8 @@ WQ_STATIC_SCRATCH_BYTES = 32 << 20
 WQ_LORA_MAX_RANK = 256
 WQ_ADAMW_BLOCK = 256
 WQ_ADAMW_KEEP_V = 256
+WQ_MOE_MAX_TOKENS = 256
+WQ_MOE_RENORM = 1
 _PATHS = {"auto": WQ_PATH_AUTO, "gemv": WQ_PATH_GEMV, "mfma": WQ_PATH_MFMA}
 _STAGES = {None: 0, "gateup": WQ_STAGE_GATEUP_ONLY, "down": WQ_STAGE_DOWN_ONLY}
 _ACTS = {None: 0, "e4m3": WQ_ACT_E4M3}
@@ -80,6 +83,8 @@ _SIGS = {
     "awq_linear_run": (_INT, [_I64, _I64, _I64, _P, _INT, _P, _INT, _P, _SZ, _P, _P]),
     "awq_linear_backward_workspace_bytes": (_SZ, [_I64, _I64, _I64, _INT, _INT]),
     "awq_linear_backward": (_INT, [_I64, _I64, _I64, _P, _INT, _P, _INT, _P, _SZ, _P, _INT, _P]),
+    "moe_awq_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I64]),
+    "moe_awq_run": (_INT, [_I64, _I64, _I64, _I64, _I64, _P, _INT, _P, _INT, _P, _P, _P, _P, _INT, _P, _SZ, _P, _INT, _INT, _P]),
     "block_norm_run": (_INT, [_I64, _I64, _P, _INT, _P, _INT, _P, _P, _INT, _P, _I64, _INT, _F, _F, _F, _P, _P, _INT, _P]),
     "block_norm_backward_workspace_bytes": (_SZ, [_I64, _I64, _I64]),
     "block_norm_backward": (_INT, [_I64, _I64, _P, _INT, _P, _INT, _P, _P, _INT, _P, _P, _INT, _P, _I64, _INT, _F, _F, _F,
@@ -639,6 +644,60 @@ def awq_linear_backward(dy, bank, K, meta_layout=3, dtype=None, out=None, worksp
                                    _ptr(out), dxt, _stream(dev))
     _check("awq_linear_backward", rc)
     return out
+
+
+def moe_awq_workspace_bytes(M, E, topk, H, I):
+    return lib().moe_awq_workspace_bytes(M, E, topk, H, I)
+
+
+def moe_awq_run(x, w13_bank, w2_bank, E, I, topk=None, router=None, ids=None, weights=None, renorm=True, meta_layout=3,
+                dtype=None, out=None, workspace=None):
+    """A mixture-of-experts layer for the M <= WQ_MOE_MAX_TOKENS rows of x [M,H] f32/bf16/f16: the router's topk experts of
+    each row, their SwiGLU MLPs with AWQ weights (banks as for moe_awq_m1_run), their weighted sum.
+
+    With router [E,H] f32/bf16/f16 the call chooses: ids and weights [M,topk] (int32, f32) are written (allocated where not
+    given), the weights a softmax over the chosen logits, or with renorm=False their share in the softmax over all.  Without
+    router, ids and weights are inputs; ids outside [0, E) contribute nothing.  out [M,H] of `dtype` (default x's type, or
+    out's).  Returns (out, ids, weights)."""
+    dev = x.device
+    if x.dim() != 2:
+        raise ValueError("x must be [M, H]")
+    M, H = x.shape
+    xt = _float_code(x.dtype, "x")
+    _want(x, "x", x.dtype, dev, M * H)
+    want = _result_dtype("dtype", dtype, x.dtype, out=out)
+    ot = _float_code(want, "out")
+    rt = 0
+    if router is not None:
+        rt = _float_code(router.dtype, "router")
+        _want(router, "router", router.dtype, dev, E * H)
+        if topk is None:
+            raise ValueError("topk must be given with router")
+        if ids is None:
+            ids = torch.empty((M, topk), dtype=torch.int32, device=dev)
+        if weights is None:
+            weights = torch.empty((M, topk), dtype=torch.float32, device=dev)
+    elif ids is None or weights is None:
+        raise ValueError("without router, ids and weights must be given")
+    elif topk is None:
+        if ids.dim() != 2:
+            raise ValueError("ids must be [M, topk]")
+        topk = ids.shape[1]
+    _want(ids, "ids", torch.int32, dev, M * topk)
+    _want(weights, "weights", torch.float32, dev, M * topk)
+    _want(w13_bank, "w13_bank", torch.uint8, dev, awq_bank_bytes(E, 2 * I, H, meta_layout))
+    _want(w2_bank, "w2_bank", torch.uint8, dev, awq_bank_bytes(E, H, I, meta_layout))
+    if out is None:
+        out = torch.empty((M, H), dtype=want, device=dev)
+    else:
+        _want(out, "out", want, dev, M * H)
+    nb = moe_awq_workspace_bytes(M, E, topk, H, I)
+    ws = _workspace(nb, dev, workspace) if nb else None
+    rc = lib().moe_awq_run(M, E, topk, H, I, _ptr(x), xt, _ptr(router), rt, _ptr(ids), _ptr(weights), _ptr(w13_bank),
+                           _ptr(w2_bank), meta_layout, _ptr(ws), 0 if ws is None else ws.numel(), _ptr(out), ot,
+                           WQ_MOE_RENORM if router is not None and renorm else 0, _stream(dev))
+    _check("moe_awq_run", rc)
+    return out, ids, weights
 
 
 def _norm_args(h, y, post, gate, pre):

@@ -14,7 +14,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 SOURCES = ["abi.cpp", "abi_adapters.cpp", "abi_blocks.cpp", "adamw.hip", "awq_linear.hip", "block_norm.hip", "gemv.hip", "gemv_fast.hip", "linear_grad.hip", "lora.hip",
            "lora_expand.hip", "lora_outer.hip", "lora_shrink.hip",
-           "mfma.hip", "moe.hip", "pack.hip", "probe.hip"]
+           "mfma.hip", "moe.hip", "moe_layer.hip", "pack.hip", "probe.hip"]
 LIB = os.path.join(HERE, "libwqmlp.so")
 ARCH = "gfx950"
 FLAGS = ["-O3", "-fPIC", "-std=c++17", f"--offload-arch={ARCH}",

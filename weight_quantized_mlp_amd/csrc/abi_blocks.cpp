@@ -23,6 +23,11 @@ bool awq_shape_ok(int64_t M, int64_t N, int64_t K) {
          M * (N > K ? N : K) <= kMaxElems;
 }
 
+bool moe_shape_ok(int64_t M, int64_t E, int64_t topk, int64_t H, int64_t I) {
+  return M >= 0 && M <= WQ_MOE_MAX_TOKENS && E > 0 && E <= kMaxDim && topk > 0 && topk <= WQ_MOE_MAX_TOPK && H > 0 &&
+         H <= kMaxDim && H % 32 == 0 && I > 0 && 2 * I <= kMaxDim && I % 32 == 0 && E <= kMaxElems / H && E <= kMaxElems / (2 * I);
+}
+
 bool norm_shape_ok(int64_t M, int64_t H, int64_t G) {
   return M >= 0 && M <= kMaxDim && H > 0 && H <= kMaxDim && H % 8 == 0 && G > 0 && G <= kMaxDim && M % G == 0 &&
          M * H <= kMaxElems && G * H <= kMaxElems;
@@ -95,6 +100,37 @@ int awq_linear_backward(int64_t M, int64_t N, int64_t K, const void* dy, int dy_
   if (rc != WQ_OK) return rc;
   return launched(wq::launch_awq_linear_grad((int)M, (int)N, (int)K, dy, xtype(dy_dtype), static_cast<const uint8_t*>(bank),
                                              meta_layout, workspace, dx, xtype(dx_dtype), reinterpret_cast<hipStream_t>(stream)));
+}
+
+size_t moe_awq_workspace_bytes(int64_t M, int64_t E, int64_t topk, int64_t H, int64_t I) {
+  if (!moe_shape_ok(M, E, topk, H, I)) return 0;
+  return wq::moe_awq_scratch_bytes((int)M, (int)E, (int)topk, (int)H, (int)I);
+}
+
+int moe_awq_run(int64_t M, int64_t E, int64_t topk, int64_t H, int64_t I, const void* x, int x_dtype, const void* router,
+                int router_dtype, int32_t* ids, float* weights, const void* w13_bank, const void* w2_bank, int meta_layout,
+                void* workspace, size_t workspace_bytes, void* out, int out_dtype, int flags, void* stream) {
+  if (!moe_shape_ok(M, E, topk, H, I) || !is_float(x_dtype) || !is_float(out_dtype)) return WQ_EINVAL;
+  if (meta_layout != 3 && meta_layout != 4) return WQ_EINVAL;
+  if (router == nullptr ? flags != 0 : (!is_float(router_dtype) || topk > E || (flags & ~WQ_MOE_RENORM) != 0)) return WQ_EINVAL;
+  if (any_null({w13_bank, w2_bank})) return WQ_EINVAL;
+  if (M == 0) return WQ_OK;
+  if (any_null({x, ids, weights, out})) return WQ_EINVAL;
+  if (!all_aligned({x, router, ids, weights, w13_bank, w2_bank, workspace, out})) return WQ_EALIGN;
+  const size_t need = moe_awq_workspace_bytes(M, E, topk, H, I);
+  if (need && (workspace == nullptr || workspace_bytes < need)) return WQ_EWORKSPACE;
+  const Rng rx{x, (size_t)M * H * xsize(x_dtype)}, ri{ids, (size_t)M * topk * 4}, rw{weights, (size_t)M * topk * 4};
+  const Rng rr{router, router ? (size_t)E * H * xsize(router_dtype) : 0};
+  const Rng r13{w13_bank, awq_bank_bytes(E, 2 * I, H, meta_layout)}, r2{w2_bank, awq_bank_bytes(E, H, I, meta_layout)};
+  const Rng ro{out, (size_t)M * H * xsize(out_dtype)}, rs{workspace, need};
+  if (router != nullptr ? any_overlap({ro, rs, ri, rw}, {rx, rr, r13, r2}) : any_overlap({ro, rs}, {rx, ri, rw, r13, r2}))
+    return WQ_EOVERLAP;
+  const int rc = check_device({x, router, ids, weights, w13_bank, w2_bank, need ? workspace : nullptr, out});
+  if (rc != WQ_OK) return rc;
+  return launched(wq::launch_moe_awq((int)M, (int)E, (int)topk, (int)H, (int)I, x, xtype(x_dtype), router, xtype(router_dtype),
+                                     (flags & WQ_MOE_RENORM) != 0, ids, weights, static_cast<const uint8_t*>(w13_bank),
+                                     static_cast<const uint8_t*>(w2_bank), meta_layout, workspace, out, xtype(out_dtype),
+                                     reinterpret_cast<hipStream_t>(stream)));
 }
 
 int block_norm_run(int64_t M, int64_t H, const void* h, int h_dtype, const void* y, int y_dtype, const void* post,

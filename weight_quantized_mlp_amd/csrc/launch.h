@@ -150,6 +150,13 @@ size_t awq_linear_grad_scratch_bytes(int M, int N, int K, XType dyt, XType dxt);
 hipError_t launch_awq_linear_grad(int M, int N, int K, const void* dy, XType dyt, const uint8_t* bank, int meta_layout, void* ws,
                                   void* dx, XType dxt, hipStream_t st);
 
+// ---- routed experts of a few tokens (include/wqmlp_blocks.h) -----------------------------------------
+// router null: ids and weights are inputs, else they are written.
+size_t moe_awq_scratch_bytes(int M, int E, int topk, int H, int I);
+hipError_t launch_moe_awq(int M, int E, int topk, int H, int I, const void* x, XType xt, const void* router, XType rt, bool renorm,
+                          int32_t* ids, float* weights, const uint8_t* w13, const uint8_t* w2, int meta_layout, void* ws, void* out,
+                          XType ot, hipStream_t st);
+
 // ---- norms around a block (include/wqmlp_blocks.h) --------------------------------------------------
 struct BlockNorm {
   const void *h, *y, *post, *pre, *gate;   // y, post, pre, gate: null where absent
