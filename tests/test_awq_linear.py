@@ -205,7 +205,8 @@ def test_empty_and_refused_calls():
         wq.awq_linear_run(x, bank, 48, meta_layout=4)
     with pytest.raises(ValueError, match="contiguous"):
         wq.awq_linear_run(x.t().contiguous().t(), bank, 48)
+    assert wq.awq_linear_workspace_bytes(40, 48, 64, F32) > 64          # rows that are packed first
     with pytest.raises(wq.WQError):
-        wq.awq_linear_run(x, bank, 48, workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
+        wq.awq_linear_run(x.repeat(10, 1), bank, 48, workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
     with pytest.raises(wq.WQError):
         wq.awq_linear_run(x, bank, 48, out=x.view(-1)[:192].view(4, 48))

@@ -101,7 +101,7 @@ LIN = ("M", "N", "K", "x", "xt", "bank", "layout", "ws", "wsb", "y")
 
 
 def lin_args(**kw):
-    a = dict(M=4, N=48, K=64, x=A, xt=1, bank=A + MB, layout=3, ws=A + 2 * MB, wsb=MB, y=A + 3 * MB)
+    a = dict(M=40, N=48, K=64, x=A, xt=1, bank=A + MB, layout=3, ws=A + 2 * MB, wsb=MB, y=A + 3 * MB)
     a.update(kw)
     return [a[k] for k in LIN] + [None]
 

@@ -7,6 +7,8 @@
 // scale, one zero), and MFMA i of the step takes the group's dword i.  A dword decodes into the pairs (k, k + 4), so the
 // activations' octets are stored in the order 0 4 1 5 2 6 3 7.
 #pragma once
+#include <type_traits>
+
 #include "dev_common.h"
 #include "launch.h"
 
@@ -50,6 +52,66 @@ __device__ __forceinline__ void awq_meta(const AwqStep& r, bool live, f16x2& s2,
   b2 = f16x2{bv, bv};
 }
 
+// A lane's share of 4 whole steps (16 groups, none past the row's end): codes of the groups g, g + 4, g + 8, g + 12, and the
+// metadata of 4 neighbouring groups from m on, which are those of the four quarters' lanes (awq_transpose).
+template <int ML>
+struct AwqBlock {
+  u32x4 c[4];
+  u32x2 s;
+  std::conditional_t<ML == 3, uint32_t, u32x2> z;
+};
+template <int ML>
+__device__ __forceinline__ AwqBlock<ML> awq_load_block(const uint8_t* codes, const uint8_t* expert, const AwqLayout& L, int64_t row, int m,
+                                                       int g) {
+  typedef uint32_t u32x2_a2 __attribute__((ext_vector_type(2), aligned(2)));
+  typedef uint32_t u32_a1 __attribute__((aligned(1)));
+  AwqBlock<ML> r;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) r.c[t] = *reinterpret_cast<const u32x4*>(codes + 16 * (g + 4 * t));
+  const int64_t at = row * L.G + m;
+  r.s = *reinterpret_cast<const u32x2_a2*>(expert + L.scale_off + 2 * at);
+  if constexpr (ML == 3) r.z = *reinterpret_cast<const u32_a1*>(expert + L.meta2_off + at);
+  else r.z = *reinterpret_cast<const u32x2_a2*>(expert + L.meta2_off + 2 * at);
+  return r;
+}
+// m[t]: scale (low half) and zero or bias (high half) of the lane's group in step t.  Quarter q holds those of groups 4 q .. 4 q + 3 and
+// wants those of q, q + 4, q + 8, q + 12: a 4 x 4 transpose over the quarters, by exchanging halves of the wave, then quarters.
+template <int ML>
+__device__ __forceinline__ void awq_transpose(const AwqBlock<ML>& b, uint32_t (&m)[4]) {
+  if constexpr (ML == 3) {
+    m[0] = (b.s.x & 0xFFFFu) | ((b.z & 255u) << 16);
+    m[1] = (b.s.x >> 16) | ((b.z & 0xFF00u) << 8);
+    m[2] = (b.s.y & 0xFFFFu) | (b.z & 0xFF0000u);
+    m[3] = (b.s.y >> 16) | ((b.z >> 8) & 0xFF0000u);
+  } else {
+    m[0] = (b.s.x & 0xFFFFu) | (b.z.x << 16);
+    m[1] = (b.s.x >> 16) | (b.z.x & 0xFFFF0000u);
+    m[2] = (b.s.y & 0xFFFFu) | (b.z.y << 16);
+    m[3] = (b.s.y >> 16) | (b.z.y & 0xFFFF0000u);
+  }
+  auto halves = [](uint32_t& a, uint32_t& c) {
+    const auto r = __builtin_amdgcn_permlane32_swap(a, c, false, false);
+    a = r[0], c = r[1];
+  };
+  auto quarters = [](uint32_t& a, uint32_t& c) {
+    const auto r = __builtin_amdgcn_permlane16_swap(a, c, false, false);
+    a = r[0], c = r[1];
+  };
+  halves(m[0], m[2]);
+  halves(m[1], m[3]);
+  quarters(m[0], m[1]);
+  quarters(m[2], m[3]);
+}
+template <int ML>
+__device__ __forceinline__ void awq_meta_of(uint32_t m, f16x2& s2, f16x2& b2) {
+  const _Float16 s = f16_from_bits((uint16_t)m);
+  _Float16 b;
+  if constexpr (ML == 3) b = awq_bias(m >> 16, s);
+  else b = f16_from_bits((uint16_t)(m >> 16));
+  s2 = f16x2{s, s};
+  b2 = f16x2{b, b};
+}
+
 // What float16 h left of x; nothing where h is infinite or NaN (x - h would be NaN and the infinity lose its sign).
 __device__ __forceinline__ _Float16 f16_rest(float x, _Float16 h) {
   const float r = x - (float)h;
@@ -75,32 +137,39 @@ __device__ __forceinline__ void octet_terms(const float* v, int e, u32x4 (&o)[TE
     o[1] = lo;
   }
 }
-// 8 elements of a row of x at element `at` (16-byte aligned).
+// 8 elements of a row of x at element `at` (16-byte aligned), as loaded and as values.
 template <int XT>
-__device__ __forceinline__ void load_octet(const void* x, size_t at, float* v) {
-  if constexpr (XT == X_F32) {
-    const f32x4* p = reinterpret_cast<const f32x4*>(reinterpret_cast<const float*>(x) + at);
-    const f32x4 a = p[0], b = p[1];
+struct RawOctet { u32x4 v[XT == X_F32 ? 2 : 1]; };
+template <int XT>
+__device__ __forceinline__ RawOctet<XT> load_raw(const void* x, size_t at) {
+  const u32x4* p = reinterpret_cast<const u32x4*>(reinterpret_cast<const uint8_t*>(x) + at * (XT == X_F32 ? 4 : 2));
+  RawOctet<XT> r;
+  r.v[0] = p[0];
+  if constexpr (XT == X_F32) r.v[1] = p[1];
+  return r;
+}
+template <int XT>
+__device__ __forceinline__ void raw_values(const RawOctet<XT>& r, float* v) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[j] = a[j];
-      v[4 + j] = b[j];
-    }
-  } else {
-    const u32x4 a = *reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(x) + at);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t u = a[j];
-      if constexpr (XT == X_BF16) {
-        v[2 * j] = __uint_as_float(u << 16);
-        v[2 * j + 1] = __uint_as_float(u & 0xFFFF0000u);
-      } else {
-        const f16x2 p = as_f16x2(u);
-        v[2 * j] = (float)p.x;
-        v[2 * j + 1] = (float)p.y;
-      }
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t u = r.v[0][j];
+    if constexpr (XT == X_F32) {
+      const uint32_t w = r.v[1][j];
+      v[j] = __uint_as_float(u);
+      v[4 + j] = __uint_as_float(w);
+    } else if constexpr (XT == X_BF16) {
+      v[2 * j] = __uint_as_float(u << 16);
+      v[2 * j + 1] = __uint_as_float(u & 0xFFFF0000u);
+    } else {
+      const f16x2 p = as_f16x2(u);
+      v[2 * j] = (float)p.x;
+      v[2 * j + 1] = (float)p.y;
     }
   }
+}
+template <int XT>
+__device__ __forceinline__ void load_octet(const void* x, size_t at, float* v) {
+  raw_values<XT>(load_raw<XT>(x, at), v);
 }
 
 // float32 rows take two float16 terms (their products' sum is off by 2^-22 of an element or 2^-39 of its row's largest), bfloat16

@@ -2,10 +2,10 @@
 //   y[m,n] = sum_k x[m,k] dq[n,k],  dq = RN_f16(q scale + bias) exactly as the routed step decodes it.
 //
 // The weights are decoded in registers, straight from the packed bytes, into matrix-core operands (awq_common.h); x is
-// turned into float16 terms once (awq_pack_kernel), in the order the matrix cores read it.
-//   Up to kSkinnyRows rows (awq_skinny_kernel): the weights' bytes bound it.  A workgroup's 8 waves split the
-//     contraction of the same weight rows and add up through LDS, so a few rows of weights still fill a CU; x comes
-//     from L2 as whole fragments.
+// turned into float16 terms (awq_pack_kernel), in the order the matrix cores read it.
+//   Up to kFewRows rows (awq_rows_kernel): the weights' bytes bound it.  A workgroup's waves split the contraction of the
+//     same weight rows and add up through LDS, so a few rows of weights still fill a CU.  Up to kOwnRows rows of x are
+//     turned into terms by the waves themselves, which spares a launch; more come from L2 as packed fragments.
 //   More rows (awq_gemm_kernel): the matrix cores bound it.  4 waves with 64 weight rows each share the tile of x through
 //     LDS (global->LDS copies, two stages); every wave decodes only its own weights, once per tile row.
 // Either splits the contraction over workgroups when there are few tiles; awq_join_kernel adds the parts in order.
@@ -19,7 +19,7 @@ namespace wq {
 
 namespace {
 
-constexpr int kSkinnyRows = 32;
+constexpr int kFewRows = 32;
 
 // ---- x -> float16 terms in fragment order ------------------------------------------------------------------------
 // xp[m / 16][step][term][i][lane][8]: lane = 16 * quarter + m % 16 holds octet i of group 4 step + quarter of row m.
@@ -73,17 +73,30 @@ __global__ void __launch_bounds__(256) awq_pack_kernel(int M, int K, int steps, 
 }
 
 // ---- few rows ----------------------------------------------------------------------------------------------------
-// RT tiles of 16 weight rows, CT tiles of 16 rows of x; part blockIdx.y of the steps.
-template <int ML, int TERMS, int RT, int CT>
-__global__ void __launch_bounds__(512) awq_skinny_kernel(int M, int N, int steps, int per, const uint8_t* __restrict__ xp,
-                                                         const float* __restrict__ rowscale, const uint8_t* __restrict__ bank,
-                                                         AwqLayout L, float* __restrict__ y, float* __restrict__ partials) {
-  constexpr int COLS = 16 * RT + 4;                          // floats of an LDS row: n, padded
-  extern __shared__ __attribute__((aligned(16))) float part[];   // [8 waves][16 CT][COLS]
+// A block is 4 steps: 16 groups, 512 k, of 16 weight rows: 4 loads of 1 KB of codes, and one 8-byte and one 4- or 8-byte load of metadata,
+// all in flight at once, the next block's behind this one's products.  A lane's 4 contiguous groups of metadata belong to one step of each
+// of the four quarters: a 4 x 4 transpose between the quarters (awq_transpose).
+constexpr int kBlockSteps = 4;
+constexpr int kOwnRows = 4;                    // rows of x that the waves turn into terms themselves
+constexpr int kPackedRows = 3;                 // in place of x's type: x comes packed
+
+struct RowsPlan {
+  int steps, blocks, per, waves;               // blocks per part, waves per workgroup
+};
+
+// XS: x's type, or kPackedRows.  In the first case MR rows of x: a wave scales its own 512 k of a row by their own power of two, so
+// that no wave waits for another before the sums meet.  In the second CT tiles of 16 rows.  Part blockIdx.y of the blocks.
+template <int ML, int TERMS, int RT, int CT, int XS, int MR>
+__global__ void __launch_bounds__(768) awq_rows_kernel(int M, int N, int K, RowsPlan p, const void* __restrict__ x,
+                                                       const float* __restrict__ rowscale, const uint8_t* __restrict__ bank,
+                                                       AwqLayout L, float* __restrict__ y, float* __restrict__ partials) {
+  constexpr bool OWN = XS != kPackedRows;
+  constexpr int COLS = 16 * RT + 4;                             // floats of an LDS row of sums: n, padded
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];   // OWN: a wave's terms [MR][TERMS][1 KB]; then the sums [wave][m][COLS]
   const AwqDecode dc = awq_decode_consts();
-  const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int n0 = (int)blockIdx.x * 16 * RT, q = lane >> 4;
-  const int s0 = (int)blockIdx.y * per, s1 = min(s0 + per, steps), last = s1 - 1;
+  const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), q = lane >> 4;
+  const int n0 = (int)blockIdx.x * 16 * RT, G = (int)L.G;
+  const int b0 = (int)blockIdx.y * p.per, b1 = min(b0 + p.per, p.blocks);
   const uint8_t* codes[RT];
   int64_t row[RT];
 #pragma unroll
@@ -96,63 +109,169 @@ __global__ void __launch_bounds__(512) awq_skinny_kernel(int M, int N, int steps
   for (int r = 0; r < RT; ++r)
 #pragma unroll
     for (int c = 0; c < CT; ++c) acc[r][c] = f32x4{0.f, 0.f, 0.f, 0.f};
-  struct Step {
-    AwqStep w[RT];
-    f16x8 x[CT][TERMS][4];
+  uint8_t* own = lds + wave * (MR * TERMS * 1024);
+  const uint8_t* xs = own + min(lane & 15, MR - 1) * (TERMS * 1024) + q * 64;
+
+  struct Block {
+    RawOctet<XS> x[OWN ? MR : 1];
+    AwqBlock<ML> w[RT];
   };
-  auto load = [&](int s, Step& d) {
-    const int sc = min(s, last);
+  auto load = [&](int b, Block& d) {                            // x first: its wait then leaves the weights out
+    if constexpr (OWN) {
+      const int o = 64 * b + lane;
 #pragma unroll
-    for (int r = 0; r < RT; ++r) d.w[r] = awq_load<ML>(codes[r], bank, L, row[r], 4 * sc + q);
+      for (int m = 0; m < MR; ++m) d.x[m] = load_raw<XS>(x, (size_t)min(m, M - 1) * K + 8 * (size_t)min(o, K / 8 - 1));
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r) d.w[r] = awq_load_block<ML>(codes[r], bank, L, row[r], 16 * b + 4 * q, 16 * b + q);
+  };
+  // A wave's 64 octets of a block of each row -> terms in its LDS; the powers of two.
+  auto own_terms = [&](int b, const RawOctet<XS>* raw, float* scale) {
+    wave_lds_fence();                                           // the last block's fragments are in registers
+#pragma unroll
+    for (int m = 0; m < MR; ++m) {
+      float v[8];
+      raw_values<XS>(raw[m], v);
+      if (64 * b + lane >= K / 8)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.f;
+      int e = 0;
+      if constexpr (XS != X_F16) {
+        float amax = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, finite_abs(v[j]));
+        e = f16_row_exp(wave64_max(amax));
+      }
+      scale[m] = ldexpf(1.f, e);
+      u32x4 t[TERMS];
+      octet_terms<TERMS>(v, e, t);
+#pragma unroll
+      for (int j = 0; j < TERMS; ++j) *reinterpret_cast<u32x4*>(own + (m * TERMS + j) * 1024 + lane * 16) = t[j];
+    }
+    wave_lds_fence();
+  };
+  auto load_x = [&](int step, int t, f16x8 (&f)[CT][TERMS][4]) {   // step t of its block
 #pragma unroll
     for (int c = 0; c < CT; ++c)
 #pragma unroll
-      for (int t = 0; t < TERMS; ++t)
+      for (int j = 0; j < TERMS; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) d.x[c][t][i] = *reinterpret_cast<const f16x8*>(xp + frag_at(c, steps, sc, TERMS, t, i, lane));
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (OWN) f[c][j][i] = *reinterpret_cast<const f16x8*>(xs + j * 1024 + t * 256 + i * 16);
+          else f[c][j][i] = *reinterpret_cast<const f16x8*>(static_cast<const uint8_t*>(x) + frag_at(c, p.steps, step, TERMS, j, i, lane));
+        }
   };
-  auto multiply = [&](int s, const Step& d) {
+  auto step_mfmas = [&](f32x4 (&sum)[RT][CT], const u32x4* c, const f16x2* s2, const f16x2* b2, const f16x8 (&f)[CT][TERMS][4]) {
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      f16x2 s2, b2;
-      awq_meta<ML>(d.w[r], 4 * s + q < (int)L.G, s2, b2);
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f16x8 w = awq_frag(d.w[r].c[i], s2, b2, dc);
+      for (int r = 0; r < RT; ++r) {
+        const f16x8 wf = awq_frag(c[r][i], s2[r], b2[r], dc);
 #pragma unroll
-        for (int c = 0; c < CT; ++c)
+        for (int j = 0; j < CT; ++j)
 #pragma unroll
-          for (int t = 0; t < TERMS; ++t) acc[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, d.x[c][t][i], acc[r][c], 0, 0, 0);
+          for (int t = 0; t < TERMS; ++t) sum[r][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wf, f[j][t][i], sum[r][j], 0, 0, 0);
       }
-    }
   };
-  int s = s0 + wave;
-  if (s < s1) {
-    Step a, b;
-    load(s, a);
-    for (; s + 8 < s1; s += 16) {
-      load(s + 8, b);
-      multiply(s, a);
-      load(s + 16, a);
-      multiply(s + 8, b);
+  // The block's sums join the wave's: scaled back, where the block has its own powers of two (lane's column = row lane % 16 of x).
+  auto join = [&](f32x4 (&sum)[RT][CT], const float* scale) {
+    float rs = scale[0];
+#pragma unroll
+    for (int m = 1; m < MR; ++m) rs = (lane & 15) >= m ? scale[m] : rs;
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[r][0][j] = fmaf(sum[r][0][j], rs, acc[r][0][j]);
+  };
+  auto whole = [&](int b, const Block& d) {
+    f32x4 sum[RT][CT];
+    float scale[MR];
+    if constexpr (OWN) {
+      own_terms(b, d.x, scale);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) sum[r][0] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
-    if (s < s1) multiply(s, a);
+    uint32_t meta[RT][4];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) awq_transpose<ML>(d.w[r], meta[r]);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      f16x8 f[CT][TERMS][4];
+      load_x(b * kBlockSteps + t, t, f);
+      f16x2 s2[RT], b2[RT];
+      u32x4 c[RT];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        awq_meta_of<ML>(meta[r][t], s2[r], b2[r]);
+        c[r] = d.w[r].c[t];
+      }
+      if constexpr (OWN) step_mfmas(sum, c, s2, b2, f);
+      else step_mfmas(acc, c, s2, b2, f);
+    }
+    if constexpr (OWN) join(sum, scale);
+  };
+  const int full = min(b1, G / 16);                             // blocks of whole rows end here
+  int b = b0 + wave;
+  if (b < full) {
+    Block u, v;
+    load(b, u);
+    for (; b + p.waves < full; b += 2 * p.waves) {
+      load(b + p.waves, v);
+      whole(b, u);
+      load(min(b + 2 * p.waves, full - 1), u);
+      whole(b + p.waves, v);
+    }
+    if (b < full) {
+      whole(b, u);
+      b += p.waves;
+    }
+  }
+  if (b == full && full < b1) {                                 // the row's last groups, fewer than a block: step by step
+    f32x4 sum[RT][CT];
+    float scale[MR];
+    if constexpr (OWN) {
+      RawOctet<XS> raw[MR];
+#pragma unroll
+      for (int m = 0; m < MR; ++m) raw[m] = load_raw<XS>(x, (size_t)min(m, M - 1) * K + 8 * (size_t)min(64 * b + lane, K / 8 - 1));
+      own_terms(b, raw, scale);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) sum[r][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    for (int s = b * kBlockSteps; s < p.steps; ++s) {
+      f16x8 f[CT][TERMS][4];
+      load_x(s, s - b * kBlockSteps, f);
+      f16x2 s2[RT], b2[RT];
+      u32x4 c[RT];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const AwqStep a = awq_load<ML>(codes[r], bank, L, row[r], 4 * s + q);
+        awq_meta<ML>(a, 4 * s + q < G, s2[r], b2[r]);
+        c[r] = a.c;
+      }
+      if constexpr (OWN) step_mfmas(sum, c, s2, b2, f);
+      else step_mfmas(acc, c, s2, b2, f);
+    }
+    if constexpr (OWN) join(sum, scale);
   }
   // the waves' sums, in order
+  if constexpr (OWN) __syncthreads();                           // every wave is done with its terms
+  float* part = reinterpret_cast<float*>(lds);
 #pragma unroll
-  for (int r = 0; r < RT; ++r)
+  for (int j = 0; j < CT; ++j) {
+    const int m = 16 * j + (lane & 15);
+    if (m < M)
 #pragma unroll
-    for (int c = 0; c < CT; ++c)
-      *reinterpret_cast<f32x4*>(part + (wave * 16 * CT + 16 * c + (lane & 15)) * COLS + 16 * r + 4 * q) = acc[r][c];
+      for (int r = 0; r < RT; ++r) *reinterpret_cast<f32x4*>(part + (wave * M + m) * COLS + 16 * r + 4 * q) = acc[r][j];
+  }
   __syncthreads();
-  for (int i = tid; i < 16 * CT * 16 * RT; i += 512) {
+  for (int i = tid; i < M * 16 * RT; i += 64 * p.waves) {
     const int m = i / (16 * RT), j = i - m * 16 * RT, n = n0 + j;
-    if (m >= M || n >= N) continue;
+    if (n >= N) continue;
     float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) v += part[(w * 16 * CT + m) * COLS + j];
+    for (int k = 0; k < p.waves; ++k) v += part[(k * M + m) * COLS + j];
+    if constexpr (!OWN) v *= rowscale[m];
     if (partials != nullptr) partials[((size_t)blockIdx.y * M + m) * N + n] = v;
-    else y[(size_t)m * N + n] = v * rowscale[m];
+    else y[(size_t)m * N + n] = v;
   }
 }
 
@@ -247,7 +366,7 @@ __global__ void __launch_bounds__(256, 2) awq_gemm_kernel(int M, int N, int step
   for (int c = 0; c < MT; ++c) {
     const int m = 16 * (mt0 + c) + (lane & 15);
     if (m >= M) continue;
-    const float rs = partials != nullptr ? 1.f : rowscale[m];
+    const float rs = rowscale[m];
 #pragma unroll
     for (int r = 0; r < NT; ++r) {
       const int n = n0 + 16 * r + 4 * q;
@@ -264,51 +383,53 @@ __global__ void __launch_bounds__(256, 2) awq_gemm_kernel(int M, int N, int step
   }
 }
 
-// y = row scale times the sum of the S parts, in order.
-__global__ void __launch_bounds__(256) awq_join_kernel(int M, int N, int S, const float* __restrict__ partials,
-                                                       const float* __restrict__ rowscale, float* __restrict__ y) {
+// y = the sum of the S parts, in order.
+__global__ void __launch_bounds__(256) awq_join_kernel(int M, int N, int S, const float* __restrict__ partials, float* __restrict__ y) {
   const int n = (int)blockIdx.x * 256 + (int)threadIdx.x, m = (int)blockIdx.y;
   if (n >= N) return;
   const size_t at = (size_t)m * N + n, part = (size_t)M * N;
   float v = partials[at];
   for (int s = 1; s < S; ++s) v += partials[s * part + at];
-  y[at] = v * rowscale[m];
+  y[at] = v;
 }
 
 // ---- plan --------------------------------------------------------------------------------------------------------
 struct AwqPlan {
-  bool skinny;
+  bool rows, own;              // few rows; so few that the waves turn them into terms themselves (no packing)
   int terms, steps, S, per;
-  int rt, ct;                  // skinny: row tiles, column tiles
-  int mt, ntm, tiles;          // gemm
+  int rt, ct, waves;           // few rows: row tiles, column tiles, waves
+  int mt, ntm, tiles;          // many rows
   size_t xp, rs, partials, total;
 };
 inline AwqPlan awq_plan(int M, int N, int K, XType xt) {
   AwqPlan p{};
   p.terms = awq_terms(xt);
   p.steps = (K + kStepK - 1) / kStepK;
-  p.skinny = M <= kSkinnyRows;
-  int64_t wgs;
-  int want, least;             // workgroups that fill the chip; least steps of a part
-  if (p.skinny) {
+  p.rows = M <= kFewRows;
+  const int64_t most = std::max<int64_t>(1, ((int64_t)64 << 20) / ((int64_t)M * N * 4));   // at most 64 MiB of parts
+  if (p.rows) {
+    const int blocks = (p.steps + kBlockSteps - 1) / kBlockSteps;
+    p.own = M <= kOwnRows;
     p.ct = M <= 16 ? 1 : 2;
-    p.rt = N >= 16 * 1024 ? 4 : (N >= 4096 ? 2 : 1);
-    wgs = (N + 16 * p.rt - 1) / (16 * p.rt);
-    want = 512, least = 32;    // four steps for each of the 8 waves
+    p.rt = 1;
+    const int64_t wgs = (N + 16 * p.rt - 1) / (16 * p.rt);
+    const int64_t S = std::min(std::max<int64_t>(1, std::min<int64_t>(256 / wgs, blocks / 12)), most);
+    p.per = (int)((blocks + S - 1) / S);
+    p.S = (blocks + p.per - 1) / p.per;
+    // waves: what the chip holds (20 per CU), at least 4 and at most 12, and no more than its number of turns needs
+    const int top = (int)std::min<int64_t>(12, std::max<int64_t>(4, 5120 / (wgs * p.S) + 1)), turns = (p.per + top - 1) / top;
+    p.waves = (p.per + turns - 1) / turns;
   } else {
     p.mt = p.terms == 2 || M <= 64 ? 4 : 8;
     p.ntm = (M + 16 * p.mt - 1) / (16 * p.mt);
     p.tiles = p.ntm * ((N + kGemmCols - 1) / kGemmCols);
-    wgs = p.tiles;
-    want = 512, least = 4;
+    const int64_t S = std::min(std::max<int64_t>(1, std::min<int64_t>(512 / p.tiles, p.steps / 4)), most);
+    p.per = (int)((p.steps + S - 1) / S);
+    p.S = (p.steps + p.per - 1) / p.per;
   }
-  int64_t S = std::max<int64_t>(1, std::min<int64_t>(want / wgs, p.steps / least));
-  S = std::min<int64_t>(S, std::max<int64_t>(1, ((int64_t)64 << 20) / ((int64_t)M * N * 4)));   // at most 64 MiB of parts
-  p.per = (int)((p.steps + S - 1) / S);
-  p.S = (p.steps + p.per - 1) / p.per;
   p.xp = 0;
-  p.rs = align256((size_t)((M + 15) / 16) * p.steps * p.terms * 4096);
-  p.partials = p.rs + align256((size_t)(M + 15) / 16 * 16 * 4);
+  p.rs = p.own ? 0 : align256((size_t)((M + 15) / 16) * p.steps * p.terms * 4096);
+  p.partials = p.own ? 0 : p.rs + align256((size_t)(M + 15) / 16 * 16 * 4);
   p.total = p.partials + (p.S > 1 ? align256((size_t)p.S * M * N * 4) : 0);
   return p;
 }
@@ -319,38 +440,58 @@ void pack_rows(int M, int K, int steps, const void* x, uint8_t* xp, float* rs, h
   hipLaunchKernelGGL((awq_pack_kernel<XT, TERMS>), dim3(grid), dim3(256), 0, st, M, K, steps, x, xp, rs);
 }
 
-template <int ML, int TERMS, int RT, int CT>
-hipError_t run_skinny(const AwqPlan& p, int M, int N, const uint8_t* xp, const float* rs, const uint8_t* bank, const AwqLayout& L,
-                      float* y, float* partials, hipStream_t st) {
-  if (!raise_lds_limit<awq_skinny_kernel<ML, TERMS, RT, CT>>()) return hipErrorInvalidValue;
-  const int lds = 8 * 16 * CT * (16 * RT + 4) * 4;
-  hipLaunchKernelGGL((awq_skinny_kernel<ML, TERMS, RT, CT>), dim3((N + 16 * RT - 1) / (16 * RT), p.S), dim3(512), lds, st, M, N,
-                     p.steps, p.per, xp, rs, bank, L, y, partials);
+template <int ML, int TERMS, int RT, int CT, int XS, int MR>
+hipError_t run_rows(const AwqPlan& p, int M, int N, int K, const void* x, const float* rs, const uint8_t* bank, const AwqLayout& L, float* y,
+                    float* partials, hipStream_t st) {
+  if (!raise_lds_limit<awq_rows_kernel<ML, TERMS, RT, CT, XS, MR>>()) return hipErrorInvalidValue;
+  const int sums = p.waves * M * (16 * RT + 4) * 4, own = XS == kPackedRows ? 0 : p.waves * MR * TERMS * 1024;
+  const RowsPlan r{p.steps, (p.steps + kBlockSteps - 1) / kBlockSteps, p.per, p.waves};
+  hipLaunchKernelGGL((awq_rows_kernel<ML, TERMS, RT, CT, XS, MR>), dim3((N + 16 * RT - 1) / (16 * RT), p.S), dim3(64 * p.waves),
+                     std::max(sums, own), st, M, N, K, r, x, rs, bank, L, y, partials);
   return hipGetLastError();
 }
 template <int ML, int TERMS, int MT>
-hipError_t run_gemm(const AwqPlan& p, int M, int N, const uint8_t* xp, const float* rs, const uint8_t* bank, const AwqLayout& L,
+hipError_t run_gemm(const AwqPlan& p, int M, int N, int, const void* xp, const float* rs, const uint8_t* bank, const AwqLayout& L,
                     float* y, float* partials, hipStream_t st) {
   if (!raise_lds_limit<awq_gemm_kernel<ML, TERMS, MT>>()) return hipErrorInvalidValue;
   hipLaunchKernelGGL((awq_gemm_kernel<ML, TERMS, MT>), dim3((p.tiles + 7) / 8 * 8, p.S), dim3(256), 2 * MT * TERMS * 4096, st, M, N,
-                     p.steps, p.per, p.ntm, p.tiles, xp, rs, bank, L, y, partials);
+                     p.steps, p.per, p.ntm, p.tiles, static_cast<const uint8_t*>(xp), rs, bank, L, y, partials);
   return hipGetLastError();
 }
-template <int ML, int TERMS, typename... A>
-hipError_t run_plan(const AwqPlan& p, A... a) {
-  if (!p.skinny) {
-    if constexpr (TERMS == 1)
-      if (p.mt == 8) return run_gemm<ML, TERMS, 8>(p, a...);
-    return run_gemm<ML, TERMS, 4>(p, a...);
+template <int ML, int XT, typename... A>
+hipError_t run_plan(const AwqPlan& p, int M, A... a) {
+  constexpr int T = XT == X_F32 ? 2 : 1;
+  if (!p.rows) {
+    if constexpr (T == 1)
+      if (p.mt == 8) return run_gemm<ML, T, 8>(p, M, a...);
+    return run_gemm<ML, T, 4>(p, M, a...);
   }
-  if (p.ct == 1) {
-    if (p.rt == 4) return run_skinny<ML, TERMS, 4, 1>(p, a...);
-    if (p.rt == 2) return run_skinny<ML, TERMS, 2, 1>(p, a...);
-    return run_skinny<ML, TERMS, 1, 1>(p, a...);
+  if (p.own) {
+    if (M == 1) return run_rows<ML, T, 1, 1, XT, 1>(p, M, a...);
+    if (M == 2) return run_rows<ML, T, 1, 1, XT, 2>(p, M, a...);
+    return run_rows<ML, T, 1, 1, XT, 4>(p, M, a...);
   }
-  if (p.rt == 4) return run_skinny<ML, TERMS, 4, 2>(p, a...);
-  if (p.rt == 2) return run_skinny<ML, TERMS, 2, 2>(p, a...);
-  return run_skinny<ML, TERMS, 1, 2>(p, a...);
+  if (p.ct == 1) return run_rows<ML, T, 1, 1, kPackedRows, 1>(p, M, a...);
+  return run_rows<ML, T, 1, 2, kPackedRows, 1>(p, M, a...);
+}
+template <int XT>
+hipError_t linear(const AwqPlan& p, int M, int N, int K, const void* x, const uint8_t* bank, int meta_layout, uint8_t* ws, float* y,
+                  hipStream_t st) {
+  const AwqLayout L = awq_layout(N, K, meta_layout);
+  uint8_t* xp = ws + p.xp;
+  float* rs = reinterpret_cast<float*>(ws + p.rs);
+  float* partials = p.S > 1 ? reinterpret_cast<float*>(ws + p.partials) : nullptr;
+  if (!p.own) {
+    pack_rows<XT, XT == X_F32 ? 2 : 1>(M, K, p.steps, x, xp, rs, st);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    x = xp;
+  }
+  const hipError_t e = meta_layout == 3 ? run_plan<3, XT>(p, M, N, K, x, rs, bank, L, y, partials, st)
+                                        : run_plan<4, XT>(p, M, N, K, x, rs, bank, L, y, partials, st);
+  if (e != hipSuccess || partials == nullptr) return e;
+  hipLaunchKernelGGL(awq_join_kernel, dim3((N + 255) / 256, M), dim3(256), 0, st, M, N, p.S, partials, y);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -360,23 +501,10 @@ size_t awq_linear_scratch_bytes(int M, int N, int K, XType xt) { return M == 0 ?
 hipError_t launch_awq_linear(int M, int N, int K, const void* x, XType xt, const uint8_t* bank, int meta_layout, void* ws, float* y,
                              hipStream_t st) {
   const AwqPlan p = awq_plan(M, N, K, xt);
-  const AwqLayout L = awq_layout(N, K, meta_layout);
-  uint8_t* base = reinterpret_cast<uint8_t*>(ws);
-  uint8_t* xp = base + p.xp;
-  float* rs = reinterpret_cast<float*>(base + p.rs);
-  float* partials = p.S > 1 ? reinterpret_cast<float*>(base + p.partials) : nullptr;
-  if (xt == X_F32) pack_rows<X_F32, 2>(M, K, p.steps, x, xp, rs, st);
-  else if (xt == X_BF16) pack_rows<X_BF16, 1>(M, K, p.steps, x, xp, rs, st);
-  else pack_rows<X_F16, 1>(M, K, p.steps, x, xp, rs, st);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  if (meta_layout == 3)
-    e = p.terms == 2 ? run_plan<3, 2>(p, M, N, xp, rs, bank, L, y, partials, st) : run_plan<3, 1>(p, M, N, xp, rs, bank, L, y, partials, st);
-  else
-    e = p.terms == 2 ? run_plan<4, 2>(p, M, N, xp, rs, bank, L, y, partials, st) : run_plan<4, 1>(p, M, N, xp, rs, bank, L, y, partials, st);
-  if (e != hipSuccess || partials == nullptr) return e;
-  hipLaunchKernelGGL(awq_join_kernel, dim3((N + 255) / 256, M), dim3(256), 0, st, M, N, p.S, partials, rs, y);
-  return hipGetLastError();
+  uint8_t* base = static_cast<uint8_t*>(ws);
+  if (xt == X_F32) return linear<X_F32>(p, M, N, K, x, bank, meta_layout, base, y, st);
+  if (xt == X_BF16) return linear<X_BF16>(p, M, N, K, x, bank, meta_layout, base, y, st);
+  return linear<X_F16>(p, M, N, K, x, bank, meta_layout, base, y, st);
 }
 
 }  // namespace wq
