@@ -4,11 +4,14 @@
 // One MFMA (16 x 16 x 32, float16) takes 8 contraction elements from each lane: lane l holds row l % 16 of the weights and
 // the octet l / 16 of the step.  Which k an octet's place stands for is free as long as both operands agree, so the weights
 // stay as they are packed: a step is 4 groups of 32 k, lane quarter l / 16 holds one whole group (16 bytes of codes, one
-// scale, one zero), and MFMA i of the step takes the group's dword i.  A dword decodes into the pairs (k, k + 4), so the
-// activations' octets are stored in the order 0 4 1 5 2 6 3 7.
+// scale, one zero), and MFMA i of the step takes the group's dword i.
+//
+// Decode of a dword.  Its low nibbles, alone in their bytes, are the E4M3 codes 0 .. 15, whose values are linear: q 2^-9
+// (below 8 subnormal, from 8 on of the first binade).  So two masks, a shift and four conversions of two bytes each, scaled by
+// 2^9, give the 8 integers as float16, and four packed fma the weights, RN_f16(q scale + bias): 11 operations, where nibbles
+// put into the mantissa of 1024 or 64 and taken out by a subtraction need 13.  Bytes hold k = 2 j (low) and 2 j + 1 (high),
+// so the activations' octets are stored in the order 0 2 4 6 1 3 5 7.
 #pragma once
-#include <type_traits>
-
 #include "dev_common.h"
 #include "launch.h"
 
@@ -18,10 +21,11 @@ constexpr int kStepK = 128;             // contraction elements of a step: 4 gro
 
 
 // 8 weights of one dword, in the order above.
-__device__ __forceinline__ f16x8 awq_frag(uint32_t w, f16x2 s2, f16x2 b2, const AwqDecode& dc) {
-  f16x2 p[4];
-  awq_quad(w, s2, b2, dc, p);
-  return f16x8{p[0].x, p[0].y, p[1].x, p[1].y, p[2].x, p[2].y, p[3].x, p[3].y};
+__device__ __forceinline__ f16x8 awq_frag(uint32_t w, f16x2 s2, f16x2 b2) {
+  const uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;
+  const f16x2 p0 = __builtin_elementwise_fma(nibbles_f16<false>(lo), s2, b2), p1 = __builtin_elementwise_fma(nibbles_f16<true>(lo), s2, b2);
+  const f16x2 p2 = __builtin_elementwise_fma(nibbles_f16<false>(hi), s2, b2), p3 = __builtin_elementwise_fma(nibbles_f16<true>(hi), s2, b2);
+  return f16x8{p0.x, p0.y, p1.x, p1.y, p2.x, p2.y, p3.x, p3.y};
 }
 
 // A lane's share of one step of 16 weight rows: raw, so that every load is issued before any is used.
@@ -52,73 +56,13 @@ __device__ __forceinline__ void awq_meta(const AwqStep& r, bool live, f16x2& s2,
   b2 = f16x2{bv, bv};
 }
 
-// A lane's share of 4 whole steps (16 groups, none past the row's end): codes of the groups g, g + 4, g + 8, g + 12, and the
-// metadata of 4 neighbouring groups from m on, which are those of the four quarters' lanes (awq_transpose).
-template <int ML>
-struct AwqBlock {
-  u32x4 c[4];
-  u32x2 s;
-  std::conditional_t<ML == 3, uint32_t, u32x2> z;
-};
-template <int ML>
-__device__ __forceinline__ AwqBlock<ML> awq_load_block(const uint8_t* codes, const uint8_t* expert, const AwqLayout& L, int64_t row, int m,
-                                                       int g) {
-  typedef uint32_t u32x2_a2 __attribute__((ext_vector_type(2), aligned(2)));
-  typedef uint32_t u32_a1 __attribute__((aligned(1)));
-  AwqBlock<ML> r;
-#pragma unroll
-  for (int t = 0; t < 4; ++t) r.c[t] = *reinterpret_cast<const u32x4*>(codes + 16 * (g + 4 * t));
-  const int64_t at = row * L.G + m;
-  r.s = *reinterpret_cast<const u32x2_a2*>(expert + L.scale_off + 2 * at);
-  if constexpr (ML == 3) r.z = *reinterpret_cast<const u32_a1*>(expert + L.meta2_off + at);
-  else r.z = *reinterpret_cast<const u32x2_a2*>(expert + L.meta2_off + 2 * at);
-  return r;
-}
-// m[t]: scale (low half) and zero or bias (high half) of the lane's group in step t.  Quarter q holds those of groups 4 q .. 4 q + 3 and
-// wants those of q, q + 4, q + 8, q + 12: a 4 x 4 transpose over the quarters, by exchanging halves of the wave, then quarters.
-template <int ML>
-__device__ __forceinline__ void awq_transpose(const AwqBlock<ML>& b, uint32_t (&m)[4]) {
-  if constexpr (ML == 3) {
-    m[0] = (b.s.x & 0xFFFFu) | ((b.z & 255u) << 16);
-    m[1] = (b.s.x >> 16) | ((b.z & 0xFF00u) << 8);
-    m[2] = (b.s.y & 0xFFFFu) | (b.z & 0xFF0000u);
-    m[3] = (b.s.y >> 16) | ((b.z >> 8) & 0xFF0000u);
-  } else {
-    m[0] = (b.s.x & 0xFFFFu) | (b.z.x << 16);
-    m[1] = (b.s.x >> 16) | (b.z.x & 0xFFFF0000u);
-    m[2] = (b.s.y & 0xFFFFu) | (b.z.y << 16);
-    m[3] = (b.s.y >> 16) | (b.z.y & 0xFFFF0000u);
-  }
-  auto halves = [](uint32_t& a, uint32_t& c) {
-    const auto r = __builtin_amdgcn_permlane32_swap(a, c, false, false);
-    a = r[0], c = r[1];
-  };
-  auto quarters = [](uint32_t& a, uint32_t& c) {
-    const auto r = __builtin_amdgcn_permlane16_swap(a, c, false, false);
-    a = r[0], c = r[1];
-  };
-  halves(m[0], m[2]);
-  halves(m[1], m[3]);
-  quarters(m[0], m[1]);
-  quarters(m[2], m[3]);
-}
-template <int ML>
-__device__ __forceinline__ void awq_meta_of(uint32_t m, f16x2& s2, f16x2& b2) {
-  const _Float16 s = f16_from_bits((uint16_t)m);
-  _Float16 b;
-  if constexpr (ML == 3) b = awq_bias(m >> 16, s);
-  else b = f16_from_bits((uint16_t)(m >> 16));
-  s2 = f16x2{s, s};
-  b2 = f16x2{b, b};
-}
-
 // What float16 h left of x; nothing where h is infinite or NaN (x - h would be NaN and the infinity lose its sign).
 __device__ __forceinline__ _Float16 f16_rest(float x, _Float16 h) {
   const float r = x - (float)h;
   return r == r ? (_Float16)r : (_Float16)0.f;
 }
 
-// 8 values of x -> float16 terms in octet order (0 4 1 5 2 6 3 7), scaled by 2^-e.
+// 8 values of x -> float16 terms in octet order (0 2 4 6 1 3 5 7), scaled by 2^-e.
 template <int TERMS>
 __device__ __forceinline__ void octet_terms(const float* v, int e, u32x4 (&o)[TERMS]) {
   float x[8];
@@ -128,12 +72,12 @@ __device__ __forceinline__ void octet_terms(const float* v, int e, u32x4 (&o)[TE
     x[j] = ldexpf(v[j], -e);
     h[j] = (_Float16)x[j];
   }
-  const u32x4 hi = {as_u32(f16x2{h[0], h[4]}), as_u32(f16x2{h[1], h[5]}), as_u32(f16x2{h[2], h[6]}), as_u32(f16x2{h[3], h[7]})};
+  const u32x4 hi = {as_u32(f16x2{h[0], h[2]}), as_u32(f16x2{h[4], h[6]}), as_u32(f16x2{h[1], h[3]}), as_u32(f16x2{h[5], h[7]})};
   o[0] = hi;
   if constexpr (TERMS == 2) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) h[j] = f16_rest(x[j], h[j]);
-    const u32x4 lo = {as_u32(f16x2{h[0], h[4]}), as_u32(f16x2{h[1], h[5]}), as_u32(f16x2{h[2], h[6]}), as_u32(f16x2{h[3], h[7]})};
+    const u32x4 lo = {as_u32(f16x2{h[0], h[2]}), as_u32(f16x2{h[4], h[6]}), as_u32(f16x2{h[1], h[3]}), as_u32(f16x2{h[5], h[7]})};
     o[1] = lo;
   }
 }

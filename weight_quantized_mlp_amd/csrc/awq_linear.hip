@@ -23,7 +23,7 @@ constexpr int kFewRows = 32;
 
 // ---- x -> float16 terms in fragment order ------------------------------------------------------------------------
 // xp[m / 16][step][term][i][lane][8]: lane = 16 * quarter + m % 16 holds octet i of group 4 step + quarter of row m.
-// Zeros past K (up to a whole step) and past M (up to a whole 16 rows).
+// Zeros past K (up to `steps`) and past M (up to a whole 16 rows).
 __device__ __forceinline__ size_t frag_at(int mt, int steps, int step, int terms, int term, int i, int lane) {
   return (((((size_t)mt * steps + step) * terms + term) * 4 + i) * 64 + lane) * 16;
 }
@@ -73,205 +73,176 @@ __global__ void __launch_bounds__(256) awq_pack_kernel(int M, int K, int steps, 
 }
 
 // ---- few rows ----------------------------------------------------------------------------------------------------
-// A block is 4 steps: 16 groups, 512 k, of 16 weight rows: 4 loads of 1 KB of codes, and one 8-byte and one 4- or 8-byte load of metadata,
-// all in flight at once, the next block's behind this one's products.  A lane's 4 contiguous groups of metadata belong to one step of each
-// of the four quarters: a 4 x 4 transpose between the quarters (awq_transpose).
+// A workgroup has 16 weight rows; its waves take blocks of 4 steps (16 groups, 512 k) in turn, a block's 4 KB of codes in flight
+// behind the products of the block before.  The 16 rows' scales and zeros are two contiguous pieces of memory, which the workgroup copies
+// to LDS at its start: read by the waves block by block, 32 and 16 bytes of a row at a time, they cost half of the codes' time (1 row
+// 5120 -> 17408: 16.2 us, without them 11.8).
 constexpr int kBlockSteps = 4;
 constexpr int kOwnRows = 4;                    // rows of x that the waves turn into terms themselves
 constexpr int kPackedRows = 3;                 // in place of x's type: x comes packed
+constexpr int kRowsGroups = 1024;              // groups of a row at most: 48 or 64 KB of metadata
 
 struct RowsPlan {
-  int steps, blocks, per, waves;               // blocks per part, waves per workgroup
+  int blocks, per, waves;                      // blocks per part, waves per workgroup; packed x holds whole blocks
 };
 
 // XS: x's type, or kPackedRows.  In the first case MR rows of x: a wave scales its own 512 k of a row by their own power of two, so
 // that no wave waits for another before the sums meet.  In the second CT tiles of 16 rows.  Part blockIdx.y of the blocks.
-template <int ML, int TERMS, int RT, int CT, int XS, int MR>
+template <int ML, int TERMS, int CT, int XS, int MR>
 __global__ void __launch_bounds__(768) awq_rows_kernel(int M, int N, int K, RowsPlan p, const void* __restrict__ x,
                                                        const float* __restrict__ rowscale, const uint8_t* __restrict__ bank,
                                                        AwqLayout L, float* __restrict__ y, float* __restrict__ partials) {
   constexpr bool OWN = XS != kPackedRows;
-  constexpr int COLS = 16 * RT + 4;                             // floats of an LDS row of sums: n, padded
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];   // OWN: a wave's terms [MR][TERMS][1 KB]; then the sums [wave][m][COLS]
-  const AwqDecode dc = awq_decode_consts();
+  constexpr int COLS = 16 + 4;                                  // floats of an LDS row of sums: n, padded
+  // The rows' scales, their zeros or biases; OWN: each wave's terms [MR][TERMS][1 KB].  All make room for the sums [wave][m][COLS].
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), q = lane >> 4;
-  const int n0 = (int)blockIdx.x * 16 * RT, G = (int)L.G;
+  const int n0 = (int)blockIdx.x * 16, G = (int)L.G, rows = min(16, N - n0), nrow = min(lane & 15, rows - 1);
   const int b0 = (int)blockIdx.y * p.per, b1 = min(b0 + p.per, p.blocks);
-  const uint8_t* codes[RT];
-  int64_t row[RT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    row[r] = min(n0 + 16 * r + (lane & 15), N - 1);
-    codes[r] = bank + row[r] * (L.G * 16);
-  }
-  f32x4 acc[RT][CT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int c = 0; c < CT; ++c) acc[r][c] = f32x4{0.f, 0.f, 0.f, 0.f};
-  uint8_t* own = lds + wave * (MR * TERMS * 1024);
+  const uint8_t* codes = bank + (size_t)(n0 + nrow) * (L.G * 16);
+  constexpr int ZB = ML == 3 ? 1 : 2;                           // bytes of a zero or bias
+  const int sc = (rows * G * 2 + 15) >> 4, zc = (rows * G * ZB + 15) >> 4;   // 16-byte pieces (the planes are padded to whole ones)
+  uint8_t* own = lds + (sc + zc) * 16 + wave * (MR * TERMS * 1024);
   const uint8_t* xs = own + min(lane & 15, MR - 1) * (TERMS * 1024) + q * 64;
 
   struct Block {
     RawOctet<XS> x[OWN ? MR : 1];
-    AwqBlock<ML> w[RT];
+    u32x4 c[4];
   };
-  auto load = [&](int b, Block& d) {                            // x first: its wait then leaves the weights out
+  auto load = [&](int b, Block& d) {
     if constexpr (OWN) {
-      const int o = 64 * b + lane;
+      const int o = min(64 * b + lane, K / 8 - 1);
 #pragma unroll
-      for (int m = 0; m < MR; ++m) d.x[m] = load_raw<XS>(x, (size_t)min(m, M - 1) * K + 8 * (size_t)min(o, K / 8 - 1));
+      for (int m = 0; m < MR; ++m) d.x[m] = load_raw<XS>(x, (size_t)min(m, M - 1) * K + 8 * (size_t)o);
     }
 #pragma unroll
-    for (int r = 0; r < RT; ++r) d.w[r] = awq_load_block<ML>(codes[r], bank, L, row[r], 16 * b + 4 * q, 16 * b + q);
+    for (int t = 0; t < 4; ++t) d.c[t] = *reinterpret_cast<const u32x4*>(codes + 16 * min(16 * b + 4 * t + q, G - 1));
   };
-  // A wave's 64 octets of a block of each row -> terms in its LDS; the powers of two.
-  auto own_terms = [&](int b, const RawOctet<XS>* raw, float* scale) {
-    wave_lds_fence();                                           // the last block's fragments are in registers
+  Block u, v;
+  int b = b0 + wave;
+  {
+    constexpr int UP = 4;                                       // pieces of a thread on their way at once
+    const u32x4* gs = reinterpret_cast<const u32x4*>(bank + L.scale_off + (size_t)n0 * G * 2);
+    const u32x4* gz = reinterpret_cast<const u32x4*>(bank + L.meta2_off + (size_t)n0 * G * ZB) - sc;
+    const int T = 64 * p.waves, last = sc + zc - 1;
+    u32x4 piece[UP];
+    auto load4 = [&](int i0) {
 #pragma unroll
-    for (int m = 0; m < MR; ++m) {
-      float v[8];
-      raw_values<XS>(raw[m], v);
-      if (64 * b + lane >= K / 8)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 0.f;
-      int e = 0;
-      if constexpr (XS != X_F16) {
-        float amax = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) amax = fmaxf(amax, finite_abs(v[j]));
-        e = f16_row_exp(wave64_max(amax));
+      for (int k = 0; k < UP; ++k) {
+        const int i = min(i0 + k * T, last);
+        piece[k] = (i < sc ? gs : gz)[i];
       }
-      scale[m] = ldexpf(1.f, e);
-      u32x4 t[TERMS];
-      octet_terms<TERMS>(v, e, t);
+    };
+    load4(tid);
+    load(min(b, b1 - 1), u);
+    for (int i0 = tid; i0 <= last; i0 += UP * T) {
+      if (i0 != tid) load4(i0);
 #pragma unroll
-      for (int j = 0; j < TERMS; ++j) *reinterpret_cast<u32x4*>(own + (m * TERMS + j) * 1024 + lane * 16) = t[j];
+      for (int k = 0; k < UP; ++k)
+        if (i0 + k * T <= last) reinterpret_cast<u32x4*>(lds)[i0 + k * T] = piece[k];
     }
-    wave_lds_fence();
-  };
-  auto load_x = [&](int step, int t, f16x8 (&f)[CT][TERMS][4]) {   // step t of its block
+    __syncthreads();
+  }
+
+  f32x4 acc[CT];
 #pragma unroll
-    for (int c = 0; c < CT; ++c)
-#pragma unroll
-      for (int j = 0; j < TERMS; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if constexpr (OWN) f[c][j][i] = *reinterpret_cast<const f16x8*>(xs + j * 1024 + t * 256 + i * 16);
-          else f[c][j][i] = *reinterpret_cast<const f16x8*>(static_cast<const uint8_t*>(x) + frag_at(c, p.steps, step, TERMS, j, i, lane));
-        }
-  };
-  auto step_mfmas = [&](f32x4 (&sum)[RT][CT], const u32x4* c, const f16x2* s2, const f16x2* b2, const f16x8 (&f)[CT][TERMS][4]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const f16x8 wf = awq_frag(c[r][i], s2[r], b2[r], dc);
-#pragma unroll
-        for (int j = 0; j < CT; ++j)
-#pragma unroll
-          for (int t = 0; t < TERMS; ++t) sum[r][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(wf, f[j][t][i], sum[r][j], 0, 0, 0);
-      }
-  };
-  // The block's sums join the wave's: scaled back, where the block has its own powers of two (lane's column = row lane % 16 of x).
-  auto join = [&](f32x4 (&sum)[RT][CT], const float* scale) {
-    float rs = scale[0];
-#pragma unroll
-    for (int m = 1; m < MR; ++m) rs = (lane & 15) >= m ? scale[m] : rs;
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[r][0][j] = fmaf(sum[r][0][j], rs, acc[r][0][j]);
-  };
-  auto whole = [&](int b, const Block& d) {
-    f32x4 sum[RT][CT];
+  for (int c = 0; c < CT; ++c) acc[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto multiply = [&](int b, const Block& d) {
+    f32x4 sum[CT];
     float scale[MR];
-    if constexpr (OWN) {
-      own_terms(b, d.x, scale);
+    if constexpr (OWN) {                                        // the wave's 64 octets of each row -> terms in its LDS
+      wave_lds_fence();                                         // the last block's fragments are in registers
 #pragma unroll
-      for (int r = 0; r < RT; ++r) sum[r][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int m = 0; m < MR; ++m) {
+        float f[8];
+        raw_values<XS>(d.x[m], f);
+        if (64 * b + lane >= K / 8)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[j] = 0.f;
+        int e = 0;
+        if constexpr (XS != X_F16) {
+          float amax = 0.f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) amax = fmaxf(amax, finite_abs(f[j]));
+          e = f16_row_exp(wave64_max(amax));
+        }
+        scale[m] = ldexpf(1.f, e);
+        u32x4 t[TERMS];
+        octet_terms<TERMS>(f, e, t);
+#pragma unroll
+        for (int j = 0; j < TERMS; ++j) *reinterpret_cast<u32x4*>(own + (m * TERMS + j) * 1024 + lane * 16) = t[j];
+      }
+      wave_lds_fence();
     }
-    uint32_t meta[RT][4];
 #pragma unroll
-    for (int r = 0; r < RT; ++r) awq_transpose<ML>(d.w[r], meta[r]);
+    for (int c = 0; c < CT; ++c) sum[c] = OWN ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[c];
+    const uint8_t* smeta = lds + nrow * G * 2;
+    const uint8_t* zmeta = lds + sc * 16 + nrow * G * ZB;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
+      const int step = b * kBlockSteps + t;
       f16x8 f[CT][TERMS][4];
-      load_x(b * kBlockSteps + t, t, f);
-      f16x2 s2[RT], b2[RT];
-      u32x4 c[RT];
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        awq_meta_of<ML>(meta[r][t], s2[r], b2[r]);
-        c[r] = d.w[r].c[t];
+      for (int c = 0; c < CT; ++c)
+#pragma unroll
+        for (int j = 0; j < TERMS; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (OWN) f[c][j][i] = *reinterpret_cast<const f16x8*>(xs + j * 1024 + t * 256 + i * 16);
+            else f[c][j][i] = *reinterpret_cast<const f16x8*>(static_cast<const uint8_t*>(x) + frag_at(c, p.blocks * kBlockSteps, step, TERMS, j, i, lane));
+          }
+      const int g = 16 * b + 4 * t + q, gc = min(g, G - 1);
+      AwqStep a;
+      a.s = *reinterpret_cast<const uint16_t*>(smeta + 2 * gc);
+      if constexpr (ML == 3) a.z = zmeta[gc];
+      else a.z = *reinterpret_cast<const uint16_t*>(zmeta + 2 * gc);
+      f16x2 s2, b2;
+      awq_meta<ML>(a, g < G, s2, b2);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f16x8 w = awq_frag(d.c[t][i], s2, b2);
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+#pragma unroll
+          for (int j = 0; j < TERMS; ++j) sum[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, f[c][j][i], sum[c], 0, 0, 0);
       }
-      if constexpr (OWN) step_mfmas(sum, c, s2, b2, f);
-      else step_mfmas(acc, c, s2, b2, f);
     }
-    if constexpr (OWN) join(sum, scale);
+    if constexpr (OWN) {                                        // scaled back; the lane's column is row lane % 16 of x
+      float rs = scale[0];
+#pragma unroll
+      for (int m = 1; m < MR; ++m) rs = (lane & 15) >= m ? scale[m] : rs;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[0][j] = fmaf(sum[0][j], rs, acc[0][j]);
+    } else {
+#pragma unroll
+      for (int c = 0; c < CT; ++c) acc[c] = sum[c];
+    }
   };
-  const int full = min(b1, G / 16);                             // blocks of whole rows end here
-  int b = b0 + wave;
-  if (b < full) {
-    Block u, v;
-    load(b, u);
-    for (; b + p.waves < full; b += 2 * p.waves) {
-      load(b + p.waves, v);
-      whole(b, u);
-      load(min(b + 2 * p.waves, full - 1), u);
-      whole(b + p.waves, v);
-    }
-    if (b < full) {
-      whole(b, u);
-      b += p.waves;
-    }
+  for (; b + p.waves < b1; b += 2 * p.waves) {
+    load(b + p.waves, v);
+    multiply(b, u);
+    load(min(b + 2 * p.waves, b1 - 1), u);
+    multiply(b + p.waves, v);
   }
-  if (b == full && full < b1) {                                 // the row's last groups, fewer than a block: step by step
-    f32x4 sum[RT][CT];
-    float scale[MR];
-    if constexpr (OWN) {
-      RawOctet<XS> raw[MR];
-#pragma unroll
-      for (int m = 0; m < MR; ++m) raw[m] = load_raw<XS>(x, (size_t)min(m, M - 1) * K + 8 * (size_t)min(64 * b + lane, K / 8 - 1));
-      own_terms(b, raw, scale);
-#pragma unroll
-      for (int r = 0; r < RT; ++r) sum[r][0] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
-    for (int s = b * kBlockSteps; s < p.steps; ++s) {
-      f16x8 f[CT][TERMS][4];
-      load_x(s, s - b * kBlockSteps, f);
-      f16x2 s2[RT], b2[RT];
-      u32x4 c[RT];
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const AwqStep a = awq_load<ML>(codes[r], bank, L, row[r], 4 * s + q);
-        awq_meta<ML>(a, 4 * s + q < G, s2[r], b2[r]);
-        c[r] = a.c;
-      }
-      if constexpr (OWN) step_mfmas(sum, c, s2, b2, f);
-      else step_mfmas(acc, c, s2, b2, f);
-    }
-    if constexpr (OWN) join(sum, scale);
-  }
+  if (b < b1) multiply(b, u);
+
   // the waves' sums, in order
-  if constexpr (OWN) __syncthreads();                           // every wave is done with its terms
+  __syncthreads();                                              // every wave is done with the metadata and its terms
   float* part = reinterpret_cast<float*>(lds);
 #pragma unroll
-  for (int j = 0; j < CT; ++j) {
-    const int m = 16 * j + (lane & 15);
-    if (m < M)
-#pragma unroll
-      for (int r = 0; r < RT; ++r) *reinterpret_cast<f32x4*>(part + (wave * M + m) * COLS + 16 * r + 4 * q) = acc[r][j];
+  for (int c = 0; c < CT; ++c) {
+    const int m = 16 * c + (lane & 15);
+    if (m < M) *reinterpret_cast<f32x4*>(part + (wave * M + m) * COLS + 4 * q) = acc[c];
   }
   __syncthreads();
-  for (int i = tid; i < M * 16 * RT; i += 64 * p.waves) {
-    const int m = i / (16 * RT), j = i - m * 16 * RT, n = n0 + j;
+  for (int i = tid; i < M * 16; i += 64 * p.waves) {
+    const int m = i >> 4, n = n0 + (i & 15);
     if (n >= N) continue;
-    float v = 0.f;
-    for (int k = 0; k < p.waves; ++k) v += part[(k * M + m) * COLS + j];
-    if constexpr (!OWN) v *= rowscale[m];
-    if (partials != nullptr) partials[((size_t)blockIdx.y * M + m) * N + n] = v;
-    else y[(size_t)m * N + n] = v;
+    float r = 0.f;
+    for (int k = 0; k < p.waves; ++k) r += part[(k * M + m) * COLS + (i & 15)];
+    if constexpr (!OWN) r *= rowscale[m];
+    if (partials != nullptr) partials[((size_t)blockIdx.y * M + m) * N + n] = r;
+    else y[(size_t)m * N + n] = r;
   }
 }
 
@@ -286,7 +257,6 @@ __global__ void __launch_bounds__(256, 2) awq_gemm_kernel(int M, int N, int step
                                                           float* __restrict__ partials) {
   constexpr int NT = 4, UNITS = MT * TERMS, STAGE = UNITS * 4096;   // a unit: one term of 16 rows, 4 KB per step
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  const AwqDecode dc = awq_decode_consts();
   const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int q = lane >> 4;
   // Workgroup b runs on XCD b % 8: each XCD gets a contiguous run of tiles, in bands of 8 tile rows, so that the tiles in
@@ -345,7 +315,7 @@ __global__ void __launch_bounds__(256, 2) awq_gemm_kernel(int M, int N, int step
     for (int i = 0; i < 4; ++i) {
       f16x8 w[NT];
 #pragma unroll
-      for (int r = 0; r < NT; ++r) w[r] = awq_frag(cur[r].c[i], s2[r], b2[r], dc);
+      for (int r = 0; r < NT; ++r) w[r] = awq_frag(cur[r].c[i], s2[r], b2[r]);
 #pragma unroll
       for (int c = 0; c < MT; ++c)
 #pragma unroll
@@ -397,7 +367,7 @@ __global__ void __launch_bounds__(256) awq_join_kernel(int M, int N, int S, cons
 struct AwqPlan {
   bool rows, own;              // few rows; so few that the waves turn them into terms themselves (no packing)
   int terms, steps, S, per;
-  int rt, ct, waves;           // few rows: row tiles, column tiles, waves
+  int ct, waves;               // few rows: column tiles, waves
   int mt, ntm, tiles;          // many rows
   size_t xp, rs, partials, total;
 };
@@ -405,20 +375,23 @@ inline AwqPlan awq_plan(int M, int N, int K, XType xt) {
   AwqPlan p{};
   p.terms = awq_terms(xt);
   p.steps = (K + kStepK - 1) / kStepK;
-  p.rows = M <= kFewRows;
+  p.rows = M <= kFewRows && K / 32 <= kRowsGroups;
   const int64_t most = std::max<int64_t>(1, ((int64_t)64 << 20) / ((int64_t)M * N * 4));   // at most 64 MiB of parts
   if (p.rows) {
     const int blocks = (p.steps + kBlockSteps - 1) / kBlockSteps;
+    p.steps = blocks * kBlockSteps;
     p.own = M <= kOwnRows;
     p.ct = M <= 16 ? 1 : 2;
-    p.rt = 1;
-    const int64_t wgs = (N + 16 * p.rt - 1) / (16 * p.rt);
+    const int64_t wgs = (N + 15) / 16;
     const int64_t S = std::min(std::max<int64_t>(1, std::min<int64_t>(256 / wgs, blocks / 12)), most);
     p.per = (int)((blocks + S - 1) / S);
     p.S = (blocks + p.per - 1) / p.per;
-    // waves: what the chip holds (20 per CU), at least 4 and at most 12, and no more than its number of turns needs
-    const int top = (int)std::min<int64_t>(12, std::max<int64_t>(4, 5120 / (wgs * p.S) + 1)), turns = (p.per + top - 1) / top;
-    p.waves = (p.per + turns - 1) / turns;
+    // waves: what the chip holds at once (20 per CU), at most 10 (two workgroups per CU) and no more than the number of turns needs; at
+    // least 4, which read the metadata
+    int top = 10;
+    while (top > 4 && wgs * p.S > 256 * (20 / top)) --top;
+    const int turns = (p.per + top - 1) / top;
+    p.waves = std::max(4, (p.per + turns - 1) / turns);
   } else {
     p.mt = p.terms == 2 || M <= 64 ? 4 : 8;
     p.ntm = (M + 16 * p.mt - 1) / (16 * p.mt);
@@ -440,14 +413,14 @@ void pack_rows(int M, int K, int steps, const void* x, uint8_t* xp, float* rs, h
   hipLaunchKernelGGL((awq_pack_kernel<XT, TERMS>), dim3(grid), dim3(256), 0, st, M, K, steps, x, xp, rs);
 }
 
-template <int ML, int TERMS, int RT, int CT, int XS, int MR>
+template <int ML, int TERMS, int CT, int XS, int MR>
 hipError_t run_rows(const AwqPlan& p, int M, int N, int K, const void* x, const float* rs, const uint8_t* bank, const AwqLayout& L, float* y,
                     float* partials, hipStream_t st) {
-  if (!raise_lds_limit<awq_rows_kernel<ML, TERMS, RT, CT, XS, MR>>()) return hipErrorInvalidValue;
-  const int sums = p.waves * M * (16 * RT + 4) * 4, own = XS == kPackedRows ? 0 : p.waves * MR * TERMS * 1024;
-  const RowsPlan r{p.steps, (p.steps + kBlockSteps - 1) / kBlockSteps, p.per, p.waves};
-  hipLaunchKernelGGL((awq_rows_kernel<ML, TERMS, RT, CT, XS, MR>), dim3((N + 16 * RT - 1) / (16 * RT), p.S), dim3(64 * p.waves),
-                     std::max(sums, own), st, M, N, K, r, x, rs, bank, L, y, partials);
+  if (!raise_lds_limit<awq_rows_kernel<ML, TERMS, CT, XS, MR>>()) return hipErrorInvalidValue;
+  const int sums = p.waves * M * 20 * 4, meta = 16 * (K / 32) * ML + 32, own = XS == kPackedRows ? 0 : p.waves * MR * TERMS * 1024;
+  const RowsPlan r{p.steps / kBlockSteps, p.per, p.waves};
+  hipLaunchKernelGGL((awq_rows_kernel<ML, TERMS, CT, XS, MR>), dim3((N + 15) / 16, p.S), dim3(64 * p.waves), std::max(sums, meta + own),
+                     st, M, N, K, r, x, rs, bank, L, y, partials);
   return hipGetLastError();
 }
 template <int ML, int TERMS, int MT>
@@ -467,12 +440,12 @@ hipError_t run_plan(const AwqPlan& p, int M, A... a) {
     return run_gemm<ML, T, 4>(p, M, a...);
   }
   if (p.own) {
-    if (M == 1) return run_rows<ML, T, 1, 1, XT, 1>(p, M, a...);
-    if (M == 2) return run_rows<ML, T, 1, 1, XT, 2>(p, M, a...);
-    return run_rows<ML, T, 1, 1, XT, 4>(p, M, a...);
+    if (M == 1) return run_rows<ML, T, 1, XT, 1>(p, M, a...);
+    if (M == 2) return run_rows<ML, T, 1, XT, 2>(p, M, a...);
+    return run_rows<ML, T, 1, XT, 4>(p, M, a...);
   }
-  if (p.ct == 1) return run_rows<ML, T, 1, 1, kPackedRows, 1>(p, M, a...);
-  return run_rows<ML, T, 1, 2, kPackedRows, 1>(p, M, a...);
+  if (p.ct == 1) return run_rows<ML, T, 1, kPackedRows, 1>(p, M, a...);
+  return run_rows<ML, T, 2, kPackedRows, 1>(p, M, a...);
 }
 template <int XT>
 hipError_t linear(const AwqPlan& p, int M, int N, int K, const void* x, const uint8_t* bank, int meta_layout, uint8_t* ws, float* y,

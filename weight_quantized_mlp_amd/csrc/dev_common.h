@@ -61,6 +61,12 @@ __device__ __forceinline__ float e4m3_byte_f32(uint32_t w) {
   return (B & 1) ? v.y : v.x;
 }
 
+// Two bytes (0, 1 or 2, 3) of w that hold 0 .. 15 -> those integers as float16: E4M3 codes below 16 are q 2^-9.
+template <bool HI>
+__device__ __forceinline__ f16x2 nibbles_f16(uint32_t w) {
+  return __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 512.0f, HI);
+}
+
 // ---- bit reinterpretation ---------------------------------------------------------------------
 // Always reinterpret a scalar VALUE: in this toolchain __builtin_bit_cast applied to an
 // ext-vector element expression (v.y) reads the vector's first element instead.

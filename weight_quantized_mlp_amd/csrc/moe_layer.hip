@@ -132,7 +132,6 @@ __global__ void __launch_bounds__(512) moe_mm_kernel(MoeShape sh, const void* __
   float* scales = reinterpret_cast<float*>(lds + kMaxRoutes * 2);                 // of the pass's columns
   uint64_t* masks = reinterpret_cast<uint64_t*>(lds + kMaxRoutes * 2 + 16 * 4);   // of each 64 ids: those that name the expert
   uint8_t* stage = lds + kHeadBytes;
-  const AwqDecode dc = awq_decode_consts();
   const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int q = lane >> 4, item = (int)blockIdx.y;
   const int e = sh.by_route ? ids[item] : item;
@@ -228,7 +227,7 @@ __global__ void __launch_bounds__(512) moe_mm_kernel(MoeShape sh, const void* __
         awq_meta<ML>(d[1], live, s2[1], b2[1]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const f16x8 w0 = awq_frag(d[0].c[i], s2[0], b2[0], dc), w1 = awq_frag(d[1].c[i], s2[1], b2[1], dc);
+          const f16x8 w0 = awq_frag(d[0].c[i], s2[0], b2[0]), w1 = awq_frag(d[1].c[i], s2[1], b2[1]);
 #pragma unroll
           for (int t = 0; t < TERMS; ++t) {
             const f16x8 xf = *reinterpret_cast<const f16x8*>(xs + t * stride + (step - k0) * 256 + i * 16);
