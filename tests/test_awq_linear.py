@@ -35,11 +35,11 @@ def check(y, x64, w64, xt, what=""):
     assert err <= norm_bound(K), f"{what}: {err:.2e} > {norm_bound(K):.2e}"
 
 
-# rows 1 .. 32: the few-row kernel with one and two column tiles; above: the tile kernel with 4 and 8; N and K inside and past a tile, a
-# step, a part; contractions long enough to be split
+# rows 1 and 2: each wave its own rows; 3 .. 32: shared rows, one and two column tiles; above: the tile kernel with 4 and 8 (also for rows
+# of more than 1024 groups); N and K inside and past a tile, a step, a part; contractions long enough to be split
 SHAPES = [(1, 512, 256), (1, 1, 32), (2, 67, 320), (15, 40, 96), (16, 16, 128), (17, 33, 160), (32, 64, 8192), (3, 40, 12320), (31, 4100, 288),
           (5, 16400, 64), (33, 67, 320), (64, 256, 544), (65, 255, 4096), (127, 300, 32), (129, 67, 320), (300, 515, 1056), (513, 1030, 512),
-          (40, 48, 16384)]
+          (40, 48, 16384), (1, 40, 32800), (2, 17, 32768), (1, 130, 12320), (4, 129, 1056), (9, 127, 2080), (24, 300, 4128), (16, 17408, 1024)]
 
 
 @pytest.mark.parametrize("xt", [F32, BF16, F16])

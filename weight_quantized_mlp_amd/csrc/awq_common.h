@@ -92,6 +92,15 @@ __device__ __forceinline__ RawOctet<XT> load_raw(const void* x, size_t at) {
   if constexpr (XT == X_F32) r.v[1] = p[1];
   return r;
 }
+// The same from a wave-uniform row and a 32-bit element offset in it.
+template <int XT>
+__device__ __forceinline__ RawOctet<XT> load_raw(const uint8_t* row, uint32_t at) {
+  const u32x4* p = reinterpret_cast<const u32x4*>(row + at * (XT == X_F32 ? 4u : 2u));
+  RawOctet<XT> r;
+  r.v[0] = p[0];
+  if constexpr (XT == X_F32) r.v[1] = p[1];
+  return r;
+}
 template <int XT>
 __device__ __forceinline__ void raw_values(const RawOctet<XT>& r, float* v) {
 #pragma unroll
@@ -114,6 +123,39 @@ __device__ __forceinline__ void raw_values(const RawOctet<XT>& r, float* v) {
 template <int XT>
 __device__ __forceinline__ void load_octet(const void* x, size_t at, float* v) {
   raw_values<XT>(load_raw<XT>(x, at), v);
+}
+
+// 8 raw elements -> their terms scaled by 2^-e, zeros where they are not `live`.  float16 is only put in order.
+template <int XT, int TERMS>
+__device__ __forceinline__ void raw_terms(const RawOctet<XT>& r, int e, bool live, u32x4 (&o)[TERMS]) {
+  if constexpr (XT == X_F16) {
+    const uint32_t a = r.v[0][0], b = r.v[0][1], c = r.v[0][2], d = r.v[0][3];
+    const u32x4 v = {__builtin_amdgcn_perm(b, a, 0x05040100), __builtin_amdgcn_perm(d, c, 0x05040100),
+                     __builtin_amdgcn_perm(b, a, 0x07060302), __builtin_amdgcn_perm(d, c, 0x07060302)};
+    const u32x4 zero = {0, 0, 0, 0};
+    o[0] = live ? v : zero;
+  } else {
+    float v[8];
+    raw_values<XT>(r, v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = live ? v[j] : 0.f;
+    octet_terms<TERMS>(v, e, o);
+  }
+}
+template <int XT>
+__device__ __forceinline__ float octet_max(const RawOctet<XT>& r) {
+  float v[8], m = 0.f;
+  raw_values<XT>(r, v);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = fmaxf(m, finite_abs(v[j]));
+  return m;
+}
+// A wave's 64 octets -> terms, scaled by the power of two that is returned.
+template <int XT, int TERMS>
+__device__ __forceinline__ float wave_terms(const RawOctet<XT>& r, bool live, u32x4 (&o)[TERMS]) {
+  const int e = XT == X_F16 ? 0 : f16_row_exp(wave64_max(live ? octet_max<XT>(r) : 0.f));
+  raw_terms<XT, TERMS>(r, e, live, o);
+  return ldexpf(1.f, e);
 }
 
 // float32 rows take two float16 terms (their products' sum is off by 2^-22 of an element or 2^-39 of its row's largest), bfloat16

@@ -3,9 +3,9 @@
 //
 // The weights are decoded in registers, straight from the packed bytes, into matrix-core operands (awq_common.h); x is
 // turned into float16 terms (awq_pack_kernel), in the order the matrix cores read it.
-//   Up to kFewRows rows (awq_rows_kernel): the weights' bytes bound it.  A workgroup's waves split the contraction of the
-//     same weight rows and add up through LDS, so a few rows of weights still fill a CU.  Up to kOwnRows rows of x are
-//     turned into terms by the waves themselves, which spares a launch; more come from L2 as packed fragments.
+//   Up to kOwnRows rows (awq_rows_kernel) and up to kFewRows (awq_shared_kernel): the weights' bytes bound it, and with them the
+//     decode, so what matters is that every CU has work from the start and reads whole cache lines.  x is turned into terms by the
+//     waves themselves, which spares a launch.
 //   More rows (awq_gemm_kernel): the matrix cores bound it.  4 waves with 64 weight rows each share the tile of x through
 //     LDS (global->LDS copies, two stages); every wave decodes only its own weights, once per tile row.
 // Either splits the contraction over workgroups when there are few tiles; awq_join_kernel adds the parts in order.
@@ -18,8 +18,6 @@
 namespace wq {
 
 namespace {
-
-constexpr int kFewRows = 32;
 
 // ---- x -> float16 terms in fragment order ------------------------------------------------------------------------
 // xp[m / 16][step][term][i][lane][8]: lane = 16 * quarter + m % 16 holds octet i of group 4 step + quarter of row m.
@@ -72,51 +70,61 @@ __global__ void __launch_bounds__(256) awq_pack_kernel(int M, int K, int steps, 
   }
 }
 
-// ---- few rows ----------------------------------------------------------------------------------------------------
+// 4 results of row m from column n on, as far as the row goes.
+__device__ __forceinline__ void store_row4(float* y, int N, int m, int n, f32x4 v) {
+  float* o = y + (size_t)m * N + n;
+  if (n + 3 < N && (N & 3) == 0) {
+    *reinterpret_cast<f32x4*>(o) = v;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (n + j < N) o[j] = v[j];
+  }
+}
+
+// ---- up to kOwnRows rows -----------------------------------------------------------------------------------------
 // A workgroup has 16 weight rows; its waves take blocks of 4 steps (16 groups, 512 k) in turn, a block's 4 KB of codes in flight
 // behind the products of the block before.  The 16 rows' scales and zeros are two contiguous pieces of memory, which the workgroup copies
 // to LDS at its start: read by the waves block by block, 32 and 16 bytes of a row at a time, they cost half of the codes' time (1 row
 // 5120 -> 17408: 16.2 us, without them 11.8).
 constexpr int kBlockSteps = 4;
-constexpr int kOwnRows = 4;                    // rows of x that the waves turn into terms themselves
-constexpr int kPackedRows = 3;                 // in place of x's type: x comes packed
+constexpr int kOwnRows = 2;                    // (4 rows 5120 -> 17408: 22.3 us here, 19.3 in awq_shared_kernel)
 constexpr int kRowsGroups = 1024;              // groups of a row at most: 48 or 64 KB of metadata
 
 struct RowsPlan {
-  int blocks, per, waves;                      // blocks per part, waves per workgroup; packed x holds whole blocks
+  int blocks, per, waves;                      // blocks per part, waves per workgroup
 };
 
-// XS: x's type, or kPackedRows.  In the first case MR rows of x: a wave scales its own 512 k of a row by their own power of two, so
-// that no wave waits for another before the sums meet.  In the second CT tiles of 16 rows.  Part blockIdx.y of the blocks.
-template <int ML, int TERMS, int CT, int XS, int MR>
-__global__ void __launch_bounds__(768) awq_rows_kernel(int M, int N, int K, RowsPlan p, const void* __restrict__ x,
-                                                       const float* __restrict__ rowscale, const uint8_t* __restrict__ bank,
-                                                       AwqLayout L, float* __restrict__ y, float* __restrict__ partials) {
-  constexpr bool OWN = XS != kPackedRows;
+// MR rows of x (of which M are there): a wave scales its own 512 k of a row by their own power of two, so that no wave waits for
+// another before the sums meet.  Part blockIdx.y of the blocks.
+template <int ML, int XS, int MR>
+__global__ void __launch_bounds__(512) awq_rows_kernel(int M, int N, int K, RowsPlan p, const void* __restrict__ x,
+                                                       const uint8_t* __restrict__ bank, AwqLayout L, float* __restrict__ y,
+                                                       float* __restrict__ partials) {
+  constexpr int TERMS = XS == X_F32 ? 2 : 1;
   constexpr int COLS = 16 + 4;                                  // floats of an LDS row of sums: n, padded
-  // The rows' scales, their zeros or biases; OWN: each wave's terms [MR][TERMS][1 KB].  All make room for the sums [wave][m][COLS].
+  // The rows' scales, their zeros or biases, each wave's terms [MR][TERMS][1 KB].  All make room for the sums [wave][m][COLS].
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), q = lane >> 4;
   const int n0 = (int)blockIdx.x * 16, G = (int)L.G, rows = min(16, N - n0), nrow = min(lane & 15, rows - 1);
   const int b0 = (int)blockIdx.y * p.per, b1 = min(b0 + p.per, p.blocks);
-  const uint8_t* codes = bank + (size_t)(n0 + nrow) * (L.G * 16);
+  const uint8_t* codes = bank + (size_t)n0 * (L.G * 16);        // (offsets from it fit 32 bits)
+  const int crow = nrow * G * 16;
   constexpr int ZB = ML == 3 ? 1 : 2;                           // bytes of a zero or bias
   const int sc = (rows * G * 2 + 15) >> 4, zc = (rows * G * ZB + 15) >> 4;   // 16-byte pieces (the planes are padded to whole ones)
   uint8_t* own = lds + (sc + zc) * 16 + wave * (MR * TERMS * 1024);
   const uint8_t* xs = own + min(lane & 15, MR - 1) * (TERMS * 1024) + q * 64;
 
   struct Block {
-    RawOctet<XS> x[OWN ? MR : 1];
+    RawOctet<XS> x[MR];
     u32x4 c[4];
   };
   auto load = [&](int b, Block& d) {
-    if constexpr (OWN) {
-      const int o = min(64 * b + lane, K / 8 - 1);
+    const int o = min(64 * b + lane, K / 8 - 1);
 #pragma unroll
-      for (int m = 0; m < MR; ++m) d.x[m] = load_raw<XS>(x, (size_t)min(m, M - 1) * K + 8 * (size_t)o);
-    }
+    for (int m = 0; m < MR; ++m) d.x[m] = load_raw<XS>(static_cast<const uint8_t*>(x) + (size_t)min(m, M - 1) * K * (XS == X_F32 ? 4 : 2), (uint32_t)(8 * o));
 #pragma unroll
-    for (int t = 0; t < 4; ++t) d.c[t] = *reinterpret_cast<const u32x4*>(codes + 16 * min(16 * b + 4 * t + q, G - 1));
+    for (int t = 0; t < 4; ++t) d.c[t] = *reinterpret_cast<const u32x4*>(codes + (uint32_t)(crow + 16 * min(16 * b + 4 * t + q, G - 1)));
   };
   Block u, v;
   int b = b0 + wave;
@@ -134,7 +142,7 @@ __global__ void __launch_bounds__(768) awq_rows_kernel(int M, int N, int K, Rows
       }
     };
     load4(tid);
-    load(min(b, b1 - 1), u);
+    if (b < b1) load(b, u);
     for (int i0 = tid; i0 <= last; i0 += UP * T) {
       if (i0 != tid) load4(i0);
 #pragma unroll
@@ -144,53 +152,23 @@ __global__ void __launch_bounds__(768) awq_rows_kernel(int M, int N, int K, Rows
     __syncthreads();
   }
 
-  f32x4 acc[CT];
-#pragma unroll
-  for (int c = 0; c < CT; ++c) acc[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  const uint8_t* smeta = lds + nrow * G * 2;
+  const uint8_t* zmeta = lds + sc * 16 + nrow * G * ZB;
   auto multiply = [&](int b, const Block& d) {
-    f32x4 sum[CT];
     float scale[MR];
-    if constexpr (OWN) {                                        // the wave's 64 octets of each row -> terms in its LDS
-      wave_lds_fence();                                         // the last block's fragments are in registers
+    wave_lds_fence();                                           // the last block's fragments are in registers
 #pragma unroll
-      for (int m = 0; m < MR; ++m) {
-        float f[8];
-        raw_values<XS>(d.x[m], f);
-        if (64 * b + lane >= K / 8)
+    for (int m = 0; m < MR; ++m) {                              // the wave's 64 octets of each row -> terms in its LDS
+      u32x4 t[TERMS];
+      scale[m] = wave_terms<XS, TERMS>(d.x[m], 64 * b + lane < K / 8, t);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) f[j] = 0.f;
-        int e = 0;
-        if constexpr (XS != X_F16) {
-          float amax = 0.f;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) amax = fmaxf(amax, finite_abs(f[j]));
-          e = f16_row_exp(wave64_max(amax));
-        }
-        scale[m] = ldexpf(1.f, e);
-        u32x4 t[TERMS];
-        octet_terms<TERMS>(f, e, t);
-#pragma unroll
-        for (int j = 0; j < TERMS; ++j) *reinterpret_cast<u32x4*>(own + (m * TERMS + j) * 1024 + lane * 16) = t[j];
-      }
-      wave_lds_fence();
+      for (int j = 0; j < TERMS; ++j) *reinterpret_cast<u32x4*>(own + (m * TERMS + j) * 1024 + lane * 16) = t[j];
     }
-#pragma unroll
-    for (int c = 0; c < CT; ++c) sum[c] = OWN ? f32x4{0.f, 0.f, 0.f, 0.f} : acc[c];
-    const uint8_t* smeta = lds + nrow * G * 2;
-    const uint8_t* zmeta = lds + sc * 16 + nrow * G * ZB;
+    wave_lds_fence();
+    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      const int step = b * kBlockSteps + t;
-      f16x8 f[CT][TERMS][4];
-#pragma unroll
-      for (int c = 0; c < CT; ++c)
-#pragma unroll
-        for (int j = 0; j < TERMS; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if constexpr (OWN) f[c][j][i] = *reinterpret_cast<const f16x8*>(xs + j * 1024 + t * 256 + i * 16);
-            else f[c][j][i] = *reinterpret_cast<const f16x8*>(static_cast<const uint8_t*>(x) + frag_at(c, p.blocks * kBlockSteps, step, TERMS, j, i, lane));
-          }
       const int g = 16 * b + 4 * t + q, gc = min(g, G - 1);
       AwqStep a;
       a.s = *reinterpret_cast<const uint16_t*>(smeta + 2 * gc);
@@ -202,47 +180,187 @@ __global__ void __launch_bounds__(768) awq_rows_kernel(int M, int N, int K, Rows
       for (int i = 0; i < 4; ++i) {
         const f16x8 w = awq_frag(d.c[t][i], s2, b2);
 #pragma unroll
-        for (int c = 0; c < CT; ++c)
-#pragma unroll
-          for (int j = 0; j < TERMS; ++j) sum[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, f[c][j][i], sum[c], 0, 0, 0);
+        for (int j = 0; j < TERMS; ++j)
+          sum = __builtin_amdgcn_mfma_f32_16x16x32_f16(w, *reinterpret_cast<const f16x8*>(xs + j * 1024 + t * 256 + i * 16), sum, 0, 0, 0);
       }
     }
-    if constexpr (OWN) {                                        // scaled back; the lane's column is row lane % 16 of x
-      float rs = scale[0];
+    float rs = scale[0];                                        // of the lane's column: row lane % 16 of x
 #pragma unroll
-      for (int m = 1; m < MR; ++m) rs = (lane & 15) >= m ? scale[m] : rs;
+    for (int m = 1; m < MR; ++m) rs = (lane & 15) >= m ? scale[m] : rs;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[0][j] = fmaf(sum[0][j], rs, acc[0][j]);
-    } else {
-#pragma unroll
-      for (int c = 0; c < CT; ++c) acc[c] = sum[c];
-    }
+    for (int j = 0; j < 4; ++j) acc[j] = fmaf(sum[j], rs, acc[j]);
   };
-  for (; b + p.waves < b1; b += 2 * p.waves) {
-    load(b + p.waves, v);
+  for (; b < b1; b += 2 * p.waves) {                            // (a load too many costs as much as one that is needed)
+    if (b + p.waves < b1) load(b + p.waves, v);
     multiply(b, u);
-    load(min(b + 2 * p.waves, b1 - 1), u);
+    if (b + p.waves >= b1) break;
+    if (b + 2 * p.waves < b1) load(b + 2 * p.waves, u);
     multiply(b + p.waves, v);
   }
-  if (b < b1) multiply(b, u);
 
   // the waves' sums, in order
   __syncthreads();                                              // every wave is done with the metadata and its terms
   float* part = reinterpret_cast<float*>(lds);
-#pragma unroll
-  for (int c = 0; c < CT; ++c) {
-    const int m = 16 * c + (lane & 15);
-    if (m < M) *reinterpret_cast<f32x4*>(part + (wave * M + m) * COLS + 4 * q) = acc[c];
-  }
+  if ((lane & 15) < M) *reinterpret_cast<f32x4*>(part + (wave * M + (lane & 15)) * COLS + 4 * q) = acc;
   __syncthreads();
   for (int i = tid; i < M * 16; i += 64 * p.waves) {
     const int m = i >> 4, n = n0 + (i & 15);
     if (n >= N) continue;
     float r = 0.f;
     for (int k = 0; k < p.waves; ++k) r += part[(k * M + m) * COLS + (i & 15)];
-    if constexpr (!OWN) r *= rowscale[m];
     if (partials != nullptr) partials[((size_t)blockIdx.y * M + m) * N + n] = r;
     else y[(size_t)m * N + n] = r;
+  }
+}
+
+// ---- up to kFewRows rows -----------------------------------------------------------------------------------------
+// 8 waves with 16 weight rows each share x: CT tiles of 16 rows, SB blocks at a time, turned into terms in LDS once for 128 weight
+// rows.  The contraction is split over workgroups until they fill the chip.  A row's metadata of SB blocks is 32 SB + 16 SB
+// bytes, read whole into the wave's own LDS: with the codes of all SB blocks and x on their way at once, a pass has one memory latency.
+constexpr int kFewRows = 32;
+constexpr int kSharedWaves = 8;
+// Blocks at a time for that many column tiles and terms: x and metadata leave room for two workgroups on a CU or more.
+constexpr int shared_blocks(int tiles) { return tiles == 1 ? 2 : 1; }
+
+template <int ML, int XS, int CT>
+__global__ void __launch_bounds__(512, 4) awq_shared_kernel(int M, int N, int K, int passes, int per, const void* __restrict__ x,
+                                                            const uint8_t* __restrict__ bank, AwqLayout L, float* __restrict__ y,
+                                                            float* __restrict__ partials) {
+  constexpr int TERMS = XS == X_F32 ? 2 : 1, SB = shared_blocks(CT * TERMS), ROW = SB * 1024 + 16;   // bytes of a staged row and term
+  constexpr int ZB = ML == 3 ? 1 : 2, SROW = SB * 32, ZROW = SB * 16 * ZB, WMETA = 16 * (SROW + ZROW);
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];   // x [16 CT][TERMS][ROW], the waves' metadata, row scales
+  const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), q = lane >> 4;
+  const int n0 = ((int)blockIdx.x * kSharedWaves + wave) * 16, G = (int)L.G, octets = K / 8;
+  uint8_t* smeta = lds + 16 * CT * TERMS * ROW + wave * WMETA;
+  uint8_t* zmeta = smeta + 16 * SROW;
+  float* scales = reinterpret_cast<float*>(lds + 16 * CT * TERMS * ROW + kSharedWaves * WMETA);
+  const int p0 = (int)blockIdx.y * per, p1 = min(p0 + per, passes);
+  // The last piece of the second plane starts here; a wave with rows whose pieces would reach further reads those one by one.
+  // Offsets from the wave's first row (or the last one there is) fit 32 bits: 16 rows of at most 4 MB.
+  const bool live_tile = n0 < N;
+  const int base = min(n0, N - 1), top = N - 1 - base;          // rows from `base` on: at most `top`
+  const int64_t zbytes = ZB * (int64_t)N * G, zat = (int64_t)base * G * ZB;
+  const int zlast = (int)min((zbytes + 15) / 16 * 16 - 16 - zat, (int64_t)1 << 30);
+  const uint8_t* codes = bank + (size_t)base * (L.G * 16);
+  const uint8_t* splane = bank + L.scale_off + (size_t)base * G * 2;
+  const uint8_t* zplane = bank + L.meta2_off + zat;
+  const int crow = min(lane & 15, top) * G * 16;
+  f32x4 acc[CT];
+#pragma unroll
+  for (int c = 0; c < CT; ++c) acc[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int p = p0; p < p1; ++p) {
+    constexpr int XR = 2 * CT;                                  // rows of x of a wave
+    const int b0 = p * SB;
+    RawOctet<XS> xr[XR][SB];
+#pragma unroll
+    for (int r = 0; r < XR; ++r)
+#pragma unroll
+      for (int j = 0; j < SB; ++j)
+        xr[r][j] = load_raw<XS>(static_cast<const uint8_t*>(x) + (size_t)min(wave + 8 * r, M - 1) * K * (XS == X_F32 ? 4 : 2),
+                                (uint32_t)(8 * min(64 * (b0 + j) + lane, octets - 1)));
+    constexpr int SP = 16 * SROW / 16, ZP = 16 * ZROW / 16, SN = (SP + 63) / 64, ZN = (ZP + 63) / 64;   // pieces of a wave, per lane
+    typedef uint32_t u32x4_a1 __attribute__((ext_vector_type(4), aligned(1)));
+    u32x4 sp[SN], zp[ZN];
+#pragma unroll
+    for (int j = 0; j < SN; ++j) {
+      const int i = min(lane + 64 * j, SP - 1), r = i / (SROW / 16), c = i % (SROW / 16);
+      sp[j] = *reinterpret_cast<const u32x4_a1*>(splane + (uint32_t)(2 * (min(r, top) * G + min(16 * b0 + 8 * c, G - 1))));
+    }
+#pragma unroll
+    for (int j = 0; j < ZN; ++j) {
+      const int i = min(lane + 64 * j, ZP - 1), r = i / (ZROW / 16), c = i % (ZROW / 16);
+      zp[j] = *reinterpret_cast<const u32x4_a1*>(zplane + min(ZB * (min(r, top) * G + min(16 * b0 + (16 / ZB) * c, G - 1)), zlast));
+    }
+    constexpr int D = SB < 2 ? SB : 2;                          // blocks of codes on their way at once (more spill)
+    u32x4 cd[D][4];
+    auto load_codes = [&](int j) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) cd[j % D][t] = *reinterpret_cast<const u32x4*>(codes + (uint32_t)(crow + 16 * min(16 * (b0 + j) + 4 * t + q, G - 1)));
+    };
+#pragma unroll
+    for (int j = 0; j < D; ++j) load_codes(j);
+    if (p != p0) __syncthreads();                               // the last pass's readers of x are done
+#pragma unroll
+    for (int r = 0; r < XR; ++r) {
+      const int m = wave + 8 * r;
+      if (m >= M) break;
+      float amax = 0.f;
+      if constexpr (XS != X_F16) {
+#pragma unroll
+        for (int j = 0; j < SB; ++j)
+          if (64 * (b0 + j) + lane < octets) amax = fmaxf(amax, octet_max<XS>(xr[r][j]));
+        amax = wave64_max(amax);
+      }
+      const int e = XS == X_F16 ? 0 : f16_row_exp(amax);
+      if (lane == 0) scales[m] = ldexpf(1.f, e);
+#pragma unroll
+      for (int j = 0; j < SB; ++j) {
+        u32x4 t[TERMS];
+        raw_terms<XS, TERMS>(xr[r][j], e, 64 * (b0 + j) + lane < octets, t);
+#pragma unroll
+        for (int k = 0; k < TERMS; ++k) *reinterpret_cast<u32x4*>(lds + (m * TERMS + k) * ROW + (64 * j + lane) * 16) = t[k];
+        __builtin_amdgcn_sched_barrier(0);                      // (interleaved, the octets' values spill)
+      }
+    }
+    wave_lds_fence();
+#pragma unroll
+    for (int j = 0; j < SN; ++j)
+      if (lane + 64 * j < SP) reinterpret_cast<u32x4*>(smeta)[lane + 64 * j] = sp[j];
+#pragma unroll
+    for (int j = 0; j < ZN; ++j)
+      if (lane + 64 * j < ZP) reinterpret_cast<u32x4*>(zmeta)[lane + 64 * j] = zp[j];
+    if (ZB * ((int64_t)min(15, top) * G + min(16 * (b0 + SB), G + 15)) > zlast) {
+      wave_lds_fence();
+      for (int i = lane; i < 16 * SB * 16; i += 64) {
+        const int r = i / (SB * 16), g = i % (SB * 16);
+        const int at = min(r, top) * G + min(16 * b0 + g, G - 1);
+        if constexpr (ML == 3) zmeta[r * ZROW + g] = zplane[at];
+        else *reinterpret_cast<uint16_t*>(zmeta + r * ZROW + 2 * g) = reinterpret_cast<const uint16_t*>(zplane)[at];
+      }
+    }
+    __syncthreads();
+    f32x4 sum[CT];
+#pragma unroll
+    for (int c = 0; c < CT; ++c) sum[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < SB; ++j) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const int at = 16 * j + 4 * t + q;
+        AwqStep a;
+        a.s = *reinterpret_cast<const uint16_t*>(smeta + (lane & 15) * SROW + 2 * at);
+        if constexpr (ML == 3) a.z = zmeta[(lane & 15) * ZROW + at];
+        else a.z = *reinterpret_cast<const uint16_t*>(zmeta + (lane & 15) * ZROW + 2 * at);
+        f16x2 s2, b2;
+        awq_meta<ML>(a, 16 * b0 + at < G, s2, b2);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f16x8 w = awq_frag(cd[j % D][t][i], s2, b2);
+#pragma unroll
+          for (int c = 0; c < CT; ++c) {
+            const int m = min(16 * c + (lane & 15), M - 1);
+#pragma unroll
+            for (int k = 0; k < TERMS; ++k)
+              sum[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                  w, *reinterpret_cast<const f16x8*>(lds + (m * TERMS + k) * ROW + (4 * at + i) * 16), sum[c], 0, 0, 0);
+          }
+        }
+      }
+      if (j + D < SB) load_codes(j + D);
+    }
+#pragma unroll
+    for (int c = 0; c < CT; ++c) {
+      const float rs = scales[min(16 * c + (lane & 15), M - 1)];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[c][j] = fmaf(sum[c][j], rs, acc[c][j]);
+    }
+  }
+  if (!live_tile) return;
+  float* out = partials != nullptr ? partials + (size_t)blockIdx.y * M * N : y;
+#pragma unroll
+  for (int c = 0; c < CT; ++c) {
+    const int m = 16 * c + (lane & 15);
+    if (m < M) store_row4(out, N, m, n0 + 4 * q, acc[c]);
   }
 }
 
@@ -341,14 +459,7 @@ __global__ void __launch_bounds__(256, 2) awq_gemm_kernel(int M, int N, int step
     for (int r = 0; r < NT; ++r) {
       const int n = n0 + 16 * r + 4 * q;
       const f32x4 v = acc[r][c];
-      float* o = out + (size_t)m * N + n;
-      if (n + 3 < N && (N & 3) == 0) {
-        *reinterpret_cast<f32x4*>(o) = f32x4{v[0] * rs, v[1] * rs, v[2] * rs, v[3] * rs};
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (n + j < N) o[j] = v[j] * rs;
-      }
+      store_row4(out, N, m, n, f32x4{v[0] * rs, v[1] * rs, v[2] * rs, v[3] * rs});
     }
   }
 }
@@ -364,34 +475,45 @@ __global__ void __launch_bounds__(256) awq_join_kernel(int M, int N, int S, cons
 }
 
 // ---- plan --------------------------------------------------------------------------------------------------------
+// Workgroups of awq_shared_kernel to split up to: three per CU with two blocks at a time, else two.  13 rows 5120 -> 17408: 256 26.5 us,
+// 512 24.4, 768 20.6, 1536 20.4; 24 rows: 256 33.7, 512 25.1, 768 26.8.
+constexpr int shared_fill(int tiles) { return tiles == 1 ? 768 : 512; }
+
 struct AwqPlan {
-  bool rows, own;              // few rows; so few that the waves turn them into terms themselves (no packing)
-  int terms, steps, S, per;
-  int ct, waves;               // few rows: column tiles, waves
-  int mt, ntm, tiles;          // many rows
+  enum { kOwn, kShared, kTiles } kind;
+  int terms, steps, S, per;    // S parts of `per` blocks (kOwn), passes (kShared) or steps (kTiles)
+  int units;                   // blocks, passes
+  int ct, waves;               // column tiles (kShared), waves (kOwn)
+  int mt, ntm, tiles;          // kTiles
   size_t xp, rs, partials, total;
 };
 inline AwqPlan awq_plan(int M, int N, int K, XType xt) {
   AwqPlan p{};
   p.terms = awq_terms(xt);
   p.steps = (K + kStepK - 1) / kStepK;
-  p.rows = M <= kFewRows && K / 32 <= kRowsGroups;
+  p.kind = M <= kOwnRows && K / 32 <= kRowsGroups ? AwqPlan::kOwn : (M <= kFewRows ? AwqPlan::kShared : AwqPlan::kTiles);
   const int64_t most = std::max<int64_t>(1, ((int64_t)64 << 20) / ((int64_t)M * N * 4));   // at most 64 MiB of parts
-  if (p.rows) {
-    const int blocks = (p.steps + kBlockSteps - 1) / kBlockSteps;
-    p.steps = blocks * kBlockSteps;
-    p.own = M <= kOwnRows;
-    p.ct = M <= 16 ? 1 : 2;
+  const int blocks = (p.steps + kBlockSteps - 1) / kBlockSteps;
+  if (p.kind == AwqPlan::kOwn) {
+    p.units = blocks;
     const int64_t wgs = (N + 15) / 16;
     const int64_t S = std::min(std::max<int64_t>(1, std::min<int64_t>(256 / wgs, blocks / 12)), most);
     p.per = (int)((blocks + S - 1) / S);
     p.S = (blocks + p.per - 1) / p.per;
-    // waves: what the chip holds at once (20 per CU), at most 10 (two workgroups per CU) and no more than the number of turns needs; at
-    // least 4, which read the metadata
-    int top = 10;
+    // waves: at most 8, fewer where there are more workgroups than the chip then holds at once (20 waves per CU), and no more than the
+    // number of turns needs; at least 4, which read the metadata.  5120 -> 17408, 1 row: 4 waves 14.3 us, 5 17.7, 8 17.2, 12 23;
+    // 17408 -> 5120: 4 waves 17.4, 8 17.2, 12 19.7.
+    int top = 8;
     while (top > 4 && wgs * p.S > 256 * (20 / top)) --top;
     const int turns = (p.per + top - 1) / top;
     p.waves = std::max(4, (p.per + turns - 1) / turns);
+  } else if (p.kind == AwqPlan::kShared) {
+    p.ct = M <= 16 ? 1 : 2;
+    const int sb = shared_blocks(p.ct * p.terms), cols = (N + 16 * kSharedWaves - 1) / (16 * kSharedWaves);
+    p.units = (blocks + sb - 1) / sb;
+    const int64_t S = std::min(std::min<int64_t>(p.units, std::max(1, (shared_fill(p.ct * p.terms) + cols - 1) / cols)), most);
+    p.per = (int)((p.units + S - 1) / S);
+    p.S = (p.units + p.per - 1) / p.per;
   } else {
     p.mt = p.terms == 2 || M <= 64 ? 4 : 8;
     p.ntm = (M + 16 * p.mt - 1) / (16 * p.mt);
@@ -401,8 +523,8 @@ inline AwqPlan awq_plan(int M, int N, int K, XType xt) {
     p.S = (p.steps + p.per - 1) / p.per;
   }
   p.xp = 0;
-  p.rs = p.own ? 0 : align256((size_t)((M + 15) / 16) * p.steps * p.terms * 4096);
-  p.partials = p.own ? 0 : p.rs + align256((size_t)(M + 15) / 16 * 16 * 4);
+  p.rs = p.kind != AwqPlan::kTiles ? 0 : align256((size_t)((M + 15) / 16) * p.steps * p.terms * 4096);
+  p.partials = p.kind != AwqPlan::kTiles ? 0 : p.rs + align256((size_t)(M + 15) / 16 * 16 * 4);
   p.total = p.partials + (p.S > 1 ? align256((size_t)p.S * M * N * 4) : 0);
   return p;
 }
@@ -413,14 +535,22 @@ void pack_rows(int M, int K, int steps, const void* x, uint8_t* xp, float* rs, h
   hipLaunchKernelGGL((awq_pack_kernel<XT, TERMS>), dim3(grid), dim3(256), 0, st, M, K, steps, x, xp, rs);
 }
 
-template <int ML, int TERMS, int CT, int XS, int MR>
-hipError_t run_rows(const AwqPlan& p, int M, int N, int K, const void* x, const float* rs, const uint8_t* bank, const AwqLayout& L, float* y,
+template <int ML, int XS, int MR>
+hipError_t run_rows(const AwqPlan& p, int M, int N, int K, const void* x, const float*, const uint8_t* bank, const AwqLayout& L, float* y,
                     float* partials, hipStream_t st) {
-  if (!raise_lds_limit<awq_rows_kernel<ML, TERMS, CT, XS, MR>>()) return hipErrorInvalidValue;
-  const int sums = p.waves * M * 20 * 4, meta = 16 * (K / 32) * ML + 32, own = XS == kPackedRows ? 0 : p.waves * MR * TERMS * 1024;
-  const RowsPlan r{p.steps / kBlockSteps, p.per, p.waves};
-  hipLaunchKernelGGL((awq_rows_kernel<ML, TERMS, CT, XS, MR>), dim3((N + 15) / 16, p.S), dim3(64 * p.waves), std::max(sums, meta + own),
-                     st, M, N, K, r, x, rs, bank, L, y, partials);
+  if (!raise_lds_limit<awq_rows_kernel<ML, XS, MR>>()) return hipErrorInvalidValue;
+  const int sums = p.waves * M * 20 * 4, held = 16 * (K / 32) * ML + 32 + p.waves * MR * p.terms * 1024;
+  hipLaunchKernelGGL((awq_rows_kernel<ML, XS, MR>), dim3((N + 15) / 16, p.S), dim3(64 * p.waves), std::max(sums, held), st, M, N, K,
+                     RowsPlan{p.units, p.per, p.waves}, x, bank, L, y, partials);
+  return hipGetLastError();
+}
+template <int ML, int XS, int CT>
+hipError_t run_shared(const AwqPlan& p, int M, int N, int K, const void* x, const float*, const uint8_t* bank, const AwqLayout& L, float* y,
+                      float* partials, hipStream_t st) {
+  if (!raise_lds_limit<awq_shared_kernel<ML, XS, CT>>()) return hipErrorInvalidValue;
+  const int sb = shared_blocks(CT * p.terms), lds = 16 * CT * p.terms * (sb * 1024 + 16) + kSharedWaves * 16 * sb * 16 * ML + 16 * CT * 4;
+  hipLaunchKernelGGL((awq_shared_kernel<ML, XS, CT>), dim3((N + 16 * kSharedWaves - 1) / (16 * kSharedWaves), p.S), dim3(64 * kSharedWaves),
+                     lds, st, M, N, K, p.units, p.per, x, bank, L, y, partials);
   return hipGetLastError();
 }
 template <int ML, int TERMS, int MT>
@@ -434,18 +564,16 @@ hipError_t run_gemm(const AwqPlan& p, int M, int N, int, const void* xp, const f
 template <int ML, int XT, typename... A>
 hipError_t run_plan(const AwqPlan& p, int M, A... a) {
   constexpr int T = XT == X_F32 ? 2 : 1;
-  if (!p.rows) {
-    if constexpr (T == 1)
-      if (p.mt == 8) return run_gemm<ML, T, 8>(p, M, a...);
-    return run_gemm<ML, T, 4>(p, M, a...);
+  switch (p.kind) {
+    case AwqPlan::kOwn:
+      if (M == 1) return run_rows<ML, XT, 1>(p, M, a...);
+      return run_rows<ML, XT, 2>(p, M, a...);
+    case AwqPlan::kShared: return p.ct == 1 ? run_shared<ML, XT, 1>(p, M, a...) : run_shared<ML, XT, 2>(p, M, a...);
+    default: break;
   }
-  if (p.own) {
-    if (M == 1) return run_rows<ML, T, 1, XT, 1>(p, M, a...);
-    if (M == 2) return run_rows<ML, T, 1, XT, 2>(p, M, a...);
-    return run_rows<ML, T, 1, XT, 4>(p, M, a...);
-  }
-  if (p.ct == 1) return run_rows<ML, T, 1, kPackedRows, 1>(p, M, a...);
-  return run_rows<ML, T, 2, kPackedRows, 1>(p, M, a...);
+  if constexpr (T == 1)
+    if (p.mt == 8) return run_gemm<ML, T, 8>(p, M, a...);
+  return run_gemm<ML, T, 4>(p, M, a...);
 }
 template <int XT>
 hipError_t linear(const AwqPlan& p, int M, int N, int K, const void* x, const uint8_t* bank, int meta_layout, uint8_t* ws, float* y,
@@ -454,7 +582,7 @@ hipError_t linear(const AwqPlan& p, int M, int N, int K, const void* x, const ui
   uint8_t* xp = ws + p.xp;
   float* rs = reinterpret_cast<float*>(ws + p.rs);
   float* partials = p.S > 1 ? reinterpret_cast<float*>(ws + p.partials) : nullptr;
-  if (!p.own) {
+  if (p.kind == AwqPlan::kTiles) {
     pack_rows<XT, XT == X_F32 ? 2 : 1>(M, K, p.steps, x, xp, rs, st);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
