@@ -65,12 +65,13 @@ int awq_linear_backward(int64_t M, int64_t N, int64_t K, const void* dy, int dy_
  *   w13_bank, w2_bank as for moe_awq_m1_run; meta_layout 3 or 4
  *   out     [M, H]    out_dtype (any of the three), rounded once
  * 0 <= M <= WQ_MOE_MAX_TOKENS, 1 <= topk <= min(E, WQ_MOE_MAX_TOPK) (given ids: topk may exceed E), H and I
- * multiples of 32.  Numerics as for awq_linear_run: products and sums are float32, float32 x and act enter as two
+ * multiples of 32 up to WQ_MOE_MAX_WIDTH.  Numerics as for awq_linear_run: products and sums are float32, float32 x and act enter as two
  * float16 terms; no intermediate is rounded to 16 bits (moe_awq_m1_run rounds g, u, act and each route's result to
  * float16).  A token's result is the same bits whatever the other tokens are and however many.  Where x holds an infinity or NaN its row's ids are those of the order above, and its out may be NaN.  An expert is
  * read once for up to 16 of its tokens.
  */
 #define WQ_MOE_MAX_TOKENS 256
+#define WQ_MOE_MAX_WIDTH 16384
 enum { WQ_MOE_RENORM = 1 };
 size_t moe_awq_workspace_bytes(int64_t M, int64_t E, int64_t topk, int64_t H, int64_t I);
 int moe_awq_run(int64_t M, int64_t E, int64_t topk, int64_t H, int64_t I, const void* x, int x_dtype, const void* router,

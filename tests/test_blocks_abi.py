@@ -169,7 +169,7 @@ def moe_args(**kw):
     (dict(x=None), EINVAL), (dict(ids=None), EINVAL), (dict(w=None), EINVAL), (dict(w13=None), EINVAL), (dict(w2=None), EINVAL),
     (dict(out=None), EINVAL), (dict(xt=3), EINVAL), (dict(rt=3), EINVAL), (dict(ot=-1), EINVAL), (dict(layout=5), EINVAL),
     (dict(M=-1), EINVAL), (dict(M=257), EINVAL), (dict(E=0), EINVAL), (dict(topk=0), EINVAL), (dict(topk=17, E=32), EINVAL),
-    (dict(topk=9), EINVAL), (dict(H=48), EINVAL), (dict(I=16), EINVAL), (dict(H=0), EINVAL), (dict(I=(1 << 22) + 32), EINVAL),
+    (dict(topk=9), EINVAL), (dict(H=48), EINVAL), (dict(I=16), EINVAL), (dict(H=0), EINVAL), (dict(I=16416), EINVAL), (dict(H=16416), EINVAL),
     (dict(E=1 << 23, H=1 << 14), EINVAL), (dict(flags=2), EINVAL), (dict(router=None), EINVAL), (dict(router=None, flags=4), EINVAL),
     (dict(x=A + 8), EALIGN), (dict(ids=A + 2 * MB + 4), EALIGN), (dict(w2=A + 5 * MB + 8), EALIGN), (dict(router=A + MB + 2), EALIGN),
     (dict(ws=None), EWORKSPACE), (dict(wsb=256), EWORKSPACE),

@@ -10,8 +10,7 @@
 // The experts' bytes bound it as soon as tokens spread over many experts, and every expert is read once for all of its
 // tokens: a workgroup belongs to one expert (or to one route, the first that names its expert, when there are fewer routes
 // than experts) and some of its rows, gathers the expert's routes from the list of ids, and multiplies its weights, decoded
-// in registers (awq_common.h), with up to 16 of them at a time on the matrix cores.  Its 8 waves split the rows and the
-// contraction.  act travels in float32 and enters W2 as two float16 terms, like float32 x, so nothing is rounded to 16 bits
+// in registers (awq_common.h), with up to 16 of them at a time on the matrix cores.  act travels in float32 and enters W2 as two float16 terms, like float32 x, so nothing is rounded to 16 bits
 // on the way.
 #include <algorithm>
 
@@ -24,247 +23,377 @@ namespace wq {
 namespace {
 
 // ---- router ------------------------------------------------------------------------------------------------------
-// A wave per expert, kRouteTokens tokens at a time: 8 elements per lane and turn, products and sums in float64 (a product of
-// two float32 is exact there).
-constexpr int kRouteTokens = 4;
-
-template <int XT, int WT>
+// A wave for TE experts and TT tokens: 8 elements per lane and turn, products and sums in float64 (a product of two float32 is exact
+// there), every element converted once.  Which elements a lane sums in which order does not depend on TE and TT.  (On the float64 matrix
+// cores, 16 x 16 tiles: as fast for 37 tokens, 10.3 us for 512 experts on 2560, but 10.3 in place of 4.4 for one.)
+template <int XT, int WT, int TE, int TT>
 __global__ void __launch_bounds__(256) route_logits_kernel(int M, int E, int H, const void* __restrict__ x,
                                                            const void* __restrict__ router, float* __restrict__ logits) {
-  const int lane = (int)threadIdx.x & 63, e = (int)blockIdx.x * 4 + ((int)threadIdx.x >> 6), m0 = (int)blockIdx.y * kRouteTokens;
-  if (e >= E) return;
-  double acc[kRouteTokens] = {};
-  for (int o = lane; o < H / 8; o += 64) {
-    float w[8];
-    load_octet<WT>(router, (size_t)e * H + 8 * (size_t)o, w);
+  const int lane = (int)threadIdx.x & 63, e0 = ((int)blockIdx.x * 4 + ((int)threadIdx.x >> 6)) * TE, m0 = (int)blockIdx.y * TT;
+  if (e0 >= E) return;
+  constexpr int UP = TT == 1 ? 4 : 2;                           // turns on their way at once
+  double acc[TE][TT] = {};
+  const int octets = H / 8;
+  for (int o0 = lane; o0 < octets; o0 += 64 * UP) {
+    RawOctet<WT> w[UP][TE];
+    RawOctet<XT> v[UP][TT];
 #pragma unroll
-    for (int t = 0; t < kRouteTokens; ++t) {
-      float v[8];
-      load_octet<XT>(x, (size_t)min(m0 + t, M - 1) * H + 8 * (size_t)o, v);
+    for (int k = 0; k < UP; ++k) {
+      const size_t at = 8 * (size_t)min(o0 + 64 * k, octets - 1);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) acc[t] = fma((double)v[j], (double)w[j], acc[t]);
+      for (int i = 0; i < TE; ++i) w[k][i] = load_raw<WT>(router, (size_t)min(e0 + i, E - 1) * H + at);
+#pragma unroll
+      for (int t = 0; t < TT; ++t) v[k][t] = load_raw<XT>(x, (size_t)min(m0 + t, M - 1) * H + at);
+    }
+#pragma unroll
+    for (int k = 0; k < UP; ++k) {
+      if (o0 + 64 * k >= octets) break;
+      double wd[TE][8];
+#pragma unroll
+      for (int i = 0; i < TE; ++i) {
+        float f[8];
+        raw_values<WT>(w[k][i], f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) wd[i][j] = f[j];
+      }
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        float f[8];
+        raw_values<XT>(v[k][t], f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const double xd = f[j];
+#pragma unroll
+          for (int i = 0; i < TE; ++i) acc[i][t] = fma(xd, wd[i][j], acc[i][t]);
+        }
+      }
     }
   }
 #pragma unroll
-  for (int t = 0; t < kRouteTokens; ++t) {
-    for (int off = 32; off >= 1; off >>= 1) acc[t] += __shfl_xor(acc[t], off, 64);
-    if (lane == 0 && m0 + t < M) logits[(size_t)(m0 + t) * E + e] = (float)acc[t];
-  }
+  for (int i = 0; i < TE; ++i)
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+      for (int off = 32; off >= 1; off >>= 1) acc[i][t] += __shfl_xor(acc[i][t], off, 64);
+      if (lane == 0 && m0 + t < M && e0 + i < E) logits[(size_t)(m0 + t) * E + e0 + i] = (float)acc[i][t];
+    }
 }
 
-// Order of selection as one number, larger first: the logit (NaN below everything, -0 as 0), then the lower index.
-__device__ __forceinline__ uint64_t route_rank(float logit, int e) {
-  const uint32_t b = __float_as_uint(logit + 0.f);
-  const uint32_t key = logit == logit ? (b & 0x80000000u ? ~b : b | 0x80000000u) : 0u;
-  return ((uint64_t)key << 32) | (uint32_t)(0x7FFFFFFF - e);
+// Order of selection as a signed number, larger first: NaN below every value, -0 as 0.  kTaken is below all.
+constexpr int kTaken = -0x7FFFFFFF - 1;
+__device__ __forceinline__ int route_key(float logit) {
+  const int b = __float_as_int(logit + 0.f);
+  return logit == logit ? (b < 0 ? b ^ 0x7FFFFFFF : b) : kTaken + 1;
 }
-// One wave: the topk largest of the token's E logits, each found as the largest one below the last.  Lane k gets the k-th
-// (topk <= 16); the weights are the softmax of the chosen (renorm) or of all.
-__device__ __forceinline__ void route_token(int E, int topk, bool renorm, const float* __restrict__ logits, int lane, int& id, float& weight) {
-  uint64_t last = ~0ull;
-  float first = 0.f, sum = 0.f, mine = 0.f;
-  id = 0;
+__device__ __forceinline__ float route_logit(int key) {
+  return key == kTaken + 1 ? __int_as_float(0x7FC00000) : __int_as_float(key < 0 ? key ^ 0x7FFFFFFF : key);
+}
+template <int CTRL>
+__device__ __forceinline__ int dpp_i32(int v) { return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, true); }
+__device__ __forceinline__ int wave64_max_i32(int v) {
+  v = max(v, dpp_i32<0xB1>(v));
+  v = max(v, dpp_i32<0x4E>(v));
+  v = max(v, dpp_i32<0x141>(v));
+  v = max(v, dpp_i32<0x140>(v));
+  return max(max(__builtin_amdgcn_readlane(v, 0), __builtin_amdgcn_readlane(v, 16)),
+             max(__builtin_amdgcn_readlane(v, 32), __builtin_amdgcn_readlane(v, 48)));
+}
+// One wave per token: lane holds the keys of experts lane, lane + 64, ... (VPL of them, or VPL = 0: any number, read again for every
+// choice).  Each turn takes the largest key, of equal ones the lowest expert.  Lane k gets the k-th choice; the weights are the softmax of
+// the chosen (renorm) or of all.
+template <int VPL>
+__global__ void __launch_bounds__(64) route_topk_kernel(int E, int topk, int renorm, const float* __restrict__ all, int32_t* __restrict__ ids,
+                                                        float* __restrict__ weights) {
+  const int lane = (int)threadIdx.x, m = (int)blockIdx.x;
+  const float* logits = all + (size_t)m * E;
+  int key[VPL > 0 ? VPL : 1];
+  if constexpr (VPL > 0) {
+    float l[VPL];
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) l[j] = logits[min(lane + 64 * j, E - 1)];
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) key[j] = lane + 64 * j < E ? route_key(l[j]) : kTaken;
+  }
+  int id = 0, last_key = 0x7FFFFFFF, last_e = -1;
+  float first = 0.f, mine = 0.f;
   for (int k = 0; k < topk; ++k) {
-    uint64_t best = 0;
-    for (int e = lane; e < E; e += 64) {
-      const uint64_t r = route_rank(logits[e], e);
-      if (r < last && r > best) best = r;
+    int best = kTaken, at = 0x7FFFFFFF;                       // the lane's largest key and its expert
+    if constexpr (VPL > 0) {
+#pragma unroll
+      for (int j = 0; j < VPL; ++j)
+        if (key[j] > best) best = key[j], at = lane + 64 * j;
+    } else {
+      for (int e = lane; e < E; e += 64) {
+        const int v = route_key(logits[e]);
+        const bool left = v < last_key || (v == last_key && e > last_e);
+        if (left && v > best) best = v, at = e;
+      }
     }
-    for (int off = 32; off >= 1; off >>= 1) {
-      const uint64_t o = __shfl_xor((unsigned long long)best, off, 64);
-      best = o > best ? o : best;
+    const int top = wave64_max_i32(best);
+    const int e = -wave64_max_i32(best == top ? -at : -0x7FFFFFFF);
+    if constexpr (VPL > 0) {
+#pragma unroll
+      for (int j = 0; j < VPL; ++j)
+        if (e == lane + 64 * j) key[j] = kTaken;
     }
-    last = best;
-    const int e = 0x7FFFFFFF - (int)(uint32_t)best;
-    const float l = logits[e];
-    if (k == 0) first = l;
-    const float p = expf(l - first);
-    sum += p;
-    if (lane == k) {
-      id = e;
-      mine = p;
-    }
+    last_key = top, last_e = e;
+    if (k == 0) first = route_logit(top);
+    if (lane == k) id = e, mine = route_logit(top);
   }
-  if (!renorm) {
-    sum = 0.f;
+  mine = lane < topk ? expf(mine - first) : 0.f;
+  float sum = 0.f;
+  if (renorm == 0)
     for (int e = lane; e < E; e += 64) sum += expf(logits[e] - first);
-    sum = group_sum<64>(sum);
-  }
-  weight = mine / sum;
-}
-__global__ void __launch_bounds__(256) route_topk_kernel(int M, int E, int topk, int renorm, const float* __restrict__ logits,
-                                                         int32_t* __restrict__ ids, float* __restrict__ weights) {
-  const int lane = (int)threadIdx.x & 63, m = (int)blockIdx.x * 4 + ((int)threadIdx.x >> 6);
-  if (m >= M) return;
-  int id;
-  float w;
-  route_token(E, topk, renorm != 0, logits + (size_t)m * E, lane, id, w);
+  sum = wave64_sum(renorm == 0 ? sum : mine);
   if (lane < topk) {
     ids[(size_t)m * topk + lane] = id;
-    weights[(size_t)m * topk + lane] = w;
+    weights[(size_t)m * topk + lane] = mine / sum;
   }
 }
 
 // ---- the experts' products ---------------------------------------------------------------------------------------
+// A pair is two tiles of 16 weight rows: W13 16 gate rows and the same 16 up rows, W2 32 rows.  A workgroup has some pairs of one
+// expert: it finds the expert's routes in the list of ids, copies its rows' scales and zeros (contiguous pieces of the bank) to LDS,
+// turns up to `cols` of the routes' rows into float16 terms there, 512 k at a time with a power of two of their own, and multiplies.
+//   Many routes: a wave takes whole pairs, block after block of 512 k, each step's codes replaced by the next block's as soon as
+//     they are used, and nothing is exchanged between waves.
+//   Few routes (SPLIT): the waves of a workgroup share one pair's blocks, so that one token's experts reach all CUs.
+// Either way a column's blocks are added in order, each scaled by a power of two, which is exact: its bits depend neither on the way nor on
+// how many columns there are.
 constexpr int kMaxRoutes = 256 * 16;
 constexpr int kPartRow = 20;                   // floats of a row of partial sums: 16, padded
-constexpr int kColBytes = 16;                  // padding of a staged column
-constexpr int kStageBytes = 16 * 2 * (8 * 256 + kColBytes);   // activations of one pass: 16 columns of two terms, a step for each
-                                                              // of 8 waves; two workgroups share a CU
-constexpr int kHeadBytes = kMaxRoutes * 2 + 16 * 4 + kMaxRoutes / 64 * 8;
-constexpr int kMoeLds = kHeadBytes + kStageBytes;
+constexpr int kBlockK = 512, kBlockSteps = 4;
 
 struct MoeShape {
   int E, routes, topk;
   int K, rows;                 // contraction; rows of weights per expert (of gate, for W13)
-  int wk;                      // waves that split the contraction (1, 2, 4 or 8); 8 / wk groups of rows per workgroup
+  int pairs;                   // of a workgroup
+  int waves, cols;
   int by_route;                // blockIdx.y is a route, else an expert
 };
+// LDS: metadata, then the terms [cols][blocks][TERMS][1 KB] and their powers of two [cols][blocks], SPLIT: the blocks' sums
+// [block][tile][cols][kPartRow], then the list of routes.
+struct MoeLds {
+  int terms, scales, part, list, total;
+};
+__host__ __device__ inline MoeLds moe_lds(const MoeShape& s, int terms, int ml, bool split) {
+  MoeLds l;
+  const int blocks = (s.K + kBlockK - 1) / kBlockK;
+  l.terms = 2 * 16 * s.pairs * (s.K / 32) * ml;
+  l.scales = l.terms + s.cols * blocks * terms * 1024;
+  l.part = (l.scales + s.cols * blocks * 4 + 15) / 16 * 16;
+  l.list = l.part + (split ? blocks * 2 * s.cols * kPartRow * 4 : 0);
+  l.total = (l.list + s.routes * 2 + 15) / 16 * 16;
+  return l;
+}
 
-// GU (W13): a wave's two row tiles are 16 gate rows and the same 16 up rows, src = x (row = token), dst = act [route][rows].
-// Else (W2): 32 rows, src = act (row = route), dst = y [route][rows].
-template <bool GU, int XT, int ML>
-__global__ void __launch_bounds__(512) moe_mm_kernel(MoeShape sh, const void* __restrict__ src, const int32_t* __restrict__ ids,
+// GU (W13): src = x (row = token), dst = act [route][rows].  Else (W2): src = act (row = route), dst = y [route][rows].
+template <bool GU, bool SPLIT, int XT, int ML>
+__global__ void __launch_bounds__(1024) moe_mm_kernel(MoeShape sh, const void* __restrict__ src, const int32_t* __restrict__ ids,
                                                      const uint8_t* __restrict__ bank, AwqLayout L, float* __restrict__ dst) {
-  constexpr int TERMS = XT == X_F32 ? 2 : 1;
+  constexpr int TERMS = XT == X_F32 ? 2 : 1, ZB = ML == 3 ? 1 : 2;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  uint16_t* list = reinterpret_cast<uint16_t*>(lds);                              // the expert's routes, ascending
-  float* scales = reinterpret_cast<float*>(lds + kMaxRoutes * 2);                 // of the pass's columns
-  uint64_t* masks = reinterpret_cast<uint64_t*>(lds + kMaxRoutes * 2 + 16 * 4);   // of each 64 ids: those that name the expert
-  uint8_t* stage = lds + kHeadBytes;
+  const MoeLds at = moe_lds(sh, TERMS, ML, SPLIT);
+  float* scales = reinterpret_cast<float*>(lds + at.scales);
+  uint16_t* list = reinterpret_cast<uint16_t*>(lds + at.list);                 // the expert's routes, ascending
   const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int q = lane >> 4, item = (int)blockIdx.y;
-  const int e = sh.by_route ? ids[item] : item;
-  if (e < 0 || e >= sh.E) return;
+  const int q = lane >> 4, item = (int)blockIdx.y, T = 64 * sh.waves;
 
-  // The list: 64 ids per wave and turn, each match's place from the matches before it.
-  const int blocks = (sh.routes + 63) >> 6;
-  for (int b = wave; b < blocks; b += 8) {
-    const int r = 64 * b + lane;
-    const uint64_t mask = __ballot(r < sh.routes && ids[r] == e);
-    if (lane == 0) masks[b] = mask;
-  }
-  __syncthreads();
-  int nc = 0;
-  for (int b = 0; b < blocks; ++b) {
-    const uint64_t mask = masks[b];
-    if (b % 8 == wave && (mask >> lane & 1)) list[nc + __popcll(mask & ((1ull << lane) - 1))] = (uint16_t)(64 * b + lane);
-    nc += __popcll(mask);
-  }
-  __syncthreads();
-  if (nc == 0 || (sh.by_route && (int)list[0] != item)) return;    // nobody's expert, or another route's workgroup has it
-
-  const int wk = wave % sh.wk, group = (int)blockIdx.x * (8 / sh.wk) + wave / sh.wk, per = GU ? 16 : 32;
-  const int groups = sh.rows / per, gc = min(group, groups - 1);
-  const uint8_t* expert = bank + (size_t)e * L.expert_bytes;
-  const uint8_t* codes[2];
-  int64_t row[2];
+  // The expert's routes, 8 x 64 ids at a time.  Every wave finds them for itself and writes the same list, so none waits for another.
+  int e = item, nc = 0;
+  for (int r0 = 0; r0 < sh.routes; r0 += 512) {
+    int id[8];
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    row[t] = gc * per + (lane & 15) + t * (GU ? sh.rows : 16);
-    codes[t] = expert + row[t] * (L.G * 16);
-  }
-  const int steps = (sh.K + kStepK - 1) / kStepK, real = sh.K / 8;
-
-  for (int c0 = 0; c0 < nc; c0 += 16) {
-    const int cols = min(16, nc - c0);
-    auto src_row = [&](int c) {
-      const int r = list[c0 + c];
-      return (size_t)(GU ? r / sh.topk : r) * sh.K;
-    };
-    __syncthreads();                                                // the last pass's readers of scales are done
-    for (int c = wave; c < cols; c += 8) {                          // column c's power of two
-      float amax = 0.f;
-      if constexpr (XT != X_F16)
-        for (int o = lane; o < real; o += 64) {
-          float v[8];
-          load_octet<XT>(src, src_row(c) + 8 * (size_t)o, v);
+    for (int k = 0; k < 8; ++k) id[k] = ids[min(r0 + 64 * k + lane, sh.routes - 1)];
+    if (r0 == 0 && sh.by_route) e = ids[item];
+    e = __builtin_amdgcn_readfirstlane(e);
+    if (e < 0 || e >= sh.E) return;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) amax = fmaxf(amax, finite_abs(v[j]));
-        }
-#pragma unroll
-      for (int off = 32; off >= 1; off >>= 1) amax = fmaxf(amax, __shfl_xor(amax, off, 64));
-      if (lane == 0) scales[c] = XT == X_F16 ? 1.f : ldexpf(1.f, f16_row_exp(amax));
+    for (int k = 0; k < 8; ++k) {
+      const int r = r0 + 64 * k + lane;
+      const uint64_t mask = __ballot(r < sh.routes && id[k] == e);
+      if (nc == 0 && mask != 0 && sh.by_route && r0 + 64 * k + __builtin_ctzll(mask) != item) return;   // an earlier route's workgroup has it
+      if (mask >> lane & 1) list[nc + __popcll(mask & ((1ull << lane) - 1))] = (uint16_t)r;
+      nc += __popcll(mask);
     }
-    f32x4 acc[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-    // steps staged at a time: a multiple of wk, so that which wave takes which step, and with it the order of every sum, does
-    // not depend on how many columns there are
-    const int room = (kStageBytes / (cols * TERMS) - kColBytes) / (kStepK * 2), chunk = room >= steps ? steps : room / sh.wk * sh.wk;
-    const int stride = chunk * kStepK * 2 + kColBytes;              // of one term of one column
-    for (int k0 = 0; k0 < steps; k0 += chunk) {
-      const int ks = min(chunk, steps - k0), end = k0 + ks;
-      int s = k0 + wk;
-      AwqStep a[2], b[2];
-      auto load = [&](int step, AwqStep* d) {
-        const int sc = min(step, steps - 1);
-        d[0] = awq_load<ML>(codes[0], expert, L, row[0], 4 * sc + q);
-        d[1] = awq_load<ML>(codes[1], expert, L, row[1], 4 * sc + q);
-      };
-      load(s, a);
-      __syncthreads();                                              // scales written; the last chunk's readers done
-      for (int i = tid; i < cols * ks * 16; i += 512) {
-        const int c = i / (ks * 16), o = i - c * ks * 16, at = k0 * 16 + o;
-        u32x4 w[TERMS];
-        if (at < real) {
-          float v[8];
-          load_octet<XT>(src, src_row(c) + 8 * (size_t)at, v);
-          int ex = 0;
-          if constexpr (XT != X_F16) ex = (int)((__float_as_uint(scales[c]) >> 23) & 255) - 127;
-          octet_terms<TERMS>(v, ex, w);
-        } else {
+  }
+  if (nc == 0) return;
+  wave_lds_fence();
+
+  const int per = GU ? 16 : 32, G = (int)L.G, steps = (sh.K + kStepK - 1) / kStepK, blocks = (steps + kBlockSteps - 1) / kBlockSteps;
+  const int p0 = (int)blockIdx.x * sh.pairs, p1 = min(p0 + sh.pairs, sh.rows / per);
+  const uint8_t* expert = bank + (size_t)e * L.expert_bytes;
+  // Tile t of pair p: rows tile_row(p, t) .. + 15 of the matrix.  Tiles 0 of the pairs, then tiles 1, lie in LDS as they do in the bank.
+  auto tile_row = [&](int p, int t) { return GU ? 16 * p + t * sh.rows : 32 * p + 16 * t; };
+  u32x4 c[2][4];                                                               // [tile][step] of a block
+  auto load_step = [&](int p, int b, int s) {
 #pragma unroll
-          for (int t = 0; t < TERMS; ++t) w[t] = u32x4{0, 0, 0, 0};
-        }
+    for (int t = 0; t < 2; ++t) {
+      const uint8_t* tile = expert + (size_t)tile_row(p, t) * (G * 16);
+      c[t][s] = *reinterpret_cast<const u32x4*>(tile + (uint32_t)((lane & 15) * G * 16 + 16 * min(16 * b + 4 * s + q, G - 1)));
+    }
+  };
+  auto load = [&](int p, int b) {
 #pragma unroll
-        for (int t = 0; t < TERMS; ++t) *reinterpret_cast<u32x4*>(stage + (c * TERMS + t) * stride + o * 16) = w[t];
+    for (int s = 0; s < 4; ++s)
+      if (s < steps - kBlockSteps * b) load_step(p, b, s);
+  };
+  const int kw = SPLIT ? wave : 0;
+  int p = SPLIT ? p0 : p0 + wave;
+  // Terms of a pass's columns: unit u is block u % blocks of column u / blocks, a wave takes every waves-th unit, two at a time.
+  const int octets = sh.K / 8;
+  constexpr int XU = 2;
+  RawOctet<XT> raw[XU];
+  auto load_units = [&](int c0, int units, int u0) {
+#pragma unroll
+    for (int k = 0; k < XU; ++k) {
+      const int u = min(u0 + k * sh.waves, units - 1), col = u / blocks, o = 64 * (u - col * blocks) + lane;
+      const int r = __builtin_amdgcn_readfirstlane((int)list[c0 + col]);
+      const uint8_t* xrow = static_cast<const uint8_t*>(src) + (size_t)(GU ? r / sh.topk : r) * sh.K * (XT == X_F32 ? 4 : 2);
+      raw[k] = load_raw<XT>(xrow, (uint32_t)(8 * min(o, octets - 1)));
+    }
+  };
+  auto put_units = [&](int units, int u0) {
+#pragma unroll
+    for (int k = 0; k < XU; ++k) {
+      const int u = u0 + k * sh.waves;
+      if (u >= units) break;
+      u32x4 t[TERMS];
+      const float scale = wave_terms<XT, TERMS>(raw[k], 64 * (u % blocks) + lane < octets, t);
+      uint8_t* to = lds + at.terms + u * (TERMS * 1024) + lane * 16;
+#pragma unroll
+      for (int j = 0; j < TERMS; ++j) *reinterpret_cast<u32x4*>(to + j * 1024) = t[j];
+      if (lane == 0) scales[u] = scale;
+    }
+  };
+  auto stage = [&](int c0) {                                                   // (the first two units are on their way)
+    const int units = min(sh.cols, nc - c0) * blocks;
+    for (int u0 = wave; u0 < units; u0 += XU * sh.waves) {
+      if (u0 != wave) load_units(c0, units, u0);
+      put_units(units, u0);
+    }
+  };
+  load_units(0, min(sh.cols, nc) * blocks, wave);
+  // Metadata of 16 np rows per piece: [tile 0: scales, zeros][tile 1: scales, zeros] for W13, one run of 32 np rows for W2.
+  const int np = p1 - p0, runs = GU ? 2 : 1, run_rows = (GU ? 16 : 32) * np, sp = run_rows * G * 2 / 16, zp = run_rows * G * ZB / 16;
+  {
+    constexpr int UP = 4;
+    const int pieces = runs * (sp + zp);
+    u32x4 v[UP];
+    auto fetch = [&](int i0) {
+#pragma unroll
+      for (int k = 0; k < UP; ++k) {
+        const int i = min(i0 + k * T, pieces - 1);
+        const bool second = i >= sp + zp;
+        const int j = second ? i - (sp + zp) : i;
+        const size_t row = (size_t)(second ? sh.rows + 16 * p0 : per * p0);
+        const uint8_t* from = j < sp ? expert + L.scale_off + row * G * 2 + 16 * (size_t)j
+                                     : expert + L.meta2_off + row * G * ZB + 16 * (size_t)(j - sp);
+        v[k] = *reinterpret_cast<const u32x4*>(from);
       }
-      __syncthreads();
-      const uint8_t* xs = stage + min(lane & 15, cols - 1) * TERMS * stride + q * 64;
-      auto multiply = [&](int step, const AwqStep* d) {
-        f16x2 s2[2], b2[2];
-        const bool live = 4 * step + q < (int)L.G;
-        awq_meta<ML>(d[0], live, s2[0], b2[0]);
-        awq_meta<ML>(d[1], live, s2[1], b2[1]);
+    };
+    fetch(tid);
+    if (p < p1 && kw < blocks) load(p, kw);
+    for (int i0 = tid; i0 < pieces; i0 += UP * T) {
+      if (i0 != tid) fetch(i0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const f16x8 w0 = awq_frag(d[0].c[i], s2[0], b2[0]), w1 = awq_frag(d[1].c[i], s2[1], b2[1]);
+      for (int k = 0; k < UP; ++k)
+        if (i0 + k * T < pieces) reinterpret_cast<u32x4*>(lds)[i0 + k * T] = v[k];
+    }
+  }
+  f32x4 acc[2], sum[2];
+  for (int c0 = 0; c0 < nc; c0 += sh.cols) {
+    const int cols = min(sh.cols, nc - c0);
+    stage(c0);
+    __syncthreads();
+    const int mycol = min(lane & 15, cols - 1);
+    const int route = list[c0 + mycol];
+    // Block b of a pair; then its registers hold block b2 of pair p2 (p2 < 0: none).
+    auto multiply = [&](int pair, int b, int p2, int b2) {
+      const int ns = min(kBlockSteps, steps - kBlockSteps * b), ns2 = p2 < 0 ? 0 : steps - kBlockSteps * b2;
+      const uint8_t* xs = lds + at.terms + (mycol * blocks + b) * (TERMS * 1024) + q * 64;
+      sum[0] = sum[1] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int t = 0; t < TERMS; ++t) {
-            const f16x8 xf = *reinterpret_cast<const f16x8*>(xs + t * stride + (step - k0) * 256 + i * 16);
-            acc[0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w0, xf, acc[0], 0, 0, 0);
-            acc[1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w1, xf, acc[1], 0, 0, 0);
+      for (int s = 0; s < 4; ++s) {
+        if (s < ns) {
+          const int g = 16 * b + 4 * s + q, gc = min(g, G - 1);
+          f16x2 s2[2], b2[2];
+  #pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int run = GU ? t * (sp + zp) * 16 : 0, row = (GU ? 16 * (pair - p0) : 32 * (pair - p0) + 16 * t) + (lane & 15);
+            AwqStep a;
+            a.s = *reinterpret_cast<const uint16_t*>(lds + run + (row * G + gc) * 2);
+            if constexpr (ML == 3) a.z = lds[run + sp * 16 + row * G + gc];
+            else a.z = *reinterpret_cast<const uint16_t*>(lds + run + sp * 16 + (row * G + gc) * 2);
+            awq_meta<ML>(a, g < G, s2[t], b2[t]);
+          }
+  #pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const f16x8 w0 = awq_frag(c[0][s][i], s2[0], b2[0]), w1 = awq_frag(c[1][s][i], s2[1], b2[1]);
+  #pragma unroll
+            for (int j = 0; j < TERMS; ++j) {
+              const f16x8 xf = *reinterpret_cast<const f16x8*>(xs + j * 1024 + s * 256 + i * 16);
+              sum[0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w0, xf, sum[0], 0, 0, 0);
+              sum[1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w1, xf, sum[1], 0, 0, 0);
+            }
           }
         }
-      };
-      for (; s + sh.wk < end; s += 2 * sh.wk) {
-        load(s + sh.wk, b);
-        multiply(s, a);
-        load(s + 2 * sh.wk, a);
-        multiply(s + sh.wk, b);
+        if (s < ns2) load_step(p2, b2, s);
       }
-      if (s < end) multiply(s, a);
-    }
-    __syncthreads();                                                // the stage becomes the waves' partial sums
-    float* part = reinterpret_cast<float*>(stage);                  // [wave][tile][column][16 rows]
+      const float rs = scales[mycol * blocks + b];
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-      *reinterpret_cast<f32x4*>(part + ((wave * 2 + t) * 16 + (lane & 15)) * kPartRow + 4 * q) = acc[t];
-    __syncthreads();
-    const int wr = 8 / sh.wk;
-    for (int i = tid; i < wr * cols * per; i += 512) {
-      const int n = i % per, c = (i / per) % cols, g = i / (per * cols), out = ((int)blockIdx.x * wr + g) * per + n;
-      if (out >= sh.rows) continue;
-      const int tile = GU ? 0 : n >> 4;
-      float v = 0.f, u = 0.f;
-      for (int w = 0; w < sh.wk; ++w) {
-        const float* p = part + (((g * sh.wk + w) * 2 + tile) * 16 + c) * kPartRow + (n & 15);
-        v += p[0];
-        if constexpr (GU) u += p[16 * kPartRow];
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[t][j] *= rs;
+    };
+    if constexpr (SPLIT) {
+      float* part = reinterpret_cast<float*>(lds + at.part);
+      for (int b = kw; b < blocks; b += sh.waves) {
+        multiply(p0, b, b + sh.waves < blocks ? p0 : -1, b + sh.waves);
+        if ((lane & 15) < cols)
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            *reinterpret_cast<f32x4*>(part + ((b * 2 + t) * sh.cols + (lane & 15)) * kPartRow + 4 * q) = sum[t];
       }
-      v *= scales[c];
-      if constexpr (GU) v = silu_f32(v) * (u * scales[c]);
-      dst[(size_t)list[c0 + c] * sh.rows + out] = v;
+      __syncthreads();
+      for (int i = tid; i < cols * per; i += T) {
+        const int n = i % per, col = i / per, t = GU ? 0 : n >> 4;
+        float v = 0.f, u = 0.f;
+        for (int b = 0; b < blocks; ++b) {
+          const float* f = part + ((b * 2 + t) * sh.cols + col) * kPartRow + (n & 15);
+          v += f[0];
+          if constexpr (GU) u += f[sh.cols * kPartRow];
+        }
+        if constexpr (GU) v = silu_f32(v) * u;
+        dst[(size_t)list[c0 + col] * sh.rows + per * p0 + n] = v;
+      }
+      if (c0 + sh.cols < nc && kw < blocks) load(p0, kw);                      // the next pass starts over
+    } else {
+      for (int pair = p, b = 0; pair < p1;) {
+        int b2 = b + 1, p2 = pair;
+        if (b2 == blocks) b2 = 0, p2 += sh.waves;
+        multiply(pair, b, p2 < p1 ? p2 : (c0 + sh.cols < nc ? p : -1), b2);    // (the next pass starts over)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[t][j] = b == 0 ? sum[t][j] : acc[t][j] + sum[t][j];
+        if (b2 == 0 && (lane & 15) < cols) {
+          float* o = dst + (size_t)route * sh.rows + per * pair + 4 * q;
+          if constexpr (GU) {
+            f32x4 v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = silu_f32(acc[0][j]) * acc[1][j];
+            *reinterpret_cast<f32x4*>(o) = v;
+          } else {
+            *reinterpret_cast<f32x4*>(o) = acc[0];
+            *reinterpret_cast<f32x4*>(o + 16) = acc[1];
+          }
+        }
+        b = b2, pair = p2;
+      }
     }
+    if (c0 + sh.cols >= nc) return;
+    load_units(c0 + sh.cols, min(sh.cols, nc - c0 - sh.cols) * blocks, wave);
+    __syncthreads();                                                           // the terms have been read
   }
 }
 
@@ -307,39 +436,72 @@ inline MoeWs moe_ws(int M, int E, int topk, int H, int I) {
   return w;
 }
 
-// Waves over the contraction: as many as leave each of them two steps or more.
-inline int waves_over_k(int K) {
-  const int steps = (K + kStepK - 1) / kStepK;
-  return steps >= 16 ? 8 : (steps >= 8 ? 4 : (steps >= 4 ? 2 : 1));
+// Columns of a pass: two and a half times what an expert has on average, in at most 64 KB of terms.  Pairs of a workgroup, in at most 48 KB
+// of metadata (or one pair): few experts are cut into 260 workgroups, whose up to 16 waves share the columns' terms; many, with a column or
+// two each, into 1200, of which several fit a CU.  130 rows, 64 experts of 704 on 1024: 260 73 us, 530 80, 800 94; 37 rows, 512 experts of
+// 160 on 2560: 400 121 us, 800 103, 1200 97, 1600 109.  The blocks are split over waves where whole pairs would leave the chip with less than
+// two waves per CU.
+struct MoePlan {
+  MoeShape s;
+  bool split;
+};
+inline MoePlan moe_plan(int E, int routes, int topk, int K, int rows, bool gu, int terms, int ml) {
+  const int blocks = (K + kBlockK - 1) / kBlockK, all = rows / (gu ? 16 : 32), items = std::min(routes, E);
+  MoePlan p{{E, routes, topk, K, rows}, blocks > 1 && (int64_t)items * all < 512};
+  p.s.cols = std::max(1, std::min({16, 64 / (blocks * terms), (5 * routes + 2 * E - 1) / (2 * E) + 1}));
+  p.s.by_route = routes < E;
+  const int chunks = std::max(1, (items <= 128 ? 260 : 1200) / items), room = std::max(1, 48 * 1024 / (32 * (K / 32) * ml));
+  p.s.pairs = p.split ? 1 : std::min((all + chunks - 1) / chunks, room);
+  const int most = items <= 128 ? 16 : 8, turns = (p.s.pairs + most - 1) / most;
+  p.s.waves = p.split ? std::min(blocks, 16) : (p.s.pairs + turns - 1) / turns;
+  return p;
 }
 
-template <bool GU, int XT, int ML>
-hipError_t run_mm(const MoeShape& sh, int items, const void* src, const int32_t* ids, const uint8_t* bank, const AwqLayout& L, float* dst,
+template <bool GU, bool SPLIT, int XT, int ML>
+hipError_t run_mm(const MoeShape& sh, const void* src, const int32_t* ids, const uint8_t* bank, const AwqLayout& L, float* dst,
                   hipStream_t st) {
-  if (!raise_lds_limit<moe_mm_kernel<GU, XT, ML>>()) return hipErrorInvalidValue;
-  const int groups = sh.rows / (GU ? 16 : 32), wr = 8 / sh.wk;
-  hipLaunchKernelGGL((moe_mm_kernel<GU, XT, ML>), dim3((groups + wr - 1) / wr, items), dim3(512), kMoeLds, st, sh, src, ids, bank, L,
-                     dst);
+  if (!raise_lds_limit<moe_mm_kernel<GU, SPLIT, XT, ML>>()) return hipErrorInvalidValue;
+  const int all = sh.rows / (GU ? 16 : 32);
+  hipLaunchKernelGGL((moe_mm_kernel<GU, SPLIT, XT, ML>), dim3((all + sh.pairs - 1) / sh.pairs, std::min(sh.routes, sh.E)),
+                     dim3(64 * sh.waves), moe_lds(sh, XT == X_F32 ? 2 : 1, ML, SPLIT).total, st, sh, src, ids, bank, L, dst);
   return hipGetLastError();
+}
+template <bool GU, int XT, int ML>
+hipError_t run_mm(int E, int routes, int topk, int K, int rows, const void* src, const int32_t* ids, const uint8_t* bank,
+                  const AwqLayout& L, float* dst, hipStream_t st) {
+  const MoePlan p = moe_plan(E, routes, topk, K, rows, GU, XT == X_F32 ? 2 : 1, ML);
+  return p.split ? run_mm<GU, true, XT, ML>(p.s, src, ids, bank, L, dst, st) : run_mm<GU, false, XT, ML>(p.s, src, ids, bank, L, dst, st);
 }
 template <int ML>
 hipError_t run_experts(int M, int E, int topk, int H, int I, const void* x, XType xt, const int32_t* ids, const uint8_t* w13,
                        const uint8_t* w2, float* act, float* y, hipStream_t st) {
-  const int routes = M * topk, by_route = routes < E, items = std::min(routes, E);
-  const MoeShape s13{E, routes, topk, H, I, waves_over_k(H), by_route}, s2{E, routes, topk, I, H, waves_over_k(I), by_route};
+  const int routes = M * topk;
   const AwqLayout L13 = awq_layout(2 * (int64_t)I, H, ML), L2 = awq_layout(H, I, ML);
-  hipError_t e = xt == X_F32    ? run_mm<true, X_F32, ML>(s13, items, x, ids, w13, L13, act, st)
-                 : xt == X_BF16 ? run_mm<true, X_BF16, ML>(s13, items, x, ids, w13, L13, act, st)
-                                : run_mm<true, X_F16, ML>(s13, items, x, ids, w13, L13, act, st);
+  hipError_t e = xt == X_F32    ? run_mm<true, X_F32, ML>(E, routes, topk, H, I, x, ids, w13, L13, act, st)
+                 : xt == X_BF16 ? run_mm<true, X_BF16, ML>(E, routes, topk, H, I, x, ids, w13, L13, act, st)
+                                : run_mm<true, X_F16, ML>(E, routes, topk, H, I, x, ids, w13, L13, act, st);
   if (e != hipSuccess) return e;
-  return run_mm<false, X_F32, ML>(s2, items, act, ids, w2, L2, y, st);
+  return run_mm<false, X_F32, ML>(E, routes, topk, I, H, act, ids, w2, L2, y, st);
+}
+template <int XT, int WT>
+void run_logits(int M, int E, int H, const void* x, const void* router, float* logits, hipStream_t st) {
+  if (M == 1)
+    hipLaunchKernelGGL((route_logits_kernel<XT, WT, 1, 1>), dim3((E + 3) / 4), dim3(256), 0, st, M, E, H, x, router, logits);
+  else
+    hipLaunchKernelGGL((route_logits_kernel<XT, WT, 2, 4>), dim3((E + 7) / 8, (M + 3) / 4), dim3(256), 0, st, M, E, H, x, router, logits);
 }
 template <int XT>
 void run_logits(int M, int E, int H, const void* x, const void* router, XType rt, float* logits, hipStream_t st) {
-  const dim3 grid((E + 3) / 4, (M + kRouteTokens - 1) / kRouteTokens);
-  if (rt == X_F32) hipLaunchKernelGGL((route_logits_kernel<XT, X_F32>), grid, dim3(256), 0, st, M, E, H, x, router, logits);
-  else if (rt == X_BF16) hipLaunchKernelGGL((route_logits_kernel<XT, X_BF16>), grid, dim3(256), 0, st, M, E, H, x, router, logits);
-  else hipLaunchKernelGGL((route_logits_kernel<XT, X_F16>), grid, dim3(256), 0, st, M, E, H, x, router, logits);
+  if (rt == X_F32) run_logits<XT, X_F32>(M, E, H, x, router, logits, st);
+  else if (rt == X_BF16) run_logits<XT, X_BF16>(M, E, H, x, router, logits, st);
+  else run_logits<XT, X_F16>(M, E, H, x, router, logits, st);
+}
+void run_topk(int M, int E, int topk, int renorm, const float* logits, int32_t* ids, float* weights, hipStream_t st) {
+  if (E <= 64) hipLaunchKernelGGL(route_topk_kernel<1>, dim3(M), dim3(64), 0, st, E, topk, renorm, logits, ids, weights);
+  else if (E <= 256) hipLaunchKernelGGL(route_topk_kernel<4>, dim3(M), dim3(64), 0, st, E, topk, renorm, logits, ids, weights);
+  else if (E <= 512) hipLaunchKernelGGL(route_topk_kernel<8>, dim3(M), dim3(64), 0, st, E, topk, renorm, logits, ids, weights);
+  else if (E <= 1024) hipLaunchKernelGGL(route_topk_kernel<16>, dim3(M), dim3(64), 0, st, E, topk, renorm, logits, ids, weights);
+  else hipLaunchKernelGGL(route_topk_kernel<0>, dim3(M), dim3(64), 0, st, E, topk, renorm, logits, ids, weights);
 }
 
 }  // namespace
@@ -360,7 +522,7 @@ hipError_t launch_moe_awq(int M, int E, int topk, int H, int I, const void* x, X
     else if (xt == X_BF16) run_logits<X_BF16>(M, E, H, x, router, rt, logits, st);
     else run_logits<X_F16>(M, E, H, x, router, rt, logits, st);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    hipLaunchKernelGGL(route_topk_kernel, dim3((M + 3) / 4), dim3(256), 0, st, M, E, topk, renorm ? 1 : 0, logits, ids, weights);
+    run_topk(M, E, topk, renorm ? 1 : 0, logits, ids, weights, st);
     if ((e = hipGetLastError()) != hipSuccess) return e;
   }
   e = meta_layout == 3 ? run_experts<3>(M, E, topk, H, I, x, xt, ids, w13, w2, act, y, st)
