@@ -90,14 +90,14 @@ __device__ __forceinline__ void store8(void* p, size_t at, int type, float (&v)[
   *reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(p) + at) = o;
 }
 
-// N sums over the workgroup (up to 16 waves), the same in every thread: waves by DPP, then the waves in order.  buf alternates
-// between two halves from call to call (`turn`), so that one barrier per call is enough.
+// N sums over the workgroup (up to 16 waves), the same in every thread: waves by DPP, then the waves' sums, one per lane of 16, by DPP
+// again.  buf alternates between two halves from call to call (`turn`), so that one barrier per call is enough.
 constexpr int kMaxWaves = 16;
 template <int N>
 __device__ __forceinline__ void block_sums(float (&v)[N], float* buf, int& turn) {
   float* b = buf + turn * N * kMaxWaves;
   turn ^= 1;
-  const int wave = (int)threadIdx.x >> 6, waves = (int)blockDim.x >> 6;
+  const int wave = (int)threadIdx.x >> 6, waves = (int)blockDim.x >> 6, lane = (int)threadIdx.x & 15;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const float s = wave64_sum(v[i]);
@@ -106,9 +106,8 @@ __device__ __forceinline__ void block_sums(float (&v)[N], float* buf, int& turn)
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    float s = 0.f;
-    for (int w = 0; w < waves; ++w) s += b[i * kMaxWaves + w];
-    v[i] = s;
+    const float s = b[i * kMaxWaves + min(lane, waves - 1)];
+    v[i] = row16_sum(lane < waves ? s : 0.f);
   }
 }
 
@@ -258,11 +257,14 @@ struct GradOut {
 struct NormRuns {
   int per, S, runs;
 };
-constexpr int kRuns = 512;
-inline NormRuns norm_runs(int M, int G) {
-  const int L = M / G;
+// Runs: about one workgroup of ten waves per CU, or as many smaller ones (up to four) as make ten waves: every run costs three rows of
+// float32 in the workspace, written and read again.
+inline int norm_grad_chunks(int H);              // chunks per thread
+inline int norm_grad_threads(int H);
+inline NormRuns norm_runs(int M, int H, int G) {
+  const int L = M / G, runs = 256 * std::max(1, std::min(4, 640 / norm_grad_threads(H)));
   NormRuns p;
-  const int want = std::max(1, (M + kRuns - 1) / kRuns);
+  const int want = std::max(1, (M + runs - 1) / runs);
   if (L >= want) {
     p.S = (L + want - 1) / want;
     p.per = (L + p.S - 1) / p.S;
@@ -296,77 +298,101 @@ __device__ __forceinline__ float norm_du(bool has_pre, bool has_dh, float ru, fl
   return has_dh ? through + dh : through;
 }
 
+// Rows in registers.  Of one chunk per thread the next row's loads are on their way while this one's sums are formed; the weights and the gate row (until it
+// changes) stay in registers as they were loaded.
 template <bool H4, bool Y4, bool X4, int RC>
-__global__ void __launch_bounds__(512) norm_grad_kernel(NormArgs a, NormRuns p, GradOut o) {
+__global__ void __launch_bounds__(RC == 1 ? 640 : 512) norm_grad_kernel(NormArgs a, NormRuns p, GradOut o) {
   __shared__ float buf2[2 * 3 * kMaxWaves], buf1[2 * kMaxWaves];
   const int C = a.H / 8, T = (int)blockDim.x, t = (int)threadIdx.x, b = (int)blockIdx.x;
   const bool has_dh = o.dh != nullptr;
   const void* dhp = has_dh ? o.dh : a.h;
   int r0, r1, turn2 = 0, turn1 = 0;
   run_rows(p, a.M, a.L, b, r0, r1);
+  const int wt = a.has_pre || a.has_post ? a.wt : (int)X_BF16, gt = a.has_gate ? a.gt : (int)X_BF16;
+  Raw8 pre[RC], post[RC], gate[RC], hr[RC], yr[RC], dhr[RC], dxr[RC];
+  int at[RC];
+#pragma unroll
+  for (int i = 0; i < RC; ++i) {
+    at[i] = 8 * min(t + i * T, C - 1);
+    pre[i] = load8(a.has_pre ? a.pre : a.h, at[i], a.has_pre ? wt : (int)X_BF16);
+    post[i] = load8(a.has_post ? a.post : a.h, at[i], a.has_post ? wt : (int)X_BF16);
+  }
+  auto load_gate = [&](int m) {
+    const int group = m / a.L;
+#pragma unroll
+    for (int i = 0; i < RC; ++i) gate[i] = load8(a.has_gate ? a.gate : a.h, a.has_gate ? (size_t)group * a.H + at[i] : (size_t)at[i], gt);
+  };
+  auto load_row = [&](int m) {
+    const size_t row = (size_t)m * a.H;
+#pragma unroll
+    for (int i = 0; i < RC; ++i) {
+      hr[i] = load8<H4>(a.h, row + at[i]);
+      yr[i] = load8<Y4>(a.y, row + at[i]);
+      dhr[i] = load8<H4>(dhp, row + at[i]);
+      dxr[i] = load8<X4>(o.dx, row + at[i]);
+    }
+  };
+  auto weight = [&](const Raw8& r, bool has, float (&w)[8]) {
+    values8(r, wt, w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = has ? w[j] + a.offset : 1.f;
+  };
   float spre[RC][8], spost[RC][8], sgate[RC][8];
 #pragma unroll
   for (int i = 0; i < RC; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) spre[i][j] = spost[i][j] = sgate[i][j] = 0.f;
   const float invH = 1.f / (float)a.H;
+  constexpr bool AHEAD = RC == 1;                 // (two chunks of two rows spill)
+  if (r0 < r1) {
+    load_gate(r0);
+    if (AHEAD) load_row(r0);
+  }
   for (int m = r0; m < r1; ++m) {
     const size_t row = (size_t)m * a.H;
-    const int group = m / a.L;
-    Raw8 hr[RC], yr[RC], dhr[RC], dxr[RC];
+    if (!AHEAD) load_row(m);
+    float h[RC][8], y[RC][8], dh[RC][8], dx[RC][8], s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < RC; ++i) {
-      const size_t at = row + 8 * min(t + i * T, C - 1);
-      hr[i] = load8<H4>(a.h, at);
-      yr[i] = load8<Y4>(a.y, at);
-      dhr[i] = load8<H4>(dhp, at);
-      dxr[i] = load8<X4>(o.dx, at);
-    }
-    float s[3] = {0.f, 0.f, 0.f};
+      float w[8];
+      values8(hr[i], a.ht, h[i]);
+      values8(yr[i], a.yt, y[i]);
+      values8(dhr[i], a.ht, dh[i]);
+      values8(dxr[i], a.xt, dx[i]);
+      weight(pre[i], a.has_pre, w);
+      if (t + i * T < C)
 #pragma unroll
-    for (int i = 0; i < RC; ++i) {
-      if (t + i * T >= C) continue;
-      float h[8], y[8], dx[8], w[8];
-      values8(hr[i], a.ht, h);
-      values8(yr[i], a.yt, y);
-      values8(dxr[i], a.xt, dx);
-      weight8(a.pre, a.has_pre, a, 8 * (t + i * T), w);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        s[0] = fmaf(h[j], h[j], s[0]);
-        s[1] = fmaf(dx[j] * w[j], h[j], s[1]);
-        s[2] = fmaf(y[j], y[j], s[2]);
-      }
+        for (int j = 0; j < 8; ++j) {
+          s[0] = fmaf(h[i][j], h[i][j], s[0]);
+          s[1] = fmaf(dx[i][j] * w[j], h[i][j], s[1]);
+          s[2] = fmaf(y[i][j], y[i][j], s[2]);
+        }
     }
+    if (AHEAD && m + 1 < r1) load_row(m + 1);
     block_sums(s, buf2, turn2);
     const float ru = a.has_pre ? 1.f / sqrtf(s[0] * invH + a.eps) : 0.f;
     const float cu = a.has_pre ? ru * ru * ru * (s[1] * invH) : 0.f;
     const float rv = a.has_post ? 1.f / sqrtf(s[2] * invH + a.eps) : 1.f;
-    float q[1] = {0.f}, dp[RC][8];                // dp: alpha gate du post+
+    float q[1] = {0.f};                           // dx becomes dp: alpha gate du post+
 #pragma unroll
     for (int i = 0; i < RC; ++i) {
-      const int c = t + i * T;
-      if (c >= C) continue;
-      float h[8], y[8], dh[8], dx[8], w[8], v[8], g[8];
-      values8(hr[i], a.ht, h);
-      values8(yr[i], a.yt, y);
-      values8(dhr[i], a.ht, dh);
-      values8(dxr[i], a.xt, dx);
-      weight8(a.pre, a.has_pre, a, 8 * c, w);
-      weight8(a.post, a.has_post, a, 8 * c, v);
-      gate8(a, group, 8 * c, g);                  // with alpha
+      if (t + i * T >= C) continue;
+      float w[8], v[8], g[8];
+      weight(pre[i], a.has_pre, w);
+      weight(post[i], a.has_post, v);
+      values8(gate[i], gt, g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float du = norm_du(a.has_pre, has_dh, ru, cu, dx[j] * w[j], h[j], dh[j]);
-        dh[j] = du;
-        spre[i][j] = fmaf(dx[j] * ru, h[j], spre[i][j]);
-        const float n = y[j] * rv;                // n(y), or y
-        spost[i][j] = fmaf(g[j] * du, n, spost[i][j]);
-        sgate[i][j] = fmaf(a.alpha * du, n * v[j], sgate[i][j]);
-        dp[i][j] = g[j] * du * v[j];
-        q[0] = fmaf(dp[i][j], y[j], q[0]);
+        const float du = norm_du(a.has_pre, has_dh, ru, cu, dx[i][j] * w[j], h[i][j], dh[i][j]);
+        dh[i][j] = du;
+        spre[i][j] = fmaf(dx[i][j] * ru, h[i][j], spre[i][j]);
+        const float n = y[i][j] * rv, da = a.alpha * du, dg = (a.has_gate ? g[j] : 1.f) * da;   // n(y), or y
+        spost[i][j] = fmaf(dg, n, spost[i][j]);
+        sgate[i][j] = fmaf(da, n * v[j], sgate[i][j]);
+        dx[i][j] = dg * v[j];
+        q[0] = fmaf(dx[i][j], y[i][j], q[0]);
       }
-      if (o.dhi != nullptr) store8(o.dhi, row + 8 * c, a.ht, dh);
+      if (o.dhi != nullptr) store8(o.dhi, row + at[i], a.ht, dh[i]);
     }
     if (o.dy != nullptr) {
       float cy = 0.f;
@@ -376,33 +402,32 @@ __global__ void __launch_bounds__(512) norm_grad_kernel(NormArgs a, NormRuns p, 
       }
 #pragma unroll
       for (int i = 0; i < RC; ++i) {
-        const int c = t + i * T;
-        if (c >= C) continue;
-        float y[8];
-        values8(yr[i], a.yt, y);
+        if (t + i * T >= C) continue;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = a.has_post ? fmaf(rv, dp[i][j], -cy * y[j]) : dp[i][j];
-        store8(o.dy, row + 8 * c, a.yt, y);
+        for (int j = 0; j < 8; ++j) y[i][j] = a.has_post ? fmaf(rv, dx[i][j], -cy * y[i][j]) : dx[i][j];
+        store8(o.dy, row + at[i], a.yt, y[i]);
       }
     }
-    // the gate row's sums, where a run holds whole gate rows and this was its last row
-    if (o.dgate != nullptr && p.S == 1 && (m + 1) % a.L == 0) {
+    if ((m + 1) % a.L == 0) {
+      // the gate row's sums, where a run holds whole gate rows and this was its last row
+      if (o.dgate != nullptr && p.S == 1) {
 #pragma unroll
-      for (int i = 0; i < RC; ++i) {
-        if (t + i * T < C) store8(o.dgate, (size_t)group * a.H + 8 * (t + i * T), X_F32, sgate[i]);
+        for (int i = 0; i < RC; ++i) {
+          if (t + i * T < C) store8(o.dgate, (size_t)(m / a.L) * a.H + at[i], X_F32, sgate[i]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sgate[i][j] = 0.f;
+          for (int j = 0; j < 8; ++j) sgate[i][j] = 0.f;
+        }
       }
+      if (m + 1 < r1) load_gate(m + 1);
     }
   }
 #pragma unroll
   for (int i = 0; i < RC; ++i) {
-    const int c = t + i * T;
-    if (c >= C) continue;
-    const size_t at = (size_t)b * a.H + 8 * c;
-    if (o.dpre != nullptr) store8(o.dpre, at, X_F32, spre[i]);
-    if (o.dpost != nullptr) store8(o.dpost, at, X_F32, spost[i]);
-    if (o.dgate != nullptr && p.S > 1) store8(o.dgate, at, X_F32, sgate[i]);
+    if (t + i * T >= C) continue;
+    const size_t to = (size_t)b * a.H + at[i];
+    if (o.dpre != nullptr) store8(o.dpre, to, X_F32, spre[i]);
+    if (o.dpost != nullptr) store8(o.dpost, to, X_F32, spost[i]);
+    if (o.dgate != nullptr && p.S > 1) store8(o.dgate, to, X_F32, sgate[i]);
   }
 }
 
@@ -544,25 +569,32 @@ __global__ void __launch_bounds__(256) norm_zero_kernel(float* __restrict__ p, s
   if (i < n) p[i] = 0.f;
 }
 
-// Chunks per thread for a row, of at most 512 threads (0: too long to hold).
-inline int held_chunks(int H, int most) {
-  const int C = H / 8;
-  const int rc = C <= 512 ? 1 : (C <= 1024 ? 2 : 4);
-  return C <= 512 * most ? rc : 0;
-}
-constexpr int kRunChunks = 4, kGradChunks = 2;    // at 4 the backward kernel spills
 inline int threads_for(int C, int rc) { return ((C + rc - 1) / rc + 63) / 64 * 64; }
+// Chunks per thread (0: too long to hold).  Forward: at most 512 threads of up to 4 chunks.  Backward: one chunk for up to 640 threads, else
+// two for up to 512 (four spill).
+inline int held_chunks(int H) {
+  const int C = H / 8;
+  return C <= 512 ? 1 : (C <= 1024 ? 2 : (C <= 2048 ? 4 : 0));
+}
+inline int norm_grad_chunks(int H) {
+  const int C = H / 8;
+  return C <= 640 ? 1 : (C <= 1024 ? 2 : 0);
+}
+inline int norm_grad_threads(int H) {
+  const int rc = norm_grad_chunks(H);
+  return rc == 0 ? 512 : threads_for(H / 8, rc);
+}
 
 // Workspace of the backward pass: the runs' sums for dpre, dpost, dgate, then the rows' scalars of long rows.
 struct NormWs {
   size_t sums, rows, total;
 };
 inline NormWs norm_ws(int M, int H, int G) {
-  const NormRuns p = norm_runs(M, G);
+  const NormRuns p = norm_runs(M, H, G);
   NormWs w;
   w.sums = align256((size_t)p.runs * H * 4);
   w.rows = 3 * w.sums;
-  w.total = w.rows + (held_chunks(H, kGradChunks) == 0 ? align256((size_t)M * sizeof(RowScalars)) : 0);
+  w.total = w.rows + (norm_grad_chunks(H) == 0 ? align256((size_t)M * sizeof(RowScalars)) : 0);
   return w;
 }
 
@@ -572,7 +604,7 @@ hipError_t launch_block_norm(int M, int H, const BlockNorm& n, void* h_out, void
   NormArgs a{M, H, M / n.G, n.h, n.y, n.post, n.pre, n.gate, n.ht, n.yt, xt, n.wt, n.gt, n.alpha, n.offset, n.eps,
              n.y != nullptr, n.post != nullptr, n.pre != nullptr, n.gate != nullptr};
   if (!a.has_y) a.y = a.h, a.yt = a.ht;
-  const int rc = held_chunks(H, kRunChunks);
+  const int rc = held_chunks(H);
   if (rc == 0) {
     hipLaunchKernelGGL(norm_run_long_kernel, dim3(M), dim3(512), 0, st, a, h_out, x);
     return hipGetLastError();
@@ -610,12 +642,12 @@ hipError_t launch_block_norm_grad(int M, int H, const BlockNorm& n, const void* 
              n.y != nullptr, n.post != nullptr, n.pre != nullptr, n.gate != nullptr};
   if (!a.has_y) a.y = a.h, a.yt = a.ht;
   if (!a.has_pre) dx = a.h, a.xt = a.ht;
-  const NormRuns p = norm_runs(M, n.G);
+  const NormRuns p = norm_runs(M, H, n.G);
   const NormWs L = norm_ws(M, H, n.G);
   uint8_t* base = reinterpret_cast<uint8_t*>(ws);
   auto runs = [&](int i) { return reinterpret_cast<float*>(base + i * L.sums); };
   GradOut o{dh, dx, dh_in, dy, dpost ? runs(1) : nullptr, dgate ? (p.S > 1 ? runs(2) : dgate) : nullptr, dpre ? runs(0) : nullptr};
-  const int rc = held_chunks(H, kGradChunks);
+  const int rc = norm_grad_chunks(H);
   if (rc == 0) {
     RowScalars* rows = reinterpret_cast<RowScalars*>(base + L.rows);
     hipLaunchKernelGGL(norm_grad_long_kernel, dim3(M), dim3(512), 0, st, a, o, rows);
@@ -623,7 +655,7 @@ hipError_t launch_block_norm_grad(int M, int H, const BlockNorm& n, const void* 
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(norm_grad_cols_kernel, dim3((H / 8 + 63) / 64, p.runs), dim3(64), 0, st, a, p, o, rows);
   } else {
-    const int T = threads_for(H / 8, rc);
+    const int T = norm_grad_threads(H);
     auto go = [&](auto h4, auto y4, auto x4, auto c) {
       hipLaunchKernelGGL((norm_grad_kernel<decltype(h4)::value, decltype(y4)::value, decltype(x4)::value, decltype(c)::value>),
                          dim3(p.runs), dim3(T), 0, st, a, p, o);
