@@ -298,29 +298,43 @@ __device__ __forceinline__ float norm_du(bool has_pre, bool has_dh, float ru, fl
   return has_dh ? through + dh : through;
 }
 
-// Rows in registers.  Of one chunk per thread the next row's loads are on their way while this one's sums are formed; the weights and the gate row (until it
-// changes) stay in registers as they were loaded.
-template <bool H4, bool Y4, bool X4, int RC>
+// Rows in registers.  Of one chunk per thread the next row's loads are on their way while this one's sums are formed; the weights and
+// the gate row (until it changes) stay in registers.  A row is some 25 operations per element, which take as long as its bytes, so
+// what is absent is zeroed once instead of selected, and the decoding of 2-byte tensors does not branch where all of them are bfloat16 (BF).
+template <bool W4, bool BF>
+__device__ __forceinline__ void row_values(const Raw8& r, int type, float (&v)[8]) {
+  if constexpr (W4) values8(r, X_F32, v);
+  else if constexpr (BF) values8(r, X_BF16, v);
+  else values8(r, type == X_BF16 ? X_BF16 : X_F16, v);
+}
+template <bool W4, bool BF>
+__device__ __forceinline__ void row_store(void* p, size_t at, int type, float (&v)[8]) {
+  if constexpr (W4) store8(p, at, X_F32, v);
+  else if constexpr (BF) store8(p, at, X_BF16, v);
+  else store8(p, at, type == X_BF16 ? X_BF16 : X_F16, v);
+}
+
+template <bool H4, bool Y4, bool X4, bool BF, int RC>
 __global__ void __launch_bounds__(RC == 1 ? 640 : 512) norm_grad_kernel(NormArgs a, NormRuns p, GradOut o) {
   __shared__ float buf2[2 * 3 * kMaxWaves], buf1[2 * kMaxWaves];
+  constexpr bool AHEAD = RC == 1;                 // (two chunks of two rows spill)
   const int C = a.H / 8, T = (int)blockDim.x, t = (int)threadIdx.x, b = (int)blockIdx.x;
   const bool has_dh = o.dh != nullptr;
   const void* dhp = has_dh ? o.dh : a.h;
   int r0, r1, turn2 = 0, turn1 = 0;
   run_rows(p, a.M, a.L, b, r0, r1);
-  const int wt = a.has_pre || a.has_post ? a.wt : (int)X_BF16, gt = a.has_gate ? a.gt : (int)X_BF16;
-  Raw8 pre[RC], post[RC], gate[RC], hr[RC], yr[RC], dhr[RC], dxr[RC];
+  Raw8 hr[RC], yr[RC], dhr[RC], dxr[RC];
+  float pre[RC][8], post[RC][8], gate[RC][8];
   int at[RC];
 #pragma unroll
   for (int i = 0; i < RC; ++i) {
     at[i] = 8 * min(t + i * T, C - 1);
-    pre[i] = load8(a.has_pre ? a.pre : a.h, at[i], a.has_pre ? wt : (int)X_BF16);
-    post[i] = load8(a.has_post ? a.post : a.h, at[i], a.has_post ? wt : (int)X_BF16);
+    weight8(a.pre, a.has_pre, a, at[i], pre[i]);
+    weight8(a.post, a.has_post, a, at[i], post[i]);
   }
   auto load_gate = [&](int m) {
-    const int group = m / a.L;
 #pragma unroll
-    for (int i = 0; i < RC; ++i) gate[i] = load8(a.has_gate ? a.gate : a.h, a.has_gate ? (size_t)group * a.H + at[i] : (size_t)at[i], gt);
+    for (int i = 0; i < RC; ++i) gate8(a, m / a.L, at[i], gate[i]);   // with alpha
   };
   auto load_row = [&](int m) {
     const size_t row = (size_t)m * a.H;
@@ -332,18 +346,13 @@ __global__ void __launch_bounds__(RC == 1 ? 640 : 512) norm_grad_kernel(NormArgs
       dxr[i] = load8<X4>(o.dx, row + at[i]);
     }
   };
-  auto weight = [&](const Raw8& r, bool has, float (&w)[8]) {
-    values8(r, wt, w);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = has ? w[j] + a.offset : 1.f;
-  };
   float spre[RC][8], spost[RC][8], sgate[RC][8];
 #pragma unroll
   for (int i = 0; i < RC; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) spre[i][j] = spost[i][j] = sgate[i][j] = 0.f;
   const float invH = 1.f / (float)a.H;
-  constexpr bool AHEAD = RC == 1;                 // (two chunks of two rows spill)
+  int left = a.L - r0 % a.L;                      // rows of the gate row from this one on
   if (r0 < r1) {
     load_gate(r0);
     if (AHEAD) load_row(r0);
@@ -354,65 +363,73 @@ __global__ void __launch_bounds__(RC == 1 ? 640 : 512) norm_grad_kernel(NormArgs
     float h[RC][8], y[RC][8], dh[RC][8], dx[RC][8], s[3] = {0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < RC; ++i) {
-      float w[8];
-      values8(hr[i], a.ht, h[i]);
-      values8(yr[i], a.yt, y[i]);
-      values8(dhr[i], a.ht, dh[i]);
-      values8(dxr[i], a.xt, dx[i]);
-      weight(pre[i], a.has_pre, w);
+      row_values<H4, BF>(hr[i], a.ht, h[i]);
+      row_values<Y4, BF>(yr[i], a.yt, y[i]);
+      row_values<H4, BF>(dhr[i], a.ht, dh[i]);
+      row_values<X4, BF>(dxr[i], a.xt, dx[i]);
+    }
+    if (!a.has_pre)
+#pragma unroll
+      for (int i = 0; i < RC; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[i][j] = dx[i][j] = 0.f;
+    if (!has_dh)
+#pragma unroll
+      for (int i = 0; i < RC; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dh[i][j] = 0.f;
+#pragma unroll
+    for (int i = 0; i < RC; ++i)
       if (t + i * T < C)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           s[0] = fmaf(h[i][j], h[i][j], s[0]);
-          s[1] = fmaf(dx[i][j] * w[j], h[i][j], s[1]);
+          s[1] = fmaf(dx[i][j] * pre[i][j], h[i][j], s[1]);
           s[2] = fmaf(y[i][j], y[i][j], s[2]);
         }
-    }
     if (AHEAD && m + 1 < r1) load_row(m + 1);
     block_sums(s, buf2, turn2);
     const float ru = a.has_pre ? 1.f / sqrtf(s[0] * invH + a.eps) : 0.f;
-    const float cu = a.has_pre ? ru * ru * ru * (s[1] * invH) : 0.f;
+    const float cu = a.has_pre ? -ru * ru * ru * (s[1] * invH) : 0.f;
     const float rv = a.has_post ? 1.f / sqrtf(s[2] * invH + a.eps) : 1.f;
     float q[1] = {0.f};                           // dx becomes dp: alpha gate du post+
 #pragma unroll
     for (int i = 0; i < RC; ++i) {
       if (t + i * T >= C) continue;
-      float w[8], v[8], g[8];
-      weight(pre[i], a.has_pre, w);
-      weight(post[i], a.has_post, v);
-      values8(gate[i], gt, g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float du = norm_du(a.has_pre, has_dh, ru, cu, dx[i][j] * w[j], h[i][j], dh[i][j]);
+        const float du = fmaf(ru, dx[i][j] * pre[i][j], fmaf(cu, h[i][j], dh[i][j]));
         dh[i][j] = du;
         spre[i][j] = fmaf(dx[i][j] * ru, h[i][j], spre[i][j]);
-        const float n = y[i][j] * rv, da = a.alpha * du, dg = (a.has_gate ? g[j] : 1.f) * da;   // n(y), or y
+        const float n = y[i][j] * rv, dg = gate[i][j] * du;              // n(y), or y
         spost[i][j] = fmaf(dg, n, spost[i][j]);
-        sgate[i][j] = fmaf(da, n * v[j], sgate[i][j]);
-        dx[i][j] = dg * v[j];
+        sgate[i][j] = fmaf(du, n * post[i][j], sgate[i][j]);             // times alpha at the end
+        dx[i][j] = dg * post[i][j];
         q[0] = fmaf(dx[i][j], y[i][j], q[0]);
       }
-      if (o.dhi != nullptr) store8(o.dhi, row + at[i], a.ht, dh[i]);
+      if (o.dhi != nullptr) row_store<H4, BF>(o.dhi, row + at[i], a.ht, dh[i]);
     }
     if (o.dy != nullptr) {
-      float cy = 0.f;
       if (a.has_post) {
         block_sums(q, buf1, turn1);
-        cy = rv * rv * rv * (q[0] * invH);
+        const float cy = -rv * rv * rv * (q[0] * invH);
+#pragma unroll
+        for (int i = 0; i < RC; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) dx[i][j] = fmaf(rv, dx[i][j], cy * y[i][j]);
       }
 #pragma unroll
-      for (int i = 0; i < RC; ++i) {
-        if (t + i * T >= C) continue;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[i][j] = a.has_post ? fmaf(rv, dx[i][j], -cy * y[i][j]) : dx[i][j];
-        store8(o.dy, row + at[i], a.yt, y[i]);
-      }
+      for (int i = 0; i < RC; ++i)
+        if (t + i * T < C) row_store<Y4, BF>(o.dy, row + at[i], a.yt, dx[i]);
     }
-    if ((m + 1) % a.L == 0) {
+    if (--left == 0) {
+      left = a.L;
       // the gate row's sums, where a run holds whole gate rows and this was its last row
       if (o.dgate != nullptr && p.S == 1) {
 #pragma unroll
         for (int i = 0; i < RC; ++i) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) sgate[i][j] *= a.alpha;
           if (t + i * T < C) store8(o.dgate, (size_t)(m / a.L) * a.H + at[i], X_F32, sgate[i]);
 #pragma unroll
           for (int j = 0; j < 8; ++j) sgate[i][j] = 0.f;
@@ -425,6 +442,8 @@ __global__ void __launch_bounds__(RC == 1 ? 640 : 512) norm_grad_kernel(NormArgs
   for (int i = 0; i < RC; ++i) {
     if (t + i * T >= C) continue;
     const size_t to = (size_t)b * a.H + at[i];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sgate[i][j] *= a.alpha;
     if (o.dpre != nullptr) store8(o.dpre, to, X_F32, spre[i]);
     if (o.dpost != nullptr) store8(o.dpost, to, X_F32, spost[i]);
     if (o.dgate != nullptr && p.S > 1) store8(o.dgate, to, X_F32, sgate[i]);
@@ -656,13 +675,16 @@ hipError_t launch_block_norm_grad(int M, int H, const BlockNorm& n, const void* 
     hipLaunchKernelGGL(norm_grad_cols_kernel, dim3((H / 8 + 63) / 64, p.runs), dim3(64), 0, st, a, p, o, rows);
   } else {
     const int T = norm_grad_threads(H);
-    auto go = [&](auto h4, auto y4, auto x4, auto c) {
-      hipLaunchKernelGGL((norm_grad_kernel<decltype(h4)::value, decltype(y4)::value, decltype(x4)::value, decltype(c)::value>),
+    const bool bf = a.ht != X_F16 && a.yt != X_F16 && a.xt != X_F16;
+    auto go = [&](auto h4, auto y4, auto x4, auto bfs, auto c) {
+      hipLaunchKernelGGL((norm_grad_kernel<decltype(h4)::value, decltype(y4)::value, decltype(x4)::value, decltype(bfs)::value,
+                                           decltype(c)::value>),
                          dim3(p.runs), dim3(T), 0, st, a, p, o);
     };
+    auto by_bf = [&](auto h4, auto y4, auto x4, auto c) { bf ? go(h4, y4, x4, std::true_type{}, c) : go(h4, y4, x4, std::false_type{}, c); };
     auto by_rc = [&](auto h4, auto y4, auto x4) {
-      if (rc == 1) go(h4, y4, x4, std::integral_constant<int, 1>{});
-      else go(h4, y4, x4, std::integral_constant<int, 2>{});
+      if (rc == 1) by_bf(h4, y4, x4, std::integral_constant<int, 1>{});
+      else by_bf(h4, y4, x4, std::integral_constant<int, 2>{});
     };
     auto by_x = [&](auto h4, auto y4) { a.xt == X_F32 ? by_rc(h4, y4, std::true_type{}) : by_rc(h4, y4, std::false_type{}); };
     auto by_y = [&](auto h4) { a.yt == X_F32 ? by_x(h4, std::true_type{}) : by_x(h4, std::false_type{}); };
