@@ -8,7 +8,7 @@
 //     waves themselves, which spares a launch.
 //   More rows (awq_gemm_kernel): the matrix cores bound it.  4 waves with 64 weight rows each share the tile of x through
 //     LDS (global->LDS copies, two stages); every wave decodes only its own weights, once per tile row.
-// Either splits the contraction over workgroups when there are few tiles; awq_join_kernel adds the parts in order.
+// All split the contraction over workgroups where there are few; a further kernel adds the parts in order.
 #include <algorithm>
 
 #include "awq_common.h"
@@ -365,43 +365,78 @@ __global__ void __launch_bounds__(512, 4) awq_shared_kernel(int M, int N, int K,
 }
 
 // ---- many rows ---------------------------------------------------------------------------------------------------
-// Tile: 16 MT rows of x by 256 weight rows, 64 per wave.
-constexpr int kGemmCols = 256;
+// Tile: 16 MT rows of x by 256 weight rows, 64 per wave.  The tiles of the last, unfilled round are cut into S parts of `per` steps.
+constexpr int kGemmCols = 256, kSlots = 512;   // workgroups the chip runs at once: two per CU
+
+struct TilePlan {
+  int mt, ntm, ntn, full, S, per, units, steps;   // tiles [0, full) run whole; units = the others' S parts
+};
+// Tile rows and columns of tile id: bands of 8 tile rows.
+__device__ __forceinline__ void tile_of(const TilePlan& p, int id, int& tm, int& tn) {
+  const int band = id / (8 * p.ntn), in = id - band * 8 * p.ntn, height = min(8, p.ntm - 8 * band);
+  tm = 8 * band + in % height;
+  tn = in / height;
+}
 
 template <int ML, int TERMS, int MT>
-__global__ void __launch_bounds__(256, 2) awq_gemm_kernel(int M, int N, int steps, int per, int ntm, int tiles,
-                                                          const uint8_t* __restrict__ xp, const float* __restrict__ rowscale,
-                                                          const uint8_t* __restrict__ bank, AwqLayout L, float* __restrict__ y,
-                                                          float* __restrict__ partials) {
+__global__ void __launch_bounds__(256, 2) awq_gemm_kernel(int M, int N, TilePlan p, const uint8_t* __restrict__ xp,
+                                                          const float* __restrict__ rowscale, const uint8_t* __restrict__ bank,
+                                                          AwqLayout L, float* __restrict__ y, float* __restrict__ partials) {
   constexpr int NT = 4, UNITS = MT * TERMS, STAGE = UNITS * 4096;   // a unit: one term of 16 rows, 4 KB per step
+  constexpr int ZB = ML == 3 ? 1 : 2;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int tid = (int)threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int q = lane >> 4;
-  // Workgroup b runs on XCD b % 8: each XCD gets a contiguous run of tiles, in bands of 8 tile rows, so that the tiles in
-  // flight there share rows and weights in its L2.
-  const int b = (int)blockIdx.x, chunk = (int)gridDim.x >> 3;
-  const int id = (b & 7) * chunk + (b >> 3);
-  if (id >= tiles) return;
-  const int ntn = (N + kGemmCols - 1) / kGemmCols;
-  const int band = id / (8 * ntn), in = id - band * 8 * ntn, height = min(8, ntm - 8 * band);
-  const int tm = 8 * band + in % height, tn = in / height;
+  const int q = lane >> 4, G = (int)L.G;
+  // Whole tiles first, then the others' parts.  Workgroup b runs on XCD b % 8: each XCD gets a contiguous run of either, so that those
+  // in flight there share rows and weights in its L2, a tile's parts the lines of its scales and zeros (128 rows 5120 -> 17408: 63 us;
+  // with the parts' tiles side by side 74).
+  const int fgrid = (p.full + 7) & ~7;
+  int b = (int)blockIdx.x, id, part = -1, s0 = 0, s1 = p.steps;
+  if (b < fgrid) {
+    id = (b & 7) * (fgrid >> 3) + (b >> 3);
+    if (id >= p.full) return;
+  } else {
+    b -= fgrid;
+    b = (b & 7) * (((int)gridDim.x - fgrid) >> 3) + (b >> 3);
+    if (b >= p.units) return;
+    const int tile = b / p.S;
+    part = b - tile * p.S;
+    id = p.full + tile;
+    s0 = part * p.per;
+    s1 = min(s0 + p.per, p.steps);
+  }
+  int tm, tn;
+  tile_of(p, id, tm, tn);
   const int n0 = tn * kGemmCols + 64 * wave, mt0 = tm * MT, mtiles = (M + 15) >> 4;
-  const int s0 = (int)blockIdx.y * per, s1 = min(s0 + per, steps), last = s1 - 1;
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
 
-  const uint8_t* codes[NT];
-  int64_t row[NT];
+  // Row tile r: rows first[r] .. + 15; past the matrix its last 16 again, of which only the rows not yet covered are stored.  Then a lane's
+  // offset in every tile and step is the same, and the scalar bases do the rest.
+  int first[NT];
 #pragma unroll
-  for (int r = 0; r < NT; ++r) {
-    row[r] = min(n0 + 16 * r + (lane & 15), N - 1);
-    codes[r] = bank + row[r] * (L.G * 16);
-  }
+  for (int r = 0; r < NT; ++r) first[r] = min(n0 + 16 * r, max(N - 16, 0));
+  const int lrow = min(lane & 15, N - 1);
+  const uint32_t coff = (uint32_t)(lrow * G * 16 + 16 * q), soff = (uint32_t)((lrow * G + q) * 2), zoff = (uint32_t)((lrow * G + q) * ZB);
+  AwqStep wa[NT], wb[NT];
+  auto load_w = [&](int step, AwqStep (&d)[NT]) {
+    // the last step may have fewer than 4 groups: its lanes past the row's end read the row's last one
+    const int back = max(4 * step + q - (G - 1), 0);
+    const uint32_t co = coff - 16 * back, so = soff - 2 * back, zo = zoff - ZB * back;
+#pragma unroll
+    for (int r = 0; r < NT; ++r) {
+      const size_t at = (size_t)first[r] * G + 4 * (size_t)step;
+      d[r].c = *reinterpret_cast<const u32x4*>(bank + 16 * at + co);
+      d[r].s = *reinterpret_cast<const uint16_t*>(bank + L.scale_off + 2 * at + so);
+      if constexpr (ML == 3) d[r].z = *(bank + L.meta2_off + at + zo);
+      else d[r].z = *reinterpret_cast<const uint16_t*>(bank + L.meta2_off + 2 * at + zo);
+    }
+  };
   // unit u = wave + 4 j: term u % TERMS of 16-row tile u / TERMS (past the end: the last one again, not stored)
   auto copy_x = [&](int step, int stage) {
 #pragma unroll
     for (int j = 0; j < UNITS / 4; ++j) {
       const int u = wave + 4 * j, mt = min(mt0 + u / TERMS, mtiles - 1);
-      const uint8_t* src = xp + frag_at(mt, steps, step, TERMS, u % TERMS, 0, 0);
+      const uint8_t* src = xp + frag_at(mt, p.steps, step, TERMS, u % TERMS, 0, 0);
       const uint8_t* bases[4] = {src, src, src, src};
       const uint32_t v = lane * 16, vs[4] = {v, v, v, v};
       lds_copy16_run<4>(vs, bases, __builtin_amdgcn_readfirstlane(lds0 + stage * STAGE + u * 4096));
@@ -412,22 +447,19 @@ __global__ void __launch_bounds__(256, 2) awq_gemm_kernel(int M, int N, int step
   for (int r = 0; r < NT; ++r)
 #pragma unroll
     for (int c = 0; c < MT; ++c) acc[r][c] = f32x4{0.f, 0.f, 0.f, 0.f};
-  AwqStep cur[NT], nxt[NT];
-  auto load_w = [&](int step, AwqStep* d) {
+  // Copies and weights are there.  (The uses of d are kept behind the wait: taken up into the step before, they would wait there.)
+  auto landed = [&](AwqStep (&d)[NT]) {
+    wait_vmem<0>();
 #pragma unroll
-    for (int r = 0; r < NT; ++r) d[r] = awq_load<ML>(codes[r], bank, L, row[r], 4 * step + q);
+    for (int r = 0; r < NT; ++r) asm volatile("" : "+v"(d[r].c), "+v"(d[r].s), "+v"(d[r].z));
   };
-  copy_x(s0, 0);
-  load_w(s0, cur);
-  wait_vmem<0>();
-  __syncthreads();
-  for (int s = s0; s < s1; ++s) {
-    const int st = (s - s0) & 1, next = min(s + 1, last);
-    load_w(next, nxt);
-    if (s < last) copy_x(next, st ^ 1);
+  // One step: the next one's weights and copies go out, this one's products, then the wait for both.
+  auto step = [&](int s, int st, const AwqStep (&cur)[NT], AwqStep (&nxt)[NT]) {
+    load_w(min(s + 1, s1 - 1), nxt);                    // (in the branch, the waits after it count for the worse of its sides)
+    if (s + 1 < s1) copy_x(s + 1, st ^ 1);
     f16x2 s2[NT], b2[NT];
 #pragma unroll
-    for (int r = 0; r < NT; ++r) awq_meta<ML>(cur[r], 4 * s + q < (int)L.G, s2[r], b2[r]);
+    for (int r = 0; r < NT; ++r) awq_meta<ML>(cur[r], 4 * s + q < G, s2[r], b2[r]);
     const uint8_t* xs = lds + st * STAGE + lane * 16;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -443,25 +475,76 @@ __global__ void __launch_bounds__(256, 2) awq_gemm_kernel(int M, int N, int step
           for (int r = 0; r < NT; ++r) acc[r][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[r], xf, acc[r][c], 0, 0, 0);
         }
     }
+    // In order: 4 octets of x ahead of the products, each product followed by a share of the next weights' decode (2048 rows 5120 ->
+    // 17408: 377 us, 381 as the compiler orders them; as two terms, 17408 -> 5120: 803 and 885; fewer rows lose by it).
+    if constexpr (UNITS == 8) {
+      __builtin_amdgcn_sched_group_barrier(0x100, 4, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, 60, 0);
 #pragma unroll
-    for (int r = 0; r < NT; ++r) cur[r] = nxt[r];
-    wait_vmem<0>();            // the next step's copies landed
+      for (int j = 0; j < 4 * UNITS; ++j) {
+#pragma unroll
+        for (int r = 0; r < NT; ++r) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          if (r == NT - 1 && j < 4 * UNITS - 4) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x002, 2, 0);
+        }
+      }
+    }
+    landed(nxt);
     wait_lds();
     __syncthreads();
+  };
+  copy_x(s0, 0);
+  load_w(s0, wa);
+  landed(wa);
+  __syncthreads();
+  for (int s = s0; s < s1; s += 2) {
+    step(s, 0, wa, wb);
+    if (s + 1 < s1) step(s + 1, 1, wb, wa);
   }
-  float* out = partials != nullptr ? partials + (size_t)blockIdx.y * M * N : y;
+  // Whole tiles: y.  Parts: [tile][part][16 MT][256], scaled, for awq_tiles_join_kernel.
+  float* pt = part < 0 ? nullptr : partials + (size_t)b * (16 * MT * kGemmCols) + 64 * wave;
 #pragma unroll
   for (int c = 0; c < MT; ++c) {
-    const int m = 16 * (mt0 + c) + (lane & 15);
+    const int ml = 16 * c + (lane & 15), m = 16 * mt0 + ml;
     if (m >= M) continue;
     const float rs = rowscale[m];
 #pragma unroll
     for (int r = 0; r < NT; ++r) {
-      const int n = n0 + 16 * r + 4 * q;
-      const f32x4 v = acc[r][c];
-      store_row4(out, N, m, n, f32x4{v[0] * rs, v[1] * rs, v[2] * rs, v[3] * rs});
+      const int n = first[r] + 4 * q, from = n0 + 16 * r;       // rows from `from` on are this tile's
+      f32x4 v = acc[r][c];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] *= rs;
+      if (part >= 0) {
+        if (first[r] == from) *reinterpret_cast<f32x4*>(pt + ml * kGemmCols + 16 * r + 4 * q) = v;
+        else
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (n + j >= from && n + j < N) pt[ml * kGemmCols + n + j - n0] = v[j];
+      } else if (first[r] == from) {
+        store_row4(y, N, m, n, v);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (n + j >= from && n + j < N) y[(size_t)m * N + n + j] = v[j];
+      }
     }
   }
+}
+
+// y of the cut tiles: a row of 256 columns per workgroup, the S parts in order.
+__global__ void __launch_bounds__(256) awq_tiles_join_kernel(int M, int N, TilePlan p, const float* __restrict__ partials,
+                                                             float* __restrict__ y) {
+  const int rows = 16 * p.mt, i = (int)blockIdx.x / rows, ml = (int)blockIdx.x - i * rows;
+  int tm, tn;
+  tile_of(p, p.full + i, tm, tn);
+  const int m = tm * rows + ml, n = tn * kGemmCols + (int)threadIdx.x;
+  if (m >= M || n >= N) return;
+  const size_t unit = (size_t)rows * kGemmCols;
+  const float* f = partials + (size_t)i * p.S * unit + ml * kGemmCols + threadIdx.x;
+  float v = f[0];
+  for (int s = 1; s < p.S; ++s) v += f[s * unit];
+  y[(size_t)m * N + n] = v;
 }
 
 // y = the sum of the S parts, in order.
@@ -484,7 +567,7 @@ struct AwqPlan {
   int terms, steps, S, per;    // S parts of `per` blocks (kOwn), passes (kShared) or steps (kTiles)
   int units;                   // blocks, passes
   int ct, waves;               // column tiles (kShared), waves (kOwn)
-  int mt, ntm, tiles;          // kTiles
+  TilePlan t;                  // kTiles
   size_t xp, rs, partials, total;
 };
 inline AwqPlan awq_plan(int M, int N, int K, XType xt) {
@@ -515,17 +598,25 @@ inline AwqPlan awq_plan(int M, int N, int K, XType xt) {
     p.per = (int)((p.units + S - 1) / S);
     p.S = (p.units + p.per - 1) / p.per;
   } else {
-    p.mt = p.terms == 2 || M <= 64 ? 4 : 8;
-    p.ntm = (M + 16 * p.mt - 1) / (16 * p.mt);
-    p.tiles = p.ntm * ((N + kGemmCols - 1) / kGemmCols);
-    const int64_t S = std::min(std::max<int64_t>(1, std::min<int64_t>(512 / p.tiles, p.steps / 4)), most);
-    p.per = (int)((p.steps + S - 1) / S);
-    p.S = (p.steps + p.per - 1) / p.per;
+    TilePlan& t = p.t;
+    t.mt = p.terms == 2 || M <= 64 ? 4 : 8;
+    t.ntm = (M + 16 * t.mt - 1) / (16 * t.mt);
+    t.ntn = (N + kGemmCols - 1) / kGemmCols;
+    t.steps = p.steps;
+    const int64_t tiles = (int64_t)t.ntm * t.ntn, tail = tiles % kSlots;
+    const int64_t room = ((int64_t)64 << 20) / ((int64_t)16 * t.mt * kGemmCols * 4);       // parts in 64 MiB
+    int64_t S = tail == 0 ? 1 : std::max<int64_t>(1, std::min<int64_t>({kSlots / tail, p.steps / 4, room / tail}));
+    t.per = (int)((p.steps + S - 1) / S);
+    S = (p.steps + t.per - 1) / t.per;
+    t.S = (int)S;
+    t.units = S > 1 ? (int)(tail * S) : 0;
+    t.full = (int)(S > 1 ? tiles - tail : tiles);
+    p.S = 1;
   }
   p.xp = 0;
   p.rs = p.kind != AwqPlan::kTiles ? 0 : align256((size_t)((M + 15) / 16) * p.steps * p.terms * 4096);
   p.partials = p.kind != AwqPlan::kTiles ? 0 : p.rs + align256((size_t)(M + 15) / 16 * 16 * 4);
-  p.total = p.partials + (p.S > 1 ? align256((size_t)p.S * M * N * 4) : 0);
+  p.total = p.partials + (p.S > 1 ? align256((size_t)p.S * M * N * 4) : 0) + (size_t)p.t.units * 16 * p.t.mt * kGemmCols * 4;
   return p;
 }
 
@@ -557,8 +648,12 @@ template <int ML, int TERMS, int MT>
 hipError_t run_gemm(const AwqPlan& p, int M, int N, int, const void* xp, const float* rs, const uint8_t* bank, const AwqLayout& L,
                     float* y, float* partials, hipStream_t st) {
   if (!raise_lds_limit<awq_gemm_kernel<ML, TERMS, MT>>()) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((awq_gemm_kernel<ML, TERMS, MT>), dim3((p.tiles + 7) / 8 * 8, p.S), dim3(256), 2 * MT * TERMS * 4096, st, M, N,
-                     p.steps, p.per, p.ntm, p.tiles, static_cast<const uint8_t*>(xp), rs, bank, L, y, partials);
+  const TilePlan& t = p.t;
+  hipLaunchKernelGGL((awq_gemm_kernel<ML, TERMS, MT>), dim3((t.full + 7) / 8 * 8 + (t.units + 7) / 8 * 8), dim3(256),
+                     2 * MT * TERMS * 4096, st, M, N, t, static_cast<const uint8_t*>(xp), rs, bank, L, y, partials);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || t.units == 0) return e;
+  hipLaunchKernelGGL(awq_tiles_join_kernel, dim3((unsigned)(t.units / t.S) * 16 * MT), dim3(256), 0, st, M, N, t, partials, y);
   return hipGetLastError();
 }
 template <int ML, int XT, typename... A>
@@ -572,7 +667,7 @@ hipError_t run_plan(const AwqPlan& p, int M, A... a) {
     default: break;
   }
   if constexpr (T == 1)
-    if (p.mt == 8) return run_gemm<ML, T, 8>(p, M, a...);
+    if (p.t.mt == 8) return run_gemm<ML, T, 8>(p, M, a...);
   return run_gemm<ML, T, 4>(p, M, a...);
 }
 template <int XT>
@@ -581,7 +676,7 @@ hipError_t linear(const AwqPlan& p, int M, int N, int K, const void* x, const ui
   const AwqLayout L = awq_layout(N, K, meta_layout);
   uint8_t* xp = ws + p.xp;
   float* rs = reinterpret_cast<float*>(ws + p.rs);
-  float* partials = p.S > 1 ? reinterpret_cast<float*>(ws + p.partials) : nullptr;
+  float* partials = p.S > 1 || p.t.units > 0 ? reinterpret_cast<float*>(ws + p.partials) : nullptr;
   if (p.kind == AwqPlan::kTiles) {
     pack_rows<XT, XT == X_F32 ? 2 : 1>(M, K, p.steps, x, xp, rs, st);
     const hipError_t e = hipGetLastError();
@@ -590,7 +685,7 @@ hipError_t linear(const AwqPlan& p, int M, int N, int K, const void* x, const ui
   }
   const hipError_t e = meta_layout == 3 ? run_plan<3, XT>(p, M, N, K, x, rs, bank, L, y, partials, st)
                                         : run_plan<4, XT>(p, M, N, K, x, rs, bank, L, y, partials, st);
-  if (e != hipSuccess || partials == nullptr) return e;
+  if (e != hipSuccess || p.S == 1) return e;
   hipLaunchKernelGGL(awq_join_kernel, dim3((N + 255) / 256, M), dim3(256), 0, st, M, N, p.S, partials, y);
   return hipGetLastError();
 }
