@@ -257,13 +257,6 @@ __device__ __forceinline__ void awq_quad(uint32_t w, f16x2 s2, f16x2 b2, const A
   p[3] = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, (w8 & d.m_hi) | d.e64) + c64, s2, b2);
 }
 
-// The low (ev) and high (od) nibbles of the dword's bytes 0 and 2, each half with its own scale and bias.
-__device__ __forceinline__ void awq_pairs(uint32_t w, f16x2 s2, f16x2 b2, const AwqDecode& d, f16x2& ev, f16x2& od) {
-  const f16x2 c1024 = {(_Float16)-1024.0f, (_Float16)-1024.0f}, c64 = {(_Float16)-64.0f, (_Float16)-64.0f};
-  ev = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, (w & d.m_lo) | d.e1024) + c1024, s2, b2);
-  od = __builtin_elementwise_fma(__builtin_bit_cast(f16x2, (w & d.m_hi) | d.e64) + c64, s2, b2);
-}
-
 // Per-group bias RN_f16(-zero * scale), a single half multiply.
 __device__ __forceinline__ _Float16 awq_bias(uint32_t zero, _Float16 s) {
   const _Float16 nz = -(_Float16)(float)zero;

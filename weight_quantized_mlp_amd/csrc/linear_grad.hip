@@ -12,8 +12,7 @@
 //     and the odd k.  The E4M3 group scales (one per n and 16 k) are held in LDS as float16, [group][n], so a
 //     lane's 8 scales are one 16-byte read; E2M1 x E4M3 products are exact float16 values.
 //   AWQ: byte columns as NVFP4; scales and biases (one each per n and 32 k) are held the same way.  A transposed dword
-//     holds the nibbles of n, n + 1, n + 2, n + 3, of which masks give the pairs (n, n + 2) and (n + 1, n + 3): each
-//     8 n of dy and of the scales are stored in the order 0 2 1 3 4 6 5 7, and no nibble has to move.
+//     holds the nibbles of n .. n + 3, which masks leave alone in their bytes as E4M3 codes of 0 .. 15.
 //
 // Tile: 4 waves compute (32 MB / TERMS) rows x 256 columns, 64 columns per wave; the waves share the activation
 // tile (64 n of float16 = 128-byte rows, moved by global->LDS copies), each decodes only its own columns.  n is
@@ -54,15 +53,11 @@ __device__ __forceinline__ _Float16 second_term(float x, _Float16 h) {
   return r == r ? (_Float16)r : (_Float16)0.f;
 }
 
-// Place of element t in the order 0 2 1 3 4 6 5 7: its two low bits change places.
-__device__ __forceinline__ int awq_place(int t) { return (t & ~3) | ((t & 1) << 1) | ((t >> 1) & 1); }
-
 // One workgroup per row of dy [M][N] (any N, so rows are only element-aligned): the row's largest finite magnitude, then the scaled
 // float16 terms, [TERMS][M][Np] with zeros from N to Np (a multiple of 64).  A thread keeps RC chunks of 8 elements in registers,
 // loaded without a branch between them so that all are in flight at once; longer rows read the rest twice.  The up to 7 elements
 // behind the last whole chunk are one thread's.
-// PERM: each 8 elements in the order 0 2 1 3 4 6 5 7 (AWQ).
-template <bool BF, bool SC, bool PERM, int TERMS, int RC>
+template <bool BF, bool SC, int TERMS, int RC>
 __global__ void __launch_bounds__(256) grad_prep_kernel(int M, int N, int Np, const void* __restrict__ dy,
                                                         const float* __restrict__ scale, uint16_t* __restrict__ a16,
                                                         float* __restrict__ rowscale) {
@@ -108,8 +103,7 @@ __global__ void __launch_bounds__(256) grad_prep_kernel(int M, int N, int Np, co
     uint32_t hi[4], lo[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int a = PERM ? 4 * (j >> 1) + (j & 1) : 2 * j, b = PERM ? a + 2 : a + 1;
-      const float x0 = ldexpf(v[a], -e), x1 = ldexpf(v[b], -e);
+      const float x0 = ldexpf(v[2 * j], -e), x1 = ldexpf(v[2 * j + 1], -e);
       const _Float16 h0 = (_Float16)x0, h1 = (_Float16)x1;
       hi[j] = as_u32(f16x2{h0, h1});
       if constexpr (TERMS == 2) lo[j] = as_u32(f16x2{second_term(x0, h0), second_term(x1, h1)});
@@ -163,7 +157,7 @@ __global__ void __launch_bounds__(256) grad_prep_kernel(int M, int N, int Np, co
   if (t < Np - 8 * nf) {                         // the last elements and the zeros behind them
     const float x = ldexpf(rest, -e);
     const _Float16 h = (_Float16)x;
-    const int at = 8 * nf + (PERM ? awq_place(t) : t);
+    const int at = 8 * nf + t;
     o[at] = __builtin_bit_cast(uint16_t, h);
     if constexpr (TERMS == 2) o[(size_t)M * Np + at] = __builtin_bit_cast(uint16_t, second_term(x, h));
   }
@@ -251,7 +245,6 @@ __global__ void __launch_bounds__(256, 2) grad_gemm_kernel(int M, int N, int Np,
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int li = lane & 31, h = lane >> 5;
-  const AwqDecode dc = awq_decode_consts();     // (AWQ only; dead elsewhere)
 
   // Parts of the split tiles first, then whole tiles: workgroup b runs on XCD b % 8, and each XCD gets a contiguous
   // run of tiles, ordered in bands of 8 tile rows so that the tiles in flight share rows and columns in its L2.
@@ -360,7 +353,7 @@ __global__ void __launch_bounds__(256, 2) grad_gemm_kernel(int M, int N, int Np,
     uint8_t* bs = lds + stage * STAGE + ASTAGE;
     const int r = tid >> 2, q = tid & 3, sw = (r >> 1) & 7;
     if constexpr (is_awq(FMT)) {
-      uint16_t* sc = reinterpret_cast<uint16_t*>(bs + 64 * 128) + 2 * q * kScaleRow + awq_place(r);
+      uint16_t* sc = reinterpret_cast<uint16_t*>(bs + 64 * 128) + 2 * q * kScaleRow + r;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         *reinterpret_cast<u32x4*>(bs + r * 128 + (((2 * q + j) ^ sw) * 16)) = rec.c[j];
@@ -429,15 +422,17 @@ __global__ void __launch_bounds__(256, 2) grad_gemm_kernel(int M, int N, int Np,
         bf[j] = f16x8{p0.x, p0.y, p1.x, p1.y, p2.x, p2.y, p3.x, p3.y};
       }
     } else if constexpr (is_awq(FMT)) {
-      // low nibbles: even k, high nibbles: odd k; dword j holds 4 n, pairs (n, n + 2) below and (n + 1, n + 3) 8 bits up
+      // low nibbles: even k, high nibbles: odd k; dword j holds 4 n
       f16x2 ev[4], od[4];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const uint32_t wd = (uint32_t)(j ? raw.q[0].y : raw.q[0].x);
-        const uint32_t s0 = j ? raw.d.z : raw.d.x, s1 = j ? raw.d.w : raw.d.y;
-        const uint32_t z0 = j ? raw.z.z : raw.z.x, z1 = j ? raw.z.w : raw.z.y;
-        awq_pairs(wd, as_f16x2(s0), as_f16x2(z0), dc, ev[2 * j], od[2 * j]);
-        awq_pairs(wd >> 8, as_f16x2(s1), as_f16x2(z1), dc, ev[2 * j + 1], od[2 * j + 1]);
+        const uint32_t wd = (uint32_t)(j ? raw.q[0].y : raw.q[0].x), lo = wd & 0x0F0F0F0Fu, hi = (wd >> 4) & 0x0F0F0F0Fu;
+        const f16x2 s0 = as_f16x2(j ? raw.d.z : raw.d.x), s1 = as_f16x2(j ? raw.d.w : raw.d.y);
+        const f16x2 z0 = as_f16x2(j ? raw.z.z : raw.z.x), z1 = as_f16x2(j ? raw.z.w : raw.z.y);
+        ev[2 * j] = __builtin_elementwise_fma(nibbles_f16<false>(lo), s0, z0);
+        ev[2 * j + 1] = __builtin_elementwise_fma(nibbles_f16<true>(lo), s1, z1);
+        od[2 * j] = __builtin_elementwise_fma(nibbles_f16<false>(hi), s0, z0);
+        od[2 * j + 1] = __builtin_elementwise_fma(nibbles_f16<true>(hi), s1, z1);
       }
       bf[0] = f16x8{ev[0].x, ev[0].y, ev[1].x, ev[1].y, ev[2].x, ev[2].y, ev[3].x, ev[3].y};
       bf[1] = f16x8{od[0].x, od[0].y, od[1].x, od[1].y, od[2].x, od[2].y, od[3].x, od[3].y};
@@ -666,17 +661,17 @@ hipError_t grad_dispatch(int M, int N, int K, int terms, const GradPlan& p, cons
 }
 
 // 3 register chunks cover rows of 6144, 9 rows of 18432.
-template <bool BF, bool SC, bool PERM, int TERMS>
+template <bool BF, bool SC, int TERMS>
 void grad_prep(int M, int N, int Np, const void* dy, const float* scale, uint16_t* a16, float* rs, hipStream_t st) {
   if (Np <= 3 * 2048)
-    hipLaunchKernelGGL((grad_prep_kernel<BF, SC, PERM, TERMS, 3>), dim3(M), dim3(256), 0, st, M, N, Np, dy, scale, a16, rs);
+    hipLaunchKernelGGL((grad_prep_kernel<BF, SC, TERMS, 3>), dim3(M), dim3(256), 0, st, M, N, Np, dy, scale, a16, rs);
   else
-    hipLaunchKernelGGL((grad_prep_kernel<BF, SC, PERM, TERMS, 9>), dim3(M), dim3(256), 0, st, M, N, Np, dy, scale, a16, rs);
+    hipLaunchKernelGGL((grad_prep_kernel<BF, SC, TERMS, 9>), dim3(M), dim3(256), 0, st, M, N, Np, dy, scale, a16, rs);
 }
-template <bool BF, bool SC, bool PERM, typename... A>
+template <bool BF, bool SC, typename... A>
 void grad_prep_terms(int terms, A... a) {
-  if (terms == 2) grad_prep<BF, SC, PERM, 2>(a...);
-  else grad_prep<BF, SC, PERM, 1>(a...);
+  if (terms == 2) grad_prep<BF, SC, 2>(a...);
+  else grad_prep<BF, SC, 1>(a...);
 }
 
 }  // namespace
@@ -698,13 +693,11 @@ hipError_t linear_grad(int fmt, int terms, int M, int N, int K, const void* dy, 
   const int Np = p.steps * 64;
   const bool bf = dxt == X_BF16;
   if (dyt == X_BF16) {
-    if (fmt == 0) grad_prep_terms<true, true, false>(terms, M, N, Np, dy, scale, a16, rs, st);
-    else if (fmt == 1) grad_prep_terms<true, false, false>(terms, M, N, Np, dy, scale, a16, rs, st);
-    else grad_prep<true, false, true, 1>(M, N, Np, dy, scale, a16, rs, st);
+    if (fmt == 0) grad_prep_terms<true, true>(terms, M, N, Np, dy, scale, a16, rs, st);
+    else grad_prep_terms<true, false>(terms, M, N, Np, dy, scale, a16, rs, st);
   } else {
-    if (fmt == 0) grad_prep_terms<false, true, false>(terms, M, N, Np, dy, scale, a16, rs, st);
-    else if (fmt == 1) grad_prep_terms<false, false, false>(terms, M, N, Np, dy, scale, a16, rs, st);
-    else grad_prep_terms<false, false, true>(terms, M, N, Np, dy, scale, a16, rs, st);
+    if (fmt == 0) grad_prep_terms<false, true>(terms, M, N, Np, dy, scale, a16, rs, st);
+    else grad_prep_terms<false, false>(terms, M, N, Np, dy, scale, a16, rs, st);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
