@@ -700,6 +700,11 @@ def moe_awq_run(x, w13_bank, w2_bank, E, I, topk=None, router=None, ids=None, we
     return out, ids, weights
 
 
+def _empty_as(t, dtype):
+    """A new tensor of t's shape (t dense); empty_like spares half a microsecond where the types agree."""
+    return torch.empty_like(t) if t.dtype is dtype else torch.empty(t.shape, dtype=dtype, device=t.device)
+
+
 def _norm_args(h, y, post, gate, pre):
     """Checks shared by block_norm_run and its backward call; (M, H, G, h code, y code, weight code, gate code)."""
     dev = h.device
@@ -750,14 +755,14 @@ def block_norm_run(h, y=None, post=None, gate=None, alpha=1.0, pre=None, eps=1e-
         want = _result_dtype("x_dtype", x_dtype, h.dtype, x=x)
         xt = _float_code(want, "x")
         if x is None:
-            x = torch.empty((M, H), dtype=want, device=dev)
+            x = _empty_as(h, want)
         else:
             _want(x, "x", want, dev, M * H)
     elif x is not None or x_dtype is not None:
         raise ValueError("x and x_dtype need pre")
     if y is not None:
         if h_out is None:
-            h_out = torch.empty((M, H), dtype=h.dtype, device=dev)
+            h_out = torch.empty_like(h)
         else:
             _want(h_out, "h_out", h.dtype, dev, M * H)
     elif h_out is not None:
@@ -792,17 +797,16 @@ def block_norm_backward(h, y=None, dh=None, dx=None, post=None, gate=None, alpha
         _want(dx, "dx", dx.dtype, dev, M * H)
     f32 = torch.float32
     outs = []
-    for t, name, src, shape, dtype, wanted in (
-            (dh_in, "dh_in", h, (M, H), h.dtype, need[0]), (dy, "dy", y, (M, H), y is not None and y.dtype, need[1]),
-            (dpost, "dpost", post, (H,), f32, need[2]), (dgate, "dgate", gate, gate is not None and gate.shape, f32, need[3]),
-            (dpre, "dpre", pre, (H,), f32, need[4])):
+    for t, name, src, dtype, wanted in ((dh_in, "dh_in", h, h.dtype, need[0]), (dy, "dy", y, y is not None and y.dtype, need[1]),
+                                        (dpost, "dpost", post, f32, need[2]), (dgate, "dgate", gate, f32, need[3]),
+                                        (dpre, "dpre", pre, f32, need[4])):
         if src is None or not wanted:
             if t is not None:
                 raise ValueError(f"{name} is given, but not computed")
             outs.append(None)
             continue
         if t is None:
-            t = torch.empty(shape, dtype=dtype, device=dev)
+            t = _empty_as(src, dtype)
         else:
             _want(t, name, dtype, dev, src.numel())
         outs.append(t)
