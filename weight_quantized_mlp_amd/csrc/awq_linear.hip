@@ -190,12 +190,32 @@ __global__ void __launch_bounds__(512) awq_rows_kernel(int M, int N, int K, Rows
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[j] = fmaf(sum[j], rs, acc[j]);
   };
-  for (; b < b1; b += 2 * p.waves) {                            // (a load too many costs as much as one that is needed)
-    if (b + p.waves < b1) load(b + p.waves, v);
-    multiply(b, u);
-    if (b + p.waves >= b1) break;
-    if (b + 2 * p.waves < b1) load(b + 2 * p.waves, u);
-    multiply(b + p.waves, v);
+  const int w = p.waves;
+  if constexpr (MR == 1) {
+    // Every path knows what it has on its way: behind a branch that the products after it share, they would wait for the next block's
+    // loads, too (1 row 17408 -> 5120: 18.8 us, so 17.7; 2 float32 rows would lose a wave per SIMD to the copies: 27.8, 32.8).
+    for (; b + w < b1; b += 2 * w) {
+      load(b + w, v);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(b, u);
+      if (b + 2 * w >= b1) {
+        multiply(b + w, v);
+        b = b1;
+        break;
+      }
+      load(b + 2 * w, u);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(b + w, v);
+    }
+    if (b < b1) multiply(b, u);
+  } else {
+    for (; b < b1; b += 2 * w) {                                // (a load too many costs as much as one that is needed)
+      if (b + w < b1) load(b + w, v);
+      multiply(b, u);
+      if (b + w >= b1) break;
+      if (b + 2 * w < b1) load(b + 2 * w, u);
+      multiply(b + w, v);
+    }
   }
 
   // the waves' sums, in order
