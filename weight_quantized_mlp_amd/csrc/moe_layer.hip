@@ -129,7 +129,9 @@ __global__ void __launch_bounds__(64) route_topk_kernel(int E, int topk, int ren
       }
     }
     const int top = wave64_max_i32(best);
-    const int e = -wave64_max_i32(best == top ? -at : -0x7FFFFFFF);
+    const uint64_t who = __ballot(best == top);               // seldom more than one lane
+    const int e = (who & (who - 1)) == 0 ? __builtin_amdgcn_readlane(at, __builtin_ctzll(who))
+                                         : -wave64_max_i32(best == top ? -at : -0x7FFFFFFF);
     if constexpr (VPL > 0) {
 #pragma unroll
       for (int j = 0; j < VPL; ++j)
@@ -159,7 +161,6 @@ __global__ void __launch_bounds__(64) route_topk_kernel(int E, int topk, int ren
 //   Few routes (SPLIT): the waves of a workgroup share one pair's blocks, so that one token's experts reach all CUs.
 // Either way a column's blocks are added in order, each scaled by a power of two, which is exact: its bits depend neither on the way nor on
 // how many columns there are.
-constexpr int kMaxRoutes = 256 * 16;
 constexpr int kPartRow = 20;                   // floats of a row of partial sums: 16, padded
 constexpr int kBlockK = 512, kBlockSteps = 4;
 
@@ -404,13 +405,25 @@ __global__ void __launch_bounds__(256) moe_sum_kernel(int E, int topk, int H, co
   const int m = (int)blockIdx.y, o = 4 * ((int)blockIdx.x * 256 + (int)threadIdx.x);
   if (o >= H) return;
   f32x4 v = {0.f, 0.f, 0.f, 0.f};
-  for (int k = 0; k < topk; ++k) {
-    const int r = m * topk + k, e = ids[r];
-    if (e < 0 || e >= E) continue;
-    const float w = weights[r];
-    const f32x4 p = *reinterpret_cast<const f32x4*>(y + (size_t)r * H + o);
+  constexpr int UP = 8;                          // routes on their way at once, valid or not (one after the other: 1 token 4.4 us,
+                                                 // so 3.0)
+  for (int k0 = 0; k0 < topk; k0 += UP) {
+    int e[UP];
+    float w[UP];
+    f32x4 p[UP];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = fmaf(w, p[j], v[j]);
+    for (int k = 0; k < UP; ++k) {
+      const int r = m * topk + min(k0 + k, topk - 1);
+      e[k] = ids[r];
+      w[k] = weights[r];
+      p[k] = *reinterpret_cast<const f32x4*>(y + (size_t)r * H + o);
+    }
+#pragma unroll
+    for (int k = 0; k < UP; ++k) {
+      if (k0 + k >= topk || e[k] < 0 || e[k] >= E) continue;                   // (such a route's y is not written)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = fmaf(w[k], p[k][j], v[j]);
+    }
   }
   const size_t at = (size_t)m * H + o;
   if (ot == X_F32) {
