@@ -572,8 +572,17 @@ __global__ void __launch_bounds__(256) awq_join_kernel(int M, int N, int S, cons
   const int n = (int)blockIdx.x * 256 + (int)threadIdx.x, m = (int)blockIdx.y;
   if (n >= N) return;
   const size_t at = (size_t)m * N + n, part = (size_t)M * N;
-  float v = partials[at];
-  for (int s = 1; s < S; ++s) v += partials[s * part + at];
+  float v = 0.f;
+  constexpr int UP = 16;                         // parts on their way at once
+  for (int s0 = 0; s0 < S; s0 += UP) {
+    float p[UP];
+#pragma unroll
+    for (int s = 0; s < UP; ++s)
+      if (s0 + s < S) p[s] = partials[(s0 + s) * part + at];
+#pragma unroll
+    for (int s = 0; s < UP; ++s)
+      if (s0 + s < S) v = s0 + s == 0 ? p[s] : v + p[s];
+  }
   y[at] = v;
 }
 
