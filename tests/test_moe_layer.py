@@ -285,3 +285,21 @@ def test_empty_and_refused_calls():
         wq.moe_awq_run(x, b13, b2, E, I, topk, router=router, out=x)
     with pytest.raises(wq.WQError):
         wq.moe_awq_run(x, b13, b2, E, I, topk, router=router, workspace=torch.empty(64, dtype=torch.uint8, device=DEV))
+
+
+@pytest.mark.parametrize("E,topk", [(65, 16), (200, 10), (300, 7), (512, 16), (1000, 10), (1024, 1), (1500, 16), (5000, 3)])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_choice_among_many_experts(E, topk, renorm):
+    """Every number of experts per lane, and more than a wave keeps; half of the logits in ties."""
+    M, H, I = 5, 32, 32
+    nb13, nb2 = wq.awq_bank_bytes(E, 2 * I, H, 3), wq.awq_bank_bytes(E, H, I, 3)
+    b13, b2 = torch.zeros(nb13, dtype=torch.uint8, device=DEV), torch.zeros(nb2, dtype=torch.uint8, device=DEV)
+    x, xd = randn(E, (M, H), F32)
+    router, rd = randn(E + 1, (E, H), F32, 0.5)
+    router[E // 2:] = router[:E - E // 2].clone()
+    rd[E // 2:] = rd[:E - E // 2].copy()
+    out, ids, weights = wq.moe_awq_run(x, b13, b2, E, I, topk, router=router, renorm=renorm)
+    ref_ids, ref_w = route_ref(xd, rd, topk, renorm)
+    assert np.array_equal(host(ids), ref_ids)
+    assert np.all(np.abs(host(weights) - ref_w) <= (64 + E / 32) * U * ref_w)      # (without renorm, E / 64 terms per lane)
+    assert (out == 0).all()                                                        # (zero scales)
