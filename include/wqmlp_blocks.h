@@ -26,8 +26,8 @@ extern "C" {
  *                 bank starts at a multiple of awq_bank_bytes(1, N, K, meta_layout)); meta_layout 3 or 4
  *   y     [M, N]  float32
  * K: a multiple of 32; N and M: any.  The products are exact in float32 and summed there: weights are float16
- * values, float16 x enters as it is, bfloat16 and float32 rows are scaled by a power of two so that their
- * largest finite magnitude lies in [2^14, 2^15) and enter as one (bfloat16) or two (float32) float16 terms: a
+ * values, float16 x enters as it is, bfloat16 and float32 rows (or pieces of 512 and 1024 k of them) are scaled by a power
+ * of two so that their largest finite magnitude lies in [2^14, 2^15) and enter as one (bfloat16) or two (float32) float16 terms: a
  * bfloat16 element is off by at most 2^-39 of its row's largest, a float32 one by 2^-22 of itself or 2^-39 of its
  * row's largest, whichever is more.  A row's result does not depend on the other rows' values; NaN and infinities
  * stay in their row.  M == 0 is a valid empty call.
@@ -65,10 +65,11 @@ int awq_linear_backward(int64_t M, int64_t N, int64_t K, const void* dy, int dy_
  *   w13_bank, w2_bank as for moe_awq_m1_run; meta_layout 3 or 4
  *   out     [M, H]    out_dtype (any of the three), rounded once
  * 0 <= M <= WQ_MOE_MAX_TOKENS, 1 <= topk <= min(E, WQ_MOE_MAX_TOPK) (given ids: topk may exceed E), H and I
- * multiples of 32 up to WQ_MOE_MAX_WIDTH.  Numerics as for awq_linear_run: products and sums are float32, float32 x and act enter as two
- * float16 terms; no intermediate is rounded to 16 bits (moe_awq_m1_run rounds g, u, act and each route's result to
- * float16).  A token's result is the same bits whatever the other tokens are and however many.  Where x holds an infinity or NaN its row's ids are those of the order above, and its out may be NaN.  An expert is
- * read once for up to 16 of its tokens.
+ * multiples of 32 up to WQ_MOE_MAX_WIDTH.  Numerics as for awq_linear_run: products and sums are float32, float32 x and
+ * act enter as two float16 terms; no intermediate is rounded to 16 bits (moe_awq_m1_run rounds g, u, act and each route's
+ * result to float16).  A token's result is the same bits whatever the other tokens are and however many.  Where x holds an
+ * infinity or NaN its row's ids are those of the order above, and its out may be NaN.  An expert is read from HBM once for
+ * all of its tokens; more tokens than a pass holds (at most 16) read it again through the caches.
  */
 #define WQ_MOE_MAX_TOKENS 256
 #define WQ_MOE_MAX_WIDTH 16384
@@ -92,8 +93,8 @@ int moe_awq_run(int64_t M, int64_t E, int64_t topk, int64_t H, int64_t I, const 
  *   gate     [G, H]  g_dtype, or NULL for one; G divides M, and gate row j serves the M/G rows from j M/G on:
  *                    G = 1 a gate per channel, G = M one for every element, between them one per sequence
  *   x        [M, H]  x_dtype: the next block's input
- * All types: WQ_F32, WQ_BF16 or WQ_F16 (the type of an absent tensor is ignored).  H: a multiple of 8.  eps >= 0.  Arithmetic is float32, rounded once to h_out
- * and once to x.  M == 0 is a valid empty call.
+ * All types: WQ_F32, WQ_BF16 or WQ_F16 (the type of an absent tensor is ignored).  H: a multiple of 8.  eps >= 0.
+ * Arithmetic is float32, rounded once to h_out and once to x.  M == 0 is a valid empty call.
  */
 int block_norm_run(int64_t M, int64_t H, const void* h, int h_dtype, const void* y, int y_dtype, const void* post,
                    const void* pre, int w_dtype, const void* gate, int64_t G, int g_dtype, float alpha, float offset,

@@ -592,6 +592,11 @@ def adamw_run(table, step, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.
     _check("adamw_run", rc)
 
 
+def _empty_as(t, dtype):
+    """A new tensor of t's shape (t dense); empty_like spares half a microsecond where the types agree."""
+    return torch.empty_like(t) if t.dtype is dtype else torch.empty(t.shape, dtype=dtype, device=t.device)
+
+
 def awq_linear_workspace_bytes(M, N, K, x_dtype=torch.float32):
     return lib().awq_linear_workspace_bytes(M, N, K, _FLOATS[x_dtype])
 
@@ -688,7 +693,7 @@ def moe_awq_run(x, w13_bank, w2_bank, E, I, topk=None, router=None, ids=None, we
     _want(w13_bank, "w13_bank", torch.uint8, dev, awq_bank_bytes(E, 2 * I, H, meta_layout))
     _want(w2_bank, "w2_bank", torch.uint8, dev, awq_bank_bytes(E, H, I, meta_layout))
     if out is None:
-        out = torch.empty((M, H), dtype=want, device=dev)
+        out = _empty_as(x, want)
     else:
         _want(out, "out", want, dev, M * H)
     nb = moe_awq_workspace_bytes(M, E, topk, H, I)
@@ -698,11 +703,6 @@ def moe_awq_run(x, w13_bank, w2_bank, E, I, topk=None, router=None, ids=None, we
                            WQ_MOE_RENORM if router is not None and renorm else 0, _stream(dev))
     _check("moe_awq_run", rc)
     return out, ids, weights
-
-
-def _empty_as(t, dtype):
-    """A new tensor of t's shape (t dense); empty_like spares half a microsecond where the types agree."""
-    return torch.empty_like(t) if t.dtype is dtype else torch.empty(t.shape, dtype=dtype, device=t.device)
 
 
 def _norm_args(h, y, post, gate, pre):

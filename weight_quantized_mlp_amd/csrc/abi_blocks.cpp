@@ -25,7 +25,8 @@ bool awq_shape_ok(int64_t M, int64_t N, int64_t K) {
 
 bool moe_shape_ok(int64_t M, int64_t E, int64_t topk, int64_t H, int64_t I) {
   return M >= 0 && M <= WQ_MOE_MAX_TOKENS && E > 0 && E <= kMaxDim && topk > 0 && topk <= WQ_MOE_MAX_TOPK && H > 0 &&
-         H <= WQ_MOE_MAX_WIDTH && H % 32 == 0 && I > 0 && I <= WQ_MOE_MAX_WIDTH && I % 32 == 0 && E <= kMaxElems / H && E <= kMaxElems / (2 * I);
+         H <= WQ_MOE_MAX_WIDTH && H % 32 == 0 && I > 0 && I <= WQ_MOE_MAX_WIDTH && I % 32 == 0 && E <= kMaxElems / H &&
+         E <= kMaxElems / (2 * I);
 }
 
 bool norm_shape_ok(int64_t M, int64_t H, int64_t G) {

@@ -5,9 +5,12 @@
 // turned into float16 terms (awq_pack_kernel), in the order the matrix cores read it.
 //   Up to kOwnRows rows (awq_rows_kernel) and up to kFewRows (awq_shared_kernel): the weights' bytes bound it, and with them the
 //     decode, so what matters is that every CU has work from the start and reads whole cache lines.  x is turned into terms by the
-//     waves themselves, which spares a launch.
+//     waves themselves, which spares a launch.  Calls in a row: 1 float16 row 5120 -> 17408 13.4 us (53 MB, 4.0 TB/s; bfloat16 15.8,
+//     float32 19), 13 bfloat16 rows 17408 -> 5120 20.7 us, of which the parts' sum takes 3.
 //   More rows (awq_gemm_kernel): the matrix cores bound it.  4 waves with 64 weight rows each share the tile of x through
-//     LDS (global->LDS copies, two stages); every wave decodes only its own weights, once per tile row.
+//     LDS (global->LDS copies, two stages); every wave decodes only its own weights, once per tile row.  2049 bfloat16 rows
+//     5120 -> 17408: 447 us (817 TFLOP/s), of which x's terms take 15 and the cut tiles' sum 15; a float16 product of those sizes in
+//     the library 409.  512 rows: 147 us; 2048 float32 rows 17408 -> 5120, twice the products: 792-836.
 // All split the contraction over workgroups where there are few; a further kernel adds the parts in order.
 #include <algorithm>
 
@@ -122,7 +125,8 @@ __global__ void __launch_bounds__(512) awq_rows_kernel(int M, int N, int K, Rows
   auto load = [&](int b, Block& d) {
     const int o = min(64 * b + lane, K / 8 - 1);
 #pragma unroll
-    for (int m = 0; m < MR; ++m) d.x[m] = load_raw<XS>(static_cast<const uint8_t*>(x) + (size_t)min(m, M - 1) * K * (XS == X_F32 ? 4 : 2), (uint32_t)(8 * o));
+    for (int m = 0; m < MR; ++m)
+      d.x[m] = load_raw<XS>(static_cast<const uint8_t*>(x) + (size_t)min(m, M - 1) * K * (XS == X_F32 ? 4 : 2), (uint32_t)(8 * o));
 #pragma unroll
     for (int t = 0; t < 4; ++t) d.c[t] = *reinterpret_cast<const u32x4*>(codes + (uint32_t)(crow + 16 * min(16 * b + 4 * t + q, G - 1)));
   };
@@ -295,7 +299,8 @@ __global__ void __launch_bounds__(512, 4) awq_shared_kernel(int M, int N, int K,
     u32x4 cd[D][4];
     auto load_codes = [&](int j) {
 #pragma unroll
-      for (int t = 0; t < 4; ++t) cd[j % D][t] = *reinterpret_cast<const u32x4*>(codes + (uint32_t)(crow + 16 * min(16 * (b0 + j) + 4 * t + q, G - 1)));
+      for (int t = 0; t < 4; ++t)
+        cd[j % D][t] = *reinterpret_cast<const u32x4*>(codes + (uint32_t)(crow + 16 * min(16 * (b0 + j) + 4 * t + q, G - 1)));
     };
 #pragma unroll
     for (int j = 0; j < D; ++j) load_codes(j);
@@ -385,7 +390,9 @@ __global__ void __launch_bounds__(512, 4) awq_shared_kernel(int M, int N, int K,
 }
 
 // ---- many rows ---------------------------------------------------------------------------------------------------
-// Tile: 16 MT rows of x by 256 weight rows, 64 per wave.  The tiles of the last, unfilled round are cut into S parts of `per` steps.
+// Tile: 16 MT rows of x by 256 weight rows, 64 per wave.  The tiles of the last, unfilled round are cut into S parts of `per` steps
+// (512 rows 5120 -> 17408: 179 us uncut, 147; 2049 rows: 461 and 447; cut tiles before the whole ones, which lets all run out of
+// step and miss L2: 15% slower).
 constexpr int kGemmCols = 256, kSlots = 512;   // workgroups the chip runs at once: two per CU
 
 struct TilePlan {
@@ -430,8 +437,8 @@ __global__ void __launch_bounds__(256, 2) awq_gemm_kernel(int M, int N, TilePlan
   const int n0 = tn * kGemmCols + 64 * wave, mt0 = tm * MT, mtiles = (M + 15) >> 4;
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
 
-  // Row tile r: rows first[r] .. + 15; past the matrix its last 16 again, of which only the rows not yet covered are stored.  Then a lane's
-  // offset in every tile and step is the same, and the scalar bases do the rest.
+  // Row tile r: rows first[r] .. + 15; past the matrix its last 16 again, of which only the rows not yet covered are stored.  Then a
+  // lane's offset in every tile and step is the same, and the scalar bases do the rest.
   int first[NT];
 #pragma unroll
   for (int r = 0; r < NT; ++r) first[r] = min(n0 + 16 * r, max(N - 16, 0));

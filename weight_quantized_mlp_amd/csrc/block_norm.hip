@@ -3,8 +3,10 @@
 //
 // Rows of H elements, each read once: a workgroup holds its row in registers (chunks of 8 elements per thread) between
 // the row sums, so a pass moves the bytes of its inputs and outputs and nothing else.  Rows above 16384 elements (backward: 8192,
-// where the columns' sums take registers, too) are read again for every pass instead (they come from L2).  HBM bounds long calls, the chain of load, row sum, row sum
-// and store short ones.
+// where the columns' sums take registers, too) are read again for every pass instead (they come from L2).  HBM bounds long calls,
+// the chain of load, row sum, row sum and store short ones.  Calls in a row: 8191 x 5120 float32 116 us (588 MB, 5.1 TB/s), one
+// bfloat16 row of 2560 3.3 us on the device (11 a call, the binding's); backward 4096 x 5120 bfloat16 65 us (252 MB, 3.9 TB/s),
+// 129 x 320 float32 8 us on the device in two launches.
 //
 // Backward: the two norms' row sums chain (dy's needs du, which needs the second norm's), while the weights' gradients
 // are sums over rows.  A workgroup walks a run of consecutive rows and keeps its columns' three sums in registers; what

@@ -10,8 +10,13 @@
 // The experts' bytes bound it as soon as tokens spread over many experts, and every expert is read once for all of its
 // tokens: a workgroup belongs to one expert (or to one route, the first that names its expert, when there are fewer routes
 // than experts) and some of its rows, gathers the expert's routes from the list of ids, and multiplies its weights, decoded
-// in registers (awq_common.h), with up to 16 of them at a time on the matrix cores.  act travels in float32 and enters W2 as two float16 terms, like float32 x, so nothing is rounded to 16 bits
-// on the way.
+// in registers (awq_common.h), with up to 16 of them at a time on the matrix cores.  act travels in float32 and enters W2 as
+// two float16 terms, like float32 x, so nothing is rounded to 16 bits on the way.
+//
+// Calls in a row, 512 experts of 160 on 2560, 10 per token: 1 token 25 us (logits 4.7, choice 4, W13 8.4, W2 5.7, sum 3: five
+// launches, each near what a launch with its chain of loads takes), 37 tokens 96 us for 195 MB (10, 5, 43, 33, 5).  64 experts of 704
+// on 1024, 130 float32 tokens, 6 each: 73 us (6, 4, 37, 24, 5).  In W13 of 37 tokens half of the CUs' issue slots go to the decode
+// and what surrounds it, a quarter of the time some CUs have run out of work.
 #include <algorithm>
 
 #include "awq_common.h"
