@@ -33,18 +33,7 @@ struct AwqStep {
   u32x4 c;
   uint32_t s, z;
 };
-// Row `row` (clamped by the caller), group g; groups past the row's end read its last one and count as zero weights.
-template <int ML>
-__device__ __forceinline__ AwqStep awq_load(const uint8_t* codes, const uint8_t* expert, const AwqLayout& L, int64_t row, int g) {
-  const int gc = min(g, (int)L.G - 1);
-  AwqStep r;
-  r.c = *reinterpret_cast<const u32x4*>(codes + 16 * gc);
-  const int64_t at = row * L.G + gc;
-  r.s = reinterpret_cast<const uint16_t*>(expert + L.scale_off)[at];
-  if constexpr (ML == 3) r.z = expert[L.meta2_off + at];
-  else r.z = reinterpret_cast<const uint16_t*>(expert + L.meta2_off)[at];
-  return r;
-}
+// The scale and bias of its group, twice each; a group that is not `live` counts as zero weights.
 template <int ML>
 __device__ __forceinline__ void awq_meta(const AwqStep& r, bool live, f16x2& s2, f16x2& b2) {
   const _Float16 s = f16_from_bits((uint16_t)r.s);
