@@ -55,6 +55,32 @@ def test_shapes(M, N, K, xt):
     check(y, xd, w[0], xt)
 
 
+# fewer weight rows than a tile of 16 has, one more or less than whole tiles; rows of one group, of a step and a part of one
+@pytest.mark.parametrize("K", [32, 96, 160, 544])
+@pytest.mark.parametrize("M,N", [(33, 1), (40, 7), (64, 15), (65, 17), (130, 5), (130, 255), (200, 257)])
+def test_narrow_tiles(M, N, K):
+    for xt, layout in ((BF16, 3), (F32, 4)):
+        print("[awq linear]", M, N, K, xt, layout, flush=True)
+        bank, w = awq_weights(M + N, 1, N, K, layout)
+        x, xd = randn(K, (M, K), xt)
+        guard = torch.full((M * N + 64,), 7.0, device=DEV)
+        y = wq.awq_linear_run(x, bank, N, layout, out=guard[: M * N].view(M, N))
+        assert (guard[M * N:] == 7.0).all()
+        check(y, xd, w[0], xt)
+
+
+@pytest.mark.parametrize("xt", [F32, F16])
+def test_whole_and_cut_tiles(xt):
+    """More tiles than the chip runs at once: the first rounds whole, the rest cut into parts."""
+    M, N, K = 1100, 16400, 1056
+    bank, w = awq_weights(7, 1, N, K, 3)
+    x, xd = randn(8, (M, K), xt)
+    guard = torch.full((M * N + 64,), 7.0, device=DEV)
+    y = wq.awq_linear_run(x, bank, N, out=guard[: M * N].view(M, N))
+    assert (guard[M * N:] == 7.0).all()
+    check(y, xd, w[0], xt)
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 96, 512), (20, 96, 512), (80, 96, 512)])
 def test_both_layouts_give_the_same_bits(M, N, K):
     x, _ = randn(1, (M, K), BF16)
