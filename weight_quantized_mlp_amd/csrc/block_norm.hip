@@ -8,7 +8,9 @@
 // bfloat16 row of 2560 3.3 us on the device (11 a call, the binding's); backward 4096 x 5120 bfloat16 65 us (252 MB, 3.9 TB/s),
 // 129 x 320 float32 8 us on the device in two launches.
 //
-// Backward: the two norms' row sums chain (dy's needs du, which needs the second norm's), while the weights' gradients
+// Backward, with n = t r the normed row and dn its gradient: dt = r (dn - n mean(dn n)).  Every factor is applied as it stands there; r^3,
+// which the mean over t itself would need, leaves float32's range where r and n do not (rows of rms 1e13, or rows of zeros under an eps
+// of 1e-26).  The two norms' row sums chain (dy's needs du, which needs the second norm's), while the weights' gradients
 // are sums over rows.  A workgroup walks a run of consecutive rows and keeps its columns' three sums in registers; what
 // it has at the end goes to the workspace and a second kernel adds the runs in order, so nothing is atomic and the
 // result does not depend on timing.  A run never crosses a gate row unless it holds whole gate rows.
@@ -292,12 +294,12 @@ __device__ __forceinline__ void run_rows(const NormRuns& p, int M, int L, int b,
 }
 
 struct RowScalars {
-  float ru, rv, cu;            // r(h), r(y) (1 without post), r(h)^3 mean(dn h)
+  float ru, rv, cu;            // r(h), r(y) (1 without post), mean(dn n(h))
 };
 // du of one element; what is absent takes no part, whatever stands in its place.
 __device__ __forceinline__ float norm_du(bool has_pre, bool has_dh, float ru, float cu, float dn, float h, float dh) {
-  const float through = has_pre ? fmaf(ru, dn, -cu * h) : 0.f;
-  return has_dh ? through + dh : through;
+  const float past = has_dh ? dh : 0.f;
+  return has_pre ? fmaf(ru, fmaf(-cu, h * ru, dn), past) : past;
 }
 
 // Rows in registers.  Of one chunk per thread the next row's loads are on their way while this one's sums are formed; the weights and
@@ -392,7 +394,7 @@ __global__ void __launch_bounds__(RC == 1 ? 640 : 512) norm_grad_kernel(NormArgs
     if (AHEAD && m + 1 < r1) load_row(m + 1);
     block_sums(s, buf2, turn2);
     const float ru = a.has_pre ? 1.f / sqrtf(s[0] * invH + a.eps) : 0.f;
-    const float cu = a.has_pre ? -ru * ru * ru * (s[1] * invH) : 0.f;
+    const float cu = a.has_pre ? -(s[1] * invH) * ru : 0.f;   // -mean(dn n(h))
     const float rv = a.has_post ? 1.f / sqrtf(s[2] * invH + a.eps) : 1.f;
     float q[1] = {0.f};                           // dx becomes dp: alpha gate du post+
 #pragma unroll
@@ -400,25 +402,26 @@ __global__ void __launch_bounds__(RC == 1 ? 640 : 512) norm_grad_kernel(NormArgs
       if (t + i * T >= C) continue;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float du = fmaf(ru, dx[i][j] * pre[i][j], fmaf(cu, h[i][j], dh[i][j]));
+        const float hn = h[i][j] * ru, du = fmaf(ru, fmaf(cu, hn, dx[i][j] * pre[i][j]), dh[i][j]);
         dh[i][j] = du;
-        spre[i][j] = fmaf(dx[i][j] * ru, h[i][j], spre[i][j]);
+        spre[i][j] = fmaf(dx[i][j], hn, spre[i][j]);
         const float n = y[i][j] * rv, dg = gate[i][j] * du;              // n(y), or y
+        y[i][j] = n;
         spost[i][j] = fmaf(dg, n, spost[i][j]);
         sgate[i][j] = fmaf(du, n * post[i][j], sgate[i][j]);             // times alpha at the end
         dx[i][j] = dg * post[i][j];
-        q[0] = fmaf(dx[i][j], y[i][j], q[0]);
+        q[0] = fmaf(dx[i][j], n, q[0]);
       }
       if (o.dhi != nullptr) row_store<H4, BF>(o.dhi, row + at[i], a.ht, dh[i]);
     }
     if (o.dy != nullptr) {
       if (a.has_post) {
         block_sums(q, buf1, turn1);
-        const float cy = -rv * rv * rv * (q[0] * invH);
+        const float cy = -q[0] * invH;            // -mean(dp post+ n(y))
 #pragma unroll
         for (int i = 0; i < RC; ++i)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) dx[i][j] = fmaf(rv, dx[i][j], cy * y[i][j]);
+          for (int j = 0; j < 8; ++j) dx[i][j] = rv * fmaf(cy, y[i][j], dx[i][j]);
       }
 #pragma unroll
       for (int i = 0; i < RC; ++i)
@@ -477,7 +480,7 @@ __global__ void __launch_bounds__(512) norm_grad_long_kernel(NormArgs a, GradOut
   }
   block_sums(s, buf2, turn2);
   const float ru = a.has_pre ? 1.f / sqrtf(s[0] * invH + a.eps) : 0.f;
-  const float cu = a.has_pre ? ru * ru * ru * (s[1] * invH) : 0.f;
+  const float cu = a.has_pre ? s[1] * invH * ru : 0.f;
   const float rv = a.has_post ? 1.f / sqrtf(s[2] * invH + a.eps) : 1.f;
   if (t == 0) rows[m] = {ru, rv, cu};
   auto du8 = [&](int c) {                         // dh becomes du, w and v the weights, g the gate with alpha
@@ -498,16 +501,16 @@ __global__ void __launch_bounds__(512) norm_grad_long_kernel(NormArgs a, GradOut
     for (int c = t; c < C; c += T) {
       du8(c);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) q[0] = fmaf(g[j] * dh[j] * v[j], y[j], q[0]);
+      for (int j = 0; j < 8; ++j) q[0] = fmaf(g[j] * dh[j] * v[j], y[j] * rv, q[0]);
     }
     block_sums(q, buf1, turn1);
-    cy = rv * rv * rv * (q[0] * invH);
+    cy = q[0] * invH;
   }
   if (o.dy != nullptr) {
     for (int c = t; c < C; c += T) {
       du8(c);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = a.has_post ? fmaf(rv, g[j] * dh[j] * v[j], -cy * y[j]) : g[j] * dh[j];
+      for (int j = 0; j < 8; ++j) y[j] = a.has_post ? rv * fmaf(-cy, y[j] * rv, g[j] * dh[j] * v[j]) : g[j] * dh[j];
       store8(o.dy, row + 8 * (size_t)c, a.yt, y);
     }
   }
@@ -535,7 +538,7 @@ __global__ void __launch_bounds__(64) norm_grad_cols_kernel(NormArgs a, NormRuns
     for (int j = 0; j < 8; ++j) {
       const float du = norm_du(a.has_pre, has_dh, k.ru, k.cu, dx[j] * w[j], h[j], dh[j]);
       const float n = y[j] * k.rv;
-      spre[j] = fmaf(dx[j] * k.ru, h[j], spre[j]);
+      spre[j] = fmaf(dx[j], h[j] * k.ru, spre[j]);
       spost[j] = fmaf(g[j] * du, n, spost[j]);
       sgate[j] = fmaf(a.alpha * du, n * v[j], sgate[j]);
       dh[j] = du;
