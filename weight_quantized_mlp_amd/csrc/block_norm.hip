@@ -137,8 +137,9 @@ __device__ __forceinline__ void gate8(const NormArgs& a, int group, int at, floa
 }
 
 // ---- forward ---------------------------------------------------------------------------------------------------
+// ho may be a.h itself (in place), so it is not declared restrict; a thread reads its elements of h before it writes them.
 template <bool H4, bool Y4, int RC>
-__global__ void __launch_bounds__(512) norm_run_kernel(NormArgs a, void* __restrict__ ho, void* __restrict__ xo) {
+__global__ void __launch_bounds__(512) norm_run_kernel(NormArgs a, void* ho, void* __restrict__ xo) {
   __shared__ float buf[2 * kMaxWaves];
   const int C = a.H / 8, T = (int)blockDim.x, t = (int)threadIdx.x, m = (int)blockIdx.x;
   const size_t row = (size_t)m * a.H;
@@ -200,7 +201,7 @@ __global__ void __launch_bounds__(512) norm_run_kernel(NormArgs a, void* __restr
 }
 
 // Rows too long to hold: every pass reads them again, each thread the elements that it wrote itself.
-__global__ void __launch_bounds__(512) norm_run_long_kernel(NormArgs a, void* __restrict__ ho, void* __restrict__ xo) {
+__global__ void __launch_bounds__(512) norm_run_long_kernel(NormArgs a, void* ho, void* __restrict__ xo) {
   __shared__ float buf[2 * kMaxWaves];
   const int C = a.H / 8, T = (int)blockDim.x, t = (int)threadIdx.x, m = (int)blockIdx.x;
   const size_t row = (size_t)m * a.H;
