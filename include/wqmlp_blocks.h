@@ -95,7 +95,8 @@ int moe_awq_run(int64_t M, int64_t E, int64_t topk, int64_t H, int64_t I, const 
  *   x        [M, H]  x_dtype: the next block's input
  * All types: WQ_F32, WQ_BF16 or WQ_F16 (the type of an absent tensor is ignored).  H: a multiple of 8.  eps >= 0.
  * Arithmetic is float32, rounded once to h_out and once to x: a row's squares, their sum and (backward) its products with the
- * gradients are formed as they stand and have to lie in float32's normal range, or below eps.  M == 0 is a valid empty call.
+ * gradients are formed as they stand and have to lie in float32's normal range, or below eps.  M == 0 is a valid empty call (with a
+ * gate of any G, 0 among them).
  */
 int block_norm_run(int64_t M, int64_t H, const void* h, int h_dtype, const void* y, int y_dtype, const void* post,
                    const void* pre, int w_dtype, const void* gate, int64_t G, int g_dtype, float alpha, float offset,

@@ -27,3 +27,27 @@ def test_in_place_with_absent_parts(H, ht, post, gate, pre):
     apart = wq.block_norm_backward(ho, y, dh, dx, **kw)
     for p, q in zip(wq.block_norm_backward(ho, y, dh, dx, dh_in=dh, **kw), apart):
         assert q is None or torch.equal(p, q)
+
+
+def test_no_rows_and_no_gate_rows():
+    """A gate for every row of an empty batch has G = M = 0 rows; with rows, G = 0 is refused."""
+    L, A, none = wq.lib(), 1 << 32, None
+    fwd = lambda M, G: L.block_norm_run(M, 64, none, 0, none, 0, A, A, 0, none, G, 0, 1.0, 0.0, 1e-6, none, none, 0, none)
+    bwd = lambda M, G: L.block_norm_backward(M, 64, none, 0, none, 0, none, none, 0, A, A, 0, none, G, 0, 1.0, 0.0, 1e-6, none, 0, none,
+                                             none, none, none, none, none)
+    assert fwd(0, 0) == 0 and bwd(0, 0) == 0 and L.block_norm_backward_workspace_bytes(0, 64, 0) == 0
+    assert fwd(4, 0) == -1 and bwd(4, 0) == -1 and L.block_norm_backward_workspace_bytes(4, 64, 0) == 0
+    assert fwd(0, -1) == -1 and bwd(0, -1) == -1
+
+
+@gpu
+def test_an_empty_batch_with_a_gate_for_every_row():
+    e = torch.empty((0, 64), device=DEV)
+    w = torch.ones(64, device=DEV)
+    ho, x = wq.block_norm_run(e, e, post=w, gate=e, pre=w)
+    assert ho.shape == x.shape == (0, 64)
+    dh, dy, dpost, dgate, dpre = wq.block_norm_backward(e, e, e, e, post=w, gate=e, pre=w, dpost=torch.ones(64, device=DEV))
+    assert dh.shape == dy.shape == dgate.shape == (0, 64)
+    assert (dpost == 0).all() and (dpre == 0).all()
+    with pytest.raises(ValueError, match="divisor"):
+        wq.block_norm_run(torch.ones((4, 64), device=DEV), torch.ones((4, 64), device=DEV), gate=e)

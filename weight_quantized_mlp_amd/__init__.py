@@ -733,7 +733,7 @@ def _norm_args(h, y, post, gate, pre):
         gt = _float_code(gate.dtype, "gate")
         if gate.dim() == 2:
             G = gate.shape[0]
-        if G == 0 or M % G:
+        if M % G if G else M:
             raise ValueError(f"gate must be [G, H] with G a divisor of the {M} rows, has {G} rows")
         _want(gate, "gate", gate.dtype, dev, G * H)
     return M, H, G, ht, yt, wt, gt

@@ -29,8 +29,9 @@ bool moe_shape_ok(int64_t M, int64_t E, int64_t topk, int64_t H, int64_t I) {
          E <= kMaxElems / (2 * I);
 }
 
+// A gate of its own for every row of none has no rows.
 bool norm_shape_ok(int64_t M, int64_t H, int64_t G) {
-  return M >= 0 && M <= kMaxDim && H > 0 && H <= kMaxDim && H % 8 == 0 && G > 0 && G <= kMaxDim && M % G == 0 &&
+  return M >= 0 && M <= kMaxDim && H > 0 && H <= kMaxDim && H % 8 == 0 && G >= 0 && G <= kMaxDim && (G == 0 ? M == 0 : M % G == 0) &&
          M * H <= kMaxElems && G * H <= kMaxElems;
 }
 

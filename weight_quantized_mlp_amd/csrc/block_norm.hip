@@ -656,7 +656,7 @@ hipError_t launch_block_norm_grad(int M, int H, const BlockNorm& n, const void* 
   if (M == 0) {
     const std::pair<float*, size_t> zeros[3] = {{dpost, (size_t)H}, {dgate, (size_t)n.G * H}, {dpre, (size_t)H}};
     for (auto [p, count] : zeros) {
-      if (p == nullptr) continue;
+      if (p == nullptr || count == 0) continue;
       hipLaunchKernelGGL(norm_zero_kernel, dim3((unsigned)((count + 255) / 256)), dim3(256), 0, st, p, count);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
