@@ -51,3 +51,26 @@ def test_an_empty_batch_with_a_gate_for_every_row():
     assert (dpost == 0).all() and (dpre == 0).all()
     with pytest.raises(ValueError, match="divisor"):
         wq.block_norm_run(torch.ones((4, 64), device=DEV), torch.ones((4, 64), device=DEV), gate=e)
+
+
+@gpu
+def test_the_most_rows_there_may_be():
+    """2^23 rows of 512 threads each: 2^32 threads, more than a grid dimension holds.  Every row's result is there, those around the
+    middle and at the ends are a small call's."""
+    M, H = 1 << 23, 3592
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 2 * M * H * 2 + (8 << 30):
+        pytest.skip("needs 129 GB of device memory")
+    h = torch.empty((M, H), dtype=BF16, device=DEV).fill_(2.0)
+    rows = torch.tensor([0, 1, (1 << 22) - 1, 1 << 22, M - 1], device=DEV)
+    h[rows] = randn(1, (5, H), BF16)[0]
+    w = torch.ones(H, dtype=BF16, device=DEV)
+    x = torch.zeros_like(h)
+    wq.block_norm_run(h, pre=w, x=x)
+    few = wq.block_norm_run(h[rows].contiguous(), pre=w, x_dtype=BF16)[1]
+    assert torch.equal(x[rows], few)
+    x[rows] = 1.0
+    for r in range(0, M, 1 << 18):                                  # 2 / sqrt(4 + 1e-6) rounds to 1
+        assert bool((x[r:r + (1 << 18)] == 1.0).all()), r
+    del h, x
+    torch.cuda.empty_cache()

@@ -18,6 +18,7 @@
 #include <type_traits>
 #include <utility>
 
+#include "../../include/wqmlp.h"
 #include "dev_common.h"
 #include "launch.h"
 
@@ -137,11 +138,17 @@ __device__ __forceinline__ void gate8(const NormArgs& a, int group, int at, floa
 }
 
 // ---- forward ---------------------------------------------------------------------------------------------------
+// A workgroup per row.  A grid dimension holds fewer than 2^32 threads; only 2^23 rows, the most there may be, of 512 threads reach
+// that, and go as two halves.  (A row test in the kernel, for any split, costs a short call 0.15 us of 4.)
+constexpr int kHalfRows = 1 << 22;
+__device__ __forceinline__ int forward_row() { return (int)blockIdx.y * kHalfRows + (int)blockIdx.x; }
+inline dim3 forward_grid(int M) { return M == 2 * kHalfRows ? dim3(kHalfRows, 2) : dim3(M); }
+static_assert(WQ_MAX_DIM == 2 * kHalfRows, "");
 // ho may be a.h itself (in place), so it is not declared restrict; a thread reads its elements of h before it writes them.
 template <bool H4, bool Y4, int RC>
 __global__ void __launch_bounds__(512) norm_run_kernel(NormArgs a, void* ho, void* __restrict__ xo) {
   __shared__ float buf[2 * kMaxWaves];
-  const int C = a.H / 8, T = (int)blockDim.x, t = (int)threadIdx.x, m = (int)blockIdx.x;
+  const int C = a.H / 8, T = (int)blockDim.x, t = (int)threadIdx.x, m = forward_row();
   const size_t row = (size_t)m * a.H;
   int turn = 0;
   Raw8 hr[RC], yr[RC];
@@ -203,7 +210,7 @@ __global__ void __launch_bounds__(512) norm_run_kernel(NormArgs a, void* ho, voi
 // Rows too long to hold: every pass reads them again, each thread the elements that it wrote itself.
 __global__ void __launch_bounds__(512) norm_run_long_kernel(NormArgs a, void* ho, void* __restrict__ xo) {
   __shared__ float buf[2 * kMaxWaves];
-  const int C = a.H / 8, T = (int)blockDim.x, t = (int)threadIdx.x, m = (int)blockIdx.x;
+  const int C = a.H / 8, T = (int)blockDim.x, t = (int)threadIdx.x, m = forward_row();
   const size_t row = (size_t)m * a.H;
   int turn = 0;
   float s[1] = {0.f}, v[8], r = 1.f;
@@ -631,13 +638,13 @@ hipError_t launch_block_norm(int M, int H, const BlockNorm& n, void* h_out, void
   if (!a.has_y) a.y = a.h, a.yt = a.ht;
   const int rc = held_chunks(H);
   if (rc == 0) {
-    hipLaunchKernelGGL(norm_run_long_kernel, dim3(M), dim3(512), 0, st, a, h_out, x);
+    hipLaunchKernelGGL(norm_run_long_kernel, forward_grid(M), dim3(512), 0, st, a, h_out, x);
     return hipGetLastError();
   }
   const int T = threads_for(H / 8, rc);
   auto go = [&](auto h4, auto y4, auto c) {
-    hipLaunchKernelGGL((norm_run_kernel<decltype(h4)::value, decltype(y4)::value, decltype(c)::value>), dim3(M), dim3(T), 0,
-                       st, a, h_out, x);
+    hipLaunchKernelGGL((norm_run_kernel<decltype(h4)::value, decltype(y4)::value, decltype(c)::value>), forward_grid(M), dim3(T),
+                       0, st, a, h_out, x);
   };
   auto by_rc = [&](auto h4, auto y4) {
     if (rc == 1) go(h4, y4, std::integral_constant<int, 1>{});
