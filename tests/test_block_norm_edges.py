@@ -74,3 +74,20 @@ def test_the_most_rows_there_may_be():
         assert bool((x[r:r + (1 << 18)] == 1.0).all()), r
     del h, x
     torch.cuda.empty_cache()
+
+
+@gpu
+def test_no_rows_and_many_gate_rows():
+    """Without rows the gate's gradient is zeros, all 2^32 + 2^23 of them."""
+    G, H = 1 << 20, 4104
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < G * H * 6 + (4 << 30):
+        pytest.skip("needs 30 GB of device memory")
+    e = torch.empty((0, H), dtype=BF16, device=DEV)
+    gate, dgate = torch.zeros((G, H), dtype=BF16, device=DEV), torch.full((G, H), 3.0, device=DEV)
+    got = wq.block_norm_backward(e, e, gate=gate, dgate=dgate)[3]
+    assert got is dgate
+    for r in range(0, G, 1 << 16):
+        assert not bool(dgate[r:r + (1 << 16)].any()), r
+    del gate, dgate, got
+    torch.cuda.empty_cache()

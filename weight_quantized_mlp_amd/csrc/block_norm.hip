@@ -596,9 +596,10 @@ __global__ void __launch_bounds__(1024) norm_join_kernel(int H, NormJoin j) {
     dst[at] = s;
   }
 }
+// (At most kZeroGrid workgroups: a gradient of gate rows may have more elements than a grid dimension holds threads.)
+constexpr size_t kZeroGrid = 1 << 20;
 __global__ void __launch_bounds__(256) norm_zero_kernel(float* __restrict__ p, size_t n) {
-  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
-  if (i < n) p[i] = 0.f;
+  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) p[i] = 0.f;
 }
 
 inline int threads_for(int C, int rc) { return ((C + rc - 1) / rc + 63) / 64 * 64; }
@@ -664,7 +665,7 @@ hipError_t launch_block_norm_grad(int M, int H, const BlockNorm& n, const void* 
     const std::pair<float*, size_t> zeros[3] = {{dpost, (size_t)H}, {dgate, (size_t)n.G * H}, {dpre, (size_t)H}};
     for (auto [p, count] : zeros) {
       if (p == nullptr || count == 0) continue;
-      hipLaunchKernelGGL(norm_zero_kernel, dim3((unsigned)((count + 255) / 256)), dim3(256), 0, st, p, count);
+      hipLaunchKernelGGL(norm_zero_kernel, dim3((unsigned)std::min((count + 255) / 256, kZeroGrid)), dim3(256), 0, st, p, count);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
