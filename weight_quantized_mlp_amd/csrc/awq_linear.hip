@@ -295,15 +295,12 @@ __global__ void __launch_bounds__(512, 4) awq_shared_kernel(int M, int N, int K,
       const int i = min(lane + 64 * j, ZP - 1), r = i / (ZROW / 16), c = i % (ZROW / 16);
       zp[j] = *reinterpret_cast<const u32x4_a1*>(zplane + min(ZB * (min(r, top) * G + min(16 * b0 + (16 / ZB) * c, G - 1)), zlast));
     }
-    constexpr int D = SB < 2 ? SB : 2;                          // blocks of codes on their way at once (more spill)
-    u32x4 cd[D][4];
-    auto load_codes = [&](int j) {
+    u32x4 cd[SB][4];
+#pragma unroll
+    for (int j = 0; j < SB; ++j)
 #pragma unroll
       for (int t = 0; t < 4; ++t)
-        cd[j % D][t] = *reinterpret_cast<const u32x4*>(codes + (uint32_t)(crow + 16 * min(16 * (b0 + j) + 4 * t + q, G - 1)));
-    };
-#pragma unroll
-    for (int j = 0; j < D; ++j) load_codes(j);
+        cd[j][t] = *reinterpret_cast<const u32x4*>(codes + (uint32_t)(crow + 16 * min(16 * (b0 + j) + 4 * t + q, G - 1)));
     if (p != p0) __syncthreads();                               // the last pass's readers of x are done
 #pragma unroll
     for (int r = 0; r < XR; ++r) {
@@ -360,7 +357,7 @@ __global__ void __launch_bounds__(512, 4) awq_shared_kernel(int M, int N, int K,
         awq_meta<ML>(a, 16 * b0 + at < G, s2, b2);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const f16x8 w = awq_frag(cd[j % D][t][i], s2, b2);
+          const f16x8 w = awq_frag(cd[j][t][i], s2, b2);
 #pragma unroll
           for (int c = 0; c < CT; ++c) {
             const int m = min(16 * c + (lane & 15), M - 1);
@@ -371,7 +368,6 @@ __global__ void __launch_bounds__(512, 4) awq_shared_kernel(int M, int N, int K,
           }
         }
       }
-      if (j + D < SB) load_codes(j + D);
     }
 #pragma unroll
     for (int c = 0; c < CT; ++c) {
@@ -663,7 +659,7 @@ void pack_rows(int M, int K, int steps, const void* x, uint8_t* xp, float* rs, h
 }
 
 template <int ML, int XS, int MR>
-hipError_t run_rows(const AwqPlan& p, int M, int N, int K, const void* x, const float*, const uint8_t* bank, const AwqLayout& L, float* y,
+hipError_t run_rows(const AwqPlan& p, int M, int N, int K, const void* x, const uint8_t* bank, const AwqLayout& L, float* y,
                     float* partials, hipStream_t st) {
   if (!raise_lds_limit<awq_rows_kernel<ML, XS, MR>>()) return hipErrorInvalidValue;
   const int sums = p.waves * M * 20 * 4, held = 16 * (K / 32) * ML + 32 + p.waves * MR * p.terms * 1024;
@@ -672,7 +668,7 @@ hipError_t run_rows(const AwqPlan& p, int M, int N, int K, const void* x, const 
   return hipGetLastError();
 }
 template <int ML, int XS, int CT>
-hipError_t run_shared(const AwqPlan& p, int M, int N, int K, const void* x, const float*, const uint8_t* bank, const AwqLayout& L, float* y,
+hipError_t run_shared(const AwqPlan& p, int M, int N, int K, const void* x, const uint8_t* bank, const AwqLayout& L, float* y,
                       float* partials, hipStream_t st) {
   if (!raise_lds_limit<awq_shared_kernel<ML, XS, CT>>()) return hipErrorInvalidValue;
   const int sb = shared_blocks(CT * p.terms), lds = 16 * CT * p.terms * (sb * 1024 + 16) + kSharedWaves * 16 * sb * 16 * ML + 16 * CT * 4;
@@ -681,7 +677,7 @@ hipError_t run_shared(const AwqPlan& p, int M, int N, int K, const void* x, cons
   return hipGetLastError();
 }
 template <int ML, int TERMS, int MT>
-hipError_t run_gemm(const AwqPlan& p, int M, int N, int, const void* xp, const float* rs, const uint8_t* bank, const AwqLayout& L,
+hipError_t run_gemm(const AwqPlan& p, int M, int N, const void* xp, const float* rs, const uint8_t* bank, const AwqLayout& L,
                     float* y, float* partials, hipStream_t st) {
   if (!raise_lds_limit<awq_gemm_kernel<ML, TERMS, MT>>()) return hipErrorInvalidValue;
   const TilePlan& t = p.t;
@@ -692,19 +688,23 @@ hipError_t run_gemm(const AwqPlan& p, int M, int N, int, const void* xp, const f
   hipLaunchKernelGGL(awq_tiles_join_kernel, dim3((unsigned)(t.units / t.S) * 16 * MT), dim3(256), 0, st, M, N, t, partials, y);
   return hipGetLastError();
 }
-template <int ML, int XT, typename... A>
-hipError_t run_plan(const AwqPlan& p, int M, A... a) {
+// x: its terms and rs their scales (kTiles), else x itself.
+template <int ML, int XT>
+hipError_t run_plan(const AwqPlan& p, int M, int N, int K, const void* x, const float* rs, const uint8_t* bank, const AwqLayout& L, float* y,
+                    float* partials, hipStream_t st) {
   constexpr int T = XT == X_F32 ? 2 : 1;
   switch (p.kind) {
     case AwqPlan::kOwn:
-      if (M == 1) return run_rows<ML, XT, 1>(p, M, a...);
-      return run_rows<ML, XT, 2>(p, M, a...);
-    case AwqPlan::kShared: return p.ct == 1 ? run_shared<ML, XT, 1>(p, M, a...) : run_shared<ML, XT, 2>(p, M, a...);
+      if (M == 1) return run_rows<ML, XT, 1>(p, M, N, K, x, bank, L, y, partials, st);
+      return run_rows<ML, XT, 2>(p, M, N, K, x, bank, L, y, partials, st);
+    case AwqPlan::kShared:
+      return p.ct == 1 ? run_shared<ML, XT, 1>(p, M, N, K, x, bank, L, y, partials, st)
+                       : run_shared<ML, XT, 2>(p, M, N, K, x, bank, L, y, partials, st);
     default: break;
   }
   if constexpr (T == 1)
-    if (p.t.mt == 8) return run_gemm<ML, T, 8>(p, M, a...);
-  return run_gemm<ML, T, 4>(p, M, a...);
+    if (p.t.mt == 8) return run_gemm<ML, T, 8>(p, M, N, x, rs, bank, L, y, partials, st);
+  return run_gemm<ML, T, 4>(p, M, N, x, rs, bank, L, y, partials, st);
 }
 template <int XT>
 hipError_t linear(const AwqPlan& p, int M, int N, int K, const void* x, const uint8_t* bank, int meta_layout, uint8_t* ws, float* y,
