@@ -30,7 +30,8 @@ extern "C" {
  * of two so that their largest finite magnitude lies in [2^14, 2^15) and enter as one (bfloat16) or two (float32) float16 terms: a
  * bfloat16 element is off by at most 2^-39 of its row's largest, a float32 one by 2^-22 of itself or 2^-39 of its
  * row's largest, whichever is more.  A row's result does not depend on the other rows' values; NaN and infinities
- * stay in their row.  M == 0 is a valid empty call.
+ * stay in their row.  Weights have to decode to finite values: an infinite one may make NaN of its results.  M == 0 is a valid
+ * empty call.
  */
 size_t awq_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int x_dtype);
 int awq_linear_run(int64_t M, int64_t N, int64_t K, const void* x, int x_dtype, const void* bank, int meta_layout,

@@ -5,8 +5,8 @@
 // turned into float16 terms (awq_pack_kernel), in the order the matrix cores read it.
 //   Up to kOwnRows rows (awq_rows_kernel) and up to kFewRows (awq_shared_kernel): the weights' bytes bound it, and with them the
 //     decode, so what matters is that every CU has work from the start and reads whole cache lines.  x is turned into terms by the
-//     waves themselves, which spares a launch.  Calls in a row: 1 float16 row 5120 -> 17408 13.4 us (53 MB, 4.0 TB/s; bfloat16 15.8,
-//     float32 19), 13 bfloat16 rows 17408 -> 5120 20.7 us, of which the parts' sum takes 3.
+//     waves themselves, which spares a launch.  Calls in a row: 1 float16 row 5120 -> 17408 13-15 us (53 MB, 3.5-4.1 TB/s; bfloat16 16,
+//     float32 18), 17408 -> 5120 17 (20.5, 23); 13 bfloat16 rows 17408 -> 5120 18-20 us, of which the parts' sum takes 4.
 //   More rows (awq_gemm_kernel): the matrix cores bound it.  4 waves with 64 weight rows each share the tile of x through
 //     LDS (global->LDS copies, two stages); every wave decodes only its own weights, once per tile row.  2049 bfloat16 rows
 //     5120 -> 17408: 447 us (817 TFLOP/s), of which x's terms take 15 and the cut tiles' sum 15; a float16 product of those sizes in
@@ -386,9 +386,10 @@ __global__ void __launch_bounds__(512, 4) awq_shared_kernel(int M, int N, int K,
 }
 
 // ---- many rows ---------------------------------------------------------------------------------------------------
-// Tile: 16 MT rows of x by 256 weight rows, 64 per wave.  The tiles of the last, unfilled round are cut into S parts of `per` steps
-// (512 rows 5120 -> 17408: 179 us uncut, 147; 2049 rows: 461 and 447; cut tiles before the whole ones, which lets all run out of
-// step and miss L2: 15% slower).
+// Tile: 16 MT rows of x by 256 weight rows, 64 per wave.  Where the tiles of the last, unfilled round fit it twice or more, they are
+// cut into S parts of `per` steps (bfloat16 rows 5120 -> 17408, uncut and cut: 48 99 and 48 us, 128 137 and 64, 256 138 and 96, 1024 297 and
+// 232, 2049 469 and 447; 17408 -> 5120: 128 429 and 73, 512 434 and 148, 1024 463 and 245; cut tiles before the whole ones, which lets all
+// run out of step and miss L2: 15% slower).  A last round of 257 to 511 tiles stays whole: 512 rows 5120 -> 17408 are 272, 148 us.
 constexpr int kGemmCols = 256, kSlots = 512;   // workgroups the chip runs at once: two per CU
 
 struct TilePlan {
@@ -590,8 +591,10 @@ __global__ void __launch_bounds__(256) awq_join_kernel(int M, int N, int S, cons
 }
 
 // ---- plan --------------------------------------------------------------------------------------------------------
-// Workgroups of awq_shared_kernel to split up to: three per CU with two blocks at a time, else two.  13 rows 5120 -> 17408: 256 26.5 us,
-// 512 24.4, 768 20.6, 1536 20.4; 24 rows: 256 33.7, 512 25.1, 768 26.8.
+// Workgroups of awq_shared_kernel to split up to: three per CU with two blocks at a time, else two.  256, 512, 768 and 1536 of them: 13
+// bfloat16 rows 5120 -> 17408 24.5, 23.0, 19.1 and 19.1 us, 17408 -> 5120 20.7, 22.9, 19.6 and 19.5; 24 rows (one block at a time) 32.6, 23.9,
+// 24.4 and 24.8, and 29.6, 23.3, 25.3 and 25.3; 8 float32 rows 28.0, 20.7, 20.8 and 20.1, and 25.8, 20.4, 21.2 and 21.4.  5120 -> 5120 and 2560 ->
+// 9728, 4 to 24 rows: within 0.3 us of each other from 512 on.
 constexpr int shared_fill(int tiles) { return tiles == 1 ? 768 : 512; }
 
 struct AwqPlan {

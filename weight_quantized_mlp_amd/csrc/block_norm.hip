@@ -5,7 +5,7 @@
 // the row sums, so a pass moves the bytes of its inputs and outputs and nothing else.  Rows above 16384 elements (backward: 8192,
 // where the columns' sums take registers, too) are read again for every pass instead (they come from L2).  HBM bounds long calls,
 // the chain of load, row sum, row sum and store short ones.  Calls in a row: 8191 x 5120 float32 116 us (588 MB, 5.1 TB/s), one
-// bfloat16 row of 2560 3.3 us on the device (11 a call, the binding's); backward 4096 x 5120 bfloat16 65 us (252 MB, 3.9 TB/s),
+// bfloat16 row of 2560 3.3 us on the device (11 a call, the binding's); backward 4096 x 5120 bfloat16 63 us (252 MB, 4.0 TB/s),
 // 129 x 320 float32 8 us on the device in two launches.
 //
 // Backward, with n = t r the normed row and dn its gradient: dt = r (dn - n mean(dn n)).  Every factor is applied as it stands there; r^3,
@@ -311,8 +311,9 @@ __device__ __forceinline__ float norm_du(bool has_pre, bool has_dh, float ru, fl
 }
 
 // Rows in registers.  Of one chunk per thread the next row's loads are on their way while this one's sums are formed; the weights and
-// the gate row (until it changes) stay in registers.  A row is some 25 operations per element, which take as long as its bytes, so
-// what is absent is zeroed once instead of selected, and the decoding of 2-byte tensors does not branch where all of them are bfloat16 (BF).
+// the gate row (until it changes) stay in registers.  One workgroup fills a CU, so a row's operations stand in its chain beside the two
+// row sums, with nothing else to run meanwhile (spread evenly over all lanes they are 13 us of the 63): what is absent is zeroed once instead of selected,
+// and the decoding of 2-byte tensors does not branch where all of them are bfloat16 (BF; 4096 x 2560: 57 us without either, 36).
 template <bool W4, bool BF>
 __device__ __forceinline__ void row_values(const Raw8& r, int type, float (&v)[8]) {
   if constexpr (W4) values8(r, X_F32, v);
@@ -463,8 +464,8 @@ __global__ void __launch_bounds__(RC == 1 ? 640 : 512) norm_grad_kernel(NormArgs
   }
 }
 
-// Rows too long to hold.  A workgroup per row: dh_in, dy and the row's scalars; the columns' sums follow in
-// norm_grad_cols_kernel, from the inputs again.
+// Rows too long to hold.  A workgroup per row: dy and the row's scalars; dh_in and the columns' sums follow in
+// norm_grad_cols_kernel, from the inputs again, so that dh_in may stand where dh does.
 __global__ void __launch_bounds__(512) norm_grad_long_kernel(NormArgs a, GradOut o, RowScalars* __restrict__ rows) {
   __shared__ float buf2[2 * 3 * kMaxWaves], buf1[2 * kMaxWaves];
   const int C = a.H / 8, T = (int)blockDim.x, t = (int)threadIdx.x, m = (int)blockIdx.x;

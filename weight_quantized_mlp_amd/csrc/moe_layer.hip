@@ -163,7 +163,8 @@ __global__ void __launch_bounds__(64) route_topk_kernel(int E, int topk, int ren
 // turns up to `cols` of the routes' rows into float16 terms there, 512 k at a time with a power of two of their own, and multiplies.
 //   Many routes: a wave takes whole pairs, block after block of 512 k, each step's codes replaced by the next block's as soon as
 //     they are used, and nothing is exchanged between waves.
-//   Few routes (SPLIT): the waves of a workgroup share one pair's blocks, so that one token's experts reach all CUs.
+//   Few routes (SPLIT): the waves of a workgroup share one pair's blocks, so that a workgroup needs no more than one pair: 10 routes of
+//     160 on 2560 are 100 workgroups of 5 waves in W13.
 // Either way a column's blocks are added in order, each scaled by a power of two, which is exact: its bits depend neither on the way nor on
 // how many columns there are.
 constexpr int kPartRow = 20;                   // floats of a row of partial sums: 16, padded
@@ -457,8 +458,11 @@ inline MoeWs moe_ws(int M, int E, int topk, int H, int I) {
 // Columns of a pass: two and a half times what an expert has on average, in at most 64 KB of terms.  Pairs of a workgroup, in at most 48 KB
 // of metadata (or one pair): few experts are cut into 260 workgroups, whose up to 16 waves share the columns' terms; many, with a column or
 // two each, into 1200, of which several fit a CU.  130 rows, 64 experts of 704 on 1024: 260 73 us, 530 80, 800 94; 37 rows, 512 experts of
-// 160 on 2560: 400 121 us, 800 103, 1200 97, 1600 109.  The blocks are split over waves where whole pairs would leave the chip with less than
-// two waves per CU.
+// 160 on 2560: 400 121 us, 800 103, 1200 97, 1600 109.  Where it changes: items are the experts or, if fewer, the routes; at 64, 128, 160
+// and 256 of them (260 workgroups of up to 16 waves against 1200 of up to 8) bfloat16 experts of 160 on 2560 with a row each take 38 and 46 us,
+// 45 and 54, 70 and 58, 86 and 73, of 512 on 2048 with two rows each 47 and 50, 77 and 82, 109 and 105, 138 and 132, float32 ones of 704 on
+// 1024 with six rows each 48 and 67, 88 and 111, 120 and 123, 163 and 178 (these would keep the 260).
+// The blocks are split over waves where whole pairs would leave the chip with less than two waves per CU.
 struct MoePlan {
   MoeShape s;
   bool split;
