@@ -91,3 +91,17 @@ def test_no_rows_and_many_gate_rows():
         assert not bool(dgate[r:r + (1 << 16)].any()), r
     del gate, dgate, got
     torch.cuda.empty_cache()
+
+
+@gpu
+def test_sums_of_runs_keep_small_ones():
+    """32 runs of a row each: a sum of 2^24 and 31 ones.  Added in pairs the chain has five roundings, each at most half of the spacing
+    (2) of what it forms: off by 5 at most.  One after the other, every one of them would be lost."""
+    h = torch.ones((32, 64), device=DEV)
+    dx = torch.ones((32, 64), device=DEV)
+    dx[3] = 2.0 ** 24
+    kw = dict(post=torch.ones(64, device=DEV), gate=torch.ones((1, 64), device=DEV), pre=torch.zeros(64, device=DEV), eps=0.0)
+    dpre = wq.block_norm_backward(h, h, h, dx, **kw)[4]
+    assert ((dpre.double() - (2.0 ** 24 + 31)).abs() <= 5).all(), dpre[0].item()
+    _, _, dpost, dgate, _ = wq.block_norm_backward(h, h, dx, h, **kw)         # pre = 0: du = dh
+    assert ((dpost.double() - (2.0 ** 24 + 31)).abs() <= 5).all() and ((dgate.double() - (2.0 ** 24 + 31)).abs() <= 5).all()

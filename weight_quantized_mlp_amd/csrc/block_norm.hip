@@ -565,8 +565,8 @@ __global__ void __launch_bounds__(64) norm_grad_cols_kernel(NormArgs a, NormRuns
   if (o.dgate != nullptr && p.S > 1) store8(o.dgate, at, X_F32, sgate);
 }
 
-// Sums of the runs, in order: thread (column, lane of 32) adds every 32nd run, then the 32 lanes in order.  blockIdx.y: dpre, dpost,
-// then the gate rows, each over its own S runs.
+// Sums of the runs, in order: thread (column, lane of 32) adds every 32nd run, then the 32 lanes' sums in pairs, 16
+// apart, then 8, ... (five roundings in a chain instead of 31).  blockIdx.y: dpre, dpost, then the gate rows, each over its own S runs.
 struct NormJoin {
   const float* src[3];
   float* dst[3];               // dpre, dpost, dgate (null: none)
@@ -592,9 +592,14 @@ __global__ void __launch_bounds__(1024) norm_join_kernel(int H, NormJoin j) {
   part[k][col] = s;
   __syncthreads();
   if (k == 0 && at < H) {
-    s = 0.f;
-    for (int i = 0; i < 32; ++i) s += part[i][col];
-    dst[at] = s;
+    float v[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = part[i][col];
+#pragma unroll
+    for (int half = 16; half >= 1; half >>= 1)
+#pragma unroll
+      for (int i = 0; i < half; ++i) v[i] += v[i + half];
+    dst[at] = v[0];
   }
 }
 // (At most kZeroGrid workgroups: a gradient of gate rows may have more elements than a grid dimension holds threads.)
