@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import weight_quantized_mlp_amd as wq
-from adapter_common import DEV, U, host, randn
+from adapter_common import DEV, host, randn
 from test_moe_layer import check, layer, layer_ref, route_ref
 
 F32, BF16, F16 = torch.float32, torch.bfloat16, torch.float16
